@@ -64,6 +64,10 @@ typedef enum {
 typedef enum { MXQ_MXFP8 = 1, MXQ_NVFP4 = 2, MXQ_BF16 = 3, MXQ_MXFP4 = 4, MXQ_BF16_NVFP4T = 5 } mxq_format;
 typedef enum { MXQ_OUT_BF16 = 0, MXQ_OUT_F32 = 1 } mxq_out_dtype;
 
+/* How the gate of a block's output (rows, cols) is laid out: none, FP32 (rows) -- one value
+ * per token --, FP32 (cols) -- one per channel --, or FP32 (rows, cols). */
+typedef enum { MXQ_GATE_NONE = 0, MXQ_GATE_TOKEN = 1, MXQ_GATE_CHANNEL = 2, MXQ_GATE_FULL = 3 } mxq_gate_mode;
+
 /* Scope of an NVFP4 FP32 (second-level) scale.
  *  ROW    : one scale per row (per token for activations), t has `rows` entries;
  *  TENSOR : one scale for the whole tensor, t has 1 entry;
@@ -603,17 +607,157 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
                        void* stream);
 
 /* ---------------------------------------------------------------------------
+ * rmsnorm_quantize -- the RMSNorm ahead of a block with the quantizer as its epilogue: one
+ * read of the hidden states gives the BF16 normed rows, their quantized copy and the row
+ * statistic that the backward pass reads.
+ *   r = (mean over the row of x^2 + eps)^(-1/2);  n = x r w, rounded once to BF16;  then the
+ *   row quantizer of the format on that BF16 row: the bytes of quantize_mxfp8 /
+ *   quantize_mxfp4 (rowwise copy) or quantize_nvfp4_per_token on n.
+ *   n is evaluated in binary64 (relative error below 2^-50) and rounded to nearest even: the
+ *   correctly rounded value unless the exact one lies that close to a rounding midpoint.
+ *
+ *   fmt    : MXQ_MXFP8, MXQ_MXFP4, MXQ_NVFP4 (per token), or MXQ_BF16 (n only; q, s, t unused).
+ *   x      : (rows, cols), x_dtype MXQ_OUT_BF16 or MXQ_OUT_F32, row stride ld_x (a multiple of
+ *            16 bytes). weight: FP32 (cols), NULL = ones.
+ *   n_bf16 : BF16 (rows, cols), NULL = not written (required for MXQ_BF16).
+ *   q, s, t: as the format's row quantizer writes them (t: MXQ_NVFP4 only).
+ *   rstd   : FP32 (rows), r rounded, NULL = not written.
+ *   Requires eps > 0 (MXQ_ERR_FORMAT), cols % 32 == 0 (MXFP8, MXFP4), % 16 (NVFP4), % 8
+ *   (BF16), and cols <= 16384 (a row is held in the registers of one workgroup).
+ * ------------------------------------------------------------------------- */
+mxq_status rmsnorm_quantize(mxq_format fmt, const void* x, mxq_out_dtype x_dtype, int64_t rows, int64_t cols,
+                            int64_t ld_x, const float* weight, double eps, void* n_bf16, void* q, void* s, float* t,
+                            float* rstd, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * rmsnorm_backward -- gradients of rmsnorm_quantize's n (the quantizer is passed straight
+ * through, as the block's own backward does), the residual branch's gradient added.
+ *   g = (dn + dn2) w;  xh = x r;  dx = r (g - xh mean over the row of g xh) + res_scale d_res;
+ *   dw = sum over the rows of (dn + dn2) xh, in a fixed order (the same bits on every run).
+ *   dn, dn2 : (rows, cols) dn_dtype; dn2 NULL = none (a block whose input feeds two consumers,
+ *             e.g. the experts and the router, hands in both gradients).
+ *   x       : (rows, cols) x_dtype, contiguous; rstd: FP32 (rows) from the forward pass.
+ *   d_res   : (rows, cols) x_dtype, NULL = none.  dx: (rows, cols) x_dtype.
+ *   dw      : FP32 (cols), NULL = not wanted; needs a weight (MXQ_ERR_FORMAT without one) and
+ *             the workspace, mxq_workspace_bytes(MXQ_OP_NORM_BACKWARD, rows, cols, 0) bytes,
+ *             16-byte aligned (rows = 0: no workspace, dw is cleared).
+ *   Requires cols % 8 == 0, cols <= 16384. dx must not overlap an input.
+ * ------------------------------------------------------------------------- */
+mxq_status rmsnorm_backward(const void* dn, const void* dn2, mxq_out_dtype dn_dtype, const void* x,
+                            mxq_out_dtype x_dtype, const float* rstd, const float* weight, const void* d_res,
+                            float res_scale, int64_t rows, int64_t cols, void* dx, float* dw, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * rmsnorm_gate_residual -- what closes a block: the RMSNorm of its output y, the block's gate,
+ * and the residual stream x, in one pass.
+ *   r = (mean over the row of y^2 + eps)^(-1/2);
+ *   out = res_scale x + branch_scale gate (y r w), in binary32, rounded once to x_dtype.
+ *   x, out : (rows, cols) x_dtype; y: (rows, cols) y_dtype; weight: FP32 (cols), NULL = ones.
+ *   gate   : FP32, laid out as gate_mode says (NULL with MXQ_GATE_NONE).
+ *   rstd   : FP32 (rows), NULL = not written. Requires eps > 0, cols % 8 == 0, cols <= 16384.
+ * ------------------------------------------------------------------------- */
+mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const void* y, mxq_out_dtype y_dtype,
+                                 const float* weight, const float* gate, mxq_gate_mode gate_mode, double eps,
+                                 float branch_scale, float res_scale, int64_t rows, int64_t cols, void* out,
+                                 float* rstd, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * rmsnorm_gate_residual_backward -- its gradients. The residual's own gradient is
+ * res_scale d_out: hand d_out and res_scale to rmsnorm_backward of the same block.
+ *   d = branch_scale d_out;  g = d gate w;  yh = y r;
+ *   dy = r (g - yh mean over the row of g yh);  dw = sum over the rows of d gate yh;
+ *   dgate = d yh w, summed over what the gate is broadcast over.
+ *   d_out : (rows, cols) d_dtype; y, dy: (rows, cols) y_dtype; rstd from the forward pass.
+ *   dw    : FP32 (cols), NULL = not wanted.  dgate: FP32 in the gate's layout, NULL = not wanted.
+ *   workspace : as rmsnorm_backward, needed for dw and for the gradient of a channel gate.
+ * ------------------------------------------------------------------------- */
+mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dtype, const void* y,
+                                          mxq_out_dtype y_dtype, const float* rstd, const float* weight,
+                                          const float* gate, mxq_gate_mode gate_mode, float branch_scale,
+                                          int64_t rows, int64_t cols, void* dy, float* dw, float* dgate,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route -- the router of an expert layer on the device: top-k choice, combine weights,
+ * per-expert counts, the expert-major slots that grouped_gemm_block_scaled and moe_combine
+ * read, and the balance loss.
+ *   A token's chosen experts are its topk largest logits, ties to the lower expert index,
+ *   listed in descending order; its weights are the softmax over all experts restricted to
+ *   them and renormalised. An expert at minus infinity (or NaN) is never chosen: a token with
+ *   fewer usable experts than topk ends its list with index -1, weight 0, slot -1. A token
+ *   with valid[t] = 0 (a padding token of the batch) or without a usable expert is not routed:
+ *   its whole list reads -1, 0, -1, and it counts nowhere. +Inf logits are outside the domain.
+ *   loss = balance_coef * experts * sum over e of (counts_e / A) (1/N) sum over t of p_te, with
+ *   p the softmax over all experts, A = the sum of the counts, N = the routed tokens (0 for
+ *   N = 0). The slots of an expert are its tokens ascending, then padding: every range is a
+ *   multiple of pad, and the slots that the routing leaves of `total` are dealt out as further
+ *   padding in units of pad, evenly, lower experts first, so that offsets[experts] = total
+ *   without the host knowing the counts.
+ *
+ *   logits    : FP32 (tokens, experts), row stride ld >= experts. valid: uint8 (tokens), NULL = all.
+ *   total     : slots, a multiple of pad, at least mxq_route_slots(tokens, experts, topk, pad).
+ *   topk_idx  : int32 (tokens, topk);  weights: FP32 (tokens, topk);
+ *   counts    : int32 (experts + 1): the tokens that chose each expert, then N;
+ *   offsets   : int64 (experts + 1);  row_index: int32 (total), the token of a slot, -1 = padding;
+ *   slot_of   : int64 (tokens, topk);  loss: FP32 (1), NULL = not wanted.
+ *   workspace : mxq_workspace_bytes(MXQ_OP_ROUTE, tokens, experts, 0) bytes, 16-byte aligned.
+ *   Requires 1 <= topk <= 32, topk <= experts <= 1024, total < 2^31.
+ * ------------------------------------------------------------------------- */
+mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
+                     int64_t topk, int64_t pad, int64_t total, float balance_coef, int32_t* topk_idx, float* weights,
+                     int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route_backward -- the gradient of the combine weights and of the balance loss to the
+ * logits (the counts are constants, as the choice is).
+ *   d = w (dw - sum over the chosen of w dw) on the chosen experts, plus
+ *   p (c - sum over e of p_e c_e) with c_e = d_loss balance_coef experts counts_e / (A N).
+ *   topk_idx, weights, counts: from moe_route; a token that is not routed gets zeros.
+ *   d_weights : FP32 (tokens, topk), NULL = none;  d_loss: FP32 (1) on the device, NULL = none.
+ *   d_logits  : FP32 (tokens, experts), contiguous. Limits as moe_route.
+ * ------------------------------------------------------------------------- */
+mxq_status moe_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
+                              const int32_t* topk_idx, const float* weights, const float* d_weights,
+                              const int32_t* counts, const float* d_loss, float balance_coef, float* d_logits,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_combine_backward -- gradients of moe_combine: to the expert outputs, in the BF16 slot
+ * layout that the experts' backward GEMMs read, and to the combine weights.
+ *   d_o[slot_of[t, j]] = w[t, j] dy[t], rounded to BF16;  d_weights[t, j] = <dy[t], O[slot_of[t, j]]>;
+ *   the rows of padding slots (row_index < 0) are cleared.
+ *   dy        : (tokens, hidden) dy_dtype;  o_slots: FP32 (total_slots, hidden);
+ *   slot_of, weights, row_index: the plan of moe_route (a slot index outside
+ *   [0, total_slots) contributes nothing and gets d_weights 0);
+ *   d_o_bf16  : BF16 (total_slots, hidden);  d_weights: FP32 (tokens, topk).
+ *   Requires hidden % 8 == 0, hidden <= 16384, topk <= 32.
+ * ------------------------------------------------------------------------- */
+mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const float* o_slots, int64_t total_slots,
+                                int64_t tokens, int64_t topk, int64_t hidden, const int64_t* slot_of,
+                                const float* weights, const int32_t* row_index, void* d_o_bf16, float* d_weights,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
  * Queries.
  * ------------------------------------------------------------------------- */
 /* Bytes of the scale matrix for a (rows, cols) tensor blocked along cols
  * (MXFP8, MXFP4: rows * cols/32, NVFP4: rows * cols/16); 0 for BF16 or bad shapes. */
 size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols);
 
-enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2 };
+enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD = 3, MXQ_OP_ROUTE = 4 };
 /* Workspace bytes for an op:
  *   MXQ_OP_QUANTIZE_NVFP4 (a = rows, b = cols, c = number of FP32 scales);
- *   MXQ_OP_GROUPED_GEMM   (a = groups). */
+ *   MXQ_OP_GROUPED_GEMM   (a = groups);
+ *   MXQ_OP_NORM_BACKWARD  (a = rows, b = cols);
+ *   MXQ_OP_ROUTE          (a = tokens, b = experts). */
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
+
+/* Slots that hold every routing of `tokens` tokens over `experts` experts, topk each, with
+ * every expert's range a multiple of pad (moe_route's smallest `total`); -1 for sizes that
+ * moe_route refuses. */
+int64_t mxq_route_slots(int64_t tokens, int64_t experts, int64_t topk, int64_t pad);
 
 const char* mxq_status_string(mxq_status s);
 int mxq_abi_version(void);

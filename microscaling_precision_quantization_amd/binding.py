@@ -24,12 +24,15 @@ BF16_NVFP4T = 5                    # grouped only: BF16 A x stacked NVFP4 weight
 _PACKED4 = (NVFP4, MXFP4)          # formats with two elements per byte
 OUT_BF16, OUT_F32 = 0, 1
 SCOPE = {"row": 0, "token": 0, "tensor": 1, "group": 2}
-OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM = 1, 2
+OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE = 1, 2, 3, 4
+GATE = {"none": 0, "token": 1, "channel": 2, "full": 3}
 
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _size = ctypes.c_size_t
+_f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 _SIGS = {
     "quantize_mxfp8": [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
@@ -64,12 +67,28 @@ _SIGS = {
                                           _int, _c_void_p, _c_void_p],
     "moe_swiglu_quantize_nvfp4": [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
     "moe_combine": [_c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    "rmsnorm_quantize": [_int, _c_void_p, _int, _i64, _i64, _i64, _c_void_p, _f64, _c_void_p, _c_void_p, _c_void_p,
+                         _c_void_p, _c_void_p, _c_void_p],
+    "rmsnorm_backward": [_c_void_p, _c_void_p, _int, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _f32, _i64, _i64,
+                         _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
+    "rmsnorm_gate_residual": [_c_void_p, _int, _c_void_p, _int, _c_void_p, _c_void_p, _int, _f64, _f32, _f32, _i64, _i64,
+                              _c_void_p, _c_void_p, _c_void_p],
+    "rmsnorm_gate_residual_backward": [_c_void_p, _int, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _int, _f32,
+                                       _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
+    "moe_route": [_c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p,
+                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
+    "moe_route_backward": [_c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                           _f32, _c_void_p, _c_void_p],
+    "moe_combine_backward": [_c_void_p, _int, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                             _c_void_p, _c_void_p, _c_void_p],
+    "mxq_route_slots": [_i64, _i64, _i64, _i64],
     "mxq_scale_bytes": [_int, _i64, _i64],
     "mxq_workspace_bytes": [_int, _i64, _i64, _i64],
     "mxq_status_string": [_int],
     "mxq_abi_version": [],
 }
-_RESTYPES = {"mxq_scale_bytes": _size, "mxq_workspace_bytes": _size, "mxq_status_string": ctypes.c_char_p}
+_RESTYPES = {"mxq_scale_bytes": _size, "mxq_workspace_bytes": _size, "mxq_route_slots": _i64,
+             "mxq_status_string": ctypes.c_char_p}
 
 _lib = None
 
@@ -111,6 +130,16 @@ def _ptr(t):
 
 def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(fn: str, dev, *args):
+    """One C-ABI call on dev's current stream (the last argument), with dev the current device:
+    a kernel is launched on the device that is current, whatever its stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
 
 
 def _bf16(x):
@@ -688,6 +717,275 @@ def moe_combine(o_slots: torch.Tensor, slot_of: torch.Tensor, weights: torch.Ten
                                             _ptr(out),
                                             _stream(o_slots.device)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Norms around a block
+# ---------------------------------------------------------------------------
+
+def _float_dtype(t, name: str) -> int:
+    """MXQ_OUT_* code of a BF16 or FP32 tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: expected a bfloat16 or float32 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor (rows, cols)")
+    return OUT_F32 if t.dtype == torch.float32 else OUT_BF16
+
+
+def _need_gate(c, gate, gate_mode: str, name: str, rows: int, cols: int) -> int:
+    if gate_mode not in GATE:
+        raise ValueError(f"gate_mode: {gate_mode!r}, expected one of {sorted(GATE)}")
+    mode = GATE[gate_mode]
+    if mode == 0 and gate is not None:
+        raise ValueError(f"{name}: gate_mode is 'none'")
+    if mode:
+        c.need(gate, name, torch.float32, {1: (rows,), 2: (cols,), 3: (rows, cols)}[mode])
+    return mode
+
+
+def _workspace(op: int, a: int, b: int, workspace, dev):
+    """The call's scratch: allocated here, or the caller's, checked for size and device."""
+    need = lib().mxq_workspace_bytes(op, a, b, 0)
+    if workspace is None:
+        return _u8((need,), dev)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace: expected contiguous uint8 memory on {dev}")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace: {workspace.numel()} bytes, the call needs {need}")
+    return workspace
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, fmt: int = NVFP4,
+                     keep_n: bool = True, out=None):
+    """RMSNorm of BF16 or FP32 x (T, H), rounded to BF16 and quantized row by row in one pass:
+    (n | None, q | None, s | None, t | None, rstd). fmt: MXFP8, MXFP4, NVFP4 (per token) or
+    BF16 (n only). `out` may supply preallocated (n, q, s, t, rstd); n None there = not written."""
+    xd = _float_dtype(x, "x")
+    if fmt not in (MXFP8, NVFP4, BF16, MXFP4):
+        raise ValueError(f"unknown format {fmt}")
+    T, H = x.shape
+    dev = x.device
+    c = _Checks(dev)
+    c.need(x, "x", x.dtype, (T, H), ld=True)
+    c.opt(weight, "weight", torch.float32, (H,))
+    if out is None:
+        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_n or fmt == BF16 else None
+        q = s = t = None
+        if fmt != BF16:
+            q, s = _u8((T, H // _elems_per_byte(fmt)), dev), _u8((T, H // _scale_block(fmt)), dev)
+        if fmt == NVFP4:
+            t = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        n, q, s, t, rstd = out
+        (c.need if fmt == BF16 else c.opt)(n, "n", torch.bfloat16, (T, H))
+        if fmt != BF16:
+            c.need(q, "q", torch.uint8, (T, H // _elems_per_byte(fmt)))
+            c.need(s, "s", torch.uint8, (T, H // _scale_block(fmt)))
+        if fmt == NVFP4:
+            c.need(t, "t", torch.float32, (T,))
+        c.opt(rstd, "rstd", torch.float32, (T,))
+    c.done()
+    _call("rmsnorm_quantize", dev, fmt, _ptr(x), xd, T, H, max(x.stride(0), H), _ptr(weight), eps, _ptr(n), _ptr(q),
+          _ptr(s), _ptr(t), _ptr(rstd))
+    return n, q, s, t, rstd
+
+
+def rmsnorm_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None,
+                     dn2: torch.Tensor | None = None, d_res: torch.Tensor | None = None, res_scale: float = 1.0,
+                     out=None, workspace: torch.Tensor | None = None):
+    """Gradients of rmsnorm_quantize's n: (dx in x's type, dw FP32 | None). dn2 is a second
+    gradient of n, d_res the residual branch's gradient (added times res_scale). `out` may
+    supply (dx, dw); dw None there = not wanted."""
+    dd, xd = _float_dtype(dn, "dn"), _float_dtype(x, "x")
+    T, H = x.shape
+    dev = x.device
+    c = _Checks(dev)
+    c.need(x, "x", x.dtype, (T, H))
+    c.need(dn, "dn", dn.dtype, (T, H))
+    c.opt(dn2, "dn2", dn.dtype, (T, H))
+    c.need(rstd, "rstd", torch.float32, (T,))
+    c.opt(weight, "weight", torch.float32, (H,))
+    c.opt(d_res, "d_res", x.dtype, (T, H))
+    dx, dw = out if out is not None else (torch.empty_like(x), None if weight is None else torch.empty_like(weight))
+    c.need(dx, "dx", x.dtype, (T, H))
+    c.opt(dw, "dw", torch.float32, (H,))
+    c.done()
+    ws = _workspace(OP_NORM_BACKWARD, T, H, workspace, dev) if dw is not None else None
+    _call("rmsnorm_backward", dev, _ptr(dn), _ptr(dn2), dd, _ptr(x), xd, _ptr(rstd), _ptr(weight), _ptr(d_res),
+          res_scale, T, H, _ptr(dx), _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel())
+    return dx, dw
+
+
+def rmsnorm_gate_residual(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor | None = None,
+                          gate: torch.Tensor | None = None, gate_mode: str = "none", eps: float = 1e-6,
+                          branch_scale: float = 1.0, res_scale: float = 1.0, out=None):
+    """res_scale x + branch_scale gate RMSNorm(y): (out in x's type, rstd). gate is FP32, (T,) for
+    gate_mode "token", (H,) for "channel", (T, H) for "full". `out` may supply (out, rstd)."""
+    xd, yd = _float_dtype(x, "x"), _float_dtype(y, "y")
+    T, H = x.shape
+    dev = x.device
+    c = _Checks(dev)
+    c.need(x, "x", x.dtype, (T, H))
+    c.need(y, "y", y.dtype, (T, H))
+    c.opt(weight, "weight", torch.float32, (H,))
+    mode = _need_gate(c, gate, gate_mode, "gate", T, H)
+    o, rstd = out if out is not None else (torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev))
+    c.need(o, "out", x.dtype, (T, H))
+    c.opt(rstd, "rstd", torch.float32, (T,))
+    c.done()
+    _call("rmsnorm_gate_residual", dev, _ptr(x), xd, _ptr(y), yd, _ptr(weight), _ptr(gate), mode, eps, branch_scale,
+          res_scale, T, H, _ptr(o), _ptr(rstd))
+    return o, rstd
+
+
+def rmsnorm_gate_residual_backward(d_out: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor,
+                                   weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                                   gate_mode: str = "none", branch_scale: float = 1.0, out=None,
+                                   workspace: torch.Tensor | None = None):
+    """Gradients of rmsnorm_gate_residual: (dy in y's type, dw FP32 | None, dgate FP32 | None); the
+    residual's own is res_scale d_out. `out` may supply (dy, dw, dgate); None there = not wanted."""
+    dd, yd = _float_dtype(d_out, "d_out"), _float_dtype(y, "y")
+    T, H = y.shape
+    dev = y.device
+    c = _Checks(dev)
+    c.need(d_out, "d_out", d_out.dtype, (T, H))
+    c.need(y, "y", y.dtype, (T, H))
+    c.need(rstd, "rstd", torch.float32, (T,))
+    c.opt(weight, "weight", torch.float32, (H,))
+    mode = _need_gate(c, gate, gate_mode, "gate", T, H)
+    if out is not None:
+        dy, dw, dgate = out
+    else:
+        dy = torch.empty_like(y)
+        dw = None if weight is None else torch.empty_like(weight)
+        dgate = None if gate is None else torch.empty_like(gate)
+    c.need(dy, "dy", y.dtype, (T, H))
+    c.opt(dw, "dw", torch.float32, (H,))
+    if dgate is not None:
+        _need_gate(c, dgate, gate_mode, "dgate", T, H)
+    c.done()
+    sums = dw is not None or (dgate is not None and mode == GATE["channel"])
+    ws = _workspace(OP_NORM_BACKWARD, T, H, workspace, dev) if sums else None
+    _call("rmsnorm_gate_residual_backward", dev, _ptr(d_out), dd, _ptr(y), yd, _ptr(rstd), _ptr(weight), _ptr(gate),
+          mode, branch_scale, T, H, _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws), 0 if ws is None else ws.numel())
+    return dy, dw, dgate
+
+
+# ---------------------------------------------------------------------------
+# Router
+# ---------------------------------------------------------------------------
+
+class RoutePlan:
+    """A routing on the device: topk_idx, weights, counts, offsets, row_index, slot_of and the
+    balance loss (None if not wanted), as moe_route writes them (include/mxq.h), with `slots`
+    (the total) and `groups` (the experts). Made once for a batch size, it serves every call."""
+
+    def __init__(self, tokens: int, experts: int, topk: int, pad: int = 1, total: int | None = None,
+                 loss: bool = False, dev="cuda"):
+        need = route_slots(tokens, experts, topk, pad)
+        total = need if total is None else total
+        if total < need or total % pad or total > 0x7FFFFFFF:
+            raise ValueError(f"total: {total} slots, expected a multiple of {pad} and at least {need}")
+        e = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+        self.tokens, self.groups, self.topk, self.pad, self.slots = tokens, experts, topk, pad, total
+        self.topk_idx = e((tokens, topk), torch.int32)
+        self.weights = e((tokens, topk), torch.float32)
+        self.counts = e((experts + 1,), torch.int32)
+        self.offsets = e((experts + 1,), torch.int64)
+        self.row_index = e((total,), torch.int32)
+        self.slot_of = e((tokens, topk), torch.int64)
+        self.loss = e((1,), torch.float32) if loss else None
+
+
+def route_slots(tokens: int, experts: int, topk: int, pad: int = 1) -> int:
+    """Slots that hold every routing of this size, each expert's range a multiple of pad."""
+    n = lib().mxq_route_slots(tokens, experts, topk, pad)
+    if n < 0:
+        raise ValueError(f"no routing of {tokens} tokens, {experts} experts, top-{topk}, pad {pad}")
+    return n
+
+
+def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor | None = None,
+              balance_coef: float | None = None, total: int | None = None, out: RoutePlan | None = None,
+              workspace: torch.Tensor | None = None) -> RoutePlan:
+    """Top-k routing of FP32 logits (T, G) with its slots, counts and (balance_coef given) balance
+    loss. valid: bool or uint8 (T,), False = a padding token that is not routed. `out`: a plan
+    of the same sizes to write into."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits: expected a 2-D tensor (tokens, experts)")
+    T, G = logits.shape
+    dev = logits.device
+    c = _Checks(dev)
+    c.need(logits, "logits", torch.float32, (T, G), ld=True)
+    if valid is not None:
+        if valid.dtype == torch.bool:
+            valid = valid.view(torch.uint8)
+        c.need(valid, "valid", torch.uint8, (T,))
+    plan = out
+    if plan is None:
+        plan = RoutePlan(T, G, topk, pad, total, balance_coef is not None, dev)
+    elif (plan.tokens, plan.groups, plan.topk, plan.pad) != (T, G, topk, pad) or (total or plan.slots) != plan.slots:
+        raise ValueError("out: a plan of other sizes")
+    elif balance_coef is not None and plan.loss is None:
+        raise ValueError("out: a plan without a loss")
+    c.need(plan.offsets, "out", torch.int64, (G + 1,))
+    c.done()
+    ws = _workspace(OP_ROUTE, T, G, workspace, dev)
+    loss = None if balance_coef is None else plan.loss
+    _call("moe_route", dev, _ptr(logits), _ptr(valid), T, G, max(logits.stride(0), G), topk, pad, plan.slots,
+          0.0 if balance_coef is None else balance_coef, _ptr(plan.topk_idx), _ptr(plan.weights), _ptr(plan.counts),
+          _ptr(plan.offsets), _ptr(plan.row_index), _ptr(plan.slot_of), _ptr(loss), _ptr(ws), ws.numel())
+    return plan
+
+
+def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, weights: torch.Tensor, counts: torch.Tensor,
+                       d_weights: torch.Tensor | None = None, d_loss: torch.Tensor | None = None,
+                       balance_coef: float = 0.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """d_logits (T, G) FP32 from the gradients of the combine weights (T, k) and of the balance
+    loss (1,), either None; topk_idx, weights and counts from moe_route."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits, topk_idx: expected 2-D tensors")
+    T, G = logits.shape
+    k = topk_idx.shape[1]
+    c = _Checks(logits.device)
+    c.need(logits, "logits", torch.float32, (T, G), ld=True)
+    c.need(topk_idx, "topk_idx", torch.int32, (T, k))
+    c.need(weights, "weights", torch.float32, (T, k))
+    c.need(counts, "counts", torch.int32, (G + 1,))
+    c.opt(d_weights, "d_weights", torch.float32, (T, k))
+    c.opt(d_loss, "d_loss", torch.float32, (1,))
+    if out is None:
+        out = torch.empty((T, G), dtype=torch.float32, device=logits.device)
+    c.need(out, "out", torch.float32, (T, G))
+    c.done()
+    _call("moe_route_backward", logits.device, _ptr(logits), T, G, max(logits.stride(0), G), k, _ptr(topk_idx),
+          _ptr(weights), _ptr(d_weights), _ptr(counts), _ptr(d_loss), balance_coef, _ptr(out))
+    return out
+
+
+def moe_combine_backward(dy: torch.Tensor, o_slots: torch.Tensor, slot_of: torch.Tensor, weights: torch.Tensor,
+                         row_index: torch.Tensor, out=None):
+    """Gradients of moe_combine: (d_o BF16 (slots, H), padding slots cleared, d_weights FP32 (T, k)).
+    `out` may supply both."""
+    dd = _float_dtype(dy, "dy")
+    T, k = slot_of.shape
+    S, H = o_slots.shape
+    dev = o_slots.device
+    c = _Checks(dev)
+    c.need(dy, "dy", dy.dtype, (T, H))
+    c.need(o_slots, "o_slots", torch.float32, (S, H))
+    c.need(slot_of, "slot_of", torch.int64, (T, k))
+    c.need(weights, "weights", torch.float32, (T, k))
+    c.need(row_index, "row_index", torch.int32, (S,))
+    d_o, d_w = out if out is not None else (torch.empty((S, H), dtype=torch.bfloat16, device=dev),
+                                            torch.empty((T, k), dtype=torch.float32, device=dev))
+    c.need(d_o, "d_o", torch.bfloat16, (S, H))
+    c.need(d_w, "d_weights", torch.float32, (T, k))
+    c.done()
+    _call("moe_combine_backward", dev, _ptr(dy), dd, _ptr(o_slots), S, T, k, H, _ptr(slot_of), _ptr(weights),
+          _ptr(row_index), _ptr(d_o), _ptr(d_w))
+    return d_o, d_w
 
 
 def scale_bytes(fmt: int, rows: int, cols: int) -> int:

@@ -42,12 +42,36 @@ hipError_t launch_gemm_batch(int fmt, int n, const int64_t* M, const int64_t* N,
                              const void* const* A, const void* const* sA, const float* const* tA, const int* tA_mode,
                              const void* const* B, const void* const* sB, const float* const* tB, const int* tB_mode,
                              float* const* C, const int64_t* ldc, hipStream_t st);
+hipError_t launch_norm_quant(int fmt, const void* x, int x32, int64_t rows, int64_t cols, int64_t ld_x,
+                             const float* weight, double eps, void* n, void* q, void* s, float* t, float* rstd,
+                             hipStream_t st);
+hipError_t launch_gate_residual(const void* x, int x32, const void* y, int y32, int64_t rows, int64_t cols,
+                                const float* weight, const float* gate, int gate_mode, double eps, float branch_scale,
+                                float res_scale, void* out, float* rstd, hipStream_t st);
+hipError_t launch_norm_backward(const void* d, const void* d2, int d32, const void* y, int y32, const float* rstd,
+                                const float* weight, const float* gate, int gate_mode, float scale, const void* res,
+                                float res_scale, int64_t rows, int64_t cols, void* dy, float* dw, float* dgate,
+                                void* ws, hipStream_t st);
+size_t norm_backward_ws_bytes(int64_t rows, int64_t cols);
+hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
+                        int64_t topk, int64_t pad, int64_t total, float coef, int32_t* topk_idx, float* weights,
+                        int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss, void* ws,
+                        hipStream_t st);
+size_t route_ws_bytes(int64_t tokens, int64_t experts);
+hipError_t launch_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
+                                 const int32_t* topk_idx, const float* weights, const float* d_weights,
+                                 const int32_t* counts, const float* d_loss, float coef, float* d_logits,
+                                 hipStream_t st);
+hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int64_t total, int64_t tokens,
+                                   int64_t topk, int64_t hidden, const int64_t* slot_of, const float* weights,
+                                   const int32_t* row_index, void* d_o, float* d_weights, hipStream_t st);
 }  // namespace mxq
 
 namespace {
 
 constexpr int64_t kMaxRowCols = 16384;       // register-resident NVFP4 row quantizer
 constexpr int64_t kMaxGridBlocks = 0x7FFFFFFF;
+constexpr int64_t kMaxExperts = 1024, kMaxTopk = 32;   // router: 16 experts a lane, a choice a lane
 // GEMM operand reads use 32-bit buffer offsets: a 256-row tile of K-contiguous rows,
 // or (gather) the whole gathered operand, must span less than 2^31 bytes.
 constexpr int64_t kMaxGemmK = int64_t(1) << 22;
@@ -57,6 +81,7 @@ inline int64_t gemm_row_bytes(mxq_format fmt, int64_t k) {
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline hipStream_t S(void* s) { return static_cast<hipStream_t>(s); }
 inline mxq_status hip_status(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
 
@@ -86,10 +111,19 @@ size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols) {
   return 0;
 }
 
+int64_t mxq_route_slots(int64_t tokens, int64_t experts, int64_t topk, int64_t pad) {
+  if (tokens < 0 || experts < 1 || topk < 1 || pad < 1 || tokens > kMaxGridBlocks || topk > kMaxTopk ||
+      experts > kMaxExperts || pad > kMaxGridBlocks)
+    return -1;
+  const int64_t n = tokens * topk, used = n < experts ? n : experts;
+  return (n + used * (pad - 1)) / pad * pad;
+}
+
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {
-  (void)b;
   if (op == MXQ_OP_QUANTIZE_NVFP4) return c > 0 ? (size_t)(((c * 4) + 255) / 256 * 256) : 0;
   if (op == MXQ_OP_GROUPED_GEMM) return a > 0 ? mxq::grouped_gemm_ws_bytes(a) : 0;
+  if (op == MXQ_OP_NORM_BACKWARD) return a > 0 && b > 0 ? mxq::norm_backward_ws_bytes(a, b) : 0;
+  if (op == MXQ_OP_ROUTE) return a > 0 && b > 0 ? mxq::route_ws_bytes(a, b) : 0;
   return 0;
 }
 
@@ -602,6 +636,163 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
   if (tokens == 0 || hidden == 0) return MXQ_OK;
   if (tokens > kMaxGridBlocks) return MXQ_ERR_SHAPE;
   return hip_status(mxq::launch_combine(o_slots, total_slots, tokens, topk, hidden, slot_of, weights, y, S(stream)));
+}
+
+namespace {
+inline bool is_dtype(mxq_out_dtype d) { return d == MXQ_OUT_BF16 || d == MXQ_OUT_F32; }
+inline bool positive(double v) { return v > 0.0 && v <= 1.79769313486231570815e308; }   // finite, not NaN
+
+mxq_status gate_check(const float* gate, mxq_gate_mode mode) {
+  if (mode != MXQ_GATE_NONE && mode != MXQ_GATE_TOKEN && mode != MXQ_GATE_CHANNEL && mode != MXQ_GATE_FULL)
+    return MXQ_ERR_FORMAT;
+  if (mode != MXQ_GATE_NONE && !gate) return MXQ_ERR_NULL;
+  if (!al16(gate)) return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+mxq_status norm_workspace(int64_t rows, int64_t cols, bool sums, void* workspace, size_t workspace_bytes) {
+  if (!sums || rows == 0) return MXQ_OK;
+  if (!workspace || workspace_bytes < mxq::norm_backward_ws_bytes(rows, cols)) return MXQ_ERR_WORKSPACE;
+  return al16(workspace) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+}  // namespace
+
+mxq_status rmsnorm_quantize(mxq_format fmt, const void* x, mxq_out_dtype x_dtype, int64_t rows, int64_t cols,
+                            int64_t ld_x, const float* weight, double eps, void* n_bf16, void* q, void* s, float* t,
+                            float* rstd, void* stream) {
+  if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
+  if ((fmt != MXQ_MXFP8 && fmt != MXQ_NVFP4 && fmt != MXQ_BF16 && fmt != MXQ_MXFP4) || !is_dtype(x_dtype) ||
+      !positive(eps))
+    return MXQ_ERR_FORMAT;
+  if (rows == 0 || cols == 0) return MXQ_OK;
+  if (!x || (fmt == MXQ_BF16 ? !n_bf16 : !q || !s) || (fmt == MXQ_NVFP4 && !t)) return MXQ_ERR_NULL;
+  if (cols % (fmt == MXQ_BF16 ? 8 : fmt == MXQ_NVFP4 ? 16 : 32) || cols > kMaxRowCols || ld_x < cols ||
+      rows > kMaxGridBlocks)
+    return MXQ_ERR_SHAPE;
+  if (ld_x % (x_dtype == MXQ_OUT_F32 ? 4 : 8) || !al16(x) || !al16(weight) || !al16(n_bf16) || !al4(t) || !al4(rstd))
+    return MXQ_ERR_ALIGN;
+  if (fmt != MXQ_BF16 && !al16(q)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_norm_quant((int)fmt, x, x_dtype == MXQ_OUT_F32, rows, cols, ld_x, weight, eps, n_bf16,
+                                           q, s, t, rstd, S(stream)));
+}
+
+mxq_status rmsnorm_backward(const void* dn, const void* dn2, mxq_out_dtype dn_dtype, const void* x,
+                            mxq_out_dtype x_dtype, const float* rstd, const float* weight, const void* d_res,
+                            float res_scale, int64_t rows, int64_t cols, void* dx, float* dw, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
+  if (!is_dtype(dn_dtype) || !is_dtype(x_dtype) || (dw && !weight)) return MXQ_ERR_FORMAT;
+  if (cols == 0) return MXQ_OK;
+  if (rows > 0 && (!dn || !x || !rstd || !dx)) return MXQ_ERR_NULL;
+  if (cols % 8 || cols > kMaxRowCols || rows > kMaxGridBlocks) return MXQ_ERR_SHAPE;
+  if (!al16(dn) || !al16(dn2) || !al16(x) || !al4(rstd) || !al16(weight) || !al16(d_res) || !al16(dx) || !al16(dw))
+    return MXQ_ERR_ALIGN;
+  const mxq_status ws = norm_workspace(rows, cols, dw != nullptr, workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
+  if (rows == 0 && !dw) return MXQ_OK;
+  return hip_status(mxq::launch_norm_backward(dn, dn2, dn_dtype == MXQ_OUT_F32, x, x_dtype == MXQ_OUT_F32, rstd,
+                                              weight, nullptr, MXQ_GATE_NONE, 1.0f, d_res, res_scale, rows, cols, dx,
+                                              dw, nullptr, workspace, S(stream)));
+}
+
+mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const void* y, mxq_out_dtype y_dtype,
+                                 const float* weight, const float* gate, mxq_gate_mode gate_mode, double eps,
+                                 float branch_scale, float res_scale, int64_t rows, int64_t cols, void* out,
+                                 float* rstd, void* stream) {
+  if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
+  if (!is_dtype(x_dtype) || !is_dtype(y_dtype) || !positive(eps)) return MXQ_ERR_FORMAT;
+  if (rows == 0 || cols == 0) return MXQ_OK;
+  const mxq_status g = gate_check(gate, gate_mode);
+  if (g != MXQ_OK) return g;
+  if (!x || !y || !out) return MXQ_ERR_NULL;
+  if (cols % 8 || cols > kMaxRowCols || rows > kMaxGridBlocks) return MXQ_ERR_SHAPE;
+  if (!al16(x) || !al16(y) || !al16(weight) || !al16(out) || !al4(rstd)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_gate_residual(x, x_dtype == MXQ_OUT_F32, y, y_dtype == MXQ_OUT_F32, rows, cols, weight,
+                                              gate, gate_mode, eps, branch_scale, res_scale, out, rstd, S(stream)));
+}
+
+mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dtype, const void* y,
+                                          mxq_out_dtype y_dtype, const float* rstd, const float* weight,
+                                          const float* gate, mxq_gate_mode gate_mode, float branch_scale,
+                                          int64_t rows, int64_t cols, void* dy, float* dw, float* dgate,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
+  if (!is_dtype(d_dtype) || !is_dtype(y_dtype) || (dw && !weight) || (dgate && gate_mode == MXQ_GATE_NONE))
+    return MXQ_ERR_FORMAT;
+  if (cols == 0) return MXQ_OK;
+  if (rows > 0) {
+    const mxq_status g = gate_check(gate, gate_mode);
+    if (g != MXQ_OK) return g;
+    if (!d_out || !y || !rstd || !dy) return MXQ_ERR_NULL;
+  }
+  if (cols % 8 || cols > kMaxRowCols || rows > kMaxGridBlocks) return MXQ_ERR_SHAPE;
+  if (!al16(d_out) || !al16(y) || !al4(rstd) || !al16(weight) || !al16(dy) || !al16(dw) || !al16(dgate))
+    return MXQ_ERR_ALIGN;
+  const bool sums = dw || (dgate && gate_mode == MXQ_GATE_CHANNEL);
+  const mxq_status ws = norm_workspace(rows, cols, sums, workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
+  if (rows == 0 && !sums) return MXQ_OK;
+  return hip_status(mxq::launch_norm_backward(d_out, nullptr, d_dtype == MXQ_OUT_F32, y, y_dtype == MXQ_OUT_F32, rstd,
+                                              weight, gate, gate_mode, branch_scale, nullptr, 0.0f, rows, cols, dy, dw,
+                                              dgate, workspace, S(stream)));
+}
+
+mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
+                     int64_t topk, int64_t pad, int64_t total, float balance_coef, int32_t* topk_idx, float* weights,
+                     int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (experts < 1 || experts > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > experts || pad < 1 || tokens < 0 ||
+      ld < experts || tokens > kMaxGridBlocks)
+    return MXQ_ERR_SHAPE;
+  const int64_t least = mxq_route_slots(tokens, experts, topk, pad);
+  if (least < 0 || total < least || total % pad || total > kMaxGridBlocks) return MXQ_ERR_SHAPE;
+  if (!counts || !offsets || (tokens > 0 && (!logits || !topk_idx || !weights || !slot_of)) || (total > 0 && !row_index))
+    return MXQ_ERR_NULL;
+  if (!al4(logits) || !al4(topk_idx) || !al4(weights) || !al4(counts) || !al8(offsets) || !al4(row_index) ||
+      !al8(slot_of) || !al4(loss))
+    return MXQ_ERR_ALIGN;
+  if (tokens > 0) {
+    if (!workspace || workspace_bytes < mxq::route_ws_bytes(tokens, experts)) return MXQ_ERR_WORKSPACE;
+    if (!al16(workspace)) return MXQ_ERR_ALIGN;
+  }
+  return hip_status(mxq::launch_route(logits, valid, tokens, experts, ld, topk, pad, total, balance_coef, topk_idx,
+                                      weights, counts, offsets, row_index, slot_of, loss, workspace, S(stream)));
+}
+
+mxq_status moe_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
+                              const int32_t* topk_idx, const float* weights, const float* d_weights,
+                              const int32_t* counts, const float* d_loss, float balance_coef, float* d_logits,
+                              void* stream) {
+  if (experts < 1 || experts > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > experts || tokens < 0 ||
+      ld < experts || tokens > kMaxGridBlocks)
+    return MXQ_ERR_SHAPE;
+  if (tokens == 0) return MXQ_OK;
+  if (!logits || !topk_idx || !d_logits || (d_weights && !weights) || (d_loss && !counts)) return MXQ_ERR_NULL;
+  if (!al4(logits) || !al4(topk_idx) || !al4(weights) || !al4(d_weights) || !al4(counts) || !al4(d_loss) ||
+      !al4(d_logits))
+    return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_route_backward(logits, tokens, experts, ld, topk, topk_idx, weights, d_weights, counts,
+                                               d_loss, balance_coef, d_logits, S(stream)));
+}
+
+mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const float* o_slots, int64_t total_slots,
+                                int64_t tokens, int64_t topk, int64_t hidden, const int64_t* slot_of,
+                                const float* weights, const int32_t* row_index, void* d_o_bf16, float* d_weights,
+                                void* stream) {
+  if (tokens < 0 || topk < 0 || hidden < 0 || total_slots < 0) return MXQ_ERR_SHAPE;
+  if (!is_dtype(dy_dtype)) return MXQ_ERR_FORMAT;
+  if (hidden % 8 || hidden > kMaxRowCols || topk > kMaxTopk || tokens > kMaxGridBlocks / 2 ||
+      total_slots > kMaxGridBlocks / 2)
+    return MXQ_ERR_SHAPE;
+  if ((tokens == 0 || topk == 0) && total_slots == 0) return MXQ_OK;
+  if ((tokens > 0 && topk > 0 && (!dy || !slot_of || !weights || !d_weights)) ||
+      (total_slots > 0 && hidden > 0 && (!o_slots || !row_index || !d_o_bf16)))
+    return MXQ_ERR_NULL;
+  if (!al16(dy) || !al16(o_slots) || !al8(slot_of) || !al4(weights) || !al4(row_index) || !al16(d_o_bf16) ||
+      !al4(d_weights))
+    return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_combine_backward(dy, dy_dtype == MXQ_OUT_F32, o_slots, total_slots, tokens, topk,
+                                                 hidden, slot_of, weights, row_index, d_o_bf16, d_weights, S(stream)));
 }
 
 }  // extern "C"

@@ -181,4 +181,68 @@ __device__ __forceinline__ float e2m1_to_f32(uint32_t c) {
   return (c & 8) ? -mag : mag;
 }
 
+// ---------------------------------------------------------------------------
+// NVFP4 scale steps and packing (the order of operations is in quant_nvfp4.hip)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void scope_scales(float A, float& s_enc, float& t) {
+  float s = 2688.0f / A;
+  if (A == 0.0f) s = 1.0f;
+  if (__builtin_isinf(s)) s = kFltMax;
+  s_enc = s;
+  t = 1.0f / s;
+}
+
+// Block scale code and element multiplier for a 16-block with amax a_b.
+__device__ __forceinline__ uint32_t block_scale(float a_b, float s_enc, float& r_b) {
+  float d = (a_b / 6.0f) * s_enc;
+  d = fminf(d, kE4M3Max);                                   // saturate (d >= 0)
+  const uint32_t code = cvt_fp8x2_f32(0u, d, 0.0f, 1.0f, false) & 0xFFu;
+  const float S = e4m3_to_f32(code);
+  float r = s_enc / S;
+  r = fminf(r, kFltMax);
+  r_b = (S == 0.0f) ? 0.0f : r;
+  return code;
+}
+
+// Eight consecutive values (a 16-block is two lanes) -> 4 packed bytes.
+__device__ __forceinline__ uint32_t pack8_e2m1(const float* v, float r) {
+  uint32_t o = 0;
+  o = cvt_fp4x2_f32<0>(o, v[0] * r, v[1] * r);
+  o = cvt_fp4x2_f32<1>(o, v[2] * r, v[3] * r);
+  o = cvt_fp4x2_f32<2>(o, v[4] * r, v[5] * r);
+  o = cvt_fp4x2_f32<3>(o, v[6] * r, v[7] * r);
+  return o;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
+  f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+  f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ float wave_max_f32(float v) {
+  uint32_t u = __float_as_uint(v);  // v >= 0: bits order like values
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = shfl_xor_u32(u, off);
+    u = u > o ? u : o;
+  }
+  return __uint_as_float(u);
+}
+
+// binary64 -> BF16 bits, one rounding: the binary32 conversion is turned into
+// round-to-odd (an inexact result is truncated toward zero and gets its last bit set),
+// and round-to-odd to 24 bits followed by nearest-even to 8 bits equals nearest-even
+// to 8 bits directly (24 >= 8 + 2). Values past the binary32 range come out as
+// FLT_MAX | 1 and then round to +-Inf, values below its subnormals as +-2^-149 and
+// then to a signed zero, as the direct rounding gives.
+__device__ __forceinline__ uint32_t f64_to_bf16_rne(double d) {
+  float f = (float)d;
+  if ((double)f != d) {
+    uint32_t b = __float_as_uint(f);
+    if (fabs((double)f) > fabs(d)) b -= 1u;          // magnitude rounded up: step back
+    f = __uint_as_float(b | 1u);
+  }
+  return f32_to_bf16_rne(f);
+}
+
 }  // namespace mxq

@@ -288,22 +288,6 @@ hipError_t launch_dequant_t(int fmt, const void* q, const void* s, const float* 
 // h = silu(g) * u = g u / (1 + e^(-g)), rounded once to BF16 (nearest, ties to even)
 // from its exact value, then the per-token quantizer's arithmetic on the BF16 row.
 // ---------------------------------------------------------------------------
-// binary64 -> BF16 bits, one rounding: the binary32 conversion is turned into
-// round-to-odd (an inexact result is truncated toward zero and gets its last bit set),
-// and round-to-odd to 24 bits followed by nearest-even to 8 bits equals nearest-even
-// to 8 bits directly (24 >= 8 + 2). Values past the binary32 range come out as
-// FLT_MAX | 1 and then round to +-Inf, values below its subnormals as +-2^-149 and
-// then to a signed zero, as the direct rounding gives.
-__device__ __forceinline__ uint32_t f64_to_bf16_rne(double d) {
-  float f = (float)d;
-  if ((double)f != d) {
-    uint32_t b = __float_as_uint(f);
-    if (fabs((double)f) > fabs(d)) b -= 1u;          // magnitude rounded up: step back
-    f = __uint_as_float(b | 1u);
-  }
-  return f32_to_bf16_rne(f);
-}
-
 // h in binary64 from P = g u (exact: two 24-bit significands):
 //   g >= 0: h = P - C with C = P e / (1 + e), e = e^(-g) <= 1 (so C <= P / 2);
 //   g <  0: h = P e / (1 + e) with e = e^g < 1 (a vanishing e gives a zero with the

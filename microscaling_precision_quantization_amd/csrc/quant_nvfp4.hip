@@ -21,36 +21,6 @@
 
 namespace mxq {
 
-__device__ __forceinline__ void scope_scales(float A, float& s_enc, float& t) {
-  float s = 2688.0f / A;
-  if (A == 0.0f) s = 1.0f;
-  if (__builtin_isinf(s)) s = kFltMax;
-  s_enc = s;
-  t = 1.0f / s;
-}
-
-// Block scale code and element multiplier for a 16-block with amax a_b.
-__device__ __forceinline__ uint32_t block_scale(float a_b, float s_enc, float& r_b) {
-  float d = (a_b / 6.0f) * s_enc;
-  d = fminf(d, kE4M3Max);                                   // saturate (d >= 0)
-  const uint32_t code = cvt_fp8x2_f32(0u, d, 0.0f, 1.0f, false) & 0xFFu;
-  const float S = e4m3_to_f32(code);
-  float r = s_enc / S;
-  r = fminf(r, kFltMax);
-  r_b = (S == 0.0f) ? 0.0f : r;
-  return code;
-}
-
-// Eight consecutive values (a 16-block is two lanes) -> 4 packed bytes.
-__device__ __forceinline__ uint32_t pack8_e2m1(const float* v, float r) {
-  uint32_t o = 0;
-  o = cvt_fp4x2_f32<0>(o, v[0] * r, v[1] * r);
-  o = cvt_fp4x2_f32<1>(o, v[2] * r, v[3] * r);
-  o = cvt_fp4x2_f32<2>(o, v[4] * r, v[5] * r);
-  o = cvt_fp4x2_f32<3>(o, v[6] * r, v[7] * r);
-  return o;
-}
-
 // ---------------------------------------------------------------------------
 // Stochastic rounding (gradients only: 7minutos.es NVFP4 page, section "La
 // metodologia de formacion de cuatro partes"). Random words come from the
@@ -102,11 +72,6 @@ __device__ __forceinline__ uint32_t pack8_e2m1_sr(const float* v, float r, const
   return o;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
-  f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
-  f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
-}
-
 // 16-point RHT of a block split over a lane pair (8 values each, even lane
 // holds elements 0..7): w = s * v; FWHT stages 1, 2, 4 inside the lane, stage 8
 // across the pair; u = w * 0.25.
@@ -129,16 +94,6 @@ __device__ __forceinline__ void rht16_pair(float* f, const float* sg, bool odd) 
     f[i] = odd ? (other - f[i]) : (f[i] + other);
     f[i] *= 0.25f;
   }
-}
-
-__device__ __forceinline__ float wave_max_f32(float v) {
-  uint32_t u = __float_as_uint(v);  // v >= 0: bits order like values
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t o = shfl_xor_u32(u, off);
-    u = u > o ? u : o;
-  }
-  return __uint_as_float(u);
 }
 
 // ---------------------------------------------------------------------------

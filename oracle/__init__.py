@@ -32,3 +32,4 @@ docstring. Present ones:
 from . import formats, mxfp8, nvfp4, gemm, moe, rng  # noqa: F401
 from . import mxfp4  # noqa: F401,E402
 from . import fp8_block  # noqa: F401,E402
+from . import norm, router  # noqa: F401,E402

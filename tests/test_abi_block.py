@@ -1,0 +1,168 @@
+"""Refusals of the norm and router entry points, on the host: every bad argument is answered
+before a launch, through the C ABI and through the binding."""
+
+import ctypes
+
+import pytest
+import torch
+
+from microscaling_precision_quantization_amd import binding as B
+
+P = 0x10000
+MIS = 0x10004
+NAN = float("nan")
+BF, F32 = B.OUT_BF16, B.OUT_F32
+
+
+def test_rmsnorm_quantize_validation():
+    def f(fmt=B.MXFP8, x=P, xd=BF, rows=4, cols=64, ld=64, w=P, eps=1e-6, n=P, q=P, s=P, t=None, rstd=P):
+        return B.lib().rmsnorm_quantize(fmt, x, xd, rows, cols, ld, w, eps, n, q, s, t, rstd, None)
+
+    assert f(rows=-1) == 2 and f(cols=-1) == 2
+    assert f(rows=0) == 0 and f(rows=0, x=None) == 0
+    assert f(fmt=9) == 4 and f(fmt=B.BF16_NVFP4T) == 4 and f(xd=2) == 4
+    assert f(eps=0.0) == 4 and f(eps=-1.0) == 4 and f(eps=NAN) == 4 and f(eps=float("inf")) == 4
+    assert f(x=None) == 1 and f(q=None) == 1 and f(s=None) == 1 and f(fmt=B.NVFP4) == 1
+    assert f(fmt=B.BF16, n=None) == 1
+    assert f(cols=48, ld=48) == 2 and f(fmt=B.MXFP4, cols=48, ld=48) == 2
+    assert f(fmt=B.NVFP4, cols=40, ld=40, t=P) == 2 and f(fmt=B.BF16, cols=12, ld=12) == 2
+    assert f(ld=32) == 2 and f(cols=16416, ld=16416) == 2
+    assert f(ld=68) == 3 and f(xd=F32, ld=66) == 3
+    assert f(x=MIS) == 3 and f(w=MIS) == 3 and f(n=MIS) == 3 and f(q=MIS) == 3 and f(rstd=P + 2) == 3
+    assert f(fmt=B.NVFP4, t=P + 2) == 3
+
+
+def test_rmsnorm_backward_validation():
+    def f(dn=P, dn2=None, dd=F32, x=P, xd=BF, rstd=P, w=P, res=None, rows=4, cols=64, dx=P, dw=P, ws=P, wsn=1 << 20):
+        return B.lib().rmsnorm_backward(dn, dn2, dd, x, xd, rstd, w, res, 1.0, rows, cols, dx, dw, ws, wsn, None)
+
+    need = B.lib().mxq_workspace_bytes(B.OP_NORM_BACKWARD, 4, 64, 0)
+    assert need > 0 and B.lib().mxq_workspace_bytes(B.OP_NORM_BACKWARD, 0, 64, 0) == 0
+    assert f(rows=-1) == 2 and f(cols=60) == 2 and f(cols=16392) == 2
+    assert f(dd=2) == 4 and f(xd=2) == 4 and f(w=None) == 4               # dw without a weight
+    assert f(dn=None) == 1 and f(x=None) == 1 and f(rstd=None) == 1 and f(dx=None) == 1
+    assert f(ws=None) == 5 and f(wsn=need - 1) == 5
+    assert f(dn=MIS) == 3 and f(dn2=MIS) == 3 and f(res=MIS) == 3 and f(dx=MIS) == 3 and f(dw=MIS) == 3
+    assert f(ws=MIS) == 3
+    assert f(rows=0, dw=None, dn=None) == 0 and f(cols=0) == 0
+
+
+def test_gate_residual_validation():
+    def f(x=P, xd=BF, y=P, yd=F32, w=P, gate=P, mode=1, eps=1e-6, rows=4, cols=64, out=P, rstd=P):
+        return B.lib().rmsnorm_gate_residual(x, xd, y, yd, w, gate, mode, eps, 1.0, 1.0, rows, cols, out, rstd, None)
+
+    assert f(rows=-1) == 2 and f(cols=60) == 2 and f(cols=16392) == 2
+    assert f(mode=4) == 4 and f(mode=-1) == 4 and f(eps=0.0) == 4 and f(xd=3) == 4 and f(yd=3) == 4
+    assert f(gate=None) == 1 and f(gate=None, mode=2) == 1 and f(x=None) == 1 and f(y=None) == 1 and f(out=None) == 1
+    assert f(gate=MIS) == 3 and f(x=MIS) == 3 and f(y=MIS) == 3 and f(out=MIS) == 3 and f(w=MIS) == 3
+    assert f(rows=0) == 0 and f(cols=0) == 0
+
+    def g(d=P, dd=BF, y=P, yd=F32, rstd=P, w=P, gate=P, mode=2, rows=4, cols=64, dy=P, dw=P, dg=P, ws=P, wsn=1 << 20):
+        return B.lib().rmsnorm_gate_residual_backward(d, dd, y, yd, rstd, w, gate, mode, 1.0, rows, cols, dy, dw, dg,
+                                                      ws, wsn, None)
+
+    assert g(rows=-1) == 2 and g(cols=60) == 2 and g(mode=5) == 4 and g(w=None) == 4
+    assert g(mode=0) == 4                                                   # dgate without a gate
+    assert g(d=None) == 1 and g(y=None) == 1 and g(rstd=None) == 1 and g(dy=None) == 1 and g(gate=None) == 1
+    assert g(ws=None) == 5 and g(ws=None, dw=None) == 5 and g(wsn=16) == 5
+    assert g(d=MIS) == 3 and g(dg=MIS) == 3 and g(ws=MIS) == 3
+    assert g(rows=0, dw=None, dg=None) == 0
+
+
+def test_route_validation():
+    def f(z=P, valid=None, T=4, G=8, ld=8, k=2, pad=4, total=32, idx=P, w=P, counts=P, off=P, row=P, slot=P, loss=P,
+          ws=P, wsn=1 << 20):
+        return B.lib().moe_route(z, valid, T, G, ld, k, pad, total, 0.1, idx, w, counts, off, row, slot, loss, ws, wsn,
+                                 None)
+
+    assert B.route_slots(4, 8, 2, 4) == 32
+    assert f(total=28) == 2 and f(total=34) == 2                            # below the worst case; no multiple of pad
+    assert f(k=0) == 2 and f(k=9) == 2 and f(G=0) == 2 and f(G=2000, ld=2000, total=1 << 20) == 2
+    assert f(pad=0) == 2 and f(T=-1) == 2 and f(ld=7) == 2 and f(total=1 << 31) == 2
+    assert f(G=64, ld=64, k=33, total=1 << 12) == 2                         # topk beyond 32
+    for name in ("z", "idx", "w", "counts", "off", "row", "slot"):
+        assert f(**{name: None}) == 1, name
+    assert f(ws=None) == 5 and f(wsn=8) == 5
+    assert f(z=P + 2) == 3 and f(off=MIS) == 3 and f(slot=MIS) == 3 and f(ws=MIS) == 3
+    assert B.lib().mxq_route_slots(4, 8, 0, 1) == -1 and B.lib().mxq_route_slots(-1, 8, 1, 1) == -1
+    with pytest.raises(ValueError, match="no routing"):
+        B.route_slots(4, 8, 40, 1)
+
+    def g(z=P, T=4, G=8, ld=8, k=2, idx=P, w=P, dw=P, counts=P, dl=P, out=P):
+        return B.lib().moe_route_backward(z, T, G, ld, k, idx, w, dw, counts, dl, 0.1, out, None)
+
+    assert g(k=9) == 2 and g(ld=4) == 2 and g(T=-1) == 2 and g(G=1025, ld=1025) == 2
+    assert g(z=None) == 1 and g(idx=None) == 1 and g(out=None) == 1 and g(w=None) == 1 and g(counts=None) == 1
+    assert g(out=P + 2) == 3 and g(T=0) == 0
+
+
+def test_combine_backward_validation():
+    def f(dy=P, dd=F32, o=P, S=8, T=4, k=2, H=64, slot=P, w=P, row=P, d_o=P, dw=P):
+        return B.lib().moe_combine_backward(dy, dd, o, S, T, k, H, slot, w, row, d_o, dw, None)
+
+    assert f(H=60) == 2 and f(H=16392) == 2 and f(k=33) == 2 and f(S=-1) == 2 and f(T=-1) == 2 and f(dd=2) == 4
+    for name in ("dy", "o", "slot", "w", "row", "d_o", "dw"):
+        assert f(**{name: None}) == 1, name
+    assert f(dy=MIS) == 3 and f(o=MIS) == 3 and f(d_o=MIS) == 3 and f(slot=MIS) == 3
+    assert f(T=0, S=0) == 0
+
+
+def test_binding_refuses_wrong_buffers():
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    f32 = lambda *s: torch.zeros(s, dtype=torch.float32)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    x, y = bf(4, 64), f32(4, 64)
+    with pytest.raises(ValueError, match="x: expected a bfloat16 or float32"):
+        B.rmsnorm_quantize(x.half())
+    with pytest.raises(ValueError, match="2-D"):
+        B.rmsnorm_quantize(bf(64))
+    with pytest.raises(ValueError, match="unknown format"):
+        B.rmsnorm_quantize(x, fmt=77)
+    with pytest.raises(ValueError, match="weight: shape"):
+        B.rmsnorm_quantize(x, f32(32))
+    with pytest.raises(ValueError, match="weight: dtype"):
+        B.rmsnorm_quantize(x, bf(64))
+    with pytest.raises(ValueError, match="innermost"):
+        B.rmsnorm_quantize(bf(64, 4).t())
+    with pytest.raises(ValueError, match="row stride"):
+        B.rmsnorm_quantize(bf(1, 64).expand(4, 64))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        B.rmsnorm_quantize(x)
+    with pytest.raises(ValueError, match="dn2: dtype"):
+        B.rmsnorm_backward(y, x, f32(4), dn2=x)
+    with pytest.raises(ValueError, match="rstd: shape"):
+        B.rmsnorm_backward(y, x, f32(3))
+    with pytest.raises(ValueError, match="d_res: dtype"):
+        B.rmsnorm_backward(y, x, f32(4), d_res=y)
+    with pytest.raises(ValueError, match="gate_mode"):
+        B.rmsnorm_gate_residual(x, y, gate=f32(4), gate_mode="row")
+    with pytest.raises(ValueError, match="gate_mode is 'none'"):
+        B.rmsnorm_gate_residual(x, y, gate=f32(4))
+    with pytest.raises(ValueError, match="gate: shape"):
+        B.rmsnorm_gate_residual(x, y, gate=f32(4), gate_mode="channel")
+    with pytest.raises(ValueError, match="gate: expected a tensor"):
+        B.rmsnorm_gate_residual(x, y, gate_mode="token")
+    with pytest.raises(ValueError, match="contiguous"):
+        B.rmsnorm_gate_residual(bf(4, 128)[:, :64], y)
+    with pytest.raises(ValueError, match="dgate: shape"):
+        B.rmsnorm_gate_residual_backward(x, y, f32(4), gate=f32(4), gate_mode="token", out=(f32(4, 64), None, f32(64)))
+    with pytest.raises(ValueError, match="logits: dtype"):
+        B.moe_route(bf(4, 8), 2)
+    with pytest.raises(ValueError, match="valid: shape"):
+        B.moe_route(f32(4, 8), 2, valid=torch.ones(3, dtype=torch.bool))
+    with pytest.raises(ValueError, match="no routing"):
+        B.moe_route(f32(4, 8), 0)
+    plan = B.RoutePlan(4, 8, 2, dev="cpu")
+    assert plan.slots == 8 and plan.loss is None
+    with pytest.raises(ValueError, match="other sizes"):
+        B.moe_route(f32(5, 8), 2, out=plan)
+    with pytest.raises(ValueError, match="without a loss"):
+        B.moe_route(f32(4, 8), 2, out=plan, balance_coef=0.1)
+    with pytest.raises(ValueError, match="total"):
+        B.RoutePlan(4, 8, 2, pad=4, total=28, dev="cpu")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        B.moe_route(f32(4, 8), 2, out=plan)
+    with pytest.raises(ValueError, match="counts: shape"):
+        B.moe_route_backward(f32(4, 8), i32(4, 2), f32(4, 2), i32(8))
+    with pytest.raises(ValueError, match="row_index: shape"):
+        B.moe_combine_backward(y, f32(8, 64), torch.zeros((4, 2), dtype=torch.int64), f32(4, 2), i32(7))
