@@ -57,6 +57,8 @@ KERNEL_SOURCES = ["microscaling_precision_quantization_amd/csrc/gemm_exact.hip",
                   "microscaling_precision_quantization_amd/csrc/quant_fp8_block.hip",
                   "microscaling_precision_quantization_amd/csrc/quant_nvfp4.hip",
                   "microscaling_precision_quantization_amd/csrc/dequant_moe.hip",
+                  "microscaling_precision_quantization_amd/csrc/norm.hip",
+                  "microscaling_precision_quantization_amd/csrc/moe_route.hip",
                   "microscaling_precision_quantization_amd/csrc/common.h"]
 
 # algorithmic bytes per element
