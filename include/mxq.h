@@ -702,7 +702,7 @@ mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dty
  *   offsets   : int64 (experts + 1);  row_index: int32 (total), the token of a slot, -1 = padding;
  *   slot_of   : int64 (tokens, topk);  loss: FP32 (1), NULL = not wanted.
  *   workspace : mxq_workspace_bytes(MXQ_OP_ROUTE, tokens, experts, 0) bytes, 16-byte aligned.
- *   Requires 1 <= topk <= 32, topk <= experts <= 1024, total < 2^31.
+ *   Requires 1 <= topk <= 32, topk <= experts <= 1024, tokens <= 2^22, total < 2^31.
  * ------------------------------------------------------------------------- */
 mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
                      int64_t topk, int64_t pad, int64_t total, float balance_coef, int32_t* topk_idx, float* weights,

@@ -125,17 +125,18 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    """The raw handle of dev's current stream (20 times cheaper than building a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
 def _call(fn: str, dev, *args):
     """One C-ABI call on dev's current stream (the last argument), with dev the current device:
     a kernel is launched on the device that is current, whatever its stream."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
     else:
         with torch.cuda.device(dev):
@@ -163,9 +164,14 @@ class _Checks:
 
     def __init__(self, dev):
         self.dev = dev
+        self.index = dev.index
         self.seen = []
 
     def need(self, t, name: str, dtype, shape, ld: bool = False):
+        # what nearly every call hands in, in one comparison each; anything else is looked at below
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == self.index and not (ld and t.stride(0) < shape[1])):
+            return t
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
         if t.dtype != dtype:
@@ -768,15 +774,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: f
     c = _Checks(dev)
     c.need(x, "x", x.dtype, (T, H), ld=True)
     c.opt(weight, "weight", torch.float32, (H,))
-    if out is None:
-        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_n or fmt == BF16 else None
-        q = s = t = None
-        if fmt != BF16:
-            q, s = _u8((T, H // _elems_per_byte(fmt)), dev), _u8((T, H // _scale_block(fmt)), dev)
-        if fmt == NVFP4:
-            t = torch.empty(T, dtype=torch.float32, device=dev)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    else:
+    if out is not None:
         n, q, s, t, rstd = out
         (c.need if fmt == BF16 else c.opt)(n, "n", torch.bfloat16, (T, H))
         if fmt != BF16:
@@ -786,6 +784,14 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: f
             c.need(t, "t", torch.float32, (T,))
         c.opt(rstd, "rstd", torch.float32, (T,))
     c.done()
+    if out is None:
+        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_n or fmt == BF16 else None
+        q = s = t = None
+        if fmt != BF16:
+            q, s = _u8((T, H // _elems_per_byte(fmt)), dev), _u8((T, H // _scale_block(fmt)), dev)
+        if fmt == NVFP4:
+            t = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
     _call("rmsnorm_quantize", dev, fmt, _ptr(x), xd, T, H, max(x.stride(0), H), _ptr(weight), eps, _ptr(n), _ptr(q),
           _ptr(s), _ptr(t), _ptr(rstd))
     return n, q, s, t, rstd
@@ -807,10 +813,13 @@ def rmsnorm_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weig
     c.need(rstd, "rstd", torch.float32, (T,))
     c.opt(weight, "weight", torch.float32, (H,))
     c.opt(d_res, "d_res", x.dtype, (T, H))
-    dx, dw = out if out is not None else (torch.empty_like(x), None if weight is None else torch.empty_like(weight))
-    c.need(dx, "dx", x.dtype, (T, H))
-    c.opt(dw, "dw", torch.float32, (H,))
+    if out is not None:
+        dx, dw = out
+        c.need(dx, "dx", x.dtype, (T, H))
+        c.opt(dw, "dw", torch.float32, (H,))
     c.done()
+    if out is None:
+        dx, dw = torch.empty_like(x), None if weight is None else torch.empty_like(weight)
     ws = _workspace(OP_NORM_BACKWARD, T, H, workspace, dev) if dw is not None else None
     _call("rmsnorm_backward", dev, _ptr(dn), _ptr(dn2), dd, _ptr(x), xd, _ptr(rstd), _ptr(weight), _ptr(d_res),
           res_scale, T, H, _ptr(dx), _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel())
@@ -830,10 +839,13 @@ def rmsnorm_gate_residual(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor
     c.need(y, "y", y.dtype, (T, H))
     c.opt(weight, "weight", torch.float32, (H,))
     mode = _need_gate(c, gate, gate_mode, "gate", T, H)
-    o, rstd = out if out is not None else (torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev))
-    c.need(o, "out", x.dtype, (T, H))
-    c.opt(rstd, "rstd", torch.float32, (T,))
+    if out is not None:
+        o, rstd = out
+        c.need(o, "out", x.dtype, (T, H))
+        c.opt(rstd, "rstd", torch.float32, (T,))
     c.done()
+    if out is None:
+        o, rstd = torch.empty_like(x), torch.empty(T, dtype=torch.float32, device=dev)
     _call("rmsnorm_gate_residual", dev, _ptr(x), xd, _ptr(y), yd, _ptr(weight), _ptr(gate), mode, eps, branch_scale,
           res_scale, T, H, _ptr(o), _ptr(rstd))
     return o, rstd
@@ -856,15 +868,15 @@ def rmsnorm_gate_residual_backward(d_out: torch.Tensor, y: torch.Tensor, rstd: t
     mode = _need_gate(c, gate, gate_mode, "gate", T, H)
     if out is not None:
         dy, dw, dgate = out
-    else:
+        c.need(dy, "dy", y.dtype, (T, H))
+        c.opt(dw, "dw", torch.float32, (H,))
+        if dgate is not None:
+            _need_gate(c, dgate, gate_mode, "dgate", T, H)
+    c.done()
+    if out is None:
         dy = torch.empty_like(y)
         dw = None if weight is None else torch.empty_like(weight)
         dgate = None if gate is None else torch.empty_like(gate)
-    c.need(dy, "dy", y.dtype, (T, H))
-    c.opt(dw, "dw", torch.float32, (H,))
-    if dgate is not None:
-        _need_gate(c, dgate, gate_mode, "dgate", T, H)
-    c.done()
     sums = dw is not None or (dgate is not None and mode == GATE["channel"])
     ws = _workspace(OP_NORM_BACKWARD, T, H, workspace, dev) if sums else None
     _call("rmsnorm_gate_residual_backward", dev, _ptr(d_out), dd, _ptr(y), yd, _ptr(rstd), _ptr(weight), _ptr(gate),
@@ -955,10 +967,10 @@ def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, weights: to
     c.need(counts, "counts", torch.int32, (G + 1,))
     c.opt(d_weights, "d_weights", torch.float32, (T, k))
     c.opt(d_loss, "d_loss", torch.float32, (1,))
+    c.opt(out, "out", torch.float32, (T, G))
+    c.done()
     if out is None:
         out = torch.empty((T, G), dtype=torch.float32, device=logits.device)
-    c.need(out, "out", torch.float32, (T, G))
-    c.done()
     _call("moe_route_backward", logits.device, _ptr(logits), T, G, max(logits.stride(0), G), k, _ptr(topk_idx),
           _ptr(weights), _ptr(d_weights), _ptr(counts), _ptr(d_loss), balance_coef, _ptr(out))
     return out
@@ -978,11 +990,13 @@ def moe_combine_backward(dy: torch.Tensor, o_slots: torch.Tensor, slot_of: torch
     c.need(slot_of, "slot_of", torch.int64, (T, k))
     c.need(weights, "weights", torch.float32, (T, k))
     c.need(row_index, "row_index", torch.int32, (S,))
-    d_o, d_w = out if out is not None else (torch.empty((S, H), dtype=torch.bfloat16, device=dev),
-                                            torch.empty((T, k), dtype=torch.float32, device=dev))
-    c.need(d_o, "d_o", torch.bfloat16, (S, H))
-    c.need(d_w, "d_weights", torch.float32, (T, k))
+    if out is not None:
+        d_o, d_w = out
+        c.need(d_o, "d_o", torch.bfloat16, (S, H))
+        c.need(d_w, "d_weights", torch.float32, (T, k))
     c.done()
+    if out is None:
+        d_o, d_w = torch.empty((S, H), dtype=torch.bfloat16, device=dev), torch.empty_like(weights)
     _call("moe_combine_backward", dev, _ptr(dy), dd, _ptr(o_slots), S, T, k, H, _ptr(slot_of), _ptr(weights),
           _ptr(row_index), _ptr(d_o), _ptr(d_w))
     return d_o, d_w

@@ -72,6 +72,7 @@ namespace {
 constexpr int64_t kMaxRowCols = 16384;       // register-resident NVFP4 row quantizer
 constexpr int64_t kMaxGridBlocks = 0x7FFFFFFF;
 constexpr int64_t kMaxExperts = 1024, kMaxTopk = 32;   // router: 16 experts a lane, a choice a lane
+constexpr int64_t kMaxRouteTokens = int64_t(1) << 22;  // router: 16 bits for the loss's count of token blocks
 // GEMM operand reads use 32-bit buffer offsets: a 256-row tile of K-contiguous rows,
 // or (gather) the whole gathered operand, must span less than 2^31 bytes.
 constexpr int64_t kMaxGemmK = int64_t(1) << 22;
@@ -112,7 +113,7 @@ size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols) {
 }
 
 int64_t mxq_route_slots(int64_t tokens, int64_t experts, int64_t topk, int64_t pad) {
-  if (tokens < 0 || experts < 1 || topk < 1 || pad < 1 || tokens > kMaxGridBlocks || topk > kMaxTopk ||
+  if (tokens < 0 || experts < 1 || topk < 1 || pad < 1 || tokens > kMaxRouteTokens || topk > kMaxTopk ||
       experts > kMaxExperts || pad > kMaxGridBlocks)
     return -1;
   const int64_t n = tokens * topk, used = n < experts ? n : experts;
@@ -742,7 +743,7 @@ mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, 
                      int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss,
                      void* workspace, size_t workspace_bytes, void* stream) {
   if (experts < 1 || experts > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > experts || pad < 1 || tokens < 0 ||
-      ld < experts || tokens > kMaxGridBlocks)
+      ld < experts || tokens > kMaxRouteTokens)
     return MXQ_ERR_SHAPE;
   const int64_t least = mxq_route_slots(tokens, experts, topk, pad);
   if (least < 0 || total < least || total % pad || total > kMaxGridBlocks) return MXQ_ERR_SHAPE;

@@ -20,7 +20,7 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kTok = 64;                         // tokens per workgroup (one bit each of a mask)
+constexpr int kTok = 64;                         // tokens of a block (one bit each of a mask)
 
 // Order-preserving key of a logit: 0 for NaN, kNegInf for -inf, larger for larger values; -0
 // equals +0. An expert is usable when its key lies above kNegInf.
@@ -34,194 +34,431 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// Reductions over the wave by DPP: rotations inside the rows of 16 lanes, then the row
+// broadcasts, then lane 63's value for all (an SGPR). Six dependent vector operations instead
+// of six trips through the LDS crossbar.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t o = shfl_xor_u32(v, off);
-    v = v > o ? v : o;
-  }
-  return v;
+  v = max(v, dpp<0x128, 0xF>(v));
+  v = max(v, dpp<0x124, 0xF>(v));
+  v = max(v, dpp<0x122, 0xF>(v));
+  v = max(v, dpp<0x121, 0xF>(v));
+  v = max(v, dpp<0x142, 0xA>(v));
+  v = max(v, dpp<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  auto add = [](float x, uint32_t o) { return x + __uint_as_float(o); };
+  v = add(v, dpp<0x128, 0xF>(__float_as_uint(v)));
+  v = add(v, dpp<0x124, 0xF>(__float_as_uint(v)));
+  v = add(v, dpp<0x122, 0xF>(__float_as_uint(v)));
+  v = add(v, dpp<0x121, 0xF>(__float_as_uint(v)));
+  v = add(v, dpp<0x142, 0xA>(__float_as_uint(v)));
+  v = add(v, dpp<0x143, 0xC>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// A lane's NE consecutive logits of a row, NaN past the row. With a whole number of lanes to the
+// row every lane takes one wide load (whatever the row's alignment), else single ones.
+template <int NE>
+__device__ __forceinline__ void load_logits(const float* row, int experts, float* z) {
+  const int e = (int)(threadIdx.x & 63) * NE;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) z[i] = __builtin_nanf("");
+  if (experts % NE == 0) {
+    if (e < experts) __builtin_memcpy(z, row + e, NE * 4);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (e + i < experts) z[i] = row[e + i];
+  }
+}
+
+// Sorts a lane's keys in descending order, equal ones as they stood (odd-even transposition: it
+// only swaps neighbours that are strictly out of order); nibble i of the result is where the
+// i-th key stood.
+template <int NE>
+__device__ __forceinline__ uint64_t sort_desc(uint32_t* key) {
+  uint32_t at[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) at[i] = i;
+#pragma unroll
+  for (int r = 0; r < NE; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < NE; i += 2) {
+      const bool swap = key[i] < key[i + 1];
+      const uint32_t k0 = key[i], k1 = key[i + 1], a0 = at[i], a1 = at[i + 1];
+      key[i] = swap ? k1 : k0;
+      key[i + 1] = swap ? k0 : k1;
+      at[i] = swap ? a1 : a0;
+      at[i + 1] = swap ? a0 : a1;
+    }
+  uint64_t order = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) order |= (uint64_t)at[i] << (4 * i);
+  return order;
+}
+
+struct Route {
+  const float* logits;
+  const uint8_t* valid;
+  int64_t tokens, ld, pad, total;
+  int experts, topk;
+  float coef;
+  int32_t* topk_idx;
+  float* weights;
+  int32_t* counts;
+  int64_t* offsets;
+  int32_t* row_index;
+  int64_t* slot_of;
+  float* loss;
+  uint8_t* hist;                                 // (blocks, hist_cols): takers per expert, then routed tokens
+  int32_t* base;                                 // (blocks, hist_cols): hist summed over earlier blocks
+  int32_t* sums;                                 // (hist_cols): hist summed over all blocks
+  float* psum;                                   // (blocks, experts): sums of p
+  uint64_t* tally;                               // the loss's sum over the blocks and their count
+};
+
+__host__ __device__ inline int hist_cols(int experts) { return (experts + 4) / 4 * 4; }
+
+// Waves of a workgroup that chooses: sixteen keep four on every SIMD; eight where sixteen rows of
+// sums would not fit beside the masks in 64 KB.
+constexpr int choose_waves(int ne) { return ne <= 8 ? 16 : 8; }
+
 // ---------------------------------------------------------------------------
-// Choice: one wave per token, NE experts per lane (expert = lane * NE + i). Writes topk_idx and
-// weights; per block and expert the number of takers and, for the loss, the sum of p.
+// Choice of one block of kTok tokens: one wave per token, NE experts per lane (expert =
+// lane * NE + i). Writes topk_idx and weights, leaves the experts' masks in LDS and adds each
+// lane's p to acc. A wave loads the logits of all its tokens before it looks at the first, so it
+// waits for memory once.
 // ---------------------------------------------------------------------------
 template <int NE>
-__global__ void __launch_bounds__(kThreads)
-route_choose_kernel(const float* __restrict__ logits, const uint8_t* __restrict__ valid, int64_t tokens, int experts,
-                    int64_t ld, int topk, int32_t* __restrict__ topk_idx, float* __restrict__ weights,
-                    int32_t* __restrict__ hist, float* __restrict__ psum, int32_t* __restrict__ routed_part) {
-  extern __shared__ uint64_t mask[];             // [experts], then kWaves * experts floats for psum
-  float* lp = reinterpret_cast<float*>(mask + experts);
-  __shared__ int32_t routed_w[kWaves];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < experts; e += kThreads) mask[e] = 0;
-  __syncthreads();
-  float acc[NE];
+__device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* acc) {
+  constexpr int W = choose_waves(NE), TPW = kTok / W;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok);
+  int routed = 0;
+  float ahead[TPW][NE];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-  int32_t routed = 0;
-  for (int tl = w; tl < kTok; tl += kWaves) {
-    const int64_t t = (int64_t)blockIdx.x * kTok + tl;
-    if (t >= tokens) break;
-    uint32_t key[NE], all[NE];
-    const bool on = !valid || valid[t];
+  for (int r = 0; r < TPW; ++r)
+    if (w + r * W < n) load_logits<NE>(a.logits + (t0 + w + r * W) * a.ld, a.experts, ahead[r]);
+  const int on = lane < n && (!a.valid || a.valid[t0 + lane]);             // lane: token of the block
+  for (int tl = w; tl < n; tl += W) {
+    const int64_t t = t0 + tl;
+    const bool live = __builtin_amdgcn_readlane(on, tl);
+    float z[NE];
+    uint32_t key[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int e = lane * NE + i;
-      key[i] = on && e < experts ? logit_key(logits[t * ld + e]) : 0u;
-      all[i] = key[i];
+      z[i] = ahead[0][i];
+      key[i] = live ? logit_key(z[i]) : 0u;
+#pragma unroll
+      for (int r = 0; r + 1 < TPW; ++r) ahead[r][i] = ahead[r + 1][i];
     }
-    float top = 0.0f, my = 0.0f;                 // largest logit; lane j: the j-th chosen one's numerator
+    uint64_t idx = sort_desc<NE>(key);           // nibble i: which of the lane's experts key[i] is
+    uint32_t top_key = 0, my_key = 0;            // lane j: the j-th chosen expert
     int my_e = -1;
-    for (int j = 0; j < topk; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
-      best = wave_max_u32(best);
+    for (int j = 0; j < a.topk; ++j) {
+      const uint32_t best = wave_max_u32(key[0]);
       if (best <= kNegInf) break;                // no usable expert left (uniform over the wave)
-      int at = NE;                               // this lane's first expert with that key
+      if (j == 0) top_key = best;
+      const int owner = __ffsll((unsigned long long)__ballot(key[0] == best)) - 1;
+      const int e = owner * NE + (__builtin_amdgcn_readlane((int)(uint32_t)idx, owner) & 15);
+      my_e = lane == j ? e : my_e;
+      my_key = lane == j ? best : my_key;
+      if (lane == owner) {                       // its next one moves up
 #pragma unroll
-      for (int i = NE - 1; i >= 0; --i)
-        if (key[i] == best) at = i;
-      const uint64_t has = __ballot(at < NE);
-      const int owner = __ffsll((unsigned long long)has) - 1;
-      const int at_o = __shfl(at, owner, 64);
-      const int e = owner * NE + at_o;
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (lane == owner && i == at_o) key[i] = 0;
-      const float z = key_logit(best);
-      if (j == 0) top = z;
-      if (lane == j) {
-        my = expf(z - top);
-        my_e = e;
+        for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
+        key[NE - 1] = 0;
+        idx >>= 4;
       }
-      if (lane == 0) atomicOr((unsigned long long*)&mask[e], 1ull << tl);
     }
-    const float sum = wave_sum(my);
-    if (lane < topk) {
-      topk_idx[t * topk + lane] = my_e;
-      weights[t * topk + lane] = my_e < 0 ? 0.0f : my / sum;
+    const float top = key_logit(top_key);
+    const float num = my_e >= 0 ? expf(key_logit(my_key) - top) : 0.0f;
+    const float den = wave_sum(num);
+    if (lane < a.topk) {
+      a.topk_idx[t * a.topk + lane] = my_e;
+      a.weights[t * a.topk + lane] = my_e >= 0 ? num / den : 0.0f;
     }
-    const bool any = __shfl(my_e, 0, 64) >= 0;
-    routed += any;
-    if (psum && any) {
-      float p[NE], z = 0.0f;
+    if (my_e >= 0) atomicOr((unsigned long long*)&mask[my_e], 1ull << tl);
+    if (top_key == 0) continue;
+    ++routed;
+    if (a.loss) {
+      float p[NE], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        p[i] = all[i] > kNegInf ? expf(key_logit(all[i]) - top) : 0.0f;
-        z += p[i];
+        p[i] = z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.0f;      // NaN: not usable either
+        sum += p[i];
       }
-      const float inv = 1.0f / wave_sum(z);
+      const float inv = 1.0f / wave_sum(sum);
 #pragma unroll
       for (int i = 0; i < NE; ++i) acc[i] += p[i] * inv;
     }
   }
+  return routed;
+}
+
+// One block's masks, routed tokens and (loss wanted) sums of p, in LDS: mask[experts], the
+// waves' routed tokens, then waves x experts floats whose first row ends up as the sums.
+template <int NE>
+__device__ __forceinline__ int choose_block(const Route& a, int64_t t0, uint64_t* mask) {
+  constexpr int waves = choose_waves(NE);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int* routed_w = reinterpret_cast<int*>(mask + a.experts);
+  float* lp = reinterpret_cast<float*>(routed_w + 16);
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) mask[e] = 0;
+  __syncthreads();
+  float acc[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+  const int routed = choose_tokens<NE>(a, t0, mask, acc);
   if (lane == 0) routed_w[w] = routed;
-  if (psum) {
+  if (a.loss) {
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (lane * NE + i < experts) lp[w * experts + lane * NE + i] = acc[i];
+      if (lane * NE + i < a.experts) lp[w * a.experts + lane * NE + i] = acc[i];
   }
   __syncthreads();
-  if (threadIdx.x == 0) routed_part[blockIdx.x] = routed_w[0] + routed_w[1] + routed_w[2] + routed_w[3];
-  for (int e = threadIdx.x; e < experts; e += kThreads) {
-    hist[(int64_t)blockIdx.x * experts + e] = __popcll((unsigned long long)mask[e]);
-    if (psum) psum[(int64_t)blockIdx.x * experts + e] = (lp[e] + lp[experts + e]) + (lp[2 * experts + e] + lp[3 * experts + e]);
+  int sum = 0;
+  for (int i = 0; i < waves; ++i) sum += routed_w[i];
+  if (a.loss)
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+      float s = lp[e];
+      for (int i = 1; i < waves; ++i) s += lp[i * a.experts + e];
+      lp[e] = s;
+    }
+  return sum;
+}
+
+size_t choose_lds(int experts, int waves, bool loss) {
+  return (size_t)experts * 8 + 64 + (loss ? (size_t)waves * experts * 4 : 0);
+}
+
+template <int NE>
+__global__ void __launch_bounds__(choose_waves(NE) * 64)
+route_choose_kernel(Route a) {
+  extern __shared__ uint64_t mask[];
+  const int routed = choose_block<NE>(a, (int64_t)blockIdx.x * kTok, mask);
+  const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
+  const int cols = hist_cols(a.experts);
+  for (int e = threadIdx.x; e < cols; e += blockDim.x)
+    a.hist[(int64_t)blockIdx.x * cols + e] =
+        (uint8_t)(e < a.experts ? __popcll((unsigned long long)mask[e]) : e == a.experts ? routed : 0);
+  if (a.loss) {
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.psum[(int64_t)blockIdx.x * a.experts + e] = lp[e];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.tally = 0;
   }
 }
 
-// ---------------------------------------------------------------------------
-// Plan: one workgroup. hist becomes its exclusive prefix over the blocks; counts, padded offsets
-// (what is left of `total` is dealt out in units of pad, low experts first), loss.
-// ---------------------------------------------------------------------------
 constexpr int kMaxExperts = 1024;
 
-__global__ void __launch_bounds__(kMaxExperts)
-route_plan_kernel(int32_t* __restrict__ hist, const float* __restrict__ psum, const int32_t* __restrict__ routed_part,
-                  int64_t blocks, int experts, int64_t pad, int64_t total, float coef, int32_t* __restrict__ counts,
-                  int64_t* __restrict__ offsets, float* __restrict__ loss) {
-  __shared__ int64_t units[kMaxExperts + 1];
-  __shared__ double dot[kMaxExperts];
-  __shared__ int64_t taken[kMaxExperts];
-  const int e = threadIdx.x;
-  int32_t c = 0;
-  double p = 0.0;
-  if (e < experts) {
-    for (int64_t b = 0; b < blocks; ++b) {
-      const int32_t h = hist[b * experts + e];
-      hist[b * experts + e] = c;
-      c += h;
-      if (psum) p += psum[b * experts + e];
-    }
-    counts[e] = c;
+__device__ __forceinline__ int wave_scan(int v) {            // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
   }
-  units[e] = (c + pad - 1) / pad;
-  dot[e] = (double)c * p;
-  taken[e] = c;
-  __syncthreads();
-  if (e == 0) {
-    int64_t used = 0, a = 0, routed = 0;
-    double s = 0.0;
-    for (int i = 0; i < experts; ++i) {
-      used += units[i];
-      a += taken[i];
-      s += dot[i];
-    }
-    for (int64_t b = 0; b < blocks; ++b) routed += routed_part[b];
-    counts[experts] = (int32_t)routed;
-    const int64_t spare = total / pad - used;
-    int64_t at = 0;
-    for (int i = 0; i < experts; ++i) {
-      offsets[i] = at;
-      at += (units[i] + spare / experts + (i < spare % experts ? 1 : 0)) * pad;
-    }
-    offsets[experts] = at;
-    if (loss) *loss = routed ? (float)((double)coef * experts * (s / ((double)a * (double)routed))) : 0.0f;
-  }
+  return v;
 }
 
-// ---------------------------------------------------------------------------
-// Slots: the choice's token blocks again; slot_of and row_index, -1 in the padding slots.
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads)
-route_slots_kernel(const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ base,
-                   const int32_t* __restrict__ counts, const int64_t* __restrict__ offsets, int64_t tokens,
-                   int experts, int topk, int32_t* __restrict__ row_index, int64_t* __restrict__ slot_of) {
-  extern __shared__ uint64_t mask[];
-  for (int e = threadIdx.x; e < experts; e += kThreads) mask[e] = 0;
+// Offsets from the counts, by one workgroup: every expert's units of pad, what is left of `total`
+// dealt out evenly, low experts first. cnt[experts] and off[experts + 1] in LDS, cnt published.
+// One wave scans (its lanes take consecutive experts): no partial sums of waves to exchange.
+__device__ __forceinline__ void padded_offsets(const Route& a, const int* cnt, int* off) {
+  const int lane = threadIdx.x & 63, G = a.experts, pad = (int)a.pad;
+  for (int e = threadIdx.x; e < G; e += blockDim.x) off[e + 1] = cnt[e] ? (cnt[e] - 1) / pad + 1 : 0;
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kTok;
-  const int n = (int)(tokens - t0 < kTok ? tokens - t0 : kTok) * topk;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int32_t e = topk_idx[t0 * topk + i];
-    if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << (i / topk));
+  if (threadIdx.x < 64) {
+    const int per = (G + 63) / 64, e0 = lane * per, e1 = min(e0 + per, G);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += off[e + 1];
+    int at = wave_scan(sum);
+    const int used = __shfl(at, 63, 64);
+    at -= sum;
+    const int spare = (int)(a.total / a.pad) - used, each = spare / G, more = spare % G;
+    for (int e = e0; e < e1; ++e) {
+      at += off[e + 1];
+      off[e + 1] = (at + (e + 1) * each + min(e + 1, more)) * pad;
+    }
+    if (lane == 0) off[0] = 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int32_t e = topk_idx[t0 * topk + i];
-    const int tl = i / topk;
+}
+
+// The slots of one block of tokens, and this workgroup's share of the padding slots' -1.
+// `start[e]`: where the block's tokens begin in expert e's slots.
+__device__ __forceinline__ void write_slots(const Route& a, int64_t t0, const uint64_t* mask, const int* cnt,
+                                            const int* off, const int* start) {
+  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int e = a.topk_idx[t0 * a.topk + i], tl = i / a.topk;
     int64_t slot = -1;
     if (e >= 0) {
-      slot = offsets[e] + base[(int64_t)blockIdx.x * experts + e] +
-             __popcll((unsigned long long)(mask[e] & ((1ull << tl) - 1)));
-      row_index[slot] = (int32_t)(t0 + tl);
+      slot = start[e] + __popcll((unsigned long long)(mask[e] & ((1ull << tl) - 1)));
+      a.row_index[slot] = (int32_t)(t0 + tl);
     }
-    slot_of[t0 * topk + i] = slot;
+    a.slot_of[t0 * a.topk + i] = slot;
   }
-  for (int e = blockIdx.x; e < experts; e += gridDim.x)
-    for (int64_t s = offsets[e] + counts[e] + threadIdx.x; s < offsets[e + 1]; s += kThreads) row_index[s] = -1;
+  const int group = (blockIdx.x * blockDim.x + threadIdx.x) / 16, groups = gridDim.x * blockDim.x / 16;
+  for (int e = group; e < a.experts; e += groups)            // 16 lanes an expert
+    for (int s = off[e] + cnt[e] + (threadIdx.x & 15); s < off[e + 1]; s += 16) a.row_index[s] = -1;
+}
+
+__device__ __forceinline__ void write_counts(const Route& a, const int* cnt, const int* off, int routed) {
+  for (int e = threadIdx.x; e <= a.experts; e += blockDim.x) {
+    a.counts[e] = e < a.experts ? cnt[e] : routed;
+    a.offsets[e] = off[e];
+  }
+}
+
+// Sum over the workgroup of one binary64 value a thread, in thread 0 (fixed order).
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  const int w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[w] = v;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int i = 1; i < waves; ++i) v += red[i];
+  return v;
+}
+
+// Thread 0: sum over the experts of counts_e times one block's sum of p, and the sum of counts.
+__device__ __forceinline__ double loss_dot(const Route& a, const int* cnt, const float* psum, double* red) {
+  double dot = 0.0;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) dot += (double)cnt[e] * (double)psum[e];
+  return block_sum(dot, red);
+}
+// experts / (A N): what turns the sum over the blocks of loss_dot into loss / coef (thread 0).
+__device__ __forceinline__ double loss_scale(const Route& a, const int* cnt, int routed, double* red) {
+  double all = 0.0;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) all += (double)cnt[e];
+  all = block_sum(all, red);
+  return routed ? (double)a.experts / (all * (double)routed) : 0.0;
 }
 
 // ---------------------------------------------------------------------------
-// Backward to the logits: one wave per token.
+// At most one block of tokens: everything in one launch.
+// ---------------------------------------------------------------------------
+template <int NE>
+__global__ void __launch_bounds__(choose_waves(NE) * 64)
+route_one_block_kernel(Route a) {
+  extern __shared__ uint64_t mask[];
+  __shared__ int cnt[NE * 64], off[NE * 64 + 1];
+  __shared__ double red[32];
+  const int routed = choose_block<NE>(a, 0, mask);
+  const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) cnt[e] = __popcll((unsigned long long)mask[e]);
+  __syncthreads();
+  padded_offsets(a, cnt, off);
+  write_counts(a, cnt, off, routed);
+  write_slots(a, 0, mask, cnt, off, off);
+  if (a.loss) {
+    const double dot = loss_dot(a, cnt, lp, red), scale = loss_scale(a, cnt, routed, red);
+    if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * scale * dot);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of the blocks' histograms, one wave per column: base (exclusive over the blocks), sums.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads)
+route_scan_kernel(Route a, int blocks) {
+  const int lane = threadIdx.x & 63, cols = hist_cols(a.experts);
+  const int c = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  if (c > a.experts) return;
+  int carry = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 64) {
+    const int b = b0 + lane;
+    const int v = b < blocks ? a.hist[(int64_t)b * cols + c] : 0;
+    const int incl = wave_scan(v);
+    if (b < blocks) a.base[(int64_t)b * cols + c] = carry + incl - v;
+    carry += __shfl(incl, 63, 64);
+  }
+  if (lane == 0) a.sums[c] = carry;
+}
+
+// ---------------------------------------------------------------------------
+// Slots of one block of tokens per workgroup. SCANNED: base and sums come from route_scan_kernel;
+// otherwise every workgroup adds up the histograms itself. The loss: each workgroup weighs its
+// block's sums of p with the counts and adds the result to a tally (cleared by
+// route_choose_kernel); the one that completes it writes the loss.
+// ---------------------------------------------------------------------------
+constexpr int kSlotThreads = 1024;               // one workgroup a CU fills its waves
+
+template <bool SCANNED>
+__global__ void __launch_bounds__(kSlotThreads)
+route_slots_kernel(Route a, int blocks) {
+  extern __shared__ uint64_t mask[];
+  __shared__ int cnt[kMaxExperts + 4], off[kMaxExperts + 1], start[kMaxExperts + 4];
+  __shared__ double red[32];
+  const int cols = hist_cols(a.experts), blk = blockIdx.x;
+  const int64_t t0 = (int64_t)blk * kTok;
+  for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) mask[e] = 0;
+  if (SCANNED) {
+    for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
+      cnt[e] = a.sums[e];
+      start[e] = a.base[(int64_t)blk * cols + e];
+    }
+  } else {
+    // four columns a thread and dword, summed as two pairs of 16 bits (fewer than 1024 blocks)
+    for (int e = threadIdx.x; e < cols; e += kSlotThreads) cnt[e] = start[e] = 0;
+    __syncthreads();
+    const int quads = cols / 4, groups = kSlotThreads / quads > 0 ? kSlotThreads / quads : 1;
+    for (int i = threadIdx.x; i < quads * groups; i += kSlotThreads) {
+      const int qd = i % quads;
+      uint32_t lo = 0, hi = 0, blo = 0, bhi = 0;
+#pragma unroll 8
+      for (int b = i / quads; b < blocks; b += groups) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(a.hist + (int64_t)b * cols + 4 * qd);
+        const uint32_t l = v & 0x00FF00FFu, h = (v >> 8) & 0x00FF00FFu;
+        lo += l;
+        hi += h;
+        blo += b < blk ? l : 0u;
+        bhi += b < blk ? h : 0u;
+      }
+      const uint32_t s[4] = {lo & 0xFFFFu, hi & 0xFFFFu, lo >> 16, hi >> 16};
+      const uint32_t f[4] = {blo & 0xFFFFu, bhi & 0xFFFFu, blo >> 16, bhi >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {              // integer sums: the order does not matter
+        atomicAdd(&cnt[4 * qd + k], (int)s[k]);
+        atomicAdd(&start[4 * qd + k], (int)f[k]);
+      }
+    }
+  }
+  __syncthreads();
+  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
+  for (int i = threadIdx.x; i < n; i += kSlotThreads) {
+    const int e = a.topk_idx[t0 * a.topk + i];
+    if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << (i / a.topk));
+  }
+  padded_offsets(a, cnt, off);
+  for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) start[e] += off[e];
+  __syncthreads();
+  write_slots(a, t0, mask, cnt, off, start);
+  if (blk == 0) write_counts(a, cnt, off, cnt[a.experts]);
+  if (!a.loss) return;
+  const double dot = loss_dot(a, cnt, a.psum + (int64_t)blk * a.experts, red);
+  const double scale = loss_scale(a, cnt, cnt[a.experts], red);
+  if (threadIdx.x != 0) return;
+  // One atomic carries the workgroups' count (above bit `frac` + 11) and the sum so far in fixed
+  // point: loss / coef is at most experts <= 2^10. Integers, so the order does not matter, and
+  // whoever makes the count complete holds the whole sum. 65536 blocks leave 34 bits of fraction.
+  const int frac = 62 - (32 - __clz(blocks)) - 11;
+  const uint64_t one = 1ull << (frac + 11);
+  const uint64_t add = one + (uint64_t)llrint(ldexp(dot * scale, frac));
+  const uint64_t now = atomicAdd((unsigned long long*)a.tally, (unsigned long long)add) + add;
+  if ((now >> (frac + 11)) == (uint64_t)blocks)
+    *a.loss = (float)((double)a.coef * ldexp((double)(now & (one - 1)), -frac));
+}
+
+// ---------------------------------------------------------------------------
+// Backward to the logits: one wave per token at a time; the counts stay in registers over the
+// tokens of a wave, and the next token's logits are on their way while it works on one.
 // ---------------------------------------------------------------------------
 template <int NE>
 __global__ void __launch_bounds__(kThreads)
@@ -229,59 +466,81 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
                       const int32_t* __restrict__ topk_idx, const float* __restrict__ weights,
                       const float* __restrict__ d_weights, const int32_t* __restrict__ counts,
                       const float* __restrict__ d_loss, float coef, float* __restrict__ d_logits) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  int64_t t = (int64_t)blockIdx.x * kWaves + w;
   if (t >= tokens) return;
-  const int my_e = lane < topk ? topk_idx[t * topk + lane] : -1;
-  float d[NE];
+  float c[NE], ahead[NE], scale = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) d[i] = 0.0f;
-  const bool any = __shfl(my_e, 0, 64) >= 0;
-  if (any && d_loss) {
-    int a = 0;
-    float z[NE], c[NE], top = -__builtin_inff();
+  for (int i = 0; i < NE; ++i) c[i] = ahead[i] = 0.0f;
+  int e_ahead = -1;
+  float w_ahead = 0.0f, dw_ahead = 0.0f;
+  auto fetch = [&](int64_t at) {
+    if (at >= tokens) return;
+    if (d_loss) load_logits<NE>(logits + at * ld, experts, ahead);
+    if (lane < topk) {
+      e_ahead = topk_idx[at * topk + lane];
+      if (d_weights) {
+        w_ahead = weights[at * topk + lane];
+        dw_ahead = d_weights[at * topk + lane];
+      }
+    }
+  };
+  fetch(t);
+  if (d_loss) {
+    float all = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = lane * NE + i;
-      z[i] = e < experts ? logits[t * ld + e] : -__builtin_inff();
-      const int n = e < experts ? counts[e] : 0;
-      c[i] = (float)n;
-      a += n;
-      top = fmaxf(top, z[i]);
+      c[i] = e < experts ? (float)counts[e] : 0.0f;
+      all += c[i];
     }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      top = fmaxf(top, __shfl_xor(top, off, 64));
-      a += __shfl_xor(a, off, 64);
-    }
-    float sum = 0.0f, pc = 0.0f;
+    scale = *d_loss * ((coef * experts) / (wave_sum(all) * (float)counts[experts]));
+  }
+  for (; t < tokens; t += step) {
+    const int my_e = e_ahead;
+    const float wj = my_e >= 0 ? w_ahead : 0.0f, dwj = my_e >= 0 ? dw_ahead : 0.0f;
+    float z[NE], d[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      z[i] = z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.0f;   // an unusable expert has p = 0
-      sum += z[i];
-      pc += z[i] * c[i];
+      z[i] = ahead[i];
+      d[i] = 0.0f;
     }
-    sum = wave_sum(sum);
-    pc = wave_sum(pc) / sum;
-    const float scale = *d_loss * ((coef * experts) / ((float)a * (float)counts[experts])) / sum;
+    fetch(t + step);
+    if (d_loss && __builtin_amdgcn_readlane(my_e, 0) >= 0) {
+      uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) d[i] = scale * z[i] * (c[i] - pc);
-  }
-  if (d_weights) {
-    const float w = my_e >= 0 ? weights[t * topk + lane] : 0.0f;
-    const float dw = my_e >= 0 ? d_weights[t * topk + lane] : 0.0f;
-    const float g = w * (dw - wave_sum(w * dw));
-    for (int j = 0; j < topk; ++j) {
-      const int e = __shfl(my_e, j, 64);
-      const float gj = __shfl(g, j, 64);
+      for (int i = 0; i < NE; ++i) best = max(best, logit_key(z[i]));
+      const float top = key_logit(wave_max_u32(best));
+      float sum = 0.0f, pc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        z[i] = z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.0f;   // an unusable expert has p = 0
+        sum += z[i];
+        pc += z[i] * c[i];
+      }
+      const float inv = 1.0f / wave_sum(sum), mean = wave_sum(pc) * inv;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) d[i] = (scale * inv) * z[i] * (c[i] - mean);
+    }
+    if (d_weights) {
+      const float g = wj * (dwj - wave_sum(wj * dwj));
+      for (int j = 0; j < topk; ++j) {
+        const int e = __builtin_amdgcn_readlane(my_e, j) - lane * NE;
+        const float gj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
+#pragma unroll
+        for (int i = 0; i < NE; ++i) d[i] += e == i ? gj : 0.0f;
+      }
+    }
+    float* out = d_logits + t * experts + lane * NE;
+    if (experts % NE == 0) {
+      if (lane * NE < experts) __builtin_memcpy(out, d, NE * 4);
+    } else {
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (e == lane * NE + i) d[i] += gj;
+        if (lane * NE + i < experts) out[i] = d[i];
     }
   }
-#pragma unroll
-  for (int i = 0; i < NE; ++i)
-    if (lane * NE + i < experts) d_logits[t * experts + lane * NE + i] = d[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -358,32 +617,46 @@ void with_experts(int64_t experts, F&& go) {                 // experts per lane
 
 int64_t route_blocks(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
 
+// Blocks up to which every slots workgroup adds up all histograms itself, which saves the scan's
+// launch; its reads grow with the square of the blocks.
+constexpr int64_t kMaxUnscanned = 256;
+
 }  // namespace
 
-// Workspace: hist (blocks, experts) int32, routed tokens per block, psum (blocks, experts) float.
+// Workspace: tally, psum, base, sums, hist (see Route).
 size_t route_ws_bytes(int64_t tokens, int64_t experts) {
-  return (size_t)(route_blocks(tokens) * (2 * experts + 1) * 4);
+  const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
+  return (size_t)(8 + 4 * nb * experts + 4 * nb * cols + 4 * cols + nb * cols);
 }
 
 hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
                         int64_t topk, int64_t pad, int64_t total, float coef, int32_t* topk_idx, float* weights,
                         int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss, void* ws,
                         hipStream_t st) {
-  const int64_t nb = route_blocks(tokens);
-  int32_t* hist = (int32_t*)ws;
-  int32_t* routed = hist + nb * experts;
-  float* psum = loss ? (float*)(routed + nb) : nullptr;
-  const size_t lds = experts * 8;
-  if (nb)
-    with_experts(experts, [&](auto NE) {
-      hipLaunchKernelGGL((route_choose_kernel<decltype(NE)::value>), dim3((unsigned)nb), dim3(kThreads),
-                         lds + kWaves * experts * 4, st, logits, valid, tokens, (int)experts, ld, (int)topk, topk_idx,
-                         weights, hist, psum, routed);
-    });
-  hipLaunchKernelGGL(route_plan_kernel, dim3(1), dim3(kMaxExperts), 0, st, hist, psum, routed, nb, (int)experts, pad,
-                     total, coef, counts, offsets, loss);
-  hipLaunchKernelGGL(route_slots_kernel, dim3((unsigned)(nb ? nb : 1)), dim3(kThreads), lds, st, topk_idx, hist, counts,
-                     offsets, tokens, (int)experts, (int)topk, row_index, slot_of);
+  const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
+  Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, coef, topk_idx, weights, counts, offsets,
+          row_index, slot_of, loss, nullptr, nullptr, nullptr, nullptr, nullptr};
+  a.tally = (uint64_t*)ws;
+  a.psum = (float*)(a.tally + 1);
+  a.base = (int32_t*)(a.psum + nb * experts);
+  a.sums = a.base + nb * cols;
+  a.hist = (uint8_t*)(a.sums + cols);
+  with_experts(experts, [&](auto N) {
+    constexpr int NE = decltype(N)::value, W = choose_waves(NE);
+    const size_t lds = choose_lds((int)experts, W, loss != nullptr);
+    if (nb <= 1)
+      hipLaunchKernelGGL((route_one_block_kernel<NE>), dim3(1), dim3(W * 64), lds, st, a);
+    else
+      hipLaunchKernelGGL((route_choose_kernel<NE>), dim3((unsigned)nb), dim3(W * 64), lds, st, a);
+  });
+  if (nb <= 1) return hipGetLastError();
+  if (nb > kMaxUnscanned) {
+    hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((experts + kWaves) / kWaves)), dim3(kThreads), 0, st, a,
+                       (int)nb);
+    hipLaunchKernelGGL((route_slots_kernel<true>), dim3((unsigned)nb), dim3(kSlotThreads), experts * 8, st, a, (int)nb);
+  } else {
+    hipLaunchKernelGGL((route_slots_kernel<false>), dim3((unsigned)nb), dim3(kSlotThreads), experts * 8, st, a, (int)nb);
+  }
   return hipGetLastError();
 }
 
@@ -391,9 +664,9 @@ hipError_t launch_route_backward(const float* logits, int64_t tokens, int64_t ex
                                  const int32_t* topk_idx, const float* weights, const float* d_weights,
                                  const int32_t* counts, const float* d_loss, float coef, float* d_logits,
                                  hipStream_t st) {
+  const int64_t want = (tokens + kWaves - 1) / kWaves, grid = want < 2048 ? want : 2048;   // eight workgroups a CU
   with_experts(experts, [&](auto NE) {
-    hipLaunchKernelGGL((route_backward_kernel<decltype(NE)::value>), dim3((unsigned)((tokens + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, st, logits, tokens, (int)experts, ld, (int)topk, topk_idx, weights, d_weights,
+    hipLaunchKernelGGL((route_backward_kernel<decltype(NE)::value>), dim3((unsigned)grid), dim3(kThreads), 0, st, logits, tokens, (int)experts, ld, (int)topk, topk_idx, weights, d_weights,
                        counts, d_loss, coef, d_logits);
   });
   return hipGetLastError();

@@ -79,6 +79,7 @@ def test_route_validation():
     assert f(total=28) == 2 and f(total=34) == 2                            # below the worst case; no multiple of pad
     assert f(k=0) == 2 and f(k=9) == 2 and f(G=0) == 2 and f(G=2000, ld=2000, total=1 << 20) == 2
     assert f(pad=0) == 2 and f(T=-1) == 2 and f(ld=7) == 2 and f(total=1 << 31) == 2
+    assert f(T=(1 << 22) + 1, total=1 << 24) == 2                           # tokens beyond 2^22
     assert f(G=64, ld=64, k=33, total=1 << 12) == 2                         # topk beyond 32
     for name in ("z", "idx", "w", "counts", "off", "row", "slot"):
         assert f(**{name: None}) == 1, name
