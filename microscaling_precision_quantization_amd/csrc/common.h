@@ -46,6 +46,58 @@ __device__ __forceinline__ uint32_t shfl_xor_u32(uint32_t v, int mask) {
   return (uint32_t)__shfl_xor((int)v, mask, 64);
 }
 
+// Reductions over the wave by DPP: rotations inside the rows of 16 lanes, then the row
+// broadcasts, then lane 63's value for all (scalar registers). Dependent vector operations
+// instead of trips through the LDS crossbar; the order of the additions is fixed.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f32(float v) { return __uint_as_float(dpp_u32<CTRL, ROWS>(__float_as_uint(v))); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)dpp_u32<CTRL, ROWS>((uint32_t)(u >> 32)) << 32 |
+                                          dpp_u32<CTRL, ROWS>((uint32_t)u)));
+}
+__device__ __forceinline__ uint32_t lane63(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_u32<0x128, 0xF>(v));
+  v = max(v, dpp_u32<0x124, 0xF>(v));
+  v = max(v, dpp_u32<0x122, 0xF>(v));
+  v = max(v, dpp_u32<0x121, 0xF>(v));
+  v = max(v, dpp_u32<0x142, 0xA>(v));
+  v = max(v, dpp_u32<0x143, 0xC>(v));
+  return lane63(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0x128, 0xF>(v);
+  v += dpp_f32<0x124, 0xF>(v);
+  v += dpp_f32<0x122, 0xF>(v);
+  v += dpp_f32<0x121, 0xF>(v);
+  v += dpp_f32<0x142, 0xA>(v);
+  v += dpp_f32<0x143, 0xC>(v);
+  return __uint_as_float(lane63(__float_as_uint(v)));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp_f64<0x128, 0xF>(v);
+  v += dpp_f64<0x124, 0xF>(v);
+  v += dpp_f64<0x122, 0xF>(v);
+  v += dpp_f64<0x121, 0xF>(v);
+  v += dpp_f64<0x142, 0xA>(v);
+  v += dpp_f64<0x143, 0xC>(v);
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)lane63((uint32_t)(u >> 32)) << 32 | lane63((uint32_t)u)));
+}
+
+// Barrier that orders LDS accesses only: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Packed maximum of two pairs of unsigned 16-bit integers (sign-cleared BF16
 // bit patterns order like their magnitudes).
 __device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {

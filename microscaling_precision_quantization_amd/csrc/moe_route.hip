@@ -34,33 +34,6 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// Reductions over the wave by DPP: rotations inside the rows of 16 lanes, then the row
-// broadcasts, then lane 63's value for all (an SGPR). Six dependent vector operations instead
-// of six trips through the LDS crossbar.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = max(v, dpp<0x128, 0xF>(v));
-  v = max(v, dpp<0x124, 0xF>(v));
-  v = max(v, dpp<0x122, 0xF>(v));
-  v = max(v, dpp<0x121, 0xF>(v));
-  v = max(v, dpp<0x142, 0xA>(v));
-  v = max(v, dpp<0x143, 0xC>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  auto add = [](float x, uint32_t o) { return x + __uint_as_float(o); };
-  v = add(v, dpp<0x128, 0xF>(__float_as_uint(v)));
-  v = add(v, dpp<0x124, 0xF>(__float_as_uint(v)));
-  v = add(v, dpp<0x122, 0xF>(__float_as_uint(v)));
-  v = add(v, dpp<0x121, 0xF>(__float_as_uint(v)));
-  v = add(v, dpp<0x142, 0xA>(__float_as_uint(v)));
-  v = add(v, dpp<0x143, 0xC>(__float_as_uint(v)));
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
-
 // A lane's NE consecutive logits of a row, NaN past the row. With a whole number of lanes to the
 // row every lane takes one wide load (whatever the row's alignment), else single ones.
 template <int NE>

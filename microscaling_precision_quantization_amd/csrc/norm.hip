@@ -16,8 +16,6 @@
 namespace mxq {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-
 // Eight consecutive elements of a BF16 or FP32 row, as FP32.
 template <bool F32>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float* f) {
@@ -58,91 +56,173 @@ __device__ __forceinline__ void zero8(float* f) {
   for (int k = 0; k < 8; ++k) f[k] = 0.0f;
 }
 
-// Sum over the workgroup, the same for all threads (fixed order). `red` holds one value per
-// wave; a barrier separates two uses of it.
-template <typename T>
+// One value per wave into LDS, all of them out again after a barrier that waits for LDS only.
+// A kernel that loops over rows alternates between two buffers, so one barrier a row is enough:
+// whoever writes a buffer again has passed the barrier in between, and all reads of it are done.
+template <int W, typename T>
 __device__ __forceinline__ T block_sum(T v, T* red) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+  v = wave_sum(v);
+  if (W == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
+  lds_barrier();
   T s = red[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) s += red[i];
-  __syncthreads();
+  for (int i = 1; i < W; ++i) s += red[i];
   return s;
 }
 
-__device__ __forceinline__ float block_max(float v, float* red) {
-  v = wave_max_f32(v);
+template <int W>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = wave_max_u32(v);
+  if (W == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = red[0];
+  lds_barrier();
+  uint32_t s = red[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) s = fmaxf(s, red[i]);
+  for (int i = 1; i < W; ++i) s = max(s, red[i]);
   return s;
 }
 
+// Eight elements as loaded, BF16 or FP32.
+template <bool F32>
+struct Raw8 {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint8_t* p = (const uint8_t*)base + at * (F32 ? 4 : 2);
+    v[0] = load_stream16(p);
+    if (F32) v[F32 ? 1 : 0] = load_stream16(p + 16);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (auto& u : v) u = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if (F32) {
+      const uint4 a = v[0], b = v[F32 ? 1 : 0];
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+      f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t amax8(const uint4& p) {  // two maxima in one dword
+  return pk_max_u16(pk_max_u16(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu), pk_max_u16(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
+}
+
+// Eight n = f r w to BF16, each rounded once from its value in binary64.
+__device__ __forceinline__ uint4 norm8_f64(const float* f, const float* w, double r) {
+  uint32_t h[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = f64_to_bf16_rne((double)f[k] * r * (double)w[k]);
+  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+}
+
+// The same eight values, mostly from binary32. v = (f r32) w carries three roundings of 2^-24
+// relative, so it lies within 3 of its own ulps of f r w; where its low 16 bits differ from
+// 0x8000 by more than 4, both lie on the same side of every BF16 midpoint and rounding v gives
+// the correctly rounded value. False where a value lies closer than that (one vector in 900), is
+// nonzero and below 2^-100, or has a weight beyond 2^20: then binary64 decides. (2^-100 and 2^20
+// keep f r32 a normal number; r itself is checked by the caller.)
+__device__ __forceinline__ bool norm8_f32(const float* f, const float* w, float r32, uint4& out) {
+  float v[8], big = 0.0f;
+  uint32_t mid = 0xFFFFFFFFu, least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = f[k] * r32 * w[k];
+    const uint32_t u = __float_as_uint(v[k]);
+    mid = min(mid, (u + 0x8004u) << 16);                    // distance above 0x8000 - 4
+    least = min(least, (u << 1) - 1u);                      // zeros wrap around to the top
+    big = fmaxf(big, fabsf(w[k]));
+  }
+  out = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+  return mid > (8u << 16) && least >= (27u << 24) && big <= 1048576.0f;
+}
+
 // ---------------------------------------------------------------------------
-// Norm before a block: one workgroup per row, the row kept in registers (NV vectors of 8 per
-// thread), so x is read once. FMT: 1 MXFP8, 2 NVFP4 per token, 3 BF16 only, 4 MXFP4.
+// Norm before a block. W waves hold a row (W = 1: four rows to a workgroup, no barrier) as it
+// was loaded, NV vectors of 8 per lane, so x is read once. FMT: 1 MXFP8, 2 NVFP4 per token,
+// 3 BF16 only, 4 MXFP4.
 // ---------------------------------------------------------------------------
-template <int FMT, bool X32, int NV>
-__global__ void __launch_bounds__(kThreads)
-norm_quant_kernel(const void* __restrict__ x, int64_t cols, int64_t ld_x, const float* __restrict__ weight, double eps,
-                  uint16_t* __restrict__ n_out, uint8_t* __restrict__ q, uint8_t* __restrict__ s,
-                  float* __restrict__ t_out, float* __restrict__ rstd) {
-  __shared__ double red[kWaves];
-  __shared__ float redm[kWaves];
-  const int64_t row = blockIdx.x;
-  float f[NV][8];
+template <int FMT, bool X32, int W, int NV>
+__global__ void __launch_bounds__(W == 1 ? 256 : W * 64)
+norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld_x, const float* __restrict__ weight,
+                  double eps, double inv_cols, uint16_t* __restrict__ n_out, uint8_t* __restrict__ q,
+                  uint8_t* __restrict__ s, float* __restrict__ t_out, float* __restrict__ rstd) {
+  __shared__ double red[W];
+  __shared__ uint32_t redm[W];
+  const int tid = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (W == 1 && row >= rows) return;
+  auto col = [&](int i) { return 8 * (i * W * 64 + tid); };
+  Raw8<X32> xr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    xr[i].clear();
+    if (col(i) < cols) xr[i].load(x, row * ld_x + col(i));
+  }
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-    zero8(f[i]);
-    if (e < cols) load8<X32>(x, row * ld_x + e, f[i]);
+    float f[8];
+    xr[i].get(f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fma((double)f[k], (double)f[k], ss);
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
-  ss = block_sum(ss, red);
-  const double r = 1.0 / sqrt(ss / (double)cols + eps);
-  if (rstd && threadIdx.x == 0) rstd[row] = (float)r;
+  ss = block_sum<W>(ss, red);
+  const double r = rsqrt(fma(ss, inv_cols, eps));
+  if (rstd && tid == 0) rstd[row] = (float)r;
+
+  // n from binary32; bit i of `redo`: vector i of this wave holds a value that needs binary64
   uint4 p[NV];
-  uint32_t amax = 0;
+  uint32_t redo = 0;
+  const bool wide = !(r >= 0x1p-60 && r <= 0x1p60);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
     p[i] = make_uint4(0, 0, 0, 0);
-    if (e >= cols) continue;
-    float w[8];
-    load8_cached(weight, e, w);
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = f64_to_bf16_rne((double)f[i][k] * r * (double)w[k]);
-    p[i] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
-    if (n_out) *reinterpret_cast<uint4*>(n_out + row * cols + e) = p[i];
-    if (FMT == 2)
-      amax = pk_max_u16(amax, pk_max_u16(pk_max_u16(p[i].x & 0x7FFF7FFFu, p[i].y & 0x7FFF7FFFu),
-                                         pk_max_u16(p[i].z & 0x7FFF7FFFu, p[i].w & 0x7FFF7FFFu)));
+    bool sure = true;
+    if (col(i) < cols) {
+      float f[8], w[8];
+      xr[i].get(f);
+      load8_cached(weight, col(i), w);
+      sure = norm8_f32(f, w, (float)r, p[i]) && !wide;
+    }
+    redo |= __any(!sure) ? 1u << i : 0u;
   }
-  if (FMT == 3) return;
+  while (redo) {                                             // uniform; its x and w come from the caches
+    const int j = __ffs(redo) - 1;
+    redo &= redo - 1;
+    if (col(j) < cols) {
+      Raw8<X32> again;
+      float f[8], w[8];
+      again.load(x, row * ld_x + col(j));
+      again.get(f);
+      load8_cached(weight, col(j), w);
+      const uint4 fixed = norm8_f64(f, w, r);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i == j) p[i] = fixed;
+    }
+  }
+
   float s_enc = 1.0f;
   if (FMT == 2) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) amax = pk_max_u16(amax, amax8(p[i]));
     float t;
-    scope_scales(block_max(__uint_as_float(max_halves(amax) << 16), redm), s_enc, t);
-    if (threadIdx.x == 0) t_out[row] = t;
+    scope_scales(__uint_as_float(block_max<W>(max_halves(amax), redm) << 16), s_enc, t);
+    if (tid == 0) t_out[row] = t;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-    // cols is a multiple of the block, so the 2 (NVFP4) or 4 lanes of a block leave together;
+    // cols is a multiple of the block, so the 2 (NVFP4) or 4 lanes of a block end together;
     // lanes past the row hold zeros and only take part in the exchanges
-    uint32_t a = pk_max_u16(pk_max_u16(p[i].x & 0x7FFF7FFFu, p[i].y & 0x7FFF7FFFu),
-                            pk_max_u16(p[i].z & 0x7FFF7FFFu, p[i].w & 0x7FFF7FFFu));
-    a = max_halves(a);
+    const int e = col(i);
+    if (n_out && e < cols) *reinterpret_cast<uint4*>(n_out + row * cols + e) = p[i];
+    if (FMT == 3) continue;
+    uint32_t a = max_halves(amax8(p[i]));
     a = max(a, dpp_xor1(a));
     if (FMT != 2) a = max(a, dpp_xor2(a));
     if (FMT == 1) {
@@ -152,7 +232,7 @@ norm_quant_kernel(const void* __restrict__ x, int64_t cols, int64_t ld_x, const 
       const uint32_t hi = cvt_fp8x2_bf16(cvt_fp8x2_bf16(0u, p[i].z, sc, false), p[i].w, sc, true);
       if (e < cols) {
         *reinterpret_cast<uint2*>(q + row * cols + e) = make_uint2(lo, hi);
-        if ((threadIdx.x & 3) == 0) s[row * (cols / 32) + e / 32] = (uint8_t)code;
+        if ((tid & 3) == 0) s[row * (cols / 32) + e / 32] = (uint8_t)code;
       }
     } else {
       float v[8], mul;
@@ -168,7 +248,7 @@ norm_quant_kernel(const void* __restrict__ x, int64_t cols, int64_t ld_x, const 
       if (e < cols) {
         *reinterpret_cast<uint32_t*>(q + row * (cols / 2) + e / 2) = packed;
         constexpr int LB = FMT == 2 ? 2 : 4;                 // lanes of a block
-        if ((threadIdx.x & (LB - 1)) == 0) s[row * (cols / (8 * LB)) + e / (8 * LB)] = (uint8_t)code;
+        if ((tid & (LB - 1)) == 0) s[row * (cols / (8 * LB)) + e / (8 * LB)] = (uint8_t)code;
       }
     }
   }
@@ -178,45 +258,50 @@ norm_quant_kernel(const void* __restrict__ x, int64_t cols, int64_t ld_x, const 
 // Norm after a block: out = res_scale x + branch_scale gate (y r w), one workgroup per row.
 // GATE: 0 none, 1 one per row, 2 one per column, 3 one per element.
 // ---------------------------------------------------------------------------
-template <bool X32, bool Y32, int GATE, int NV>
-__global__ void __launch_bounds__(kThreads)
+template <bool X32, bool Y32, int GATE, int W, int NV>
+__global__ void __launch_bounds__(W * 64)
 gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int64_t cols,
                      const float* __restrict__ weight, const float* __restrict__ gate, double eps, float branch_scale,
                      float res_scale, void* __restrict__ out, float* __restrict__ rstd) {
-  __shared__ double red[kWaves];
+  __shared__ double red[W];
   const int64_t row = blockIdx.x;
-  float f[NV][8], xv[NV][8];
+  auto col = [&](int i) { return 8 * (int64_t)(i * W * 64 + (int)threadIdx.x); };
+  Raw8<Y32> yr[NV];
+  Raw8<X32> xr[NV];
+  float f[NV][8];
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-    zero8(f[i]);
-    if (e < cols) {
-      load8<Y32>(y, row * cols + e, f[i]);
-      load8<X32>(x, row * cols + e, xv[i]);
+    yr[i].clear();
+    if (col(i) < cols) {
+      yr[i].load(y, row * cols + col(i));
+      xr[i].load(x, row * cols + col(i));
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    yr[i].get(f[i]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
-  ss = block_sum(ss, red);
+  }
+  ss = block_sum<W>(ss, red);
   const float r = (float)(1.0 / sqrt(ss / (double)cols + eps));
   if (rstd && threadIdx.x == 0) rstd[row] = r;
   const float c = GATE == 1 ? branch_scale * gate[row] : branch_scale;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
+    const int64_t e = col(i);
     if (e >= cols) continue;
-    float w[8], g[8], o[8];
+    float w[8], g[8], xv[8], o[8];
     load8_cached(weight, e, w);
     if (GATE == 2) load8_cached(gate, e, g);
     if (GATE == 3) load8<true>(gate, row * cols + e, g);
+    xr[i].get(xv);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float b = f[i][k] * r * w[k];
       if (GATE >= 2) b *= g[k];
-      o[k] = fmaf(b, c, res_scale * xv[i][k]);
+      o[k] = fmaf(b, c, res_scale * xv[k]);
     }
     store8<X32>(out, row * cols + e, o);
   }
@@ -237,55 +322,69 @@ struct NormGrad {
   float *dw_part, *dg_part, *dgate;   // partial sums (NULL: not wanted); gate gradient (GATE 1 and 3)
 };
 
-template <bool D32, bool Y32, int GATE, int NV>
-__global__ void __launch_bounds__(kThreads)
+template <bool D32, bool Y32, int GATE, int W, int NV>
+__global__ void __launch_bounds__(W * 64)
 norm_backward_kernel(NormGrad a) {
-  __shared__ float red[kWaves];
+  __shared__ float red[2][W], redg[2][W];
   const int64_t cols = a.cols;
+  auto col = [&](int i) { return 8 * (int64_t)(i * W * 64 + (int)threadIdx.x); };
   float w[NV][8], dw[NV][8], gc[GATE == 2 ? NV : 1][8], dgc[GATE == 2 ? NV : 1][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
     zero8(w[i]);
     zero8(dw[i]);
-    if (e < cols) load8_cached(a.weight, e, w[i]);
+    if (col(i) < cols) load8_cached(a.weight, col(i), w[i]);
     if (GATE == 2) {
       zero8(gc[i]);
       zero8(dgc[i]);
-      if (e < cols) load8_cached(a.gate, e, gc[i]);
+      if (col(i) < cols) load8_cached(a.gate, col(i), gc[i]);
     }
   }
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float r = a.rstd[row];
-    const float gr = GATE == 1 ? a.gate[row] : 1.0f;
-    float d[NV][8], yh[NV][8];
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+    Raw8<D32> dr[NV], d2r[NV];
+    Raw8<Y32> yr[NV], rr[NV];
+    const int64_t at = row * cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-      zero8(d[i]);
-      zero8(yh[i]);
-      if (e < cols) {
-        load8<D32>(a.d, row * cols + e, d[i]);
-        load8<Y32>(a.y, row * cols + e, yh[i]);
+      dr[i].clear();
+      yr[i].clear();
+      if (col(i) < cols) {
+        dr[i].load(a.d, at + col(i));
+        yr[i].load(a.y, at + col(i));
       }
     }
     if (a.d2) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-        if (e >= cols) continue;
+        d2r[i].clear();
+        if (col(i) < cols) d2r[i].load(a.d2, at + col(i));
+      }
+    }
+    if (a.res) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < cols) rr[i].load(a.res, at + col(i));
+    }
+    const float r = a.rstd[row];
+    const float gr = GATE == 1 ? a.gate[row] : 1.0f;
+    float d[NV][8], yh[NV][8], m = 0.0f, dgr = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t e = col(i);
+      dr[i].get(d[i]);
+      yr[i].get(yh[i]);
+      if (a.d2) {
         float d2[8];
-        load8<D32>(a.d2, row * cols + e, d2);
+        d2r[i].get(d2);
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[i][k] += d2[k];
       }
-    }
-    float m = 0.0f, dgr = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
       float ge[8];
-      if (GATE == 3 && e < cols) load8<true>(a.gate, row * cols + e, ge);
+      if (GATE == 3) {
+        zero8(ge);
+        if (e < cols) load8<true>(a.gate, at + e, ge);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         yh[i][k] *= r;
@@ -296,51 +395,50 @@ norm_backward_kernel(NormGrad a) {
         if (GATE == 1) dn *= gr;
         if (GATE == 2) dn *= gc[i][k];
         if (GATE == 3) {
-          dn = e < cols ? dn * ge[k] : 0.0f;
+          dn *= ge[k];
           ge[k] = dg;
         }
         dw[i][k] += dn * yh[i][k];
         d[i][k] = dn * w[i][k];
         m = fmaf(d[i][k], yh[i][k], m);
       }
-      if (GATE == 3 && e < cols && a.dgate) store8<true>(a.dgate, row * cols + e, ge);
+      if (GATE == 3 && e < cols && a.dgate) store8<true>(a.dgate, at + e, ge);
     }
-    m = block_sum(m, red) / (float)cols;
+    m = block_sum<W>(m, red[buf]) / (float)cols;
     if (GATE == 1 && a.dgate) {
-      dgr = block_sum(dgr, red);
+      dgr = block_sum<W>(dgr, redg[buf]);
       if (threadIdx.x == 0) a.dgate[row] = dgr;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-      if (e >= cols) continue;
+      if (col(i) >= cols) continue;
       float o[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[k] = r * fmaf(-yh[i][k], m, d[i][k]);
       if (a.res) {
         float rs[8];
-        load8<Y32>(a.res, row * cols + e, rs);
+        rr[i].get(rs);
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = fmaf(a.res_scale, rs[k], o[k]);
       }
-      store8<Y32>(a.dy, row * cols + e, o);
+      store8<Y32>(a.dy, at + col(i), o);
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + threadIdx.x);
-    if (e >= cols) continue;
-    if (a.dw_part) store8<true>(a.dw_part, (int64_t)blockIdx.x * cols + e, dw[i]);
-    if (GATE == 2 && a.dg_part) store8<true>(a.dg_part, (int64_t)blockIdx.x * cols + e, dgc[i]);
+    if (col(i) >= cols) continue;
+    if (a.dw_part) store8<true>(a.dw_part, (int64_t)blockIdx.x * cols + col(i), dw[i]);
+    if (GATE == 2 && a.dg_part) store8<true>(a.dg_part, (int64_t)blockIdx.x * cols + col(i), dgc[i]);
   }
 }
 
-// out[c] = sum over `parts` rows of part[., c]: 64 columns per workgroup, its four waves on
-// every fourth row, joined in wave order. blockIdx.y picks one of two (partials, sums) pairs.
-__global__ void __launch_bounds__(kThreads)
+// out[c] = sum over `parts` rows of part[., c]: 64 columns per workgroup, its sixteen waves on
+// every sixteenth row, joined in wave order. blockIdx.y picks one of two (partials, sums) pairs.
+constexpr int kSumWaves = 16;
+__global__ void __launch_bounds__(kSumWaves * 64)
 column_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, const float* __restrict__ part1,
                   float* __restrict__ out1, int64_t parts, int64_t cols) {
-  __shared__ float red[kWaves][64];
+  __shared__ float red[kSumWaves][64];
   const float* part = blockIdx.y ? part1 : part0;
   float* out = blockIdx.y ? out1 : out0;
   if (!out) return;
@@ -348,23 +446,31 @@ column_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, con
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
   if (c < cols)
-    for (int64_t p = w; p < parts; p += kWaves) s += part[p * cols + c];
+#pragma unroll 8
+    for (int64_t p = w; p < parts; p += kSumWaves) s += part[p * cols + c];
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) s += red[i][lane];
+    for (int i = 1; i < kSumWaves; ++i) s += red[i][lane];
     out[c] = s;
   }
 }
 
+// Waves that hold a row and vectors of 8 per lane: two vectors wherever the row has them. More
+// vectors to a lane cost registers and with them rows in flight, more waves cost barriers and
+// reductions (norm + MXFP8, 16384 x 7168: one wave of 16 vectors 138 us, 2 x 8 118, 4 x 4 119,
+// 8 x 2 115, 16 x 1 137; NVFP4, 16384 x 4096: 1 x 8 66, 2 x 4 59, 4 x 2 59, 8 x 1 79).
 template <typename F>
-void with_vectors(int64_t cols, F&& go) {                   // vectors of 8 per thread
-  const int64_t nv = (cols / 8 + kThreads - 1) / kThreads;
-  if (nv <= 1) go(std::integral_constant<int, 1>{});
-  else if (nv <= 2) go(std::integral_constant<int, 2>{});
-  else if (nv <= 4) go(std::integral_constant<int, 4>{});
-  else go(std::integral_constant<int, 8>{});                // cols <= 16384
+void with_row(int64_t cols, F&& go) {
+  using std::integral_constant;
+  const int64_t v = (cols / 8 + 63) / 64;                   // vectors a lane of one wave would hold
+  if (v <= 1) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  else if (v <= 2) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  else if (v <= 4) go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  else if (v <= 8) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  else if (v <= 16) go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  else go(integral_constant<int, 16>{}, integral_constant<int, 2>{});   // cols <= 16384
 }
 
 template <typename F>
@@ -392,12 +498,14 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t cols) {
 hipError_t launch_norm_quant(int fmt, const void* x, int x32, int64_t rows, int64_t cols, int64_t ld_x,
                              const float* weight, double eps, void* n, void* q, void* s, float* t, float* rstd,
                              hipStream_t st) {
-  const dim3 grid((unsigned)rows), block(kThreads);
   auto go = [&](auto F) {
     with_bool(x32, [&](auto X) {
-      with_vectors(cols, [&](auto V) {
-        hipLaunchKernelGGL((norm_quant_kernel<decltype(F)::value, decltype(X)::value, decltype(V)::value>), grid, block,
-                           0, st, x, cols, ld_x, weight, eps, (uint16_t*)n, (uint8_t*)q, (uint8_t*)s, t, rstd);
+      with_row(cols, [&](auto N, auto V) {
+        constexpr int W = decltype(N)::value;
+        hipLaunchKernelGGL((norm_quant_kernel<decltype(F)::value, decltype(X)::value, W, decltype(V)::value>),
+                           dim3((unsigned)(W == 1 ? (rows + 3) / 4 : rows)), dim3(W == 1 ? 256 : W * 64), 0, st, x, rows,
+                           (int)cols, ld_x, weight, eps, 1.0 / (double)cols, (uint16_t*)n, (uint8_t*)q, (uint8_t*)s, t,
+                           rstd);
       });
     });
   };
@@ -414,10 +522,11 @@ hipError_t launch_gate_residual(const void* x, int x32, const void* y, int y32, 
   with_bool(x32, [&](auto X) {
     with_bool(y32, [&](auto Y) {
       with_gate(gate_mode, [&](auto G) {
-        with_vectors(cols, [&](auto V) {
+        with_row(cols, [&](auto N, auto V) {
+          constexpr int W = decltype(N)::value;
           hipLaunchKernelGGL(
-              (gate_residual_kernel<decltype(X)::value, decltype(Y)::value, decltype(G)::value, decltype(V)::value>),
-              dim3((unsigned)rows), dim3(kThreads), 0, st, x, y, cols, weight, gate, eps, branch_scale, res_scale, out,
+              (gate_residual_kernel<decltype(X)::value, decltype(Y)::value, decltype(G)::value, W, decltype(V)::value>),
+              dim3((unsigned)rows), dim3(W * 64), 0, st, x, y, cols, weight, gate, eps, branch_scale, res_scale, out,
               rstd);
         });
       });
@@ -439,18 +548,19 @@ hipError_t launch_norm_backward(const void* d, const void* d2, int d32, const vo
     with_bool(d32, [&](auto D) {
       with_bool(y32, [&](auto Y) {
         with_gate(gate_mode, [&](auto G) {
-          with_vectors(cols, [&](auto V) {
+          with_row(cols, [&](auto N, auto V) {
+            constexpr int W = decltype(N)::value;
             hipLaunchKernelGGL(
-                (norm_backward_kernel<decltype(D)::value, decltype(Y)::value, decltype(G)::value, decltype(V)::value>),
-                dim3((unsigned)parts), dim3(kThreads), 0, st, a);
+                (norm_backward_kernel<decltype(D)::value, decltype(Y)::value, decltype(G)::value, W, decltype(V)::value>),
+                dim3((unsigned)parts), dim3(W * 64), 0, st, a);
           });
         });
       });
     });
   }
   if (dw || dg_sum)
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + 63) / 64), dg_sum ? 2 : 1), dim3(kThreads), 0, st,
-                       dw_part, dw, dg_part, dg_sum, parts, cols);
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + 63) / 64), dg_sum ? 2 : 1), dim3(kSumWaves * 64), 0,
+                       st, dw_part, dw, dg_part, dg_sum, parts, cols);
   return hipGetLastError();
 }
 

@@ -116,6 +116,27 @@ def test_norm_quantize_special_rows_strides_and_preallocated_outputs():
             assert bool((b[0] == 85).all()) and bool((b[-1] == 85).all())
 
 
+def test_norm_quantize_outside_the_binary32_range():
+    """Weights and rows at which binary32 products would leave the normal range, and weights that
+    put many values next to BF16 rounding midpoints: still the correctly rounded values."""
+    g = inputs.rng(304, 0)
+    v = g.standard_normal((6, 512)).astype(np.float32)
+    v[0] *= 2.0 ** -120
+    v[1] *= 2.0 ** 115
+    v[2, ::2] *= 2.0 ** -110
+    v[3] = np.sign(v[3])                                     # r = 1 / sqrt(1 + eps)
+    bits = inputs.to_bf16_bits(v)
+    xv = inputs.bf16_bits_to_float(bits)
+    for n, w in enumerate([np.ones(512), np.full(512, 2.0 ** 60), np.full(512, 2.0 ** -90),
+                           1 + np.arange(512) / 256 + 2.0 ** -8,
+                           np.where(np.arange(512) % 3, 1.0, 2.0 ** 30)]):
+        w = w.astype(np.float32)
+        for eps in (EPS, 1e-30):
+            got = B.rmsnorm_quantize(dev_bf16(bits), dev(w), eps=eps, fmt=B.BF16)[0]
+            with np.errstate(over="ignore"):
+                assert_bytes_equal(host(got), norm.rmsnorm_bf16(xv, w, eps), f"weights {n}, eps {eps}")
+
+
 def test_norm_quantize_equals_the_row_quantizers():
     x, _ = _values(9, 130, 512, "bf16")
     w = dev(_weight(9, 512))
