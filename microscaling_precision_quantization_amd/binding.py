@@ -152,7 +152,7 @@ def _bf16(x):
 
 
 def _u8(shape, dev):
-    return torch.empty(shape, dtype=torch.uint8, device=dev)
+    return torch.empty(*shape, dtype=torch.uint8, device=dev)
 
 
 class _Checks:
@@ -785,7 +785,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: f
         c.opt(rstd, "rstd", torch.float32, (T,))
     c.done()
     if out is None:
-        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if keep_n or fmt == BF16 else None
+        n = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if keep_n or fmt == BF16 else None
         q = s = t = None
         if fmt != BF16:
             q, s = _u8((T, H // _elems_per_byte(fmt)), dev), _u8((T, H // _scale_block(fmt)), dev)
@@ -891,7 +891,8 @@ def rmsnorm_gate_residual_backward(d_out: torch.Tensor, y: torch.Tensor, rstd: t
 class RoutePlan:
     """A routing on the device: topk_idx, weights, counts, offsets, row_index, slot_of and the
     balance loss (None if not wanted), as moe_route writes them (include/mxq.h), with `slots`
-    (the total) and `groups` (the experts). Made once for a batch size, it serves every call."""
+    (the total), `groups` (the experts) and the call's scratch, all in one allocation. Made once
+    for a batch size, it serves every call."""
 
     def __init__(self, tokens: int, experts: int, topk: int, pad: int = 1, total: int | None = None,
                  loss: bool = False, dev="cuda"):
@@ -899,15 +900,17 @@ class RoutePlan:
         total = need if total is None else total
         if total < need or total % pad or total > 0x7FFFFFFF:
             raise ValueError(f"total: {total} slots, expected a multiple of {pad} and at least {need}")
-        e = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
         self.tokens, self.groups, self.topk, self.pad, self.slots = tokens, experts, topk, pad, total
-        self.topk_idx = e((tokens, topk), torch.int32)
-        self.weights = e((tokens, topk), torch.float32)
-        self.counts = e((experts + 1,), torch.int32)
-        self.offsets = e((experts + 1,), torch.int64)
-        self.row_index = e((total,), torch.int32)
-        self.slot_of = e((tokens, topk), torch.int64)
-        self.loss = e((1,), torch.float32) if loss else None
+        ws = (lib().mxq_workspace_bytes(OP_ROUTE, tokens, experts, 0) + 15) // 16 * 4
+        n = tokens * topk
+        sizes = (ws, 2 * experts + 2, 2 * n, n, n, experts + 1, total, 1)          # in dwords, 8-byte values first
+        (self.workspace, offsets, slot_of, topk_idx, weights, self.counts, self.row_index, loss_) = torch.empty(
+            sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
+        self.offsets = offsets.view(torch.int64)
+        self.slot_of = slot_of.view(torch.int64).view(tokens, topk)
+        self.topk_idx = topk_idx.view(tokens, topk)
+        self.weights = weights.view(torch.float32).view(tokens, topk)
+        self.loss = loss_.view(torch.float32) if loss else None
 
 
 def route_slots(tokens: int, experts: int, topk: int, pad: int = 1) -> int:
@@ -919,8 +922,8 @@ def route_slots(tokens: int, experts: int, topk: int, pad: int = 1) -> int:
 
 
 def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor | None = None,
-              balance_coef: float | None = None, total: int | None = None, out: RoutePlan | None = None,
-              workspace: torch.Tensor | None = None) -> RoutePlan:
+              balance_coef: float | None = None, total: int | None = None,
+              out: RoutePlan | None = None) -> RoutePlan:
     """Top-k routing of FP32 logits (T, G) with its slots, counts and (balance_coef given) balance
     loss. valid: bool or uint8 (T,), False = a padding token that is not routed. `out`: a plan
     of the same sizes to write into."""
@@ -943,11 +946,11 @@ def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor
         raise ValueError("out: a plan without a loss")
     c.need(plan.offsets, "out", torch.int64, (G + 1,))
     c.done()
-    ws = _workspace(OP_ROUTE, T, G, workspace, dev)
+    ws = plan.workspace
     loss = None if balance_coef is None else plan.loss
     _call("moe_route", dev, _ptr(logits), _ptr(valid), T, G, max(logits.stride(0), G), topk, pad, plan.slots,
           0.0 if balance_coef is None else balance_coef, _ptr(plan.topk_idx), _ptr(plan.weights), _ptr(plan.counts),
-          _ptr(plan.offsets), _ptr(plan.row_index), _ptr(plan.slot_of), _ptr(loss), _ptr(ws), ws.numel())
+          _ptr(plan.offsets), _ptr(plan.row_index), _ptr(plan.slot_of), _ptr(loss), _ptr(ws), 4 * ws.numel())
     return plan
 
 
@@ -970,7 +973,7 @@ def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, weights: to
     c.opt(out, "out", torch.float32, (T, G))
     c.done()
     if out is None:
-        out = torch.empty((T, G), dtype=torch.float32, device=logits.device)
+        out = torch.empty(T, G, dtype=torch.float32, device=logits.device)
     _call("moe_route_backward", logits.device, _ptr(logits), T, G, max(logits.stride(0), G), k, _ptr(topk_idx),
           _ptr(weights), _ptr(d_weights), _ptr(counts), _ptr(d_loss), balance_coef, _ptr(out))
     return out
@@ -996,7 +999,7 @@ def moe_combine_backward(dy: torch.Tensor, o_slots: torch.Tensor, slot_of: torch
         c.need(d_w, "d_weights", torch.float32, (T, k))
     c.done()
     if out is None:
-        d_o, d_w = torch.empty((S, H), dtype=torch.bfloat16, device=dev), torch.empty_like(weights)
+        d_o, d_w = torch.empty(S, H, dtype=torch.bfloat16, device=dev), torch.empty_like(weights)
     _call("moe_combine_backward", dev, _ptr(dy), dd, _ptr(o_slots), S, T, k, H, _ptr(slot_of), _ptr(weights),
           _ptr(row_index), _ptr(d_o), _ptr(d_w))
     return d_o, d_w

@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t shfl_xor_u32(uint32_t v, int mask) {
 // instead of trips through the LDS crossbar; the order of the additions is fixed.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF);   // other rows: 0
 }
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_f32(float v) { return __uint_as_float(dpp_u32<CTRL, ROWS>(__float_as_uint(v))); }

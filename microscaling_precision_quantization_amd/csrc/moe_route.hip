@@ -22,23 +22,38 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTok = 64;                         // tokens of a block (one bit each of a mask)
 
-// Order-preserving key of a logit: 0 for NaN, kNegInf for -inf, larger for larger values; -0
-// equals +0. An expert is usable when its key lies above kNegInf.
-constexpr uint32_t kNegInf = 0x007FFFFFu;
+// Order-preserving key of a logit: larger for larger values, -0 as +0, NaN as -inf. An expert is
+// usable when its key lies above that of -inf, 0x007FFFFF.
 __device__ __forceinline__ uint32_t logit_key(float z) {
-  if (z != z) return 0;
-  const uint32_t u = __float_as_uint(z + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(z, -__builtin_inff()) + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// Key and expert in one binary64: the key as an integer, and below its units bit `rest`, larger
+// for lower experts. Every expert of a token has another value, in the order of the choice, so a
+// maximum names its expert and sorting by maxima and minima (two instructions an exchange) keeps
+// equal logits in order. (A 32-bit integer leaves 21 bits of the significand.)
+__device__ __forceinline__ double ranked(uint32_t key, uint32_t rest) {
+  return __longlong_as_double(__double_as_longlong((double)key) | rest);
+}
+constexpr double kUsable = 8388608.0;            // 0x00800000
+
+// e^(z - top) for z <= top; 0 for an expert that is not usable (-inf, NaN: fmaxf drops it). The
+// exponent of two is formed with log2(e) in two parts, so it carries the roundings of z - top and
+// of the fused multiply-add only: 2 u |z - top| relative, and an ulp of the instruction.
+__device__ __forceinline__ float softmax_term(float z, float top) {
+  const float x = fmaxf(z, -__builtin_inff()) - top;
+  return __builtin_amdgcn_exp2f(fmaf(x, 1.44269502e+00f, x * 1.92596299e-08f));
+}
+
 // A lane's NE consecutive logits of a row, NaN past the row. With a whole number of lanes to the
 // row every lane takes one wide load (whatever the row's alignment), else single ones.
 template <int NE>
-__device__ __forceinline__ void load_logits(const float* row, int experts, float* z) {
-  const int e = (int)(threadIdx.x & 63) * NE;
+__device__ __forceinline__ void load_logits(const float* row, int experts, int lane, float* z) {
+  const int e = lane * NE;
 #pragma unroll
   for (int i = 0; i < NE; ++i) z[i] = __builtin_nanf("");
   if (experts % NE == 0) {
@@ -50,29 +65,53 @@ __device__ __forceinline__ void load_logits(const float* row, int experts, float
   }
 }
 
-// Sorts a lane's keys in descending order, equal ones as they stood (odd-even transposition: it
-// only swaps neighbours that are strictly out of order); nibble i of the result is where the
-// i-th key stood.
+// Sorts a lane's values in descending order (Batcher's odd-even merge sort, 1968: 63 exchanges for
+// 16 values).
 template <int NE>
-__device__ __forceinline__ uint64_t sort_desc(uint32_t* key) {
-  uint32_t at[NE];
+__device__ __forceinline__ void sort_desc(double* v) {
 #pragma unroll
-  for (int i = 0; i < NE; ++i) at[i] = i;
+  for (int p = 1; p < NE; p *= 2)
 #pragma unroll
-  for (int r = 0; r < NE; ++r)
+    for (int k = p; k >= 1; k /= 2)
 #pragma unroll
-    for (int i = r & 1; i + 1 < NE; i += 2) {
-      const bool swap = key[i] < key[i + 1];
-      const uint32_t k0 = key[i], k1 = key[i + 1], a0 = at[i], a1 = at[i + 1];
-      key[i] = swap ? k1 : k0;
-      key[i + 1] = swap ? k0 : k1;
-      at[i] = swap ? a1 : a0;
-      at[i + 1] = swap ? a0 : a1;
-    }
-  uint64_t order = 0;
+      for (int j = k % p; j + k < NE; j += 2 * k)
 #pragma unroll
-  for (int i = 0; i < NE; ++i) order |= (uint64_t)at[i] << (4 * i);
-  return order;
+        for (int i = j; i < j + k && i + k < NE; ++i)
+          if (i / (2 * p) == (i + k) / (2 * p)) {
+            const double hi = fmax(v[i], v[i + k]), lo = fmin(v[i], v[i + k]);
+            v[i] = hi;
+            v[i + k] = lo;
+          }
+}
+
+// The maximum of two ordinary numbers, as the one instruction: fmax() first quiets operands that
+// could be signalling NaNs, which ranked values never are.
+__device__ __forceinline__ double max2(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// Reductions over the L lanes of a token (a row of 16, or the wave), in all of them.
+template <int L>
+__device__ __forceinline__ double lanes_max(double v) {
+  v = max2(v, dpp_f64<0x128, 0xF>(v));
+  v = max2(v, dpp_f64<0x124, 0xF>(v));
+  v = max2(v, dpp_f64<0x122, 0xF>(v));
+  v = max2(v, dpp_f64<0x121, 0xF>(v));
+  if (L == 16) return v;
+  v = max2(v, dpp_f64<0x142, 0xA>(v));           // positive values: the zeros of the other rows lose
+  v = max2(v, dpp_f64<0x143, 0xC>(v));
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)lane63((uint32_t)(u >> 32)) << 32 | lane63((uint32_t)u)));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if (L == 64) return wave_sum(v);
+  v += dpp_f32<0x128, 0xF>(v);
+  v += dpp_f32<0x124, 0xF>(v);
+  v += dpp_f32<0x122, 0xF>(v);
+  return v + dpp_f32<0x121, 0xF>(v);
 }
 
 struct Route {
@@ -99,100 +138,128 @@ __host__ __device__ inline int hist_cols(int experts) { return (experts + 4) / 4
 
 // Waves of a workgroup that chooses: sixteen keep four on every SIMD; eight where sixteen rows of
 // sums would not fit beside the masks in 64 KB.
-constexpr int choose_waves(int ne) { return ne <= 8 ? 16 : 8; }
+constexpr int choose_waves(int lanes, int ne) { return lanes * ne <= 512 ? 16 : 8; }
+
+// Sums of N values over the wave's four rows, lane by lane, spread over the rows: row r is left
+// with value i + N/4 * (r % 2) + N/2 * (r / 2) in v[i], i < N/4. Each step swaps halves of the
+// wave between two values and adds, so it sums two at once.
+template <int N>
+__device__ __forceinline__ void sum_of_rows(float* v) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + N / 2]), false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + N / 4]), false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+}
 
 // ---------------------------------------------------------------------------
-// Choice of one block of kTok tokens: one wave per token, NE experts per lane (expert =
-// lane * NE + i). Writes topk_idx and weights, leaves the experts' masks in LDS and adds each
-// lane's p to acc. A wave loads the logits of all its tokens before it looks at the first, so it
-// waits for memory once.
+// Choice of one block of kTok tokens: L lanes to a token, NE experts per lane (expert =
+// lane * NE + i). Every lane sorts its experts and keeps the first KEEP >= min(topk, NE); then the
+// token's largest first value is chosen topk times and its lane moves on to the next. Writes
+// topk_idx and weights, leaves the experts' masks in LDS and the waves' sums of p in lp (waves,
+// experts). With L = 16 sixteen waves take all 64 tokens at once, four tokens sharing every
+// instruction; L = 64 serves more experts (NE <= 16) or more choices than a row of lanes holds.
+// (16384 x 256, top-8: 6 us with L = 16, 14 us with L = 64.)
 // ---------------------------------------------------------------------------
-template <int NE>
-__device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* acc) {
-  constexpr int W = choose_waves(NE), TPW = kTok / W;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <int L, int NE, int KEEP>
+__device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* lp) {
+  constexpr int W = choose_waves(L, NE), GROUPS = W * 64 / L, M = L * NE - 1;
+  const int lane = threadIdx.x & (L - 1), w = threadIdx.x >> 6;
+  const int group = L == 64 ? __builtin_amdgcn_readfirstlane(w) : threadIdx.x / L;
   const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok);
   int routed = 0;
-  float ahead[TPW][NE];
+  float next[NE], acc[NE];
+  bool on_next = false;
+  auto fetch = [&](int tl) {
+    on_next = tl < n;
+    if (!on_next) return;
+    load_logits<NE>(a.logits + (t0 + tl) * a.ld, a.experts, lane, next);
+    if (a.valid) on_next = a.valid[t0 + tl];
+  };
 #pragma unroll
-  for (int r = 0; r < TPW; ++r)
-    if (w + r * W < n) load_logits<NE>(a.logits + (t0 + w + r * W) * a.ld, a.experts, ahead[r]);
-  const int on = lane < n && (!a.valid || a.valid[t0 + lane]);             // lane: token of the block
-  for (int tl = w; tl < n; tl += W) {
+  for (int i = 0; i < NE; ++i) {
+    next[i] = __builtin_nanf("");
+    acc[i] = 0.0f;
+  }
+  fetch(group);
+  for (int tl = group; tl < n; tl += GROUPS) {
     const int64_t t = t0 + tl;
-    const bool live = __builtin_amdgcn_readlane(on, tl);
+    const bool on = on_next;
     float z[NE];
-    uint32_t key[NE];
+    double v[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      z[i] = ahead[0][i];
-      key[i] = live ? logit_key(z[i]) : 0u;
-#pragma unroll
-      for (int r = 0; r + 1 < TPW; ++r) ahead[r][i] = ahead[r + 1][i];
+      z[i] = next[i];
+      v[i] = ranked(logit_key(z[i]), (uint32_t)((M - (NE - 1) - lane * NE) | (NE - 1 - i)));
     }
-    uint64_t idx = sort_desc<NE>(key);           // nibble i: which of the lane's experts key[i] is
-    uint32_t top_key = 0, my_key = 0;            // lane j: the j-th chosen expert
-    int my_e = -1;
+    if (GROUPS < kTok) fetch(tl + GROUPS);
+    sort_desc<NE>(v);
+    double head[KEEP + 1], my_v = 0.0;           // lane j: the j-th chosen expert
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) head[i] = v[i];
+    head[KEEP] = 0.0;
+    const double top_v = lanes_max<L>(v[0]);
     for (int j = 0; j < a.topk; ++j) {
-      const uint32_t best = wave_max_u32(key[0]);
-      if (best <= kNegInf) break;                // no usable expert left (uniform over the wave)
-      if (j == 0) top_key = best;
-      const int owner = __ffsll((unsigned long long)__ballot(key[0] == best)) - 1;
-      const int e = owner * NE + (__builtin_amdgcn_readlane((int)(uint32_t)idx, owner) & 15);
-      my_e = lane == j ? e : my_e;
-      my_key = lane == j ? best : my_key;
-      if (lane == owner) {                       // its next one moves up
+      const double best = lanes_max<L>(head[0]);
+      my_v = lane == j ? best : my_v;
+      const bool up = head[0] == best;           // its lane's next one moves up
 #pragma unroll
-        for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
-        key[NE - 1] = 0;
-        idx >>= 4;
-      }
+      for (int i = 0; i < KEEP; ++i) head[i] = up ? head[i + 1] : head[i];
     }
-    const float top = key_logit(top_key);
-    const float num = my_e >= 0 ? expf(key_logit(my_key) - top) : 0.0f;
-    const float den = wave_sum(num);
+    const bool mine = on && my_v >= kUsable, any = on && top_v >= kUsable;
+    const int my_e = mine ? M - (int)((uint32_t)__double_as_longlong(my_v) & M) : -1;
+    const float top = key_logit((uint32_t)top_v);                          // conversions truncate `rest`
+    const float num = mine ? expf(key_logit((uint32_t)my_v) - top) : 0.0f;
+    const float den = lanes_sum<L>(num);
     if (lane < a.topk) {
       a.topk_idx[t * a.topk + lane] = my_e;
-      a.weights[t * a.topk + lane] = my_e >= 0 ? num / den : 0.0f;
+      a.weights[t * a.topk + lane] = mine ? num / den : 0.0f;
     }
-    if (my_e >= 0) atomicOr((unsigned long long*)&mask[my_e], 1ull << tl);
-    if (top_key == 0) continue;
-    ++routed;
+    if (mine) atomicOr((unsigned long long*)&mask[my_e], 1ull << tl);
+    routed += __popcll(__ballot(any && lane == 0));
     if (a.loss) {
-      float p[NE], sum = 0.0f;
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        p[i] = z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.0f;      // NaN: not usable either
-        sum += p[i];
+        z[i] = softmax_term(z[i], top);
+        sum += z[i];
       }
-      const float inv = 1.0f / wave_sum(sum);
+      sum = lanes_sum<L>(sum);
+      const float inv = any ? 1.0f / sum : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] += p[i] * inv;
+      for (int i = 0; i < NE; ++i) acc[i] = any ? fmaf(z[i], inv, acc[i]) : acc[i];
     }
+  }
+  if (a.loss) {
+    int e0 = lane * NE;
+    if (L == 16) {
+      sum_of_rows<NE>(acc);
+      e0 += NE / 4 * ((threadIdx.x >> 4) & 3);
+    }
+#pragma unroll
+    for (int i = 0; i < (L == 16 ? NE / 4 : NE); ++i)
+      if (e0 + i < a.experts) lp[w * a.experts + e0 + i] = acc[i];
   }
   return routed;
 }
 
 // One block's masks, routed tokens and (loss wanted) sums of p, in LDS: mask[experts], the
 // waves' routed tokens, then waves x experts floats whose first row ends up as the sums.
-template <int NE>
+template <int L, int NE, int KEEP>
 __device__ __forceinline__ int choose_block(const Route& a, int64_t t0, uint64_t* mask) {
-  constexpr int waves = choose_waves(NE);
+  constexpr int waves = choose_waves(L, NE);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int* routed_w = reinterpret_cast<int*>(mask + a.experts);
   float* lp = reinterpret_cast<float*>(routed_w + 16);
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) mask[e] = 0;
   __syncthreads();
-  float acc[NE];
-#pragma unroll
-  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-  const int routed = choose_tokens<NE>(a, t0, mask, acc);
+  const int routed = choose_tokens<L, NE, KEEP>(a, t0, mask, lp);
   if (lane == 0) routed_w[w] = routed;
-  if (a.loss) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (lane * NE + i < a.experts) lp[w * a.experts + lane * NE + i] = acc[i];
-  }
   __syncthreads();
   int sum = 0;
   for (int i = 0; i < waves; ++i) sum += routed_w[i];
@@ -209,11 +276,11 @@ size_t choose_lds(int experts, int waves, bool loss) {
   return (size_t)experts * 8 + 64 + (loss ? (size_t)waves * experts * 4 : 0);
 }
 
-template <int NE>
-__global__ void __launch_bounds__(choose_waves(NE) * 64)
+template <int L, int NE, int KEEP>
+__global__ void __launch_bounds__(choose_waves(L, NE) * 64)
 route_choose_kernel(Route a) {
   extern __shared__ uint64_t mask[];
-  const int routed = choose_block<NE>(a, (int64_t)blockIdx.x * kTok, mask);
+  const int routed = choose_block<L, NE, KEEP>(a, (int64_t)blockIdx.x * kTok, mask);
   const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
   const int cols = hist_cols(a.experts);
   for (int e = threadIdx.x; e < cols; e += blockDim.x)
@@ -287,43 +354,41 @@ __device__ __forceinline__ void write_counts(const Route& a, const int* cnt, con
   }
 }
 
-// Sum over the workgroup of one binary64 value a thread, in thread 0 (fixed order).
-__device__ __forceinline__ double block_sum(double v, double* red) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+// loss / coef of one block of tokens, in thread 0: experts / (A N) sum over e of counts_e psum_e.
+// `p` is psum_e of expert threadIdx.x + i blockDim.x, in turn.
+template <typename P>
+__device__ __forceinline__ double block_loss(const Route& a, const int* cnt, int routed, P&& p, double (*red)[2]) {
+  double dot = 0.0, all = 0.0;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    dot += (double)cnt[e] * (double)p(e);
+    all += (double)cnt[e];
+  }
+  dot = wave_sum(dot);
+  all = wave_sum(all);
   const int w = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[w] = v;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    for (int i = 1; i < waves; ++i) v += red[i];
-  return v;
-}
-
-// Thread 0: sum over the experts of counts_e times one block's sum of p, and the sum of counts.
-__device__ __forceinline__ double loss_dot(const Route& a, const int* cnt, const float* psum, double* red) {
-  double dot = 0.0;
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) dot += (double)cnt[e] * (double)psum[e];
-  return block_sum(dot, red);
-}
-// experts / (A N): what turns the sum over the blocks of loss_dot into loss / coef (thread 0).
-__device__ __forceinline__ double loss_scale(const Route& a, const int* cnt, int routed, double* red) {
-  double all = 0.0;
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) all += (double)cnt[e];
-  all = block_sum(all, red);
-  return routed ? (double)a.experts / (all * (double)routed) : 0.0;
+  if ((threadIdx.x & 63) == 0) {
+    red[w][0] = dot;
+    red[w][1] = all;
+  }
+  lds_barrier();
+  if (threadIdx.x != 0) return 0.0;
+  for (int i = 1; i < waves; ++i) {
+    dot += red[i][0];
+    all += red[i][1];
+  }
+  return routed ? (double)a.experts * dot / (all * (double)routed) : 0.0;
 }
 
 // ---------------------------------------------------------------------------
 // At most one block of tokens: everything in one launch.
 // ---------------------------------------------------------------------------
-template <int NE>
-__global__ void __launch_bounds__(choose_waves(NE) * 64)
+template <int L, int NE, int KEEP>
+__global__ void __launch_bounds__(choose_waves(L, NE) * 64)
 route_one_block_kernel(Route a) {
   extern __shared__ uint64_t mask[];
-  __shared__ int cnt[NE * 64], off[NE * 64 + 1];
-  __shared__ double red[32];
-  const int routed = choose_block<NE>(a, 0, mask);
+  __shared__ int cnt[NE * L], off[NE * L + 1];
+  __shared__ double red[16][2];
+  const int routed = choose_block<L, NE, KEEP>(a, 0, mask);
   const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) cnt[e] = __popcll((unsigned long long)mask[e]);
   __syncthreads();
@@ -331,8 +396,8 @@ route_one_block_kernel(Route a) {
   write_counts(a, cnt, off, routed);
   write_slots(a, 0, mask, cnt, off, off);
   if (a.loss) {
-    const double dot = loss_dot(a, cnt, lp, red), scale = loss_scale(a, cnt, routed, red);
-    if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * scale * dot);
+    const double l = block_loss(a, cnt, routed, [&](int e) { return lp[e]; }, red);
+    if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * l);
   }
 }
 
@@ -368,9 +433,10 @@ __global__ void __launch_bounds__(kSlotThreads)
 route_slots_kernel(Route a, int blocks) {
   extern __shared__ uint64_t mask[];
   __shared__ int cnt[kMaxExperts + 4], off[kMaxExperts + 1], start[kMaxExperts + 4];
-  __shared__ double red[32];
+  __shared__ double red[16][2];
   const int cols = hist_cols(a.experts), blk = blockIdx.x;
   const int64_t t0 = (int64_t)blk * kTok;
+  const float psum = a.loss && threadIdx.x < a.experts ? a.psum[(int64_t)blk * a.experts + threadIdx.x] : 0.0f;
   for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) mask[e] = 0;
   if (SCANNED) {
     for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
@@ -415,15 +481,14 @@ route_slots_kernel(Route a, int blocks) {
   write_slots(a, t0, mask, cnt, off, start);
   if (blk == 0) write_counts(a, cnt, off, cnt[a.experts]);
   if (!a.loss) return;
-  const double dot = loss_dot(a, cnt, a.psum + (int64_t)blk * a.experts, red);
-  const double scale = loss_scale(a, cnt, cnt[a.experts], red);
+  const double part = block_loss(a, cnt, cnt[a.experts], [&](int) { return psum; }, red);   // an expert a thread
   if (threadIdx.x != 0) return;
   // One atomic carries the workgroups' count (above bit `frac` + 11) and the sum so far in fixed
   // point: loss / coef is at most experts <= 2^10. Integers, so the order does not matter, and
   // whoever makes the count complete holds the whole sum. 65536 blocks leave 34 bits of fraction.
   const int frac = 62 - (32 - __clz(blocks)) - 11;
   const uint64_t one = 1ull << (frac + 11);
-  const uint64_t add = one + (uint64_t)llrint(ldexp(dot * scale, frac));
+  const uint64_t add = one + (uint64_t)llrint(ldexp(part, frac));
   const uint64_t now = atomicAdd((unsigned long long*)a.tally, (unsigned long long)add) + add;
   if ((now >> (frac + 11)) == (uint64_t)blocks)
     *a.loss = (float)((double)a.coef * ldexp((double)(now & (one - 1)), -frac));
@@ -439,7 +504,10 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
                       const int32_t* __restrict__ topk_idx, const float* __restrict__ weights,
                       const float* __restrict__ d_weights, const int32_t* __restrict__ counts,
                       const float* __restrict__ d_loss, float coef, float* __restrict__ d_logits) {
+  __shared__ __attribute__((aligned(16))) float share[kWaves][NE * 64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < NE; ++i) share[w][lane * NE + i] = 0.0f;    // a row per wave: no barrier
   const int64_t step = (int64_t)gridDim.x * kWaves;
   int64_t t = (int64_t)blockIdx.x * kWaves + w;
   if (t >= tokens) return;
@@ -450,7 +518,7 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
   float w_ahead = 0.0f, dw_ahead = 0.0f;
   auto fetch = [&](int64_t at) {
     if (at >= tokens) return;
-    if (d_loss) load_logits<NE>(logits + at * ld, experts, ahead);
+    if (d_loss) load_logits<NE>(logits + at * ld, experts, lane, ahead);
     if (lane < topk) {
       e_ahead = topk_idx[at * topk + lane];
       if (d_weights) {
@@ -481,14 +549,14 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
     }
     fetch(t + step);
     if (d_loss && __builtin_amdgcn_readlane(my_e, 0) >= 0) {
-      uint32_t best = 0;
+      float most = -__builtin_inff();
 #pragma unroll
-      for (int i = 0; i < NE; ++i) best = max(best, logit_key(z[i]));
-      const float top = key_logit(wave_max_u32(best));
+      for (int i = 0; i < NE; ++i) most = fmaxf(most, z[i]);
+      const float top = key_logit(wave_max_u32(logit_key(most)));
       float sum = 0.0f, pc = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        z[i] = z[i] > -__builtin_inff() ? expf(z[i] - top) : 0.0f;   // an unusable expert has p = 0
+        z[i] = softmax_term(z[i], top);
         sum += z[i];
         pc += z[i] * c[i];
       }
@@ -497,13 +565,15 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
       for (int i = 0; i < NE; ++i) d[i] = (scale * inv) * z[i] * (c[i] - mean);
     }
     if (d_weights) {
+      // lane j's share goes to its expert's lane through a row of LDS that is zero in between
       const float g = wj * (dwj - wave_sum(wj * dwj));
-      for (int j = 0; j < topk; ++j) {
-        const int e = __builtin_amdgcn_readlane(my_e, j) - lane * NE;
-        const float gj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
+      const bool in = my_e >= 0 && my_e < experts;
+      if (in) share[w][my_e] = g;
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < NE; ++i) d[i] += e == i ? gj : 0.0f;
-      }
+      for (int i = 0; i < NE; ++i) d[i] += share[w][lane * NE + i];
+      __builtin_amdgcn_wave_barrier();
+      if (in) share[w][my_e] = 0.0f;
     }
     float* out = d_logits + t * experts + lane * NE;
     if (experts % NE == 0) {
@@ -588,6 +658,19 @@ void with_experts(int64_t experts, F&& go) {                 // experts per lane
   else go(std::integral_constant<int, 16>{});                // experts <= kMaxExperts
 }
 
+template <typename F>
+void with_choice(int64_t tokens, int64_t experts, int64_t topk, F&& go) {   // lanes per token, experts per lane, kept
+  using std::integral_constant;
+  if (tokens > 16 && experts <= 256 && topk <= 16) {
+    if (experts <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    else if (experts <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    else if (topk <= 8) go(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    else go(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 16>{});
+  } else {
+    with_experts(experts, [&](auto N) { go(integral_constant<int, 64>{}, N, N); });
+  }
+}
+
 int64_t route_blocks(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
 
 // Blocks up to which every slots workgroup adds up all histograms itself, which saves the scan's
@@ -614,13 +697,13 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
   a.base = (int32_t*)(a.psum + nb * experts);
   a.sums = a.base + nb * cols;
   a.hist = (uint8_t*)(a.sums + cols);
-  with_experts(experts, [&](auto N) {
-    constexpr int NE = decltype(N)::value, W = choose_waves(NE);
+  with_choice(tokens, experts, topk, [&](auto J, auto N, auto K) {
+    constexpr int L = decltype(J)::value, NE = decltype(N)::value, KEEP = decltype(K)::value, W = choose_waves(L, NE);
     const size_t lds = choose_lds((int)experts, W, loss != nullptr);
     if (nb <= 1)
-      hipLaunchKernelGGL((route_one_block_kernel<NE>), dim3(1), dim3(W * 64), lds, st, a);
+      hipLaunchKernelGGL((route_one_block_kernel<L, NE, KEEP>), dim3(1), dim3(W * 64), lds, st, a);
     else
-      hipLaunchKernelGGL((route_choose_kernel<NE>), dim3((unsigned)nb), dim3(W * 64), lds, st, a);
+      hipLaunchKernelGGL((route_choose_kernel<L, NE, KEEP>), dim3((unsigned)nb), dim3(W * 64), lds, st, a);
   });
   if (nb <= 1) return hipGetLastError();
   if (nb > kMaxUnscanned) {

@@ -60,7 +60,8 @@ def _check_plan(plan, z, k, pad, valid, loss, what):
 @pytest.mark.parametrize("T,G,k,pad", [(1, 1, 1, 1), (1, 8, 8, 1), (3, 5, 2, 4), (8, 256, 8, 1), (63, 64, 6, 8),
                                        (64, 65, 4, 32), (65, 128, 8, 1), (129, 129, 3, 8), (200, 300, 12, 32),
                                        (511, 513, 32, 1), (1000, 1024, 2, 16), (1300, 16, 4, 32),
-                                       (16384, 20, 2, 8), (16385, 20, 2, 8), (17001, 70, 3, 1)])
+                                       (100, 60, 20, 4), (100, 100, 24, 1),
+                                       (130, 250, 32, 8), (90, 256, 16, 1), (90, 250, 17, 1), (16384, 20, 2, 8), (16385, 20, 2, 8), (17001, 70, 3, 1)])
 def test_route_plan_is_exact(T, G, k, pad):
     z = _logits(T, T, G)
     plan = B.moe_route(dev(z), k, pad=pad, balance_coef=COEF)
