@@ -716,12 +716,13 @@ mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, 
  *   p (c - sum over e of p_e c_e) with c_e = d_loss balance_coef experts counts_e / (A N).
  *   topk_idx, weights, counts: from moe_route; a token that is not routed gets zeros.
  *   d_weights : FP32 (tokens, topk), NULL = none;  d_loss: FP32 (1) on the device, NULL = none.
- *   d_logits  : FP32 (tokens, experts), contiguous. Limits as moe_route.
+ *   d_logits  : d_dtype (tokens, experts), contiguous; BF16 is what the router's own backward
+ *               GEMMs read. Limits as moe_route.
  * ------------------------------------------------------------------------- */
 mxq_status moe_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
                               const int32_t* topk_idx, const float* weights, const float* d_weights,
-                              const int32_t* counts, const float* d_loss, float balance_coef, float* d_logits,
-                              void* stream);
+                              const int32_t* counts, const float* d_loss, float balance_coef, void* d_logits,
+                              mxq_out_dtype d_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * moe_combine_backward -- gradients of moe_combine: to the expert outputs, in the BF16 slot

@@ -78,7 +78,7 @@ _SIGS = {
     "moe_route": [_c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p,
                   _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
     "moe_route_backward": [_c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
-                           _f32, _c_void_p, _c_void_p],
+                           _f32, _c_void_p, _int, _c_void_p],
     "moe_combine_backward": [_c_void_p, _int, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                              _c_void_p, _c_void_p, _c_void_p],
     "mxq_route_slots": [_i64, _i64, _i64, _i64],
@@ -957,25 +957,29 @@ def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor
 def moe_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, weights: torch.Tensor, counts: torch.Tensor,
                        d_weights: torch.Tensor | None = None, d_loss: torch.Tensor | None = None,
                        balance_coef: float = 0.0, out: torch.Tensor | None = None) -> torch.Tensor:
-    """d_logits (T, G) FP32 from the gradients of the combine weights (T, k) and of the balance
-    loss (1,), either None; topk_idx, weights and counts from moe_route."""
+    """d_logits (T, G) from the gradients of the combine weights (T, k) and of the balance loss
+    (1,), either None; topk_idx, weights and counts from moe_route. FP32, or `out`'s type (FP32
+    or BF16)."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits, topk_idx: expected 2-D tensors")
     T, G = logits.shape
     k = topk_idx.shape[1]
-    c = _Checks(logits.device)
+    dev = logits.device
+    c = _Checks(dev)
     c.need(logits, "logits", torch.float32, (T, G), ld=True)
     c.need(topk_idx, "topk_idx", torch.int32, (T, k))
     c.need(weights, "weights", torch.float32, (T, k))
     c.need(counts, "counts", torch.int32, (G + 1,))
     c.opt(d_weights, "d_weights", torch.float32, (T, k))
     c.opt(d_loss, "d_loss", torch.float32, (1,))
-    c.opt(out, "out", torch.float32, (T, G))
+    od = OUT_F32 if out is None else _float_dtype(out, "out")
+    if out is not None:
+        c.need(out, "out", out.dtype, (T, G))
     c.done()
     if out is None:
-        out = torch.empty(T, G, dtype=torch.float32, device=logits.device)
-    _call("moe_route_backward", logits.device, _ptr(logits), T, G, max(logits.stride(0), G), k, _ptr(topk_idx),
-          _ptr(weights), _ptr(d_weights), _ptr(counts), _ptr(d_loss), balance_coef, _ptr(out))
+        out = torch.empty(T, G, dtype=torch.float32, device=dev)
+    _call("moe_route_backward", dev, _ptr(logits), T, G, max(logits.stride(0), G), k, _ptr(topk_idx), _ptr(weights),
+          _ptr(d_weights), _ptr(counts), _ptr(d_loss), balance_coef, _ptr(out), od)
     return out
 
 

@@ -60,7 +60,7 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
 size_t route_ws_bytes(int64_t tokens, int64_t experts);
 hipError_t launch_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
                                  const int32_t* topk_idx, const float* weights, const float* d_weights,
-                                 const int32_t* counts, const float* d_loss, float coef, float* d_logits,
+                                 const int32_t* counts, const float* d_loss, float coef, void* d_logits, int out32,
                                  hipStream_t st);
 hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int64_t total, int64_t tokens,
                                    int64_t topk, int64_t hidden, const int64_t* slot_of, const float* weights,
@@ -762,18 +762,19 @@ mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, 
 
 mxq_status moe_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
                               const int32_t* topk_idx, const float* weights, const float* d_weights,
-                              const int32_t* counts, const float* d_loss, float balance_coef, float* d_logits,
-                              void* stream) {
+                              const int32_t* counts, const float* d_loss, float balance_coef, void* d_logits,
+                              mxq_out_dtype d_dtype, void* stream) {
   if (experts < 1 || experts > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > experts || tokens < 0 ||
       ld < experts || tokens > kMaxGridBlocks)
     return MXQ_ERR_SHAPE;
+  if (!is_dtype(d_dtype)) return MXQ_ERR_FORMAT;
   if (tokens == 0) return MXQ_OK;
   if (!logits || !topk_idx || !d_logits || (d_weights && !weights) || (d_loss && !counts)) return MXQ_ERR_NULL;
   if (!al4(logits) || !al4(topk_idx) || !al4(weights) || !al4(d_weights) || !al4(counts) || !al4(d_loss) ||
       !al4(d_logits))
     return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_route_backward(logits, tokens, experts, ld, topk, topk_idx, weights, d_weights, counts,
-                                               d_loss, balance_coef, d_logits, S(stream)));
+                                               d_loss, balance_coef, d_logits, d_dtype == MXQ_OUT_F32, S(stream)));
 }
 
 mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const float* o_slots, int64_t total_slots,

@@ -498,12 +498,12 @@ route_slots_kernel(Route a, int blocks) {
 // Backward to the logits: one wave per token at a time; the counts stay in registers over the
 // tokens of a wave, and the next token's logits are on their way while it works on one.
 // ---------------------------------------------------------------------------
-template <int NE>
+template <bool OUT32, int NE>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int experts, int64_t ld, int topk,
                       const int32_t* __restrict__ topk_idx, const float* __restrict__ weights,
                       const float* __restrict__ d_weights, const int32_t* __restrict__ counts,
-                      const float* __restrict__ d_loss, float coef, float* __restrict__ d_logits) {
+                      const float* __restrict__ d_loss, float coef, void* __restrict__ d_logits) {
   __shared__ __attribute__((aligned(16))) float share[kWaves][NE * 64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
@@ -575,13 +575,23 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
       __builtin_amdgcn_wave_barrier();
       if (in) share[w][my_e] = 0.0f;
     }
-    float* out = d_logits + t * experts + lane * NE;
-    if (experts % NE == 0) {
-      if (lane * NE < experts) __builtin_memcpy(out, d, NE * 4);
-    } else {
+    const int64_t at = t * experts + lane * NE;
+    const int some = max(0, min(NE, experts - lane * NE));   // this lane's experts
+    if (OUT32) {
+      if (some == NE) __builtin_memcpy((float*)d_logits + at, d, NE * 4);
+      else
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (lane * NE + i < experts) out[i] = d[i];
+        for (int i = 0; i < NE; ++i)
+          if (i < some) ((float*)d_logits)[at + i] = d[i];
+    } else {
+      uint16_t h[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) h[i] = (uint16_t)bf16x2_rne(d[i], 0.0f);
+      if (some == NE) __builtin_memcpy((uint16_t*)d_logits + at, h, NE * 2);
+      else
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (i < some) ((uint16_t*)d_logits)[at + i] = h[i];
     }
   }
 }
@@ -718,13 +728,19 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
 
 hipError_t launch_route_backward(const float* logits, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
                                  const int32_t* topk_idx, const float* weights, const float* d_weights,
-                                 const int32_t* counts, const float* d_loss, float coef, float* d_logits,
+                                 const int32_t* counts, const float* d_loss, float coef, void* d_logits, int out32,
                                  hipStream_t st) {
-  const int64_t want = (tokens + kWaves - 1) / kWaves, grid = want < 2048 ? want : 2048;   // eight workgroups a CU
-  with_experts(experts, [&](auto NE) {
-    hipLaunchKernelGGL((route_backward_kernel<decltype(NE)::value>), dim3((unsigned)grid), dim3(kThreads), 0, st, logits, tokens, (int)experts, ld, (int)topk, topk_idx, weights, d_weights,
-                       counts, d_loss, coef, d_logits);
-  });
+  const int64_t want = (tokens + kWaves - 1) / kWaves;
+  const dim3 grid((unsigned)(want < 2048 ? want : 2048)), block(kThreads);       // eight workgroups a CU
+  auto go = [&](auto O) {
+    with_experts(experts, [&](auto N) {
+      hipLaunchKernelGGL((route_backward_kernel<decltype(O)::value, decltype(N)::value>), grid, block, 0, st, logits,
+                         tokens, (int)experts, ld, (int)topk, topk_idx, weights, d_weights, counts, d_loss, coef,
+                         d_logits);
+    });
+  };
+  if (out32) go(std::true_type{});
+  else go(std::false_type{});
   return hipGetLastError();
 }
 

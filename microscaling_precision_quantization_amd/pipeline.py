@@ -323,6 +323,85 @@ class MoeDequantBackward:
                 "gate_up_dgrad": 2 * live * 2 * f.I * f.H, "gate_up_wgrad": 2 * live * 2 * f.I * f.H}
 
 
+class MoeBlockNvfp4:
+    """An expert block from the residual stream back to it, routed on the device:
+        n = RMSNorm(x) w_pre       BF16, and per-token NVFP4 from the same launch
+        z = n W_r^T                 router logits (BF16 GEMM); plan: top-k, slots, balance loss
+        y = sum_j w_j E_j(n)        MoeNvfp4 on the plan
+        out = res_scale x + branch_scale gate (RMSNorm(y) w_post)
+    The plan's slots are a fixed number (every expert's range padded to `pad`, the rest dealt
+    out), so nothing waits for the counts and a step can be captured in a HIP graph."""
+
+    def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, pad: int = 1,
+                 balance_coef: float | None = None, gate_mode: str = "none", branch_scale: float = 1.0,
+                 res_scale: float = 1.0, eps: float = 1e-6, backward: bool = False):
+        T, H, G = tokens, hidden, experts
+        self.topk, self.pad, self.coef, self.eps = topk, pad, balance_coef, eps
+        self.gate_mode, self.branch_scale, self.res_scale = gate_mode, branch_scale, res_scale
+        self.plan = B.RoutePlan(T, G, topk, pad, loss=balance_coef is not None, dev=dev)
+        self.moe = MoeNvfp4(T, H, G, inter, self.plan, dev, keep_h=False)
+        self.n, self.logits, self.out = _bf16((T, H), dev), _f32((T, G), dev), _bf16((T, H), dev)
+        self.rstd_pre, self.rstd_post = _f32((T,), dev), _f32((T,), dev)
+        if backward:                                               # needs pad, tokens and experts % 8 == 0
+            self.bwd = MoeDequantBackward(self.moe)
+            self.d_y, self.d_o, self.d_w = _f32((T, H), dev), _bf16((self.plan.slots, H), dev), _f32((T, topk), dev)
+            self.dw_post = _f32((H,), dev)
+            shape = {"none": None, "token": (T,), "channel": (H,), "full": (T, H)}[gate_mode]
+            self.d_gate = None if shape is None else _f32(shape, dev)
+            self.ones = torch.ones((T, topk), dtype=torch.float32, device=dev)
+            self.dn_experts, self.dn_router = _f32((T, H), dev), _f32((T, H), dev)
+            self.d_logits, self.dw_router = _bf16((T, G), dev), _f32((G, H), dev)
+            self.w_rT, self.nT, self.d_logitsT = _bf16((1, H, G), dev), _bf16((1, H, T), dev), _bf16((1, G, T), dev)
+            self.dx, self.dw_pre = _bf16((T, H), dev), _f32((H,), dev)
+            self.ws = _u8((B.lib().mxq_workspace_bytes(B.OP_NORM_BACKWARD, T, H, 0),), dev)
+
+    def forward(self, x, w_pre, w_router, w_post, gate=None, valid=None):
+        """x (T, H) BF16, w_router (G, H) BF16, norm weights FP32 (H). The expert weights are
+        quantized by self.moe.quantize_weights."""
+        m = self.moe
+        B.rmsnorm_quantize(x, w_pre, self.eps, B.NVFP4, out=(self.n, m.qx, m.sx, m.tx, self.rstd_pre))
+        B.gemm_block_scaled(B.BF16, self.n, None, w_router, None, out=self.logits)
+        B.moe_route(self.logits, self.topk, self.pad, valid=valid, balance_coef=self.coef, out=self.plan)
+        m.gate_up()
+        m.swiglu()
+        m.down()
+        m.combine()
+        B.rmsnorm_gate_residual(x, m.y, w_post, gate, self.gate_mode, self.eps, self.branch_scale, self.res_scale,
+                                out=(self.out, self.rstd_post))
+        return self.out
+
+    def backward_out(self, d_out, w_post, gate=None):
+        """From d_out (T, H) BF16 to the experts' outputs: d_y, dw_post, d_gate, d_o and d_w."""
+        B.rmsnorm_gate_residual_backward(d_out, self.moe.y, self.rstd_post, w_post, gate, self.gate_mode,
+                                         self.branch_scale, out=(self.d_y, self.dw_post, self.d_gate), workspace=self.ws)
+        B.moe_combine_backward(self.d_y, self.moe.o, self.plan.slot_of, self.plan.weights, self.plan.row_index,
+                               out=(self.d_o, self.d_w))
+
+    def backward_in(self, x, d_out, w_pre, w_router, d_loss=None):
+        """From the experts' input gradients (self.bwd.dx) and the combine weights' to dx, dw_router
+        and dw_pre; d_out also passes by on the residual."""
+        p = self.plan
+        B.moe_combine(self.bwd.dx, p.slot_of, self.ones, out=self.dn_experts)      # each token's slots, added up
+        B.moe_route_backward(self.logits, p.topk_idx, p.weights, p.counts, self.d_w, d_loss, self.coef or 0.0,
+                             out=self.d_logits)
+        T, G, H = self.d_logits.shape[0], self.d_logits.shape[1], x.shape[1]
+        B.dequantize_transposed(B.BF16, w_router, groups=1, group_rows=G, cols=H, out=self.w_rT)
+        B.dequantize_transposed(B.BF16, self.n, groups=1, group_rows=T, cols=H, out=self.nT)
+        B.dequantize_transposed(B.BF16, self.d_logits, groups=1, group_rows=T, cols=G, out=self.d_logitsT)
+        B.gemm_block_scaled(B.BF16, self.d_logits, None, self.w_rT[0], None, out=self.dn_router)
+        B.gemm_block_scaled(B.BF16, self.d_logitsT[0], None, self.nT[0], None, out=self.dw_router)
+        B.rmsnorm_backward(self.dn_experts, x, self.rstd_pre, w_pre, dn2=self.dn_router, d_res=d_out,
+                           res_scale=self.res_scale, out=(self.dx, self.dw_pre), workspace=self.ws)
+
+    def backward(self, x, d_out, d_gu, w_pre, w_router, w_post, gate=None, d_loss=None):
+        """All of it, given the upstream gradient dGU (slots, 2I) of the gate_up outputs, as
+        MoeDequantBackward is."""
+        self.backward_out(d_out, w_post, gate)
+        self.bwd.backward(self.d_o, d_gu)
+        self.backward_in(x, d_out, w_pre, w_router, d_loss)
+        return self.dx
+
+
 class SharedExpertBf16:
     """The shared expert in BF16 (it sees every token; kept in higher precision):
     GU = X W_sgu^T, h = silu(gate) * up (BF16), O = h W_sd^T; backward with upstream

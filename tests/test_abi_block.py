@@ -89,12 +89,12 @@ def test_route_validation():
     with pytest.raises(ValueError, match="no routing"):
         B.route_slots(4, 8, 40, 1)
 
-    def g(z=P, T=4, G=8, ld=8, k=2, idx=P, w=P, dw=P, counts=P, dl=P, out=P):
-        return B.lib().moe_route_backward(z, T, G, ld, k, idx, w, dw, counts, dl, 0.1, out, None)
+    def g(z=P, T=4, G=8, ld=8, k=2, idx=P, w=P, dw=P, counts=P, dl=P, out=P, od=F32):
+        return B.lib().moe_route_backward(z, T, G, ld, k, idx, w, dw, counts, dl, 0.1, out, od, None)
 
     assert g(k=9) == 2 and g(ld=4) == 2 and g(T=-1) == 2 and g(G=1025, ld=1025) == 2
     assert g(z=None) == 1 and g(idx=None) == 1 and g(out=None) == 1 and g(w=None) == 1 and g(counts=None) == 1
-    assert g(out=P + 2) == 3 and g(T=0) == 0
+    assert g(out=P + 2) == 3 and g(od=2) == 4 and g(T=0) == 0
 
 
 def test_combine_backward_validation():

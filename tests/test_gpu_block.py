@@ -1,0 +1,203 @@
+"""A whole expert block (pipeline.MoeBlockNvfp4) with its device routing, forward and backward:
+every stage against the oracle on the device's own input to that stage, the chain of gradients
+through the router against FP64 autograd, and graph replays against the eager step."""
+
+import numpy as np
+import pytest
+import torch
+
+from microscaling_precision_quantization_amd import binding as B
+from microscaling_precision_quantization_amd import inputs, pipeline
+from oracle import moe as omoe
+from oracle import norm, nvfp4, router
+from tests.gpu_util import assert_bytes_equal, assert_gemm_close, dev, dev_bf16, host
+from tests.test_gpu_graph import _check_graph
+from tests.test_gpu_norm import BF16, U, _dw_bound, _dx_bound
+from tests.test_gpu_route import _check_plan
+
+pytestmark = pytest.mark.gpu
+T, H, G, I, K, PAD = 192, 512, 16, 256, 3, 32
+COEF, EPS = 0.01, 1e-6
+
+
+class Case:
+    def __init__(self, seed, gate_mode="channel"):
+        d = torch.device("cuda")
+        self.block = pipeline.MoeBlockNvfp4(T, H, G, I, K, d, pad=PAD, balance_coef=COEF, gate_mode=gate_mode,
+                                            branch_scale=0.5, res_scale=0.75, backward=True)
+        e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=d)
+        bf = torch.bfloat16
+        self.x, self.d_out = e(T, H, dt=bf), e(T, H, dt=bf)
+        self.w_r, self.w_gu, self.w_d = e(G, H, dt=bf), e(G * 2 * I, H, dt=bf), e(G * H, I, dt=bf)
+        self.w_pre, self.w_post, self.gate = e(H), e(H), e({"token": T, "channel": H}[gate_mode])
+        self.valid = torch.empty(T, dtype=torch.bool, device=d)
+        self.d_gu = e(self.block.plan.slots, 2 * I, dt=bf)
+        self.d_loss = e(1)
+        self.feed(seed)
+
+    def feed(self, seed):
+        g = inputs.rng(320, seed)
+        put = lambda t, v: t.copy_(dev_bf16(inputs.to_bf16_bits(v)) if t.dtype == torch.bfloat16 else dev(v))
+        put(self.x, g.standard_normal((T, H)) * g.lognormal(0, 1, (T, 1)))
+        put(self.d_out, 1e-3 * g.standard_normal((T, H)))
+        put(self.w_r, 0.05 * g.standard_normal((G, H)))
+        put(self.w_gu, 0.02 * g.standard_normal((G * 2 * I, H)))
+        put(self.w_d, 0.02 * g.standard_normal((G * H, I)))
+        for t in (self.w_pre, self.w_post):
+            put(t, (1 + 0.2 * g.standard_normal(H)).astype(np.float32))
+        put(self.gate, g.uniform(0.1, 1, self.gate.shape).astype(np.float32))
+        put(self.valid, g.uniform(size=T) < 0.9)
+        self.d_gu_all = dev_bf16(inputs.to_bf16_bits(1e-3 * g.standard_normal(tuple(self.d_gu.shape))))
+        put(self.d_loss, np.float32([1.25]))
+
+    def step(self):
+        b = self.block
+        b.moe.quantize_weights(self.w_gu, self.w_d)
+        b.forward(self.x, self.w_pre, self.w_r, self.w_post, self.gate, self.valid)
+        # the upstream gradient of the gate_up outputs: padding slots zero
+        torch.mul(self.d_gu_all, (b.plan.row_index >= 0)[:, None], out=self.d_gu)
+        b.backward(self.x, self.d_out, self.d_gu, self.w_pre, self.w_r, self.w_post, self.gate, self.d_loss)
+
+
+def _f(t):
+    return inputs.bf16_bits_to_float(host(t)) if t.dtype == torch.bfloat16 else host(t)
+
+
+@pytest.mark.parametrize("gate_mode", ["channel", "token"])
+def test_block_forward_and_backward_stage_by_stage(gate_mode):
+    c = Case(0, gate_mode)
+    c.step()
+    b, m, p = c.block, c.block.moe, c.block.plan
+    x = _f(c.x)
+    n = norm.rmsnorm_bf16(x, host(c.w_pre), EPS)
+    assert_bytes_equal(host(b.n), n, "n")
+    for got, exp in zip((m.qx, m.sx, m.tx), nvfp4.quantize_per_token(n)):
+        assert_bytes_equal(host(got), exp, "NVFP4 tokens")
+    nv = inputs.bf16_bits_to_float(n).astype(np.float64)
+    assert_gemm_close(host(b.logits), nv @ _f(c.w_r).astype(np.float64).T, "router logits")
+    _check_plan(p, host(b.logits), K, PAD, host(c.valid), True, "plan")
+    slot_of, w = host(p.slot_of), host(p.weights)
+    o = host(m.o)
+    y = np.zeros((T, H))
+    for j in range(K):
+        on = slot_of[:, j] >= 0
+        y[on] += w[on, j, None].astype(np.float64) * o[slot_of[on, j]]
+    assert_gemm_close(host(m.y), y, "combine")
+    gate = host(c.gate)
+    gb = np.broadcast_to(gate[:, None] if gate_mode == "token" else gate, (T, H))
+    ref = norm.gate_residual(x, host(m.y), host(c.w_post), gb, EPS, 0.5, 0.75)
+    arith = 8 * U * np.abs(ref - 0.75 * x) + 3 * U * (np.abs(0.75 * x) + np.abs(ref))
+    assert np.all(np.abs(_f(b.out) - ref) <= arith + BF16 * (np.abs(ref) + arith))
+    assert bool((b.out[~c.valid] == (0.75 * c.x.float()[~c.valid]).bfloat16()).all())     # an unrouted token passes by
+
+    # backward: after the experts
+    up = 0.5 * _f(c.d_out).astype(np.float64)
+    r = host(b.rstd_post).astype(np.float64)[:, None]
+    yv, wp = host(m.y), host(c.w_post)
+    ref, ref_w = norm.backward(up * gb, yv, host(b.rstd_post), wp)
+    assert np.all(np.abs(host(b.d_y) - ref) <= _dx_bound(up * gb * wp, yv * r, r, 0.0, False, ref))
+    assert np.all(np.abs(host(b.dw_post) - ref_w) <= _dw_bound(up * gb * (yv * r), T))
+    terms = up * (yv * r) * wp
+    axis = 1 if gate_mode == "token" else 0
+    assert np.all(np.abs(host(b.d_gate) - terms.sum(axis)) <= 140 * U * np.abs(terms).sum(axis) + 1e-44)
+    ref_o, ref_dw = router.combine_backward(host(b.d_y), o, slot_of, w)
+    assert np.all(np.abs(_f(b.d_o) - ref_o) <= (BF16 + 2 * U) * np.abs(ref_o))
+    mag = np.abs(host(b.d_y)).astype(np.float64) @ np.abs(o).astype(np.float64).T
+    big = np.where(slot_of >= 0, np.take_along_axis(mag, np.maximum(slot_of, 0), 1), 0.0)
+    assert np.all(np.abs(host(b.d_w) - ref_dw) <= 84 * U * big)
+    # the experts (their own tests check them), then the way back in
+    dx_slots = host(b.bwd.dx).astype(np.float64)
+    dn = np.zeros((T, H))
+    for j in range(K):
+        on = slot_of[:, j] >= 0
+        dn[on] += dx_slots[slot_of[on, j]]
+    assert_gemm_close(host(b.dn_experts), dn, "gradient of n from the experts")
+    d_logits = router.backward(host(b.logits), host(p.topk_idx), w, host(p.counts), host(b.d_w), 1.25,
+                               float(np.float32(COEF)))
+    assert np.max(np.abs(_f(b.d_logits) - d_logits)) <= (BF16 + 100 * U) * np.max(np.abs(d_logits))
+    dz = _f(b.d_logits).astype(np.float64)
+    assert_gemm_close(host(b.dn_router), dz @ _f(c.w_r), "gradient of n from the router")
+    assert_gemm_close(host(b.dw_router), dz.T @ nv, "router weight gradient")
+    up = host(b.dn_experts).astype(np.float64) + host(b.dn_router)
+    r = host(b.rstd_pre).astype(np.float64)[:, None]
+    ref, ref_w = norm.backward(up, x, host(b.rstd_pre), host(c.w_pre))
+    res = 0.75 * _f(c.d_out).astype(np.float64)
+    ref = ref + res
+    assert np.all(np.abs(_f(b.dx) - ref) <= _dx_bound(up * host(c.w_pre), x * r, r, 2 * U * np.abs(res), True, ref))
+    mags = (np.abs(host(b.dn_experts)) + np.abs(host(b.dn_router))) * np.abs(x * r)
+    assert np.all(np.abs(host(b.dw_pre) - ref_w) <= _dw_bound(mags, T))
+
+
+def test_gradient_from_the_combine_to_the_logits_matches_autograd():
+    """<dy, combine(O, w(z))> + d_loss * balance loss, differentiated by FP64 autograd, against
+    moe_combine_backward followed by moe_route_backward."""
+    g = inputs.rng(321, 0)
+    t, e, k, h = 150, 24, 4, 256
+    z = (1.5 * g.standard_normal((t, e))).astype(np.float32)
+    plan = B.moe_route(dev(z), k, balance_coef=COEF)
+    o = g.standard_normal((plan.slots, h)).astype(np.float32)
+    dy = g.standard_normal((t, h)).astype(np.float32)
+    _, d_w = B.moe_combine_backward(dev(dy), dev(o), plan.slot_of, plan.weights, plan.row_index)
+    got = host(B.moe_route_backward(dev(z), plan.topk_idx, plan.weights, plan.counts, d_w, dev(np.float32([0.75])), COEF))
+    zt = torch.from_numpy(z).double().requires_grad_()
+    idx = torch.from_numpy(host(plan.topk_idx)).long()
+    w = torch.softmax(zt.gather(1, idx), 1)
+    picked = torch.from_numpy(o).double()[torch.from_numpy(host(plan.slot_of))]
+    counts = torch.from_numpy(host(plan.counts)).double()
+    balance = COEF * e * (counts[:e] / counts[:e].sum() * torch.softmax(zt, 1).mean(0)).sum()
+    ((w.unsqueeze(2) * picked).sum(1) * torch.from_numpy(dy).double()).sum().add(0.75 * balance).backward()
+    ref = zt.grad.numpy()
+    # d_w: 84 u of sum |dy o|; the weights: 32 u; the rest a few u of terms no larger than those
+    mag = np.abs(dy).astype(np.float64) @ np.abs(o).T.astype(np.float64)
+    bound = 200 * U * np.max(np.take_along_axis(mag, host(plan.slot_of), 1), axis=1, keepdims=True)
+    assert np.all(np.abs(got - ref) <= bound)
+
+
+def test_block_graph_replays_equal_the_eager_step():
+    c = Case(1)
+    c.d_gu_fixed = c.d_gu_all.clone()
+
+    def feed(seed):
+        def f():
+            c.feed(seed)
+            c.d_gu_fixed.copy_(c.d_gu_all)
+        return f
+
+    def step():
+        b = c.block
+        b.moe.quantize_weights(c.w_gu, c.w_d)
+        b.forward(c.x, c.w_pre, c.w_r, c.w_post, c.gate, c.valid)
+        torch.mul(c.d_gu_fixed, (b.plan.row_index >= 0)[:, None], out=c.d_gu)
+        b.backward(c.x, c.d_out, c.d_gu, c.w_pre, c.w_r, c.w_post, c.gate, c.d_loss)
+
+    b, p = c.block, c.block.plan
+    outputs = lambda: [b.n, b.logits, p.topk_idx, p.weights, p.counts, p.offsets, p.row_index, p.slot_of, p.loss,
+                       b.out, b.d_y, b.dw_post, b.d_gate, b.d_o, b.d_w, b.d_logits, b.dw_router, b.dx, b.dw_pre]
+    _check_graph(step, outputs, [feed(s) for s in (1, 2, 3)], "expert block")
+
+
+def test_many_token_router_graph_replays():
+    """The two- and the three-launch plan, captured, with the tally cleared inside the graph."""
+    for tokens in (3000, 17000):
+        z = torch.empty((tokens, 40), device="cuda")
+        plan = B.RoutePlan(tokens, 40, 4, 8, loss=True)
+        feeds = [lambda s=s: z.copy_(dev(inputs.rng(322, s).standard_normal((tokens, 40)).astype(np.float32)))
+                 for s in range(3)]
+        outputs = lambda: [plan.topk_idx, plan.weights, plan.counts, plan.offsets, plan.row_index, plan.slot_of, plan.loss]
+        _check_graph(lambda: B.moe_route(z, 4, pad=8, balance_coef=COEF, out=plan), outputs, feeds, f"{tokens} tokens")
+
+
+def test_forward_only_block_matches_the_host_routed_layer():
+    """The same layer with its routing made on the host: identical expert outputs and y."""
+    d = torch.device("cuda")
+    c = Case(4)
+    block = pipeline.MoeBlockNvfp4(T, H, G, I, K, d)
+    block.moe.quantize_weights(c.w_gu, c.w_d)
+    block.forward(c.x, c.w_pre, c.w_r, c.w_post)
+    r = inputs.route_topk(host(block.logits), K)
+    ref = pipeline.MoeNvfp4(T, H, G, I, pipeline.MoeRoutingDevice(r, d), d)
+    ref.quantize_weights(c.w_gu, c.w_d)
+    ref.r.weights.copy_(block.plan.weights)                  # the host's own differ in the last place
+    ref.forward(block.n)
+    assert torch.equal(block.moe.gu, ref.gu) and torch.equal(block.moe.o, ref.o) and torch.equal(block.moe.y, ref.y)
+    assert np.allclose(omoe.combine_ref(host(ref.o), r.slot_of, r.topk_w), host(block.moe.y), rtol=1e-4, atol=1e-6)

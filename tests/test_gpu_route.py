@@ -149,7 +149,12 @@ def test_route_backward(T, G, k, which):
         c = abs(float(dl)) * c32 * G * counts[:G] / (counts[:G].sum() * float(counts[G]))
         far = np.max(_far(z), axis=1, keepdims=True)
         bound += (3 * far + 80) * U * p * (c + (p @ c)[:, None])
-    assert np.all(np.abs(got - ref) <= bound + U * np.abs(ref) + 1e-44), float(np.max(np.abs(got - ref) - bound))
+    bound += U * np.abs(ref) + 1e-44
+    assert np.all(np.abs(got - ref) <= bound), float(np.max(np.abs(got - ref) - bound))
+    half = torch.empty((T, G), dtype=torch.bfloat16, device="cuda")
+    B.moe_route_backward(dev(z), plan.topk_idx, plan.weights, plan.counts, d_weights=None if dw is None else dev(dw),
+                         d_loss=None if dl is None else dev(np.array([dl])), balance_coef=COEF, out=half)
+    assert_bytes_equal(host(half), inputs.to_bf16_bits(got), "BF16 logit gradients")
 
 
 @pytest.mark.parametrize("T,G,k,pad,H,dt", [(1, 4, 1, 1, 8, "f32"), (5, 8, 3, 4, 96, "bf16"), (70, 16, 8, 8, 2048, "f32"),
