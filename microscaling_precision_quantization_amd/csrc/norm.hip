@@ -309,17 +309,19 @@ gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int
 
 // ---------------------------------------------------------------------------
 // Backward of both: dn = scale (d + d2) gate,  dy = r (g - yh mean(g yh)) + res_scale res.
-// Workgroups take rows b, b + grid, ...; each keeps the sums over its rows of dw (and of a
-// column gate's gradient) in registers and leaves them as one row of the workspace, which
-// column_sum_kernel adds up in row order: no atomics, the same bits on every run.
+// Workgroups take rows b, b + grid, ...; each keeps the column sums of its rows in registers and
+// leaves them as one row of the workspace, which column_sum_kernel adds up in row order: no
+// atomics, the same bits on every run. GATE: 0 none, 1 one per row, 3 one per element. A gate per
+// column is constant over the rows as the weight is, so it is multiplied into the weight (GATE 0)
+// and one sum, S = sum over the rows of scale d yh, gives both gradients: dw = gate S, dgate = w S.
 // ---------------------------------------------------------------------------
 struct NormGrad {
   const void *d, *d2, *y, *res;
-  const float *rstd, *weight, *gate;
+  const float *rstd, *weight, *gate;  // gate: per row or element, or (GATE 0) per column or NULL
   float scale, res_scale;
   int64_t rows, cols;
   void* dy;
-  float *dw_part, *dg_part, *dgate;   // partial sums (NULL: not wanted); gate gradient (GATE 1 and 3)
+  float *part, *dgate;                // partial sums (NULL: not wanted); gate gradient (GATE 1 and 3)
 };
 
 template <bool D32, bool Y32, int GATE, int W, int NV>
@@ -328,16 +330,19 @@ norm_backward_kernel(NormGrad a) {
   __shared__ float red[2][W], redg[2][W];
   const int64_t cols = a.cols;
   auto col = [&](int i) { return 8 * (int64_t)(i * W * 64 + (int)threadIdx.x); };
-  float w[NV][8], dw[NV][8], gc[GATE == 2 ? NV : 1][8], dgc[GATE == 2 ? NV : 1][8];
+  float w[NV][8], sum[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     zero8(w[i]);
-    zero8(dw[i]);
-    if (col(i) < cols) load8_cached(a.weight, col(i), w[i]);
-    if (GATE == 2) {
-      zero8(gc[i]);
-      zero8(dgc[i]);
-      if (col(i) < cols) load8_cached(a.gate, col(i), gc[i]);
+    zero8(sum[i]);
+    if (col(i) < cols) {
+      load8_cached(a.weight, col(i), w[i]);
+      if (GATE == 0) {
+        float g[8];
+        load8_cached(a.gate, col(i), g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[i][k] *= g[k];
+      }
     }
   }
   int buf = 0;
@@ -389,16 +394,16 @@ norm_backward_kernel(NormGrad a) {
       for (int k = 0; k < 8; ++k) {
         yh[i][k] *= r;
         float dn = a.scale * d[i][k];
-        const float dg = dn * (yh[i][k] * w[i][k]);
-        if (GATE == 1) dgr += dg;
-        if (GATE == 2) dgc[i][k] += dg;
-        if (GATE == 1) dn *= gr;
-        if (GATE == 2) dn *= gc[i][k];
+        if (GATE == 1) {
+          dgr += dn * (yh[i][k] * w[i][k]);
+          dn *= gr;
+        }
         if (GATE == 3) {
+          const float dg = dn * (yh[i][k] * w[i][k]);
           dn *= ge[k];
           ge[k] = dg;
         }
-        dw[i][k] += dn * yh[i][k];
+        sum[i][k] = fmaf(dn, yh[i][k], sum[i][k]);
         d[i][k] = dn * w[i][k];
         m = fmaf(d[i][k], yh[i][k], m);
       }
@@ -424,24 +429,20 @@ norm_backward_kernel(NormGrad a) {
       store8<Y32>(a.dy, at + col(i), o);
     }
   }
+  if (!a.part) return;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (col(i) >= cols) continue;
-    if (a.dw_part) store8<true>(a.dw_part, (int64_t)blockIdx.x * cols + col(i), dw[i]);
-    if (GATE == 2 && a.dg_part) store8<true>(a.dg_part, (int64_t)blockIdx.x * cols + col(i), dgc[i]);
-  }
+  for (int i = 0; i < NV; ++i)
+    if (col(i) < cols) store8<true>(a.part, (int64_t)blockIdx.x * cols + col(i), sum[i]);
 }
 
-// out[c] = sum over `parts` rows of part[., c]: 64 columns per workgroup, its sixteen waves on
-// every sixteenth row, joined in wave order. blockIdx.y picks one of two (partials, sums) pairs.
+// S[c] = sum over `parts` rows of part[., c]: 64 columns per workgroup, its sixteen waves on
+// every sixteenth row, joined in wave order. dw = S times the channel gate (NULL: S), and
+// dgate = S times the weight (NULL: S); either may be NULL.
 constexpr int kSumWaves = 16;
 __global__ void __launch_bounds__(kSumWaves * 64)
-column_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, const float* __restrict__ part1,
-                  float* __restrict__ out1, int64_t parts, int64_t cols) {
+column_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t cols, const float* __restrict__ weight,
+                  const float* __restrict__ gate, float* __restrict__ dw, float* __restrict__ dgate) {
   __shared__ float red[kSumWaves][64];
-  const float* part = blockIdx.y ? part1 : part0;
-  float* out = blockIdx.y ? out1 : out0;
-  if (!out) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
@@ -453,7 +454,8 @@ column_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, con
   if (w == 0 && c < cols) {
 #pragma unroll
     for (int i = 1; i < kSumWaves; ++i) s += red[i][lane];
-    out[c] = s;
+    if (dw) dw[c] = gate ? s * gate[c] : s;
+    if (dgate) dgate[c] = weight ? s * weight[c] : s;
   }
 }
 
@@ -492,7 +494,7 @@ int64_t backward_parts(int64_t rows) { return rows < 512 ? rows : 512; }
 }  // namespace
 
 size_t norm_backward_ws_bytes(int64_t rows, int64_t cols) {
-  return (size_t)(2 * backward_parts(rows) * cols * 4);    // dw and a column gate's gradient
+  return (size_t)(backward_parts(rows) * cols * 4);        // one row of column sums per workgroup
 }
 
 hipError_t launch_norm_quant(int fmt, const void* x, int x32, int64_t rows, int64_t cols, int64_t ld_x,
@@ -540,27 +542,26 @@ hipError_t launch_norm_backward(const void* d, const void* d2, int d32, const vo
                                 float res_scale, int64_t rows, int64_t cols, void* dy, float* dw, float* dgate,
                                 void* ws, hipStream_t st) {
   const int64_t parts = backward_parts(rows);
-  float* dg_sum = gate_mode == 2 ? dgate : nullptr;
-  float *dw_part = (float*)ws, *dg_part = (float*)ws + parts * cols;
+  const bool channel = gate_mode == 2, sums = dw || (channel && dgate);
   if (rows > 0) {
-    const NormGrad a{d, d2, y, res, rstd, weight, gate, scale, res_scale, rows, cols, dy, dw ? dw_part : nullptr,
-                     dg_sum ? dg_part : nullptr, dgate};
+    const NormGrad a{d, d2, y, res, rstd, weight, gate, scale, res_scale, rows, cols, dy, sums ? (float*)ws : nullptr,
+                     dgate};
     with_bool(d32, [&](auto D) {
       with_bool(y32, [&](auto Y) {
-        with_gate(gate_mode, [&](auto G) {
-          with_row(cols, [&](auto N, auto V) {
-            constexpr int W = decltype(N)::value;
-            hipLaunchKernelGGL(
-                (norm_backward_kernel<decltype(D)::value, decltype(Y)::value, decltype(G)::value, W, decltype(V)::value>),
-                dim3((unsigned)parts), dim3(W * 64), 0, st, a);
-          });
+        with_row(cols, [&](auto N, auto V) {
+          constexpr int W = decltype(N)::value, NV = decltype(V)::value;
+          constexpr bool DF = decltype(D)::value, YF = decltype(Y)::value;
+          const dim3 grid((unsigned)parts), block(W * 64);
+          if (gate_mode == 1) hipLaunchKernelGGL((norm_backward_kernel<DF, YF, 1, W, NV>), grid, block, 0, st, a);
+          else if (gate_mode == 3) hipLaunchKernelGGL((norm_backward_kernel<DF, YF, 3, W, NV>), grid, block, 0, st, a);
+          else hipLaunchKernelGGL((norm_backward_kernel<DF, YF, 0, W, NV>), grid, block, 0, st, a);
         });
       });
     });
   }
-  if (dw || dg_sum)
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + 63) / 64), dg_sum ? 2 : 1), dim3(kSumWaves * 64), 0,
-                       st, dw_part, dw, dg_part, dg_sum, parts, cols);
+  if (sums)
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(kSumWaves * 64), 0, st,
+                       (const float*)ws, parts, cols, weight, channel ? gate : nullptr, dw, channel ? dgate : nullptr);
   return hipGetLastError();
 }
 
