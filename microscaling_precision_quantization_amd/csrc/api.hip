@@ -647,7 +647,7 @@ mxq_status gate_check(const float* gate, mxq_gate_mode mode) {
   if (mode != MXQ_GATE_NONE && mode != MXQ_GATE_TOKEN && mode != MXQ_GATE_CHANNEL && mode != MXQ_GATE_FULL)
     return MXQ_ERR_FORMAT;
   if (mode != MXQ_GATE_NONE && !gate) return MXQ_ERR_NULL;
-  if (!al16(gate)) return MXQ_ERR_ALIGN;
+  if (mode == MXQ_GATE_TOKEN ? !al4(gate) : !al16(gate)) return MXQ_ERR_ALIGN;   // a token's is one value
   return MXQ_OK;
 }
 
@@ -727,7 +727,8 @@ mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dty
     if (!d_out || !y || !rstd || !dy) return MXQ_ERR_NULL;
   }
   if (cols % 8 || cols > kMaxRowCols || rows > kMaxGridBlocks) return MXQ_ERR_SHAPE;
-  if (!al16(d_out) || !al16(y) || !al4(rstd) || !al16(weight) || !al16(dy) || !al16(dw) || !al16(dgate))
+  if (!al16(d_out) || !al16(y) || !al4(rstd) || !al16(weight) || !al16(dy) || !al16(dw) ||
+      (gate_mode == MXQ_GATE_TOKEN ? !al4(dgate) : !al16(dgate)))
     return MXQ_ERR_ALIGN;
   const bool sums = dw || (dgate && gate_mode == MXQ_GATE_CHANNEL);
   const mxq_status ws = norm_workspace(rows, cols, sums, workspace, workspace_bytes);

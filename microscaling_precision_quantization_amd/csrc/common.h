@@ -188,6 +188,17 @@ __device__ __forceinline__ float4 load_stream16f(const float* p) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+// A BF16 output beyond this size leaves with non-temporal stores: half of the memory-side cache,
+// which the inputs stream through too; a smaller one stays there for the kernel that reads it next.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
+template <bool STREAM>                            // not a run-time flag: the compiler would merge the two stores
+__device__ __forceinline__ void store16(void* p, const uint4& v) {
+  u32x4_nt* const to = static_cast<u32x4_nt*>(p);
+  const u32x4_nt u = {v.x, v.y, v.z, v.w};
+  if (STREAM) __builtin_nontemporal_store(u, to);
+  else *to = u;
+}
+
 // BF16 element j (0/1) of a dword, widened to FP32 exactly.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -600,13 +600,13 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
 // Backward of the combine: one workgroup of W waves per token, dy kept in registers (NV vectors
 // of 8 per lane) over its slots; the dot products meet in LDS. HBM bounds it. A barrier that waits
 // for LDS only keeps the waves on the same slot's rows, which are contiguous (8192 tokens x 8 slots
-// x 7168: 638 us without it, 624 with it). NT: dO larger than the memory-side cache leaves with
-// non-temporal stores (1 GB: 650 -> 624 us; 33 MB, kept for the GEMM that reads it next, 22.6 us
-// against 21.8 with plain ones). The grid's last workgroups clear the padding slots of dO.
+// x 7168: 638 us without it, 624 with it). A large dO leaves with non-temporal stores (1 GB: 650 ->
+// 624 us; 33 MB with plain ones 21.8 us, non-temporal 22.6). The grid's last workgroups clear the
+// padding slots of dO.
 // ---------------------------------------------------------------------------
 constexpr int kMaxTopk = 32;
 
-template <bool D32, bool NT, int W, int NV>
+template <bool D32, bool STREAM, int W, int NV>
 __global__ void __launch_bounds__(W * 64)
 combine_backward_kernel(const void* __restrict__ dy, const float* __restrict__ o, int64_t total, int64_t tokens,
                         int topk, int64_t hidden, const int64_t* __restrict__ slot_of,
@@ -652,11 +652,9 @@ combine_backward_kernel(const void* __restrict__ dy, const float* __restrict__ o
         const float4 a = load_stream16f(p), b = load_stream16f(p + 4);
         dot = fmaf(d[i][0], a.x, fmaf(d[i][1], a.y, fmaf(d[i][2], a.z, fmaf(d[i][3], a.w, dot))));
         dot = fmaf(d[i][4], b.x, fmaf(d[i][5], b.y, fmaf(d[i][6], b.z, fmaf(d[i][7], b.w, dot))));
-        const u32x4_nt h = {bf16x2_rne(w * d[i][0], w * d[i][1]), bf16x2_rne(w * d[i][2], w * d[i][3]),
-                            bf16x2_rne(w * d[i][4], w * d[i][5]), bf16x2_rne(w * d[i][6], w * d[i][7])};
-        u32x4_nt* const to = reinterpret_cast<u32x4_nt*>(d_o + slot * hidden + col(i));
-        if (NT) __builtin_nontemporal_store(h, to);
-        else *to = h;
+        store16<STREAM>(d_o + slot * hidden + col(i),
+                        make_uint4(bf16x2_rne(w * d[i][0], w * d[i][1]), bf16x2_rne(w * d[i][2], w * d[i][3]),
+                                   bf16x2_rne(w * d[i][4], w * d[i][5]), bf16x2_rne(w * d[i][6], w * d[i][7])));
       }
     }
     dot = wave_sum(dot);
@@ -761,16 +759,13 @@ hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int6
                                    const int32_t* row_index, void* d_o, float* d_weights, hipStream_t st) {
   using std::integral_constant;
   const dim3 grid((unsigned)(tokens + (total + 63) / 64));
-  const bool large = total * hidden * 2 > (int64_t)256 << 20;
+  const bool large = total * hidden * 2 > kStreamBytes;
   auto go = [&](auto D, auto N, auto V) {
     constexpr int W = decltype(N)::value, NV = decltype(V)::value;
     constexpr bool DF = decltype(D)::value;
-    if (large)
-      hipLaunchKernelGGL((combine_backward_kernel<DF, true, W, NV>), grid, dim3(W * 64), 0, st, dy, o, total, tokens,
-                         (int)topk, hidden, slot_of, weights, row_index, (uint16_t*)d_o, d_weights);
-    else
-      hipLaunchKernelGGL((combine_backward_kernel<DF, false, W, NV>), grid, dim3(W * 64), 0, st, dy, o, total, tokens,
-                         (int)topk, hidden, slot_of, weights, row_index, (uint16_t*)d_o, d_weights);
+    const auto kernel = large ? combine_backward_kernel<DF, true, W, NV> : combine_backward_kernel<DF, false, W, NV>;
+    hipLaunchKernelGGL(kernel, grid, dim3(W * 64), 0, st, dy, o, total, tokens, (int)topk, hidden, slot_of, weights,
+                       row_index, (uint16_t*)d_o, d_weights);
   };
   auto vectors = [&](auto D) {
     const int64_t v = (hidden / 8 + 63) / 64;               // vectors a lane of one wave would hold

@@ -54,7 +54,7 @@ def test_gate_residual_validation():
     assert f(rows=-1) == 2 and f(cols=60) == 2 and f(cols=16392) == 2
     assert f(mode=4) == 4 and f(mode=-1) == 4 and f(eps=0.0) == 4 and f(xd=3) == 4 and f(yd=3) == 4
     assert f(gate=None) == 1 and f(gate=None, mode=2) == 1 and f(x=None) == 1 and f(y=None) == 1 and f(out=None) == 1
-    assert f(gate=MIS) == 3 and f(x=MIS) == 3 and f(y=MIS) == 3 and f(out=MIS) == 3 and f(w=MIS) == 3
+    assert f(gate=P + 2) == 3 and f(gate=MIS, mode=2) == 3 and f(gate=MIS, mode=3) == 3 and f(x=MIS) == 3 and f(y=MIS) == 3 and f(out=MIS) == 3 and f(w=MIS) == 3
     assert f(rows=0) == 0 and f(cols=0) == 0
 
     def g(d=P, dd=BF, y=P, yd=F32, rstd=P, w=P, gate=P, mode=2, rows=4, cols=64, dy=P, dw=P, dg=P, ws=P, wsn=1 << 20):

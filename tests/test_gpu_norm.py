@@ -300,3 +300,36 @@ def test_norms_on_a_side_stream_and_with_one_workspace():
     assert torch.equal(got[1], q) and torch.equal(one[0], dx) and torch.equal(one[1], dw) and torch.equal(two[1], dw)
     with pytest.raises(ValueError, match="workspace"):
         B.rmsnorm_backward(dn, x, rstd, w, workspace=ws[:64])
+
+
+def test_outputs_beyond_the_streaming_size_equal_smaller_calls():
+    """More than 128 MB of BF16 output (non-temporal stores) against the same rows in small calls:
+    every row's result is its own, whatever the call's size."""
+    rows, cols = 16500, 4128
+    assert rows * cols * 2 > 128 << 20
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda s=1.0, dt=torch.bfloat16: (s * torch.randn((rows, cols), generator=g, device="cuda")).to(dt)
+    x, dn, d_res, w = rand(), rand(1e-3, torch.float32), rand(1e-3), dev(_weight(0, cols))
+    parts = [slice(0, 70), slice(8000, 8061), slice(rows - 33, rows)]
+    for fmt in (B.MXFP8, B.NVFP4, B.MXFP4, B.BF16):
+        whole = B.rmsnorm_quantize(x, w, fmt=fmt)
+        for p in parts:
+            for a, b in zip(whole, B.rmsnorm_quantize(x[p], w, fmt=fmt)):
+                assert (a is None and b is None) or torch.equal(a[p], b)
+    rstd = whole[4]
+    dx, dw = B.rmsnorm_backward(dn, x, rstd, w, d_res=d_res, res_scale=0.5)
+    for p in parts:
+        assert torch.equal(dx[p], B.rmsnorm_backward(dn[p], x[p], rstd[p], w, d_res=d_res[p], res_scale=0.5)[0])
+    ref = torch.zeros(cols, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    for i in range(0, rows, 1100):
+        t = dn[i:i + 1100].double() * x[i:i + 1100].double() * rstd[i:i + 1100, None].double()
+        ref += t.sum(0)
+        mag += t.abs().sum(0)
+    assert bool(((dw.double() - ref).abs() <= (rows / 512 + 140) * U * mag).all())
+    for mode, gate in (("none", None), ("token", torch.rand(rows, generator=g, device="cuda")),
+                       ("full", torch.rand((rows, cols), generator=g, device="cuda"))):
+        dy = B.rmsnorm_gate_residual_backward(d_res, x, rstd, w, gate, gate_mode=mode)[0]
+        for p in parts:
+            part = None if gate is None else gate[p]
+            assert torch.equal(dy[p], B.rmsnorm_gate_residual_backward(d_res[p], x[p], rstd[p], w, part, gate_mode=mode)[0])

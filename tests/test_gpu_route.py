@@ -212,3 +212,23 @@ def test_combine_backward_is_the_gradient_of_combine():
     want = (loss(o, plan.weights + f) - loss(o, plan.weights - f)) / 2
     got = float((d_w.double() * f.double()).sum())
     assert abs(got - want) <= 200 * U * float((dy.abs().double() @ o.abs().double().t()).sum())
+
+
+def test_combine_backward_beyond_the_streaming_size():
+    """More than 128 MB of dO (non-temporal stores): every slot against w dy in torch, rounded once."""
+    T, G, k, H = 2100, 16, 8, 4160
+    plan = B.moe_route(dev(_logits(77, T, G)), k, pad=32)
+    assert plan.slots * H * 2 > 128 << 20
+    g = torch.Generator(device="cuda").manual_seed(6)
+    o = torch.randn((plan.slots, H), generator=g, device="cuda")
+    dy = torch.randn((T, H), generator=g, device="cuda")
+    d_o, d_w = B.moe_combine_backward(dy, o, plan.slot_of, plan.weights, plan.row_index)
+    live = torch.zeros(plan.slots, dtype=torch.bool, device="cuda")
+    for j in range(k):
+        s = plan.slot_of[:, j]
+        live[s] = True
+        assert torch.equal(d_o[s], (plan.weights[:, j, None] * dy).bfloat16())
+        ref = (dy.double() * o[s].double()).sum(1)
+        mag = (dy.double() * o[s].double()).abs().sum(1)
+        assert bool(((d_w[:, j].double() - ref).abs() <= 84 * U * mag).all())
+    assert bool((d_o[~live] == 0).all())
