@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTok = 64;                         // tokens of a block (one bit each of a mask)
+constexpr int kTallies = 16;
 
 // Order-preserving key of a logit: larger for larger values, -0 as +0, NaN as -inf. An expert is
 // usable when its key lies above that of -inf, 0x007FFFFF.
@@ -131,7 +132,7 @@ struct Route {
   int32_t* base;                                 // (blocks, hist_cols): hist summed over earlier blocks
   int32_t* sums;                                 // (hist_cols): hist summed over all blocks
   float* psum;                                   // (blocks, experts): sums of p
-  uint64_t* tally;                               // the loss's sum over the blocks and their count
+  uint64_t* tally;                               // (1 + kTallies), 64 bytes apart: sums of the loss and counts
 };
 
 __host__ __device__ inline int hist_cols(int experts) { return (experts + 4) / 4 * 4; }
@@ -288,7 +289,7 @@ route_choose_kernel(Route a) {
         (uint8_t)(e < a.experts ? __popcll((unsigned long long)mask[e]) : e == a.experts ? routed : 0);
   if (a.loss) {
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.psum[(int64_t)blockIdx.x * a.experts + e] = lp[e];
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.tally = 0;
+    if (blockIdx.x == 0 && threadIdx.x <= kTallies) a.tally[8 * threadIdx.x] = 0;
   }
 }
 
@@ -424,7 +425,7 @@ route_scan_kernel(Route a, int blocks) {
 // Slots of one block of tokens per workgroup. SCANNED: base and sums come from route_scan_kernel;
 // otherwise every workgroup adds up the histograms itself. The loss: each workgroup weighs its
 // block's sums of p with the counts and adds the result to a tally (cleared by
-// route_choose_kernel); the one that completes it writes the loss.
+// route_choose_kernel); the one that completes the last writes the loss.
 // ---------------------------------------------------------------------------
 constexpr int kSlotThreads = 1024;               // one workgroup a CU fills its waves
 
@@ -444,7 +445,8 @@ route_slots_kernel(Route a, int blocks) {
       start[e] = a.base[(int64_t)blk * cols + e];
     }
   } else {
-    // four columns a thread and dword, summed as two pairs of 16 bits (fewer than 1024 blocks)
+    // four columns a thread and dword, summed as two pairs of 16 bits (at most kMaxUnscanned
+    // blocks of 64)
     for (int e = threadIdx.x; e < cols; e += kSlotThreads) cnt[e] = start[e] = 0;
     __syncthreads();
     const int quads = cols / 4, groups = kSlotThreads / quads > 0 ? kSlotThreads / quads : 1;
@@ -486,12 +488,22 @@ route_slots_kernel(Route a, int blocks) {
   // One atomic carries the workgroups' count (above bit `frac` + 11) and the sum so far in fixed
   // point: loss / coef is at most experts <= 2^10. Integers, so the order does not matter, and
   // whoever makes the count complete holds the whole sum. 65536 blocks leave 34 bits of fraction.
+  // Workgroups meet in kTallies first ones, whose last arrivals meet in one more: atomics on one
+  // address follow one another 10 ns apart.
   const int frac = 62 - (32 - __clz(blocks)) - 11;
   const uint64_t one = 1ull << (frac + 11);
-  const uint64_t add = one + (uint64_t)llrint(ldexp(part, frac));
-  const uint64_t now = atomicAdd((unsigned long long*)a.tally, (unsigned long long)add) + add;
-  if ((now >> (frac + 11)) == (uint64_t)blocks)
-    *a.loss = (float)((double)a.coef * ldexp((double)(now & (one - 1)), -frac));
+  auto meet = [&](int tally, uint64_t sum, int parties, uint64_t& total) {
+    const uint64_t add = one + sum;
+    total = atomicAdd((unsigned long long*)(a.tally + 8 * tally), (unsigned long long)add) + add;
+    const bool complete = (total >> (frac + 11)) == (uint64_t)parties;
+    total &= one - 1;
+    return complete;
+  };
+  const int first = blk % kTallies;
+  uint64_t sum = (uint64_t)llrint(ldexp(part, frac));
+  if (meet(1 + first, sum, (blocks - first + kTallies - 1) / kTallies, sum) &&
+      meet(0, sum, min(blocks, kTallies), sum))
+    *a.loss = (float)((double)a.coef * ldexp((double)sum, -frac));
 }
 
 // ---------------------------------------------------------------------------
@@ -694,15 +706,17 @@ void with_choice(int64_t tokens, int64_t experts, int64_t topk, F&& go) {   // l
 int64_t route_blocks(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
 
 // Blocks up to which every slots workgroup adds up all histograms itself, which saves the scan's
-// launch; its reads grow with the square of the blocks.
-constexpr int64_t kMaxUnscanned = 256;
+// launch; its reads grow with the square of the blocks. (top-8, without and with the scan: 64
+// blocks of 256 experts 16.4 / 17.1 us, 256 blocks 18.9 / 21.6, 512 blocks 31.0 / 32.7, 938 blocks
+// 60.8 / 55.9.)
+constexpr int64_t kMaxUnscanned = 512;
 
 }  // namespace
 
 // Workspace: tally, psum, base, sums, hist (see Route).
 size_t route_ws_bytes(int64_t tokens, int64_t experts) {
   const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
-  return (size_t)(8 + 4 * nb * experts + 4 * nb * cols + 4 * cols + nb * cols);
+  return (size_t)(64 * (1 + kTallies) + 4 * nb * experts + 4 * nb * cols + 4 * cols + nb * cols);
 }
 
 hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t tokens, int64_t experts, int64_t ld,
@@ -713,7 +727,7 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
   Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, coef, topk_idx, weights, counts, offsets,
           row_index, slot_of, loss, nullptr, nullptr, nullptr, nullptr, nullptr};
   a.tally = (uint64_t*)ws;
-  a.psum = (float*)(a.tally + 1);
+  a.psum = (float*)(a.tally + 8 * (1 + kTallies));
   a.base = (int32_t*)(a.psum + nb * experts);
   a.sums = a.base + nb * cols;
   a.hist = (uint8_t*)(a.sums + cols);

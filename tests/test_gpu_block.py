@@ -178,7 +178,7 @@ def test_block_graph_replays_equal_the_eager_step():
 
 def test_many_token_router_graph_replays():
     """The two- and the three-launch plan, captured, with the tally cleared inside the graph."""
-    for tokens in (3000, 17000):
+    for tokens in (3000, 33000):
         z = torch.empty((tokens, 40), device="cuda")
         plan = B.RoutePlan(tokens, 40, 4, 8, loss=True)
         feeds = [lambda s=s: z.copy_(dev(inputs.rng(322, s).standard_normal((tokens, 40)).astype(np.float32)))

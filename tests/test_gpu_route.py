@@ -61,7 +61,8 @@ def _check_plan(plan, z, k, pad, valid, loss, what):
                                        (64, 65, 4, 32), (65, 128, 8, 1), (129, 129, 3, 8), (200, 300, 12, 32),
                                        (511, 513, 32, 1), (1000, 1024, 2, 16), (1300, 16, 4, 32),
                                        (100, 60, 20, 4), (100, 100, 24, 1),
-                                       (130, 250, 32, 8), (90, 256, 16, 1), (90, 250, 17, 1), (16384, 20, 2, 8), (16385, 20, 2, 8), (17001, 70, 3, 1)])
+                                       (130, 250, 32, 8), (90, 256, 16, 1), (90, 250, 17, 1), (16384, 20, 2, 8), (32768, 20, 2, 8), (32769, 20, 2, 8),
+                                       (33001, 70, 3, 1)])
 def test_route_plan_is_exact(T, G, k, pad):
     z = _logits(T, T, G)
     plan = B.moe_route(dev(z), k, pad=pad, balance_coef=COEF)
