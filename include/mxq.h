@@ -623,7 +623,8 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
  *   q, s, t: as the format's row quantizer writes them (t: MXQ_NVFP4 only).
  *   rstd   : FP32 (rows), r rounded, NULL = not written.
  *   Requires eps > 0 (MXQ_ERR_FORMAT), cols % 32 == 0 (MXFP8, MXFP4), % 16 (NVFP4), % 8
- *   (BF16), and cols <= 16384 (a row is held in the registers of one workgroup).
+ *   (BF16), and cols <= 16384 (a row is held in the registers of one workgroup). Outputs must
+ *   not overlap x.
  * ------------------------------------------------------------------------- */
 mxq_status rmsnorm_quantize(mxq_format fmt, const void* x, mxq_out_dtype x_dtype, int64_t rows, int64_t cols,
                             int64_t ld_x, const float* weight, double eps, void* n_bf16, void* q, void* s, float* t,
@@ -656,6 +657,7 @@ mxq_status rmsnorm_backward(const void* dn, const void* dn2, mxq_out_dtype dn_dt
  *   x, out : (rows, cols) x_dtype; y: (rows, cols) y_dtype; weight: FP32 (cols), NULL = ones.
  *   gate   : FP32, laid out as gate_mode says (NULL with MXQ_GATE_NONE).
  *   rstd   : FP32 (rows), NULL = not written. Requires eps > 0, cols % 8 == 0, cols <= 16384.
+ *   out must not overlap an input.
  * ------------------------------------------------------------------------- */
 mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const void* y, mxq_out_dtype y_dtype,
                                  const float* weight, const float* gate, mxq_gate_mode gate_mode, double eps,
@@ -671,6 +673,7 @@ mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const voi
  *   d_out : (rows, cols) d_dtype; y, dy: (rows, cols) y_dtype; rstd from the forward pass.
  *   dw    : FP32 (cols), NULL = not wanted.  dgate: FP32 in the gate's layout, NULL = not wanted.
  *   workspace : as rmsnorm_backward, needed for dw and for the gradient of a channel gate.
+ *   rows = 0 clears dw and a channel gate's gradient. Outputs must not overlap inputs.
  * ------------------------------------------------------------------------- */
 mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dtype, const void* y,
                                           mxq_out_dtype y_dtype, const float* rstd, const float* weight,
@@ -687,7 +690,8 @@ mxq_status rmsnorm_gate_residual_backward(const void* d_out, mxq_out_dtype d_dty
  *   them and renormalised. An expert at minus infinity (or NaN) is never chosen: a token with
  *   fewer usable experts than topk ends its list with index -1, weight 0, slot -1. A token
  *   with valid[t] = 0 (a padding token of the batch) or without a usable expert is not routed:
- *   its whole list reads -1, 0, -1, and it counts nowhere. +Inf logits are outside the domain.
+ *   its whole list reads -1, 0, -1, and it counts nowhere. A +Inf logit is outside the domain (its
+ *   token's weights and the loss are unspecified).
  *   loss = balance_coef * experts * sum over e of (counts_e / A) (1/N) sum over t of p_te, with
  *   p the softmax over all experts, A = the sum of the counts, N = the routed tokens (0 for
  *   N = 0). The slots of an expert are its tokens ascending, then padding: every range is a

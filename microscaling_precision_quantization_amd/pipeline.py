@@ -342,7 +342,7 @@ class MoeBlockNvfp4:
         self.moe = MoeNvfp4(T, H, G, inter, self.plan, dev, keep_h=False)
         self.n, self.logits, self.out = _bf16((T, H), dev), _f32((T, G), dev), _bf16((T, H), dev)
         self.rstd_pre, self.rstd_post = _f32((T,), dev), _f32((T,), dev)
-        if backward:                                               # needs pad, tokens and experts % 8 == 0
+        if backward:                                               # needs pad % 8 == tokens % 8 == experts % 16 == 0
             self.bwd = MoeDequantBackward(self.moe)
             self.d_y, self.d_o, self.d_w = _f32((T, H), dev), _bf16((self.plan.slots, H), dev), _f32((T, topk), dev)
             self.dw_post = _f32((H,), dev)

@@ -282,6 +282,26 @@ def test_gate_residual_without_rows_or_weight():
     assert dy.shape == (0, 64) and bool((dw == 0).all()) and bool((dg == 0).all())
 
 
+@pytest.mark.parametrize("mode", MODES)
+def test_gate_residual_backward_without_weight(mode):
+    rows, cols = 21, 136
+    y, yv = _values(40, rows, cols, "f32")
+    d, dv = _values(41, rows, cols, "f32", 1e-3)
+    gate, gb = _gate(2, mode, rows, cols)
+    gt = None if gate is None else dev(gate)
+    rstd = norm.rstd(yv, EPS).astype(np.float32)
+    dy, dw, dgate = B.rmsnorm_gate_residual_backward(d, y, dev(rstd), None, gt, gate_mode=mode)
+    assert dw is None
+    up, yh = dv.astype(np.float64), yv * rstd.astype(np.float64)[:, None]
+    dn = up if gb is None else up * gb
+    ref, _ = norm.backward(dn, yv, rstd, None)
+    assert np.all(np.abs(host(dy) - ref) <= _dx_bound(dn, yh, rstd.astype(np.float64)[:, None], 0.0, False, ref))
+    if mode != "none":
+        axis = {"token": 1, "channel": 0, "full": ()}[mode]
+        t = up * yh
+        assert np.all(np.abs(host(dgate) - t.sum(axis)) <= 150 * U * np.abs(t).sum(axis) + 1e-44)
+
+
 def test_norms_on_a_side_stream_and_with_one_workspace():
     """Calls on a stream of their own, one workspace for several calls in order."""
     x, _ = _values(30, 700, 256, "bf16")

@@ -87,6 +87,24 @@ def test_route_with_masked_tokens_and_unusable_experts(T, G, k, pad, total):
     _check_plan(plan, zz, k, pad, valid, True, "masked")
 
 
+def test_route_out_of_domain_logits_stay_in_range():
+    """+Inf has no defined weights, but the plan it leaves is a plan: indices in range, every
+    routed pair in a slot of its own, and other tokens untouched."""
+    for T in (9, 200):
+        z = _logits(8, T, 40)
+        z[3, 5] = np.inf
+        plan = B.moe_route(dev(z), 4, pad=8, balance_coef=COEF)
+        finite = z.copy()
+        finite[3, 5] = np.finfo(np.float32).max
+        idx, w = router.choose(finite, 4)
+        counts, offsets, row_index, slot_of = router.plan(idx, 40, 8, plan.slots)
+        assert_bytes_equal(host(plan.topk_idx), idx, "topk_idx")
+        assert_bytes_equal(host(plan.slot_of), slot_of, "slot_of")
+        assert_bytes_equal(host(plan.row_index), row_index, "row_index")
+        rest = np.arange(T) != 3
+        assert np.all(np.abs(host(plan.weights)[rest] - w[rest]) <= _weight_bound(finite, idx, w)[rest])
+
+
 def test_route_nothing_routed_and_no_tokens():
     z = _logits(5, 40, 12)
     plan = B.moe_route(dev(z), 2, pad=4, valid=torch.zeros(40, dtype=torch.bool, device="cuda"), balance_coef=COEF)
