@@ -934,7 +934,7 @@ def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor
     c = _Checks(dev)
     c.need(logits, "logits", torch.float32, (T, G), ld=True)
     if valid is not None:
-        if valid.dtype == torch.bool:
+        if isinstance(valid, torch.Tensor) and valid.dtype == torch.bool:
             valid = valid.view(torch.uint8)
         c.need(valid, "valid", torch.uint8, (T,))
     plan = out

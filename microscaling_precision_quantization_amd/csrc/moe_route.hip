@@ -775,14 +775,24 @@ hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int6
                                    int64_t topk, int64_t hidden, const int64_t* slot_of, const float* weights,
                                    const int32_t* row_index, void* d_o, float* d_weights, hipStream_t st) {
   using std::integral_constant;
-  const dim3 grid((unsigned)(tokens + (total + 63) / 64));
   const bool large = total * hidden * 2 > kStreamBytes;
+  // a grid holds fewer than 2^32 threads (1024 to a token at most): more tokens take more launches,
+  // and the last one clears the padding slots
+  constexpr int64_t kLaunchTokens = (int64_t)1 << 21;
   auto go = [&](auto D, auto N, auto V) {
     constexpr int W = decltype(N)::value, NV = decltype(V)::value;
     constexpr bool DF = decltype(D)::value;
     const auto kernel = large ? combine_backward_kernel<DF, true, W, NV> : combine_backward_kernel<DF, false, W, NV>;
-    hipLaunchKernelGGL(kernel, grid, dim3(W * 64), 0, st, dy, o, total, tokens, (int)topk, hidden, slot_of, weights,
-                       row_index, (uint16_t*)d_o, d_weights);
+    int64_t t0 = 0;
+    do {
+      const bool last = tokens - t0 <= kLaunchTokens;
+      const int64_t some = last ? tokens - t0 : kLaunchTokens;
+      const dim3 grid((unsigned)(some + (last ? (total + 63) / 64 : 0)));
+      hipLaunchKernelGGL(kernel, grid, dim3(W * 64), 0, st, (const uint8_t*)dy + t0 * hidden * (DF ? 4 : 2), o, total,
+                         some, (int)topk, hidden, slot_of + t0 * topk, weights + t0 * topk, row_index,
+                         (uint16_t*)d_o, d_weights + t0 * topk);
+      t0 += some;
+    } while (t0 < tokens);
   };
   auto vectors = [&](auto D) {
     const int64_t v = (hidden / 8 + 63) / 64;               // vectors a lane of one wave would hold

@@ -5,10 +5,10 @@
 //   r = (mean(x^2) + eps)^(-1/2),  n = x r w
 //   dn -> g = dn w,  xh = x r,  dx = r (g - xh mean(g xh)),  dw = sum over rows of dn xh
 //   out = res_scale x + branch_scale gate (y r w)
-// The forward norm that feeds a quantizer is evaluated in binary64 from the squares on and
-// rounded once to BF16: its relative error stays below 2^-50, so the BF16 value is the
-// correctly rounded one unless the exact value lies that close to a rounding midpoint, and
-// the quantized bytes are those of the library's quantizers on it.
+// The forward norm that feeds a quantizer is rounded once to BF16 from a value whose relative
+// error stays below 2^-50 (binary64 from the squares on; binary32 where its roundings cannot
+// change the result): the correctly rounded one unless the exact value lies that close to a
+// rounding midpoint. The quantized bytes are those of the library's quantizers on it.
 #include <type_traits>
 
 #include "common.h"
@@ -493,6 +493,10 @@ void with_gate(int gate, F&& go) {
   else go(std::integral_constant<int, 3>{});
 }
 
+// Rows of a launch: a grid holds fewer than 2^32 threads (1024 to a row at most). More rows take
+// more launches.
+constexpr int64_t kLaunchRows = (int64_t)1 << 21;
+
 int64_t backward_parts(int64_t rows) { return rows < 512 ? rows : 512; }
 
 }  // namespace
@@ -504,15 +508,21 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t cols) {
 hipError_t launch_norm_quant(int fmt, const void* x, int x32, int64_t rows, int64_t cols, int64_t ld_x,
                              const float* weight, double eps, void* n, void* q, void* s, float* t, float* rstd,
                              hipStream_t st) {
+  const int64_t q_row = fmt == 1 ? cols : cols / 2, s_row = cols / (fmt == 2 ? 16 : 32);   // bytes
   auto go = [&](auto F) {
     with_bool(x32, [&](auto X) {
       with_bool(n && rows * cols * 2 > kStreamBytes, [&](auto L) {
         with_row(cols, [&](auto N, auto V) {
           constexpr int W = decltype(N)::value;
-          hipLaunchKernelGGL(
-              (norm_quant_kernel<decltype(F)::value, decltype(X)::value, decltype(L)::value, W, decltype(V)::value>),
-              dim3((unsigned)(W == 1 ? (rows + 3) / 4 : rows)), dim3(W == 1 ? 256 : W * 64), 0, st, x, rows, (int)cols,
-              ld_x, weight, eps, 1.0 / (double)cols, (uint16_t*)n, (uint8_t*)q, (uint8_t*)s, t, rstd);
+          for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+            const int64_t some = rows - r0 < kLaunchRows ? rows - r0 : kLaunchRows;
+            hipLaunchKernelGGL(
+                (norm_quant_kernel<decltype(F)::value, decltype(X)::value, decltype(L)::value, W, decltype(V)::value>),
+                dim3((unsigned)(W == 1 ? (some + 3) / 4 : some)), dim3(W == 1 ? 256 : W * 64), 0, st,
+                (const uint8_t*)x + r0 * ld_x * (x32 ? 4 : 2), some, (int)cols, ld_x, weight, eps, 1.0 / (double)cols,
+                n ? (uint16_t*)n + r0 * cols : nullptr, q ? (uint8_t*)q + r0 * q_row : nullptr,
+                s ? (uint8_t*)s + r0 * s_row : nullptr, t ? t + r0 : nullptr, rstd ? rstd + r0 : nullptr);
+          }
         });
       });
     });
@@ -531,11 +541,16 @@ hipError_t launch_gate_residual(const void* x, int x32, const void* y, int y32, 
     with_bool(y32, [&](auto Y) {
       with_gate(gate_mode, [&](auto G) {
         with_row(cols, [&](auto N, auto V) {
-          constexpr int W = decltype(N)::value;
-          hipLaunchKernelGGL(
-              (gate_residual_kernel<decltype(X)::value, decltype(Y)::value, decltype(G)::value, W, decltype(V)::value>),
-              dim3((unsigned)rows), dim3(W * 64), 0, st, x, y, cols, weight, gate, eps, branch_scale, res_scale, out,
-              rstd);
+          constexpr int W = decltype(N)::value, GATE = decltype(G)::value;
+          for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+            const int64_t some = rows - r0 < kLaunchRows ? rows - r0 : kLaunchRows;
+            hipLaunchKernelGGL(
+                (gate_residual_kernel<decltype(X)::value, decltype(Y)::value, GATE, W, decltype(V)::value>),
+                dim3((unsigned)some), dim3(W * 64), 0, st, (const uint8_t*)x + r0 * cols * (x32 ? 4 : 2),
+                (const uint8_t*)y + r0 * cols * (y32 ? 4 : 2), cols, weight,
+                GATE == 1 ? gate + r0 : GATE == 3 ? gate + r0 * cols : gate, eps, branch_scale, res_scale,
+                (uint8_t*)out + r0 * cols * (x32 ? 4 : 2), rstd ? rstd + r0 : nullptr);
+          }
         });
       });
     });

@@ -353,3 +353,26 @@ def test_outputs_beyond_the_streaming_size_equal_smaller_calls():
         for p in parts:
             part = None if gate is None else gate[p]
             assert torch.equal(dy[p], B.rmsnorm_gate_residual_backward(d_res[p], x[p], rstd[p], w, part, gate_mode=mode)[0])
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^21 rows to a launch: the rows on both sides of the seam equal calls of their own."""
+    seam, rows, cols = 1 << 21, (1 << 21) + 9, 32
+    g = torch.Generator(device="cuda").manual_seed(9)
+    wide = torch.randn((rows, cols + 8), generator=g, device="cuda").bfloat16()
+    x, y = wide[:, :cols], torch.randn((rows, cols), generator=g, device="cuda")
+    w = dev(_weight(0, cols))
+    gates = {"token": torch.randn(rows, generator=g, device="cuda"), "full": torch.randn_like(y)}
+    parts = [slice(seam - 70, seam), slice(seam, rows)]
+    for fmt in (B.MXFP8, B.MXFP4, B.NVFP4, B.BF16):
+        whole = B.rmsnorm_quantize(x, w, fmt=fmt)
+        for p in parts:
+            for a, b in zip(whole, B.rmsnorm_quantize(x[p], w, fmt=fmt)):
+                assert (a is None) == (b is None)
+                assert a is None or torch.equal(a[p], b)
+    for mode, gate in gates.items():
+        res = x.contiguous()
+        out, rstd = B.rmsnorm_gate_residual(res, y, w, gate, mode)
+        for p in parts:
+            o, r = B.rmsnorm_gate_residual(res[p], y[p], w, gate[p].clone(), mode)
+            assert torch.equal(out[p], o) and torch.equal(rstd[p], r)

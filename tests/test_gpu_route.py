@@ -251,3 +251,18 @@ def test_combine_backward_beyond_the_streaming_size():
         mag = (dy.double() * o[s].double()).abs().sum(1)
         assert bool(((d_w[:, j].double() - ref).abs() <= 84 * U * mag).all())
     assert bool((d_o[~live] == 0).all())
+
+
+def test_combine_backward_of_more_tokens_than_one_launch_takes():
+    """2^21 tokens to a launch: top-1 with slots in reverse order and padding in front."""
+    T, H = (1 << 21) + 9, 8
+    g = torch.Generator(device="cuda").manual_seed(10)
+    slot_of = (T + 2 - torch.arange(T, device="cuda"))[:, None].contiguous()            # slots 3 .. T + 2
+    row_index = torch.full((T + 3,), -1, dtype=torch.int32, device="cuda")
+    row_index[slot_of[:, 0]] = torch.arange(T, dtype=torch.int32, device="cuda")
+    o, dy = torch.randn((T + 3, H), generator=g, device="cuda"), torch.randn((T, H), generator=g, device="cuda")
+    w = torch.randn((T, 1), generator=g, device="cuda")
+    d_o, d_w = B.moe_combine_backward(dy, o, slot_of, w, row_index)
+    assert torch.equal(d_o[slot_of[:, 0]], (w * dy).bfloat16()) and bool((d_o[:3] == 0).all())
+    terms = dy.double() * o[slot_of[:, 0]].double()
+    assert bool(((d_w[:, 0].double() - terms.sum(1)).abs() <= 84 * U * terms.abs().sum(1)).all())
