@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTok = 64;                         // tokens of a block (one bit each of a mask)
 constexpr int kTallies = 16;
+constexpr int kMaxTopk = 32;
 
 // Order-preserving key of a logit: larger for larger values, -0 as +0, NaN as -inf. An expert is
 // usable when its key lies above that of -inf, 0x007FFFFF.
@@ -51,7 +52,7 @@ __device__ __forceinline__ float softmax_term(float z, float top) {
 }
 
 // A lane's NE consecutive logits of a row, NaN past the row. With a whole number of lanes to the
-// row every lane takes one wide load (whatever the row's alignment), else single ones.
+// row every lane takes wide loads (whatever the row's alignment), else single ones.
 template <int NE>
 __device__ __forceinline__ void load_logits(const float* row, int experts, int lane, float* z) {
   const int e = lane * NE;
@@ -119,7 +120,7 @@ struct Route {
   const float* logits;
   const uint8_t* valid;
   int64_t tokens, ld, pad, total;
-  int experts, topk;
+  int experts, topk, units;                      // units: total / pad
   float coef;
   int32_t* topk_idx;
   float* weights;
@@ -165,8 +166,10 @@ __device__ __forceinline__ void sum_of_rows(float* v) {
 // topk_idx and weights, leaves the experts' masks in LDS and the waves' sums of p in lp (waves,
 // experts). With L = 16 sixteen waves take all 64 tokens at once, four tokens sharing every
 // instruction; L = 64 serves more experts (NE <= 16) or more choices than a row of lanes holds.
-// (16384 x 256, top-8: 7.7 us with L = 16, 14 us with L = 64. Bound by vector instructions and
-// the chain from one choice to the next.)
+// A choice moves only as many heads as there are choices to come. (16384 x 256, top-8: 6.9 us with
+// L = 16, 7.7 with all heads moved, 14 with L = 64. Bound by vector instructions and the chain from
+// one choice to the next; lanes that hold four chunks of four experts, so that a load takes whole
+// lines, are no faster.)
 // ---------------------------------------------------------------------------
 template <int L, int NE, int KEEP>
 __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* lp) {
@@ -206,13 +209,19 @@ __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_
     for (int i = 0; i < KEEP; ++i) head[i] = v[i];
     head[KEEP] = 0.0;
     const double top_v = lanes_max<L>(v[0]);
-    for (int j = 0; j < a.topk; ++j) {
+    auto take = [&](int j, int left) {           // `left`: the choices still to come, as many heads to keep
       const double best = lanes_max<L>(head[0]);
       my_v = lane == j ? best : my_v;
       const bool up = head[0] == best;           // its lane's next one moves up
 #pragma unroll
-      for (int i = 0; i < KEEP; ++i) head[i] = up ? head[i + 1] : head[i];
-    }
+      for (int i = 0; i < KEEP; ++i)
+        if (i < left) head[i] = up ? head[i + 1] : head[i];
+    };
+    int j = 0;
+    for (; j < a.topk - KEEP; ++j) take(j, KEEP);
+#pragma unroll
+    for (int left = KEEP - 1; left >= 0; --left)
+      if (left < a.topk) take(j++, left);
     const bool mine = on && my_v >= kUsable, any = on && top_v >= kUsable;
     const int my_e = mine ? M - (int)((uint32_t)__double_as_longlong(my_v) & M) : -1;
     const float top = key_logit((uint32_t)top_v);                          // conversions truncate `rest`
@@ -224,17 +233,16 @@ __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_
     }
     if (mine) atomicOr((unsigned long long*)&mask[my_e], 1ull << tl);
     routed += __popcll(__ballot(any && lane == 0));
-    if (a.loss) {
+    if (a.loss && any) {                         // all lanes of a token or none
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         z[i] = softmax_term(z[i], top);
         sum += z[i];
       }
-      sum = lanes_sum<L>(sum);
-      const float inv = any ? 1.0f / sum : 0.0f;
+      const float inv = 1.0f / lanes_sum<L>(sum);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] = any ? fmaf(z[i], inv, acc[i]) : acc[i];
+      for (int i = 0; i < NE; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
     }
   }
   if (a.loss) {
@@ -297,55 +305,59 @@ route_choose_kernel(Route a) {
 constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ int wave_scan(int v) {            // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
+  v += (int)dpp_u32<0x111, 0xF>((uint32_t)v);                // inside the rows of 16 lanes, shifted by 1, 2, 4, 8
+  v += (int)dpp_u32<0x112, 0xF>((uint32_t)v);
+  v += (int)dpp_u32<0x114, 0xF>((uint32_t)v);
+  v += (int)dpp_u32<0x118, 0xF>((uint32_t)v);
+  v += (int)dpp_u32<0x142, 0xA>((uint32_t)v);                // the rows' sums onwards
+  v += (int)dpp_u32<0x143, 0xC>((uint32_t)v);
   return v;
 }
 
 // Offsets from the counts, by one workgroup: every expert's units of pad, what is left of `total`
 // dealt out evenly, low experts first. cnt[experts] and off[experts + 1] in LDS, cnt published.
-// One wave scans (its lanes take consecutive experts): no partial sums of waves to exchange.
-__device__ __forceinline__ void padded_offsets(const Route& a, const int* cnt, int* off) {
+// One wave scans (its lanes take consecutive experts): no partial sums of waves to exchange. The
+// last thread, of another wave where there is one, does `beside` meanwhile.
+template <typename F>
+__device__ __forceinline__ void padded_offsets(const Route& a, const int* cnt, int* off, F&& beside) {
   const int lane = threadIdx.x & 63, G = a.experts, pad = (int)a.pad;
   for (int e = threadIdx.x; e < G; e += blockDim.x) off[e + 1] = cnt[e] ? (cnt[e] - 1) / pad + 1 : 0;
-  __syncthreads();
+  lds_barrier();
   if (threadIdx.x < 64) {
     const int per = (G + 63) / 64, e0 = lane * per, e1 = min(e0 + per, G);
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += off[e + 1];
     int at = wave_scan(sum);
-    const int used = __shfl(at, 63, 64);
+    const int used = (int)lane63((uint32_t)at);
     at -= sum;
-    const int spare = (int)(a.total / a.pad) - used, each = spare / G, more = spare % G;
+    const int spare = a.units - used, each = spare / G, more = spare % G;
     for (int e = e0; e < e1; ++e) {
       at += off[e + 1];
       off[e + 1] = (at + (e + 1) * each + min(e + 1, more)) * pad;
     }
     if (lane == 0) off[0] = 0;
   }
-  __syncthreads();
+  if (threadIdx.x == blockDim.x - 1) beside();
+  lds_barrier();
 }
 
-// The slots of one block of tokens, and this workgroup's share of the padding slots' -1.
-// `start[e]`: where the block's tokens begin in expert e's slots.
-__device__ __forceinline__ void write_slots(const Route& a, int64_t t0, const uint64_t* mask, const int* cnt,
-                                            const int* off, const int* start) {
-  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = a.topk_idx[t0 * a.topk + i], tl = i / a.topk;
-    int64_t slot = -1;
-    if (e >= 0) {
-      slot = start[e] + __popcll((unsigned long long)(mask[e] & ((1ull << tl) - 1)));
-      a.row_index[slot] = (int32_t)(t0 + tl);
-    }
-    a.slot_of[t0 * a.topk + i] = slot;
+// The slot of choice i of a block of tokens, expert e (-1: none). `start[e]`: where the block's
+// tokens begin in expert e's slots.
+__device__ __forceinline__ void write_slot(const Route& a, int64_t t0, int i, int e, const uint64_t* mask,
+                                           const int* start) {
+  const int tl = i / a.topk;
+  int64_t slot = -1;
+  if (e >= 0) {
+    slot = start[e] + __popcll((unsigned long long)(mask[e] & ((1ull << tl) - 1)));
+    a.row_index[slot] = (int32_t)(t0 + tl);
   }
+  a.slot_of[t0 * a.topk + i] = slot;
+}
+
+// This workgroup's share of the padding slots' -1, 16 lanes an expert.
+__device__ __forceinline__ void write_padding(const Route& a, const int* cnt, const int* off) {
   const int group = (blockIdx.x * blockDim.x + threadIdx.x) / 16, groups = gridDim.x * blockDim.x / 16;
-  for (int e = group; e < a.experts; e += groups)            // 16 lanes an expert
+  for (int e = group; e < a.experts; e += groups)
     for (int64_t s = (int64_t)off[e] + cnt[e] + (threadIdx.x & 15); s < off[e + 1]; s += 16) a.row_index[s] = -1;
 }
 
@@ -356,10 +368,11 @@ __device__ __forceinline__ void write_counts(const Route& a, const int* cnt, con
   }
 }
 
-// loss / coef of one block of tokens, in thread 0: experts / (A N) sum over e of counts_e psum_e.
-// `p` is psum_e of expert threadIdx.x + i blockDim.x, in turn.
+// loss / coef of one block of tokens: experts / (A N) sum over e of counts_e psum_e. loss_terms()
+// leaves the waves' sums in LDS (`p` is psum_e of expert threadIdx.x + i blockDim.x, in turn); after
+// a barrier block_loss() adds them up.
 template <typename P>
-__device__ __forceinline__ double block_loss(const Route& a, const int* cnt, int routed, P&& p, double (*red)[2]) {
+__device__ __forceinline__ void loss_terms(const Route& a, const int* cnt, P&& p, double (*red)[2]) {
   double dot = 0.0, all = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
     dot += (double)cnt[e] * (double)p(e);
@@ -367,14 +380,16 @@ __device__ __forceinline__ double block_loss(const Route& a, const int* cnt, int
   }
   dot = wave_sum(dot);
   all = wave_sum(all);
-  const int w = threadIdx.x >> 6, waves = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) {
-    red[w][0] = dot;
-    red[w][1] = all;
+    red[threadIdx.x >> 6][0] = dot;
+    red[threadIdx.x >> 6][1] = all;
   }
-  lds_barrier();
-  if (threadIdx.x != 0) return 0.0;
-  for (int i = 1; i < waves; ++i) {
+}
+template <int W>
+__device__ __forceinline__ double block_loss(const Route& a, int routed, const double (*red)[2]) {
+  double dot = red[0][0], all = red[0][1];
+#pragma unroll
+  for (int i = 1; i < W; ++i) {
     dot += red[i][0];
     all += red[i][1];
   }
@@ -394,13 +409,14 @@ route_one_block_kernel(Route a) {
   const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) cnt[e] = __popcll((unsigned long long)mask[e]);
   __syncthreads();
-  padded_offsets(a, cnt, off);
+  if (a.loss) loss_terms(a, cnt, [&](int e) { return lp[e]; }, red);
+  padded_offsets(a, cnt, off, [&] {
+    if (a.loss) *a.loss = (float)((double)a.coef * block_loss<choose_waves(L, NE)>(a, routed, red));
+  });
   write_counts(a, cnt, off, routed);
-  write_slots(a, 0, mask, cnt, off, off);
-  if (a.loss) {
-    const double l = block_loss(a, cnt, routed, [&](int e) { return lp[e]; }, red);
-    if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * l);
-  }
+  const int n = (int)a.tokens * a.topk;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) write_slot(a, 0, i, a.topk_idx[i], mask, off);
+  write_padding(a, cnt, off);
 }
 
 // ---------------------------------------------------------------------------
@@ -417,94 +433,129 @@ route_scan_kernel(Route a, int blocks) {
     const int v = b < blocks ? a.hist[(int64_t)b * cols + c] : 0;
     const int incl = wave_scan(v);
     if (b < blocks) a.base[(int64_t)b * cols + c] = carry + incl - v;
-    carry += __shfl(incl, 63, 64);
+    carry += (int)lane63((uint32_t)incl);
   }
   if (lane == 0) a.sums[c] = carry;
 }
 
+// A block's share of loss / coef goes into the tallies (cleared by route_choose_kernel); whoever
+// completes them writes the loss. One atomic carries the workgroups' count (above bit `frac` + 11)
+// and the sum so far in fixed point: loss / coef is at most experts <= 2^10. Integers, so the order
+// does not matter, and whoever makes the count complete holds the whole sum. 65536 blocks leave 34
+// bits of fraction. Workgroups meet in kTallies first ones, whose last arrivals meet in one more:
+// atomics on one address follow one another 10 ns apart.
+struct Tally {
+  int frac;
+  __device__ explicit Tally(int blocks) : frac(62 - (32 - __clz(blocks)) - 11) {}
+  __device__ uint64_t one() const { return 1ull << (frac + 11); }
+  __device__ uint64_t fixed(double v) const {                // in range whatever the logits
+    return (uint64_t)llrint(ldexp(fmin(fmax(v, 0.0), 1024.0), frac));
+  }
+  __device__ uint64_t add(uint64_t* tally, uint64_t sum) const {
+    return atomicAdd((unsigned long long*)tally, (unsigned long long)(one() + sum)) + one() + sum;
+  }
+  __device__ bool complete(uint64_t total, int parties) const { return total >> (frac + 11) == (uint64_t)parties; }
+  __device__ uint64_t sum(uint64_t total) const { return total & (one() - 1); }
+};
+
 // ---------------------------------------------------------------------------
 // Slots of one block of tokens per workgroup. SCANNED: base and sums come from route_scan_kernel;
-// otherwise every workgroup adds up the histograms itself. The loss: each workgroup weighs its
-// block's sums of p with the counts and adds the result to a tally (cleared by
-// route_choose_kernel); the one that completes the last writes the loss.
+// otherwise every workgroup adds up the histograms itself. Each workgroup weighs its block's sums
+// of p with the counts for the loss; its atomic starts beside the scan of the offsets and is
+// waited for at the end. Latency bounds it: 16384 tokens, 256 experts, about 6 us of which the
+// histograms' loads take 1, their sums and the offsets' scan 1 each.
 // ---------------------------------------------------------------------------
 constexpr int kSlotThreads = 1024;               // one workgroup a CU fills its waves
+constexpr int kAhead = 18;                       // histogram loads in flight: 270 blocks of 256 experts in one trip
 
 template <bool SCANNED>
 __global__ void __launch_bounds__(kSlotThreads)
 route_slots_kernel(Route a, int blocks) {
   extern __shared__ uint64_t mask[];
   __shared__ int cnt[kMaxExperts + 4], off[kMaxExperts + 1], start[kMaxExperts + 4];
+  __shared__ uint32_t pairs[4][kMaxExperts / 4 + 1];         // sums of 16 bits, columns 4 i and 4 i + 2, 4 i + 1 and
+                                                             // 4 i + 3: over all blocks, then over earlier ones
   __shared__ double red[16][2];
   const int cols = hist_cols(a.experts), blk = blockIdx.x;
   const int64_t t0 = (int64_t)blk * kTok;
+  // what does not depend on the histograms is on its way while they are added up
   const float psum = a.loss && threadIdx.x < a.experts ? a.psum[(int64_t)blk * a.experts + threadIdx.x] : 0.0f;
+  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
+  constexpr int kChoices = kTok * kMaxTopk / kSlotThreads;
+  int choice[kChoices];
+#pragma unroll
+  for (int m = 0; m < kChoices; ++m) {
+    const int i = threadIdx.x + m * kSlotThreads;
+    choice[m] = i < n ? a.topk_idx[t0 * a.topk + i] : -1;
+  }
   for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) mask[e] = 0;
   if (SCANNED) {
     for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
       cnt[e] = a.sums[e];
       start[e] = a.base[(int64_t)blk * cols + e];
     }
+    __syncthreads();
   } else {
     // four columns a thread and dword, summed as two pairs of 16 bits (at most kMaxUnscanned
     // blocks of 64)
-    for (int e = threadIdx.x; e < cols; e += kSlotThreads) cnt[e] = start[e] = 0;
-    __syncthreads();
-    const int quads = cols / 4, groups = kSlotThreads / quads > 0 ? kSlotThreads / quads : 1;
-    for (int i = threadIdx.x; i < quads * groups; i += kSlotThreads) {
-      const int qd = i % quads;
+    for (int i = threadIdx.x; i < cols / 4; i += kSlotThreads) pairs[0][i] = pairs[1][i] = pairs[2][i] = pairs[3][i] = 0;
+    lds_barrier();
+    const int quads = cols / 4, groups = kSlotThreads / quads;         // quads <= 257
+    const int qd = threadIdx.x % quads, first = threadIdx.x / quads;
+    if (first < groups) {
       uint32_t lo = 0, hi = 0, blo = 0, bhi = 0;
-#pragma unroll 8
-      for (int b = i / quads; b < blocks; b += groups) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(a.hist + (int64_t)b * cols + 4 * qd);
-        const uint32_t l = v & 0x00FF00FFu, h = (v >> 8) & 0x00FF00FFu;
-        lo += l;
-        hi += h;
-        blo += b < blk ? l : 0u;
-        bhi += b < blk ? h : 0u;
-      }
-      const uint32_t s[4] = {lo & 0xFFFFu, hi & 0xFFFFu, lo >> 16, hi >> 16};
-      const uint32_t f[4] = {blo & 0xFFFFu, bhi & 0xFFFFu, blo >> 16, bhi >> 16};
+      for (int b0 = first; b0 < blocks; b0 += kAhead * groups) {
+        uint32_t v[kAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {              // integer sums: the order does not matter
-        atomicAdd(&cnt[4 * qd + k], (int)s[k]);
-        atomicAdd(&start[4 * qd + k], (int)f[k]);
+        for (int u = 0; u < kAhead; ++u)                     // past the end: the last one, not counted
+          v[u] = *reinterpret_cast<const uint32_t*>(a.hist + (int64_t)min(b0 + u * groups, blocks - 1) * cols + 4 * qd);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int b = b0 + u * groups;
+          const uint32_t some = b < blocks ? v[u] : 0u;
+          const uint32_t l = some & 0x00FF00FFu, h = (some >> 8) & 0x00FF00FFu;
+          lo += l;
+          hi += h;
+          blo += b < blk ? l : 0u;
+          bhi += b < blk ? h : 0u;
+        }
       }
+      atomicAdd(&pairs[0][qd], lo);                          // integer sums: the order does not matter
+      atomicAdd(&pairs[1][qd], hi);
+      atomicAdd(&pairs[2][qd], blo);
+      atomicAdd(&pairs[3][qd], bhi);
+    }
+    lds_barrier();
+    for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
+      cnt[e] = (int)((pairs[e & 1][e / 4] >> (8 * (e & 2))) & 0xFFFFu);
+      start[e] = (int)((pairs[2 + (e & 1)][e / 4] >> (8 * (e & 2))) & 0xFFFFu);
     }
   }
-  __syncthreads();
-  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
-  for (int i = threadIdx.x; i < n; i += kSlotThreads) {
-    const int e = a.topk_idx[t0 * a.topk + i];
-    if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << (i / a.topk));
-  }
-  padded_offsets(a, cnt, off);
+#pragma unroll
+  for (int m = 0; m < kChoices; ++m)
+    if (choice[m] >= 0)
+      atomicOr((unsigned long long*)&mask[choice[m]], 1ull << ((threadIdx.x + m * kSlotThreads) / a.topk));
+  if (a.loss) loss_terms(a, cnt, [&](int) { return psum; }, red);      // an expert a thread, as cnt above
+  const Tally tally(blocks);
+  const int first_tally = blk % kTallies;
+  uint64_t met = 0;                                          // not waited for before the slots are written
+  padded_offsets(a, cnt, off, [&] {
+    if (a.loss) met = tally.add(a.tally + 8 * (1 + first_tally), tally.fixed(block_loss<kSlotThreads / 64>(a, cnt[a.experts], red)));
+  });
   for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) start[e] += off[e];
-  __syncthreads();
-  write_slots(a, t0, mask, cnt, off, start);
+  lds_barrier();
+#pragma unroll
+  for (int m = 0; m < kChoices; ++m) {
+    const int i = threadIdx.x + m * kSlotThreads;
+    if (i < n) write_slot(a, t0, i, choice[m], mask, start);
+  }
+  write_padding(a, cnt, off);
   if (blk == 0) write_counts(a, cnt, off, cnt[a.experts]);
-  if (!a.loss) return;
-  const double part = block_loss(a, cnt, cnt[a.experts], [&](int) { return psum; }, red);   // an expert a thread
-  if (threadIdx.x != 0) return;
-  // One atomic carries the workgroups' count (above bit `frac` + 11) and the sum so far in fixed
-  // point: loss / coef is at most experts <= 2^10. Integers, so the order does not matter, and
-  // whoever makes the count complete holds the whole sum. 65536 blocks leave 34 bits of fraction.
-  // Workgroups meet in kTallies first ones, whose last arrivals meet in one more: atomics on one
-  // address follow one another 10 ns apart.
-  const int frac = 62 - (32 - __clz(blocks)) - 11;
-  const uint64_t one = 1ull << (frac + 11);
-  auto meet = [&](int tally, uint64_t sum, int parties, uint64_t& total) {
-    const uint64_t add = one + sum;
-    total = atomicAdd((unsigned long long*)(a.tally + 8 * tally), (unsigned long long)add) + add;
-    const bool complete = (total >> (frac + 11)) == (uint64_t)parties;
-    total &= one - 1;
-    return complete;
-  };
-  const int first = blk % kTallies;
-  uint64_t sum = (uint64_t)llrint(ldexp(fmin(fmax(part, 0.0), 1024.0), frac));   // in range whatever the logits
-  if (meet(1 + first, sum, (blocks - first + kTallies - 1) / kTallies, sum) &&
-      meet(0, sum, min(blocks, kTallies), sum))
-    *a.loss = (float)((double)a.coef * ldexp((double)sum, -frac));
+  if (!a.loss || threadIdx.x != kSlotThreads - 1) return;
+  if (!tally.complete(met, (blocks - first_tally + kTallies - 1) / kTallies)) return;
+  met = tally.add(a.tally, tally.sum(met));
+  if (tally.complete(met, min(blocks, kTallies)))
+    *a.loss = (float)((double)a.coef * ldexp((double)tally.sum(met), -tally.frac));
 }
 
 // ---------------------------------------------------------------------------
@@ -617,8 +668,6 @@ route_backward_kernel(const float* __restrict__ logits, int64_t tokens, int expe
 // 624 us; 33 MB with plain ones 21.8 us, non-temporal 22.6). The grid's last workgroups clear the
 // padding slots of dO.
 // ---------------------------------------------------------------------------
-constexpr int kMaxTopk = 32;
-
 template <bool D32, bool STREAM, int W, int NV>
 __global__ void __launch_bounds__(W * 64)
 combine_backward_kernel(const void* __restrict__ dy, const float* __restrict__ o, int64_t total, int64_t tokens,
@@ -708,11 +757,12 @@ void with_choice(int64_t tokens, int64_t experts, int64_t topk, F&& go) {
 
 int64_t route_blocks(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
 
-// Blocks up to which every slots workgroup adds up all histograms itself, which saves the scan's
-// launch; its reads grow with the square of the blocks. (top-8, without and with the scan: 64
-// blocks of 256 experts 16.4 / 17.1 us, 256 blocks 18.9 / 21.6, 512 blocks 31.0 / 32.7, 938 blocks
-// 60.8 / 55.9.)
-constexpr int64_t kMaxUnscanned = 512;
+// Whether every slots workgroup adds up all histograms itself, which saves the scan's launch; its
+// reads grow with the square of the blocks. (us without and with the scan: 256 blocks of 256 experts
+// 16.6 / 18.2, 512 of 256 30.3 / 28.8, 938 of 256 63.0 / 48.3, 512 of 64 17.0 / 18.3, 938 of 64
+// 27.8 / 29.5.) The sums have 16 bits, 64 a block.
+constexpr int64_t kMaxUnscanned = 1023, kUnscannedBytes = 96 << 10;
+bool unscanned(int64_t blocks, int64_t cols) { return blocks <= kMaxUnscanned && blocks * cols <= kUnscannedBytes; }
 
 }  // namespace
 
@@ -727,8 +777,8 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
                         int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss, void* ws,
                         hipStream_t st) {
   const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
-  Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, coef, topk_idx, weights, counts, offsets,
-          row_index, slot_of, loss, nullptr, nullptr, nullptr, nullptr, nullptr};
+  Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, (int)(total / pad), coef, topk_idx, weights, counts,
+          offsets, row_index, slot_of, loss, nullptr, nullptr, nullptr, nullptr, nullptr};
   a.tally = (uint64_t*)ws;
   a.psum = (float*)(a.tally + 8 * (1 + kTallies));
   a.base = (int32_t*)(a.psum + nb * experts);
@@ -743,7 +793,7 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
       hipLaunchKernelGGL((route_choose_kernel<L, NE, KEEP>), dim3((unsigned)nb), dim3(W * 64), lds, st, a);
   });
   if (nb <= 1) return hipGetLastError();
-  if (nb > kMaxUnscanned) {
+  if (!unscanned(nb, cols)) {
     hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((experts + kWaves) / kWaves)), dim3(kThreads), 0, st, a,
                        (int)nb);
     hipLaunchKernelGGL((route_slots_kernel<true>), dim3((unsigned)nb), dim3(kSlotThreads), experts * 8, st, a, (int)nb);

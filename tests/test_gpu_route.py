@@ -105,6 +105,34 @@ def test_route_out_of_domain_logits_stay_in_range():
         assert np.all(np.abs(host(plan.weights)[rest] - w[rest]) <= _weight_bound(finite, idx, w)[rest])
 
 
+@pytest.mark.parametrize("T,G,k,pad", [(65472, 15, 2, 1), (65473, 15, 2, 1),     # 1023 and 1024 blocks of 64
+                                       (24960, 250, 2, 8), (24961, 250, 2, 8)])  # 96 KB of histograms, and more
+def test_route_plan_where_the_histograms_are_summed_elsewhere(T, G, k, pad):
+    z = _logits(T, T, G)
+    z[:, 0] = 50.0                                           # one expert takes every token
+    plan = B.moe_route(dev(z), k, pad=pad, balance_coef=COEF)
+    _check_plan(plan, z, k, pad, None, True, f"{T}x{G}")
+
+
+@pytest.mark.parametrize("T,G,k", [(9, 40, 4), (200, 40, 4), (200, 256, 8), (130, 300, 5)])
+def test_padding_tokens_may_hold_anything(T, G, k):
+    """Inf, NaN and huge logits in the rows that `valid` masks change no bit of the plan, of the
+    loss or of the gradient, forward and backward."""
+    g = inputs.rng(316, T + G)
+    z = _logits(17, T, G)
+    valid = np.ones(T, bool)
+    valid[1::3] = False
+    junk = z.copy()
+    junk[1::3] = g.choice(np.array([np.inf, -np.inf, np.nan, 3e38, -3e38, 1e30], np.float32), junk[1::3].shape)
+    a = B.moe_route(dev(z), k, pad=8, valid=dev(valid), balance_coef=COEF)
+    b = B.moe_route(dev(junk), k, pad=8, valid=dev(valid), balance_coef=COEF)
+    for n in ("topk_idx", "weights", "counts", "offsets", "row_index", "slot_of", "loss"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    d_w, d_loss = dev(g.standard_normal((T, k)).astype(np.float32)), torch.ones(1, device="cuda")
+    da, db = (B.moe_route_backward(dev(x), a.topk_idx, a.weights, a.counts, d_w, d_loss, COEF) for x in (z, junk))
+    assert torch.equal(da, db) and bool((db[1::3] == 0).all())
+
+
 def test_route_nothing_routed_and_no_tokens():
     z = _logits(5, 40, 12)
     plan = B.moe_route(dev(z), 2, pad=4, valid=torch.zeros(40, dtype=torch.bool, device="cuda"), balance_coef=COEF)
