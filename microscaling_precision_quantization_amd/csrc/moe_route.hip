@@ -166,10 +166,10 @@ __device__ __forceinline__ void sum_of_rows(float* v) {
 // topk_idx and weights, leaves the experts' masks in LDS and the waves' sums of p in lp (waves,
 // experts). With L = 16 sixteen waves take all 64 tokens at once, four tokens sharing every
 // instruction; L = 64 serves more experts (NE <= 16) or more choices than a row of lanes holds.
-// A choice moves only as many heads as there are choices to come. (16384 x 256, top-8: 6.9 us with
-// L = 16, 7.7 with all heads moved, 14 with L = 64. Bound by vector instructions and the chain from
-// one choice to the next; lanes that hold four chunks of four experts, so that a load takes whole
-// lines, are no faster.)
+// A choice moves only as many heads as there are choices to come. (16384 x 256, top-8, the whole
+// call: 16.9 us with L = 16, 17.7 without the last KEEP choices unrolled, 25.0 with L = 64. Bound by
+// vector instructions and the chain from one choice to the next; lanes that hold four chunks of four
+// experts, so that a load takes whole lines, are no faster.)
 // ---------------------------------------------------------------------------
 template <int L, int NE, int KEEP>
 __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* lp) {
@@ -740,12 +740,12 @@ void with_experts(int64_t experts, F&& go) {                 // experts per lane
   else go(std::integral_constant<int, 16>{});                // experts <= kMaxExperts
 }
 
-// Lanes per token, experts per lane, sorted ones kept. Few tokens get a wave each, so that no wave
-// holds two: its lanes sort fewer experts (8 tokens, 256 experts: 5.5 us, 8.3 us with 16 lanes).
+// Lanes per token, experts per lane, sorted ones kept. (A wave per token gains nothing where there
+// are few: 8 tokens of 256 experts 5.2 us either way.)
 template <typename F>
-void with_choice(int64_t tokens, int64_t experts, int64_t topk, F&& go) {
+void with_choice(int64_t experts, int64_t topk, F&& go) {
   using std::integral_constant;
-  if (tokens > 16 && experts <= 256 && topk <= 16) {
+  if (experts <= 256 && topk <= 16) {
     if (experts <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
     else if (experts <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{}, integral_constant<int, 8>{});
     else if (topk <= 8) go(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 8>{});
@@ -784,7 +784,7 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
   a.base = (int32_t*)(a.psum + nb * experts);
   a.sums = a.base + nb * cols;
   a.hist = (uint8_t*)(a.sums + cols);
-  with_choice(tokens, experts, topk, [&](auto J, auto N, auto K) {
+  with_choice(experts, topk, [&](auto J, auto N, auto K) {
     constexpr int L = decltype(J)::value, NE = decltype(N)::value, KEEP = decltype(K)::value, W = choose_waves(L, NE);
     const size_t lds = choose_lds((int)experts, W, loss != nullptr);
     if (nb <= 1)
