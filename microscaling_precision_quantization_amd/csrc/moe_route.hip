@@ -560,7 +560,9 @@ route_slots_kernel(Route a, int blocks) {
 
 // ---------------------------------------------------------------------------
 // Backward to the logits: one wave per token at a time; the counts stay in registers over the
-// tokens of a wave, and the next token's logits are on their way while it works on one.
+// tokens of a wave, and the next token's logits are on their way while it works on one. (16384 x
+// 256, top-8, both gradients: 11.0 us, 3.2 TB/s of logits and gradients; four tokens to a wave, 16
+// lanes each, leave too few waves to wait for memory: 13.6.)
 // ---------------------------------------------------------------------------
 template <bool OUT32, int NE>
 __global__ void __launch_bounds__(kThreads)
