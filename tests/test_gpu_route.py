@@ -294,3 +294,22 @@ def test_combine_backward_of_more_tokens_than_one_launch_takes():
     assert torch.equal(d_o[slot_of[:, 0]], (w * dy).bfloat16()) and bool((d_o[:3] == 0).all())
     terms = dy.double() * o[slot_of[:, 0]].double()
     assert bool(((d_w[:, 0].double() - terms.sum(1)).abs() <= 84 * U * terms.abs().sum(1)).all())
+
+
+def test_route_the_most_tokens():
+    """2^22 tokens, the documented limit: 65536 histograms and shares of the loss."""
+    T, G = 1 << 22, 5
+    g = torch.Generator(device="cuda").manual_seed(11)
+    z = torch.randn((T, G), generator=g, device="cuda")
+    plan = B.moe_route(z, 1, balance_coef=COEF)
+    best = torch.sort(z, dim=1, descending=True, stable=True).indices[:, 0]
+    order = torch.sort(best, stable=True).indices
+    counts = torch.bincount(best, minlength=G)
+    assert torch.equal(plan.topk_idx[:, 0].long(), best) and bool((plan.weights == 1).all())
+    assert torch.equal(plan.row_index.long(), order) and torch.equal(plan.slot_of[order, 0], torch.arange(T, device="cuda"))
+    assert torch.equal(plan.counts.long(), torch.cat([counts, counts.sum()[None]]))
+    assert torch.equal(plan.offsets[1:], counts.cumsum(0)) and int(plan.offsets[0]) == 0
+    p = torch.softmax(z.double(), 1).mean(0)
+    ref = COEF * G * float((counts.double() / T * p).sum())
+    far = float((z.max(1).values - z.min(1).values).max())
+    assert abs(float(plan.loss) - ref) <= (2 * far + 120) * U * ref
