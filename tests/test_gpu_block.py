@@ -178,7 +178,7 @@ def test_block_graph_replays_equal_the_eager_step():
 
 def test_many_token_router_graph_replays():
     """The two- and the three-launch plan, captured, with the tally cleared inside the graph."""
-    for tokens in (3000, 33000):
+    for tokens in (3000, 33000, 66000):
         z = torch.empty((tokens, 40), device="cuda")
         plan = B.RoutePlan(tokens, 40, 4, 8, loss=True)
         feeds = [lambda s=s: z.copy_(dev(inputs.rng(322, s).standard_normal((tokens, 40)).astype(np.float32)))
@@ -201,3 +201,37 @@ def test_forward_only_block_matches_the_host_routed_layer():
     ref.forward(block.n)
     assert torch.equal(block.moe.gu, ref.gu) and torch.equal(block.moe.o, ref.o) and torch.equal(block.moe.y, ref.y)
     assert np.allclose(omoe.combine_ref(host(ref.o), r.slot_of, r.topk_w), host(block.moe.y), rtol=1e-4, atol=1e-6)
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_decode_steps_of_the_block(tokens):
+    """A few tokens, as a serving step hands them in: norm and quantizer give the bits of the batch,
+    the experts its outputs, and one plan serves step after step."""
+    d = torch.device("cuda")
+    c = Case(5)
+    full = c.block
+    full.moe.quantize_weights(c.w_gu, c.w_d)
+    full.forward(c.x, c.w_pre, c.w_r, c.w_post, c.gate)
+    step = pipeline.MoeBlockNvfp4(tokens, H, G, I, K, d, gate_mode="channel", branch_scale=0.5, res_scale=0.75)
+    step.moe.quantize_weights(c.w_gu, c.w_d)
+    for at in (0, 7, 64 + tokens):
+        rows = slice(at, at + tokens)
+        out = step.forward(c.x[rows], c.w_pre, c.w_r, c.w_post, c.gate)
+        assert torch.equal(step.n, full.n[rows]) and torch.equal(step.moe.qx, full.moe.qx[rows])
+        _check_plan(step.plan, host(step.logits), K, 1, None, False, "plan")
+        # the GEMMs' tiles differ with the row count; a token's logits may move in their last place
+        ref = norm.gate_residual(_f(c.x[rows]), host(step.moe.y), host(c.w_post), np.broadcast_to(host(c.gate), (tokens, H)),
+                                 EPS, 0.5, 0.75)
+        x = 0.75 * _f(c.x[rows])
+        arith = 8 * U * np.abs(ref - x) + 3 * U * (np.abs(x) + np.abs(ref))
+        assert np.all(np.abs(_f(out) - ref) <= arith + BF16 * (np.abs(ref) + arith))
+        slot_of, w, o = host(step.plan.slot_of), host(step.plan.weights).astype(np.float64), host(step.moe.o)
+        y = np.zeros((tokens, H))
+        for j in range(K):
+            y += w[:, j, None] * o[slot_of[:, j]]
+        assert_gemm_close(host(step.moe.y), y, "combine")
+        same = host((step.plan.topk_idx == full.plan.topk_idx[rows]).all(1))
+        for t in np.flatnonzero(same):                        # the experts' outputs against the batch's
+            got, exp = o[slot_of[t]], host(full.moe.o)[host(full.plan.slot_of)[at + t]]
+            assert_gemm_close(got, exp.astype(np.float64), "experts")
+        assert same.any()
