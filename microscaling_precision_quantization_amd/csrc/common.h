@@ -179,6 +179,7 @@ __device__ __forceinline__ uint32_t cvt_fp4x2_f32(uint32_t old, float a, float b
 // measured on MI355X to lift read-heavy streams (a 268 MB BF16 input read once by the
 // MXFP8 quantizer: 4.5 -> 5.6 TB/s); plain loads otherwise.
 typedef unsigned int u32x4_nt __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_nt __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint4 load_stream16(const void* p) {
   const u32x4_nt v = __builtin_nontemporal_load(static_cast<const u32x4_nt*>(p));
   return make_uint4(v.x, v.y, v.z, v.w);
@@ -188,7 +189,7 @@ __device__ __forceinline__ float4 load_stream16f(const float* p) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// A BF16 output beyond this size leaves with non-temporal stores: half of the memory-side cache,
+// An output beyond this size leaves with non-temporal stores: half of the memory-side cache,
 // which the inputs stream through too; a smaller one stays there for the kernel that reads it next.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 template <bool STREAM>                            // not a run-time flag: the compiler would merge the two stores

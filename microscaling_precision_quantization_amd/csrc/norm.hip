@@ -16,45 +16,79 @@
 namespace mxq {
 namespace {
 
-// Eight consecutive elements of a BF16 or FP32 row, as FP32.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float* f) {
-  if (F32) {
-    const float4 a = load_stream16f((const float*)base + at), b = load_stream16f((const float*)base + at + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    unpack8(load_stream16((const uint16_t*)base + at), f);
+// E consecutive elements of a BF16 or FP32 row in a lane, as loaded. E = 8 is 16 bytes of BF16, but
+// for FP32 two accesses whose lanes lie 32 bytes apart; E = 4 is 16 bytes of FP32 in whole lines, 8 of
+// BF16. A kernel takes 4 where it writes FP32 or its normed rows are (times at the kernels; FP32
+// gradients alone gain nothing).
+template <bool F32, int E = 8>
+struct Raw {
+  static constexpr int N = F32 ? E : E / 2;
+  uint32_t v[N];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint8_t* p = (const uint8_t*)base + at * (F32 ? 4 : 2);
+    if (N == 2) {
+      const u32x2_nt u = __builtin_nontemporal_load((const u32x2_nt*)p);
+      v[0] = u.x;
+      v[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i + 3 < N; i += 4) {
+        const uint4 u = load_stream16(p + 4 * i);
+        v[i] = u.x;
+        v[i + 1] = u.y;
+        v[i + 2] = u.z;
+        v[i + 3] = u.w;
+      }
+    }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0;
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      f[k] = F32 ? __uint_as_float(v[F32 ? k : 0]) : k & 1 ? bf16_hi(v[F32 ? 0 : k / 2]) : bf16_lo(v[F32 ? 0 : k / 2]);
+  }
+};
 
-// STREAM: BF16 leaves with non-temporal stores (two FP32 halves of 16 bytes a lane do not gain).
-template <bool F32, bool STREAM = false>
-__device__ __forceinline__ void store8(void* base, int64_t at, const float* f) {
+// STREAM: non-temporal stores.
+template <bool F32, int E, bool STREAM = false>
+__device__ __forceinline__ void store_row(void* base, int64_t at, const float* f) {
   if (F32) {
-    float4* o = reinterpret_cast<float4*>((float*)base + at);
-    o[0] = make_float4(f[0], f[1], f[2], f[3]);
-    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+    for (int k = 0; k < E; k += 4)
+      store16<STREAM>((float*)base + at + k, make_uint4(__float_as_uint(f[k]), __float_as_uint(f[k + 1]),
+                                                        __float_as_uint(f[k + 2]), __float_as_uint(f[k + 3])));
+  } else if (E == 4) {
+    const u32x2_nt u = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])};
+    u32x2_nt* const to = (u32x2_nt*)((uint16_t*)base + at);
+    if (STREAM) __builtin_nontemporal_store(u, to);
+    else *to = u;
   } else {
     store16<STREAM>((uint16_t*)base + at, make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
-                                                     bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])));
+                                                     bf16x2_rne(f[E - 4], f[E - 3]), bf16x2_rne(f[E - 2], f[E - 1])));
   }
 }
 
-// Eight values read again by every row (weights, channel gates): cached loads. A null
-// pointer stands for ones.
-__device__ __forceinline__ void load8_cached(const float* p, int64_t at, float* f) {
-  if (!p) {
+// Values read again by every row (weights, channel gates): cached loads. A null pointer stands
+// for ones.
+template <int E>
+__device__ __forceinline__ void load_cached(const float* p, int64_t at, float* f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = 1.0f;
-    return;
+  for (int k = 0; k < E; k += 4) {
+    const float4 a = p ? *reinterpret_cast<const float4*>(p + at + k) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    f[k] = a.x;
+    f[k + 1] = a.y;
+    f[k + 2] = a.z;
+    f[k + 3] = a.w;
   }
-  const float4 a = *reinterpret_cast<const float4*>(p + at), b = *reinterpret_cast<const float4*>(p + at + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-__device__ __forceinline__ void zero8(float* f) {
+template <int E>
+__device__ __forceinline__ void zero(float* f) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+  for (int k = 0; k < E; ++k) f[k] = 0.0f;
 }
 
 // One value per wave into LDS, all of them out again after a barrier that waits for LDS only.
@@ -83,30 +117,6 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
   for (int i = 1; i < W; ++i) s = max(s, red[i]);
   return s;
 }
-
-// Eight elements as loaded, BF16 or FP32.
-template <bool F32>
-struct Raw8 {
-  uint4 v[F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    const uint8_t* p = (const uint8_t*)base + at * (F32 ? 4 : 2);
-    v[0] = load_stream16(p);
-    if (F32) v[F32 ? 1 : 0] = load_stream16(p + 16);
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (auto& u : v) u = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(float* f) const {
-    if (F32) {
-      const uint4 a = v[0], b = v[F32 ? 1 : 0];
-      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-      f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-    } else {
-      unpack8(v[0], f);
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t amax8(const uint4& p) {  // two maxima in one dword
   return pk_max_u16(pk_max_u16(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu), pk_max_u16(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
@@ -157,7 +167,7 @@ norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (W == 1 && row >= rows) return;
   auto col = [&](int i) { return 8 * (i * W * 64 + tid); };
-  Raw8<X32> xr[NV];
+  Raw<X32> xr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     xr[i].clear();
@@ -186,7 +196,7 @@ norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld
     if (col(i) < cols) {
       float f[8], w[8];
       xr[i].get(f);
-      load8_cached(weight, col(i), w);
+      load_cached<8>(weight, col(i), w);
       sure = norm8_f32(f, w, (float)r, p[i]) && !wide;
     }
     redo |= __any(!sure) ? 1u << i : 0u;
@@ -195,11 +205,11 @@ norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld
     const int j = __ffs(redo) - 1;
     redo &= redo - 1;
     if (col(j) < cols) {
-      Raw8<X32> again;
+      Raw<X32> again;
       float f[8], w[8];
       again.load(x, row * ld_x + col(j));
       again.get(f);
-      load8_cached(weight, col(j), w);
+      load_cached<8>(weight, col(j), w);
       const uint4 fixed = norm8_f64(f, w, r);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -257,20 +267,21 @@ norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld
 
 // ---------------------------------------------------------------------------
 // Norm after a block: out = res_scale x + branch_scale gate (y r w), one workgroup per row. HBM
-// bounds it: 16384 x 7168, FP32 y, 179 us, 5.2 TB/s.
+// bounds it: 16384 x 7168, BF16 x, FP32 y 165 us, 5.7 TB/s (176 with E = 8; 172 with plain stores
+// and a new output each call); all FP32 178 (262 with E = 8); all BF16 106 (121 with E = 4).
 // GATE: 0 none, 1 one per row, 2 one per column, 3 one per element.
 // ---------------------------------------------------------------------------
-template <bool X32, bool Y32, int GATE, int W, int NV>
+template <bool X32, bool Y32, int GATE, bool STREAM, int W, int NV, int E>
 __global__ void __launch_bounds__(W * 64)
 gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int64_t cols,
                      const float* __restrict__ weight, const float* __restrict__ gate, double eps, float branch_scale,
                      float res_scale, void* __restrict__ out, float* __restrict__ rstd) {
   __shared__ double red[W];
   const int64_t row = blockIdx.x;
-  auto col = [&](int i) { return 8 * (int64_t)(i * W * 64 + (int)threadIdx.x); };
-  Raw8<Y32> yr[NV];
-  Raw8<X32> xr[NV];
-  float f[NV][8];
+  auto col = [&](int i) { return E * (int64_t)(i * W * 64 + (int)threadIdx.x); };
+  Raw<Y32, E> yr[NV];
+  Raw<X32, E> xr[NV];
+  float f[NV][E];
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -284,7 +295,7 @@ gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int
   for (int i = 0; i < NV; ++i) {
     yr[i].get(f[i]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
+    for (int k = 0; k < E; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
   }
   ss = block_sum<W>(ss, red);
   const float r = (float)(1.0 / sqrt(ss / (double)cols + eps));
@@ -294,18 +305,22 @@ gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int
   for (int i = 0; i < NV; ++i) {
     const int64_t e = col(i);
     if (e >= cols) continue;
-    float w[8], g[8], xv[8], o[8];
-    load8_cached(weight, e, w);
-    if (GATE == 2) load8_cached(gate, e, g);
-    if (GATE == 3) load8<true>(gate, row * cols + e, g);
+    float w[E], g[E], xv[E], o[E];
+    load_cached<E>(weight, e, w);
+    if (GATE == 2) load_cached<E>(gate, e, g);
+    if (GATE == 3) {
+      Raw<true, E> gr;
+      gr.load(gate, row * cols + e);
+      gr.get(g);
+    }
     xr[i].get(xv);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < E; ++k) {
       float b = f[i][k] * r * w[k];
       if (GATE >= 2) b *= g[k];
       o[k] = fmaf(b, c, res_scale * xv[k]);
     }
-    store8<X32>(out, row * cols + e, o);
+    store_row<X32, E, STREAM>(out, row * cols + e, o);
   }
 }
 
@@ -317,7 +332,8 @@ gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int
 // column is constant over the rows as the weight is, so it is multiplied into the weight (GATE 0)
 // and one sum, S = sum over the rows of scale d yh, gives both gradients: dw = gate S, dgate = w S.
 // HBM bounds it: 16381 x 7168 with two FP32 gradients and the residual's 300 us, 5.5 TB/s (317 us
-// with plain stores of dx); 8191 x 7168 after a block 110 us, 5.4 TB/s.
+// with plain stores of dx); 8191 x 7168 after a block, FP32 y, 109 us, 5.4 TB/s (119 with E = 8, 117
+// with plain stores); all FP32, 16384 x 7168, 193 us (244 with E = 8).
 // ---------------------------------------------------------------------------
 struct NormGrad {
   const void *d, *d2, *y, *res;
@@ -328,31 +344,31 @@ struct NormGrad {
   float *part, *dgate;                // partial sums (NULL: not wanted); gate gradient (GATE 1 and 3)
 };
 
-template <bool D32, bool Y32, int GATE, bool STREAM, int W, int NV>
+template <bool D32, bool Y32, int GATE, bool STREAM, int W, int NV, int E>
 __global__ void __launch_bounds__(W * 64)
 norm_backward_kernel(NormGrad a) {
   __shared__ float red[2][W], redg[2][W];
   const int64_t cols = a.cols;
-  auto col = [&](int i) { return 8 * (int64_t)(i * W * 64 + (int)threadIdx.x); };
-  float w[NV][8], sum[NV][8];
+  auto col = [&](int i) { return E * (int64_t)(i * W * 64 + (int)threadIdx.x); };
+  float w[NV][E], sum[NV][E];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    zero8(w[i]);
-    zero8(sum[i]);
+    zero<E>(w[i]);
+    zero<E>(sum[i]);
     if (col(i) < cols) {
-      load8_cached(a.weight, col(i), w[i]);
+      load_cached<E>(a.weight, col(i), w[i]);
       if (GATE == 0) {
-        float g[8];
-        load8_cached(a.gate, col(i), g);
+        float g[E];
+        load_cached<E>(a.gate, col(i), g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[i][k] *= g[k];
+        for (int k = 0; k < E; ++k) w[i][k] *= g[k];
       }
     }
   }
   int buf = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
-    Raw8<D32> dr[NV], d2r[NV];
-    Raw8<Y32> yr[NV], rr[NV];
+    Raw<D32, E> dr[NV], d2r[NV];
+    Raw<Y32, E> yr[NV], rr[NV];
     const int64_t at = row * cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -377,25 +393,29 @@ norm_backward_kernel(NormGrad a) {
     }
     const float r = a.rstd[row];
     const float gr = GATE == 1 ? a.gate[row] : 1.0f;
-    float d[NV][8], yh[NV][8], m = 0.0f, dgr = 0.0f;
+    float d[NV][E], yh[NV][E], m = 0.0f, dgr = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t e = col(i);
       dr[i].get(d[i]);
       yr[i].get(yh[i]);
       if (a.d2) {
-        float d2[8];
+        float d2[E];
         d2r[i].get(d2);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[i][k] += d2[k];
+        for (int k = 0; k < E; ++k) d[i][k] += d2[k];
       }
-      float ge[8];
+      float ge[E];
       if (GATE == 3) {
-        zero8(ge);
-        if (e < cols) load8<true>(a.gate, at + e, ge);
+        zero<E>(ge);
+        if (e < cols) {
+          Raw<true, E> gr;
+          gr.load(a.gate, at + e);
+          gr.get(ge);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < E; ++k) {
         yh[i][k] *= r;
         float dn = a.scale * d[i][k];
         if (GATE == 1) {
@@ -411,7 +431,7 @@ norm_backward_kernel(NormGrad a) {
         d[i][k] = dn * w[i][k];
         m = fmaf(d[i][k], yh[i][k], m);
       }
-      if (GATE == 3 && e < cols && a.dgate) store8<true>(a.dgate, at + e, ge);
+      if (GATE == 3 && e < cols && a.dgate) store_row<true, E>(a.dgate, at + e, ge);
     }
     m = block_sum<W>(m, red[buf]) / (float)cols;
     if (GATE == 1 && a.dgate) {
@@ -421,22 +441,22 @@ norm_backward_kernel(NormGrad a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (col(i) >= cols) continue;
-      float o[8];
+      float o[E];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = r * fmaf(-yh[i][k], m, d[i][k]);
+      for (int k = 0; k < E; ++k) o[k] = r * fmaf(-yh[i][k], m, d[i][k]);
       if (a.res) {
-        float rs[8];
+        float rs[E];
         rr[i].get(rs);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = fmaf(a.res_scale, rs[k], o[k]);
+        for (int k = 0; k < E; ++k) o[k] = fmaf(a.res_scale, rs[k], o[k]);
       }
-      store8<Y32, STREAM>(a.dy, at + col(i), o);
+      store_row<Y32, E, STREAM>(a.dy, at + col(i), o);
     }
   }
   if (!a.part) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (col(i) < cols) store8<true>(a.part, (int64_t)blockIdx.x * cols + col(i), sum[i]);
+    if (col(i) < cols) store_row<true, E>(a.part, (int64_t)blockIdx.x * cols + col(i), sum[i]);
 }
 
 // S[c] = sum over `parts` rows of part[., c]: 64 columns per workgroup, its sixteen waves on
@@ -537,22 +557,25 @@ hipError_t launch_norm_quant(int fmt, const void* x, int x32, int64_t rows, int6
 hipError_t launch_gate_residual(const void* x, int x32, const void* y, int y32, int64_t rows, int64_t cols,
                                 const float* weight, const float* gate, int gate_mode, double eps, float branch_scale,
                                 float res_scale, void* out, float* rstd, hipStream_t st) {
+  auto go = [&](auto X, auto Y, auto G, auto L) {
+    with_row(cols, [&](auto N, auto V) {
+      constexpr bool XF = decltype(X)::value, YF = decltype(Y)::value;
+      constexpr int W = decltype(N)::value, GATE = decltype(G)::value, E = XF || YF ? 4 : 8;
+      for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+        const int64_t some = rows - r0 < kLaunchRows ? rows - r0 : kLaunchRows;
+        hipLaunchKernelGGL(
+            (gate_residual_kernel<XF, YF, GATE, decltype(L)::value, W, decltype(V)::value * 8 / E, E>),
+            dim3((unsigned)some), dim3(W * 64), 0, st, (const uint8_t*)x + r0 * cols * (x32 ? 4 : 2),
+            (const uint8_t*)y + r0 * cols * (y32 ? 4 : 2), cols, weight,
+            GATE == 1 ? gate + r0 : GATE == 3 ? gate + r0 * cols : gate, eps, branch_scale, res_scale,
+            (uint8_t*)out + r0 * cols * (x32 ? 4 : 2), rstd ? rstd + r0 : nullptr);
+      }
+    });
+  };
+  const bool large = rows * cols * (x32 ? 4 : 2) > kStreamBytes;
   with_bool(x32, [&](auto X) {
     with_bool(y32, [&](auto Y) {
-      with_gate(gate_mode, [&](auto G) {
-        with_row(cols, [&](auto N, auto V) {
-          constexpr int W = decltype(N)::value, GATE = decltype(G)::value;
-          for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
-            const int64_t some = rows - r0 < kLaunchRows ? rows - r0 : kLaunchRows;
-            hipLaunchKernelGGL(
-                (gate_residual_kernel<decltype(X)::value, decltype(Y)::value, GATE, W, decltype(V)::value>),
-                dim3((unsigned)some), dim3(W * 64), 0, st, (const uint8_t*)x + r0 * cols * (x32 ? 4 : 2),
-                (const uint8_t*)y + r0 * cols * (y32 ? 4 : 2), cols, weight,
-                GATE == 1 ? gate + r0 : GATE == 3 ? gate + r0 * cols : gate, eps, branch_scale, res_scale,
-                (uint8_t*)out + r0 * cols * (x32 ? 4 : 2), rstd ? rstd + r0 : nullptr);
-          }
-        });
-      });
+      with_bool(large, [&](auto L) { with_gate(gate_mode, [&](auto G) { go(X, Y, G, L); }); });
     });
   });
   return hipGetLastError();
@@ -567,12 +590,13 @@ hipError_t launch_norm_backward(const void* d, const void* d2, int d32, const vo
   if (rows > 0) {
     const NormGrad a{d, d2, y, res, rstd, weight, gate, scale, res_scale, rows, cols, dy, sums ? (float*)ws : nullptr,
                      dgate};
-    const bool large = !y32 && rows * cols * 2 > kStreamBytes;
+    const bool large = rows * cols * (y32 ? 4 : 2) > kStreamBytes;
     auto go = [&](auto D, auto Y, auto G, auto L) {
       with_row(cols, [&](auto N, auto V) {
-        constexpr int W = decltype(N)::value;
-        hipLaunchKernelGGL((norm_backward_kernel<decltype(D)::value, decltype(Y)::value, decltype(G)::value,
-                                                 decltype(L)::value, W, decltype(V)::value>),
+        constexpr bool YF = decltype(Y)::value;
+        constexpr int W = decltype(N)::value, E = YF ? 4 : 8;
+        hipLaunchKernelGGL((norm_backward_kernel<decltype(D)::value, YF, decltype(G)::value, decltype(L)::value, W,
+                                                 decltype(V)::value * 8 / E, E>),
                            dim3((unsigned)parts), dim3(W * 64), 0, st, a);
       });
     };
@@ -582,8 +606,7 @@ hipError_t launch_norm_backward(const void* d, const void* d2, int d32, const vo
       else go(D, Y, std::integral_constant<int, 0>{}, L);
     };
     with_bool(d32, [&](auto D) {
-      if (y32) gate_kind(D, std::true_type{}, std::false_type{});
-      else with_bool(large, [&](auto L) { gate_kind(D, std::false_type{}, L); });
+      with_bool(y32, [&](auto Y) { with_bool(large, [&](auto L) { gate_kind(D, Y, L); }); });
     });
   }
   if (sums)

@@ -376,3 +376,29 @@ def test_more_rows_than_one_launch_takes():
         for p in parts:
             o, r = B.rmsnorm_gate_residual(res[p], y[p], w, gate[p].clone(), mode)
             assert torch.equal(out[p], o) and torch.equal(rstd[p], r)
+
+
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_gate_residual_beyond_the_streaming_size(xt, yt):
+    """More than 128 MB of out and dy (non-temporal stores): every row equals a smaller call's."""
+    rows, cols = 16500, 4104
+    g = torch.Generator(device="cuda").manual_seed(12)
+    make = lambda t: torch.randn((rows, cols), generator=g, device="cuda").to(torch.bfloat16 if t == "bf16" else torch.float32)
+    x, y = make(xt), make(yt)
+    w, gate = dev(_weight(3, cols)), torch.rand(cols, generator=g, device="cuda")
+    assert x.numel() * x.element_size() > 128 << 20
+    out, rstd = B.rmsnorm_gate_residual(x, y, w, gate, "channel", branch_scale=0.5, res_scale=0.75)
+    dy, dw, dgate = B.rmsnorm_gate_residual_backward(x, y, rstd, w, gate, "channel", branch_scale=0.5)
+    sums = torch.zeros(2, cols, dtype=torch.float64, device="cuda")
+    for r0 in range(0, rows, 5000):
+        r = slice(r0, min(r0 + 5000, rows))
+        o, s = B.rmsnorm_gate_residual(x[r], y[r], w, gate, "channel", branch_scale=0.5, res_scale=0.75)
+        assert torch.equal(out[r], o) and torch.equal(rstd[r], s)
+        d, a, b = B.rmsnorm_gate_residual_backward(x[r], y[r], rstd[r].clone(), w, gate, "channel", branch_scale=0.5)
+        assert torch.equal(dy[r], d)
+        sums += torch.stack([a, b]).double()
+    yh = y.double() * rstd.double()[:, None]
+    mag = (0.5 * x.double() * yh).abs().sum(0)
+    for got, ref, f in ((dw, sums[0], gate), (dgate, sums[1], w)):
+        # both sides are ordered binary32 sums: at most 33 + 33 terms deep a workgroup and joined wave, and the factors
+        assert bool(((got.double() - ref).abs() <= 2 * 80 * U * mag * f.abs().double()).all())
