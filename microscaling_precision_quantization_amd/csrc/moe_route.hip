@@ -20,7 +20,7 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kTok = 64;                         // tokens of a block (one bit each of a mask)
+constexpr int kMaxTok = 64;                      // most tokens of a block (one bit each of a mask)
 constexpr int kTallies = 16;
 constexpr int kMaxTopk = 32;
 
@@ -51,19 +51,25 @@ __device__ __forceinline__ float softmax_term(float z, float top) {
   return __builtin_amdgcn_exp2f(fmaf(x, 1.44269502e+00f, x * 1.92596299e-08f));
 }
 
-// A lane's NE consecutive logits of a row, NaN past the row. With a whole number of lanes to the
-// row every lane takes wide loads (whatever the row's alignment), else single ones.
+// A lane's NE consecutive logits of a row, NaN past the row, in loads as wide as the row's end
+// allows (whatever its alignment).
 template <int NE>
 __device__ __forceinline__ void load_logits(const float* row, int experts, int lane, float* z) {
-  const int e = lane * NE;
+  constexpr int C = NE < 4 ? NE : 4;
+  const int e = lane * NE, left = experts - e;
 #pragma unroll
   for (int i = 0; i < NE; ++i) z[i] = __builtin_nanf("");
   if (experts % NE == 0) {
-    if (e < experts) __builtin_memcpy(z, row + e, NE * 4);
-  } else {
+    if (left > 0) __builtin_memcpy(z, row + e, NE * 4);
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (e + i < experts) z[i] = row[e + i];
+  for (int i = 0; i < NE; i += C) {
+    if (left >= i + C) __builtin_memcpy(z + i, row + e + i, C * 4);
+    else
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (left > i + k) z[i + k] = row[e + i + k];
   }
 }
 
@@ -94,7 +100,19 @@ __device__ __forceinline__ double max2(double a, double b) {
   return r;
 }
 
-// Reductions over the L lanes of a token (a row of 16, or the wave), in all of them.
+// Reductions over the L lanes of a token (a row of 16, two rows, or the wave), in all of them. The
+// swap of a value with itself leaves both rows of a pair the even row's and the odd row's.
+__device__ __forceinline__ double pair_max(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  return max2(__longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0])),
+              __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1])));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
 template <int L>
 __device__ __forceinline__ double lanes_max(double v) {
   v = max2(v, dpp_f64<0x128, 0xF>(v));
@@ -102,6 +120,7 @@ __device__ __forceinline__ double lanes_max(double v) {
   v = max2(v, dpp_f64<0x122, 0xF>(v));
   v = max2(v, dpp_f64<0x121, 0xF>(v));
   if (L == 16) return v;
+  if (L == 32) return pair_max(v);
   v = max2(v, dpp_f64<0x142, 0xA>(v));           // positive values: the zeros of the other rows lose
   v = max2(v, dpp_f64<0x143, 0xC>(v));
   const uint64_t u = (uint64_t)__double_as_longlong(v);
@@ -113,14 +132,15 @@ __device__ __forceinline__ float lanes_sum(float v) {
   v += dpp_f32<0x128, 0xF>(v);
   v += dpp_f32<0x124, 0xF>(v);
   v += dpp_f32<0x122, 0xF>(v);
-  return v + dpp_f32<0x121, 0xF>(v);
+  v += dpp_f32<0x121, 0xF>(v);
+  return L == 32 ? pair_sum(v) : v;
 }
 
 struct Route {
   const float* logits;
   const uint8_t* valid;
   int64_t tokens, ld, pad, total;
-  int experts, topk, units;                      // units: total / pad
+  int experts, topk, units, tok;                 // units: total / pad; tok: tokens of a block
   float coef;
   int32_t* topk_idx;
   float* weights;
@@ -142,16 +162,18 @@ __host__ __device__ inline int hist_cols(int experts) { return (experts + 4) / 4
 // sums would not fit beside the masks in 64 KB.
 constexpr int choose_waves(int lanes, int ne) { return lanes * ne <= 512 ? 16 : 8; }
 
-// Sums of N values over the wave's four rows, lane by lane, spread over the rows: row r is left
-// with value i + N/4 * (r % 2) + N/2 * (r / 2) in v[i], i < N/4. Each step swaps halves of the
-// wave between two values and adds, so it sums two at once.
-template <int N>
-__device__ __forceinline__ void sum_of_rows(float* v) {
+// Sums of N values over the wave's tokens (four rows, or two halves), lane by lane, spread over
+// them: row r is left with value i + N/4 * (r % 2) + N/2 * (r / 2) in v[i], i < N/4; half h with
+// value i + N/2 * h, i < N/2. Each step swaps halves of the wave between two values and adds, so it
+// sums two at once.
+template <int L, int N>
+__device__ __forceinline__ void sum_of_tokens(float* v) {
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + N / 2]), false, false);
     v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
   }
+  if (L == 32) return;
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + N / 4]), false, false);
@@ -160,23 +182,23 @@ __device__ __forceinline__ void sum_of_rows(float* v) {
 }
 
 // ---------------------------------------------------------------------------
-// Choice of one block of kTok tokens: L lanes to a token, NE experts per lane (expert =
+// Choice of one block of a.tok tokens: L lanes to a token, NE experts per lane (expert =
 // lane * NE + i). Every lane sorts its experts and keeps the first KEEP >= min(topk, NE); then the
 // token's largest first value is chosen topk times and its lane moves on to the next. Writes
 // topk_idx and weights, leaves the experts' masks in LDS and the waves' sums of p in lp (waves,
-// experts). With L = 16 sixteen waves take all 64 tokens at once, four tokens sharing every
-// instruction; L = 64 serves more experts (NE <= 16) or more choices than a row of lanes holds.
-// A choice moves only as many heads as there are choices to come. (16384 x 256, top-8, the whole
-// call: 16.9 us with L = 16, 17.7 without the last KEEP choices unrolled, 25.0 with L = 64. Bound by
-// vector instructions and the chain from one choice to the next; lanes that hold four chunks of four
-// experts, so that a load takes whole lines, are no faster.)
+// experts). With L = 16 sixteen waves take 64 tokens at once, four tokens sharing every
+// instruction; L = 32 and 64 serve more experts (NE <= 16) or more choices than a row of lanes holds.
+// A choice moves only as many heads as there are choices to come. (Top-8, the whole call: 16384 x 256
+// 16.8 us with L = 16, 17.7 without the last KEEP choices unrolled, 25.0 with L = 64; 16384 x 384 24.5
+// with L = 32, 29.8 with 64. Bound by vector instructions and the chain from one choice to the next;
+// lanes that hold four chunks of four experts, so that a load takes whole lines, are no faster.)
 // ---------------------------------------------------------------------------
 template <int L, int NE, int KEEP>
 __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_t* mask, float* lp) {
   constexpr int W = choose_waves(L, NE), GROUPS = W * 64 / L, M = L * NE - 1;
   const int lane = threadIdx.x & (L - 1), w = threadIdx.x >> 6;
   const int group = L == 64 ? __builtin_amdgcn_readfirstlane(w) : threadIdx.x / L;
-  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok);
+  const int n = (int)(a.tokens - t0 < a.tok ? a.tokens - t0 : a.tok);
   int routed = 0;
   float next[NE], acc[NE];
   bool on_next = false;
@@ -202,7 +224,7 @@ __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_
       z[i] = next[i];
       v[i] = ranked(logit_key(z[i]), (uint32_t)((M - (NE - 1) - lane * NE) | (NE - 1 - i)));
     }
-    if (GROUPS < kTok) fetch(tl + GROUPS);
+    if (GROUPS < kMaxTok) fetch(tl + GROUPS);
     sort_desc<NE>(v);
     double head[KEEP + 1], my_v = 0.0;           // lane j: the j-th chosen expert
 #pragma unroll
@@ -246,13 +268,11 @@ __device__ __forceinline__ int choose_tokens(const Route& a, int64_t t0, uint64_
     }
   }
   if (a.loss) {
-    int e0 = lane * NE;
-    if (L == 16) {
-      sum_of_rows<NE>(acc);
-      e0 += NE / 4 * ((threadIdx.x >> 4) & 3);
-    }
+    if (L < 64) sum_of_tokens<L, NE>(acc);
+    constexpr int MINE = NE * L / 64;            // the wave's tokens share out the experts
+    const int e0 = lane * NE + MINE * ((threadIdx.x & 63) / L);
 #pragma unroll
-    for (int i = 0; i < (L == 16 ? NE / 4 : NE); ++i)
+    for (int i = 0; i < MINE; ++i)
       if (e0 + i < a.experts) lp[w * a.experts + e0 + i] = acc[i];
   }
   return routed;
@@ -290,7 +310,7 @@ template <int L, int NE, int KEEP>
 __global__ void __launch_bounds__(choose_waves(L, NE) * 64)
 route_choose_kernel(Route a) {
   extern __shared__ uint64_t mask[];
-  const int routed = choose_block<L, NE, KEEP>(a, (int64_t)blockIdx.x * kTok, mask);
+  const int routed = choose_block<L, NE, KEEP>(a, (int64_t)blockIdx.x * a.tok, mask);
   const float* lp = reinterpret_cast<const float*>(mask + a.experts) + 16;
   const int cols = hist_cols(a.experts);
   for (int e = threadIdx.x; e < cols; e += blockDim.x)
@@ -477,11 +497,11 @@ route_slots_kernel(Route a, int blocks) {
                                                              // 4 i + 3: over all blocks, then over earlier ones
   __shared__ double red[16][2];
   const int cols = hist_cols(a.experts), blk = blockIdx.x;
-  const int64_t t0 = (int64_t)blk * kTok;
+  const int64_t t0 = (int64_t)blk * a.tok;
   // what does not depend on the histograms is on its way while they are added up
   const float psum = a.loss && threadIdx.x < a.experts ? a.psum[(int64_t)blk * a.experts + threadIdx.x] : 0.0f;
-  const int n = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok) * a.topk;
-  constexpr int kChoices = kTok * kMaxTopk / kSlotThreads;
+  const int n = (int)(a.tokens - t0 < a.tok ? a.tokens - t0 : a.tok) * a.topk;
+  constexpr int kChoices = kMaxTok * kMaxTopk / kSlotThreads;
   int choice[kChoices];
 #pragma unroll
   for (int m = 0; m < kChoices; ++m) {
@@ -742,22 +762,42 @@ void with_experts(int64_t experts, F&& go) {                 // experts per lane
   else go(std::integral_constant<int, 16>{});                // experts <= kMaxExperts
 }
 
-// Lanes per token, experts per lane, sorted ones kept. (A wave per token gains nothing where there
-// are few: 8 tokens of 256 experts 5.2 us either way.)
+// Lanes per token, experts per lane, sorted ones kept: as few lanes as hold 16 experts each and the
+// choices. (A wave per token gains nothing where there are few: 8 tokens of 256 experts 5.2 us either
+// way.)
 template <typename F>
 void with_choice(int64_t experts, int64_t topk, F&& go) {
   using std::integral_constant;
+  const integral_constant<int, 16> i16;
+  const integral_constant<int, 32> i32;
+  const integral_constant<int, 8> i8;
+  const integral_constant<int, 4> i4;
   if (experts <= 256 && topk <= 16) {
-    if (experts <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
-    else if (experts <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    else if (topk <= 8) go(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 8>{});
-    else go(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    if (experts <= 64) go(i16, i4, i4);
+    else if (experts <= 128) go(i16, i8, i8);
+    else if (topk <= 8) go(i16, i16, i8);
+    else go(i16, i16, i16);
+  } else if (experts <= 512) {
+    if (experts <= 128) go(i32, i4, i4);
+    else if (experts <= 256) go(i32, i8, i8);
+    else if (topk <= 8) go(i32, i16, i8);
+    else go(i32, i16, i16);
   } else {
-    with_experts(experts, [&](auto N) { go(integral_constant<int, 64>{}, N, N); });
+    go(integral_constant<int, 64>{}, i16, i16);
   }
 }
 
-int64_t route_blocks(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
+// Tokens of a block: as few as keep 256 blocks, one a CU (with the balance loss, 2048 x 256, top-12
+// 15.4 -> 12.5 us, 4096 x 256, top-8 14.1 -> 12.0, 8192 x 256 15.3 -> 13.4, against 64), but few
+// tokens (those that a workgroup's lanes take at once) are one block and one launch.
+int64_t block_tokens(int64_t tokens, int64_t experts) {
+  if (tokens <= (experts <= 256 ? 64 : experts <= 512 ? 32 : 16) || tokens > 8192) return 64;
+  return tokens <= 4096 ? 16 : 32;
+}
+int64_t route_blocks(int64_t tokens, int64_t experts) {
+  const int64_t tok = block_tokens(tokens, experts);
+  return (tokens + tok - 1) / tok;
+}
 
 // Whether every slots workgroup adds up all histograms itself, which saves the scan's launch; its
 // reads grow with the square of the blocks. (us without and with the scan: 256 blocks of 256 experts
@@ -770,7 +810,7 @@ bool unscanned(int64_t blocks, int64_t cols) { return blocks <= kMaxUnscanned &&
 
 // Workspace: tally, psum, base, sums, hist (see Route).
 size_t route_ws_bytes(int64_t tokens, int64_t experts) {
-  const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
+  const int64_t nb = route_blocks(tokens, experts), cols = hist_cols((int)experts);
   return (size_t)(64 * (1 + kTallies) + 4 * nb * experts + 4 * nb * cols + 4 * cols + nb * cols);
 }
 
@@ -778,9 +818,10 @@ hipError_t launch_route(const float* logits, const uint8_t* valid, int64_t token
                         int64_t topk, int64_t pad, int64_t total, float coef, int32_t* topk_idx, float* weights,
                         int32_t* counts, int64_t* offsets, int32_t* row_index, int64_t* slot_of, float* loss, void* ws,
                         hipStream_t st) {
-  const int64_t nb = route_blocks(tokens), cols = hist_cols((int)experts);
-  Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, (int)(total / pad), coef, topk_idx, weights, counts,
-          offsets, row_index, slot_of, loss, nullptr, nullptr, nullptr, nullptr, nullptr};
+  const int64_t nb = route_blocks(tokens, experts), cols = hist_cols((int)experts);
+  Route a{logits, valid, tokens, ld, pad, total, (int)experts, (int)topk, (int)(total / pad),
+          (int)block_tokens(tokens, experts), coef, topk_idx, weights, counts, offsets, row_index, slot_of, loss, nullptr,
+          nullptr, nullptr, nullptr, nullptr};
   a.tally = (uint64_t*)ws;
   a.psum = (float*)(a.tally + 8 * (1 + kTallies));
   a.base = (int32_t*)(a.psum + nb * experts);

@@ -313,3 +313,15 @@ def test_route_the_most_tokens():
     ref = COEF * G * float((counts.double() / T * p).sum())
     far = float((z.max(1).values - z.min(1).values).max())
     assert abs(float(plan.loss) - ref) <= (2 * far + 120) * U * ref
+
+
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 64, 65, 4096, 4097, 8192, 8193])
+@pytest.mark.parametrize("G,k", [(60, 4), (250, 9), (300, 5), (500, 20), (610, 3)])
+def test_route_where_the_blocks_change_size(T, G, k):
+    """Both sides of every size at which tokens are blocked otherwise, masked, with a loss."""
+    if T > 4096 and G > 300:
+        T -= 4032                                            # the large ones with few experts are enough
+    z = _logits(T + G, T, G, dead=1)
+    valid = inputs.rng(318, T + G).uniform(size=T) < 0.8
+    plan = B.moe_route(dev(z), k, pad=8, valid=dev(valid), balance_coef=COEF)
+    _check_plan(plan, z, k, 8, valid, True, f"{T}x{G}")
