@@ -134,8 +134,11 @@ __device__ __forceinline__ uint4 norm8_f64(const float* f, const float* w, doubl
 // relative, so it lies within 3 of its own ulps of f r w; where its low 16 bits differ from
 // 0x8000 by more than 4, both lie on the same side of every BF16 midpoint and rounding v gives
 // the correctly rounded value. False where a value lies closer than that (one vector in 900), is
-// nonzero and below 2^-100, or has a weight beyond 2^20: then binary64 decides. (2^-100 and 2^20
-// keep f r32 a normal number; r itself is checked by the caller.)
+// nonzero and below 2^-100, or has a weight beyond 2^15: then binary64 decides. (2^-100 and 2^15
+// keep f r32 a normal number; r itself is checked by the caller. A zero v is a zero f or w, or a
+// product that underflowed: |f r32| <= 2^-150, and with the weight at most 2^-135, or f r32 was not
+// zero and v's own rounding was, |f r w| <= 1.5 x 2^-150. Both lie below 2^-134, half of BF16's
+// smallest subnormal, so zero is the correctly rounded value.)
 __device__ __forceinline__ bool norm8_f32(const float* f, const float* w, float r32, uint4& out) {
   float v[8], big = 0.0f;
   uint32_t mid = 0xFFFFFFFFu, least = 0xFFFFFFFFu;
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool norm8_f32(const float* f, const float* w, float 
     big = fmaxf(big, fabsf(w[k]));
   }
   out = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-  return mid > (8u << 16) && least >= (27u << 24) && big <= 1048576.0f;
+  return mid > (8u << 16) && least >= (27u << 24) && big <= 32768.0f;
 }
 
 // ---------------------------------------------------------------------------

@@ -402,3 +402,29 @@ def test_gate_residual_beyond_the_streaming_size(xt, yt):
     for got, ref, f in ((dw, sums[0], gate), (dgate, sums[1], w)):
         # both sides are ordered binary32 sums: at most 33 + 33 terms deep a workgroup and joined wave, and the factors
         assert bool(((got.double() - ref).abs() <= 2 * 80 * U * mag * f.abs().double()).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("log_w", [-3, 14, 15, 16, 18, 20, 40])
+def test_norm_quantize_where_a_binary32_product_underflows(log_w, dtype):
+    """A row statistic of one large element, others so small that x r leaves the binary32 range, and
+    weights that bring the product back into BF16's: n is still the correctly rounded value, zeros
+    and signs included."""
+    cols = 512
+    v = np.zeros((4, cols), np.float32)
+    v[:, 0] = [2.0 ** 24, 2.0 ** 40, 2.0 ** 55, 2.0 ** 4]
+    e = np.arange(1, cols)
+    v[:, 1:] = np.where(e % 2, 1, -1) * np.ldexp(1 + (e % 5) / 8, -(90 + e % 60)).astype(np.float32)
+    v[0, 1] = 2.0 ** -133
+    x = dev(v)
+    if dtype == "bf16":
+        bits = inputs.to_bf16_bits(v)
+        x, v = dev_bf16(bits), inputs.bf16_bits_to_float(bits)
+    for w in (np.full(cols, 2.0 ** log_w), np.ldexp(1 + np.arange(cols) % 9 / 16, log_w)):
+        w = w.astype(np.float32)
+        exp = norm.rmsnorm_bf16(v, w, EPS)
+        assert ((exp & 0x7FFF) - 1 < 0x7F).any()            # BF16 subnormals among them
+        assert_bytes_equal(host(B.rmsnorm_quantize(x, dev(w), eps=EPS, fmt=B.BF16)[0]), exp, "n")
+        n, q, s, t, _ = B.rmsnorm_quantize(x, dev(w), eps=EPS, fmt=B.NVFP4)
+        assert_bytes_equal(host(n), exp, "n beside NVFP4")
+        _check_quantized(B.NVFP4, exp, q, s, t, "underflow")
