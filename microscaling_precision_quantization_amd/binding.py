@@ -129,7 +129,9 @@ def _ptr(t):
 
 
 def _stream(dev):
-    """The raw handle of dev's current stream (20 times cheaper than building a Stream object)."""
+    """The raw handle of dev's current stream (20 times cheaper than building a Stream object); dev
+    as torch names devices: a torch.device, a string or an index."""
+    dev = torch.device(dev)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 

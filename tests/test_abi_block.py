@@ -167,3 +167,13 @@ def test_binding_refuses_wrong_buffers():
         B.moe_route_backward(f32(4, 8), i32(4, 2), f32(4, 2), i32(8))
     with pytest.raises(ValueError, match="row_index: shape"):
         B.moe_combine_backward(y, f32(8, 64), torch.zeros((4, 2), dtype=torch.int64), f32(4, 2), i32(7))
+
+
+@pytest.mark.parametrize("name,index", [("cuda", 3), ("cuda:1", 1), (2, 2), (torch.device("cuda"), 3),
+                                        (torch.device("cuda", 1), 1)])
+def test_streams_of_devices_named_in_any_way(monkeypatch, name, index):
+    """A device may be a torch.device, a string or an index, as for torch's own calls; without an
+    index it is the current one."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    assert B._stream(name) == 100 + index

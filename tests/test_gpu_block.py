@@ -235,3 +235,17 @@ def test_decode_steps_of_the_block(tokens):
             got, exp = o[slot_of[t]], host(full.moe.o)[host(full.plan.slot_of)[at + t]]
             assert_gemm_close(got, exp.astype(np.float64), "experts")
         assert same.any()
+
+
+def test_block_on_a_device_named_by_a_string():
+    """The block made with "cuda" for its device, forward and backward: the bits of the same block on
+    torch.device("cuda")."""
+    c = Case(6)
+    c.step()
+    b = pipeline.MoeBlockNvfp4(T, H, G, I, K, "cuda", pad=PAD, balance_coef=COEF, gate_mode="channel",
+                               branch_scale=0.5, res_scale=0.75, backward=True)
+    b.moe.quantize_weights(c.w_gu, c.w_d)
+    out = b.forward(c.x, c.w_pre, c.w_r, c.w_post, c.gate, c.valid)
+    dx = b.backward(c.x, c.d_out, c.d_gu, c.w_pre, c.w_r, c.w_post, c.gate, c.d_loss)
+    assert torch.equal(out, c.block.out) and torch.equal(dx, c.block.dx)
+    assert torch.equal(b.bwd.dw_d, c.block.bwd.dw_d) and torch.equal(b.bwd.dw_gu, c.block.bwd.dw_gu)
