@@ -928,7 +928,8 @@ def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor
               out: RoutePlan | None = None) -> RoutePlan:
     """Top-k routing of FP32 logits (T, G) with its slots, counts and (balance_coef given) balance
     loss. valid: bool or uint8 (T,), False = a padding token that is not routed. `out`: a plan
-    of the same sizes to write into."""
+    of the same sizes to write into, made with a loss if balance_coef is given and without one if
+    not."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits: expected a 2-D tensor (tokens, experts)")
     T, G = logits.shape
@@ -946,6 +947,8 @@ def moe_route(logits: torch.Tensor, topk: int, pad: int = 1, valid: torch.Tensor
         raise ValueError("out: a plan of other sizes")
     elif balance_coef is not None and plan.loss is None:
         raise ValueError("out: a plan without a loss")
+    elif balance_coef is None and plan.loss is not None:     # it would keep an earlier call's
+        raise ValueError("out: a plan with a loss, which a call without balance_coef does not write")
     c.need(plan.offsets, "out", torch.int64, (G + 1,))
     c.done()
     ws = plan.workspace

@@ -177,3 +177,12 @@ def test_streams_of_devices_named_in_any_way(monkeypatch, name, index):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
     assert B._stream(name) == 100 + index
+
+
+def test_a_plan_keeps_no_loss_of_another_call():
+    """A plan with a loss is refused where the call would leave that loss as it was."""
+    plan = B.RoutePlan(4, 8, 2, loss=True, dev="cpu")
+    with pytest.raises(ValueError, match="a plan with a loss"):
+        B.moe_route(torch.zeros(4, 8), 2, out=plan)
+    with pytest.raises(ValueError, match="GPU tensor"):      # with a coefficient, even zero, it is written
+        B.moe_route(torch.zeros(4, 8), 2, out=plan, balance_coef=0.0)
