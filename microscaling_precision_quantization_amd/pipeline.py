@@ -15,6 +15,8 @@ All GEMMs are "TN": C[m, n] = sum_k A[m, k] B[n, k], both operands K-contiguous.
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import binding as B
@@ -141,9 +143,11 @@ class LinearFp8Block:
 # ---------------------------------------------------------------------------
 
 class MoeRoutingDevice:
-    """Device copies of a host routing (offsets may be padded per expert)."""
+    """Device copies of a host routing (offsets may be padded per expert; `pad` is what they are
+    multiples of)."""
 
     def __init__(self, r, dev):
+        self.pad = math.gcd(*map(int, r.offsets))
         self.offsets = torch.from_numpy(r.offsets.astype("int64")).to(dev)
         self.row_index = torch.from_numpy(r.row_index.astype("int32")).to(dev)
         self.slot_of = torch.from_numpy(r.slot_of.astype("int64")).to(dev)
@@ -254,10 +258,15 @@ class MoeDequantBackward:
     transposed BF16 dequantization, the BF16_NVFP4T format); with fused_weights=False
     they read BF16 transposes written by dequantize_transposed first. The wgrads read dO and
     dGU as they are (slot-major, K-major A, vary_k=2); their other operands, the NVFP4
-    activations, are dequantized into K-contiguous BF16 transposes by dequantize_transposed."""
+    activations, are dequantized into K-contiguous BF16 transposes by dequantize_transposed.
+    Every expert's slots begin at a multiple of 8 (16 bytes of BF16 along K)."""
 
     def __init__(self, fwd: MoeNvfp4, fused_weights: bool = True):
         f = fwd
+        # the weight-gradient GEMMs see the offsets on the device only, and leave dW as it was where
+        # one is not a multiple of 8
+        if getattr(f.r, "pad", 0) % 8:
+            raise ValueError(f"routing: slot offsets in steps of {f.r.pad}, the backward needs a multiple of 8")
         dev, G, H, I, S = f.dev, f.G, f.H, f.I, f.S
         self.f = f
         self.fused = fused_weights
@@ -330,19 +339,23 @@ class MoeBlockNvfp4:
         y = sum_j w_j E_j(n)        MoeNvfp4 on the plan
         out = res_scale x + branch_scale gate (RMSNorm(y) w_post)
     The plan's slots are a fixed number (every expert's range padded to `pad`, the rest dealt
-    out), so nothing waits for the counts and a step can be captured in a HIP graph."""
+    out), so nothing waits for the counts and a step can be captured in a HIP graph. backward=True
+    needs pad and tokens to be multiples of 8 and experts of 16 (they are reduction axes of its
+    weight gradients and of the router's GEMMs)."""
 
     def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, pad: int = 1,
                  balance_coef: float | None = None, gate_mode: str = "none", branch_scale: float = 1.0,
                  res_scale: float = 1.0, eps: float = 1e-6, backward: bool = False):
         T, H, G = tokens, hidden, experts
+        if backward and (pad % 8 or T % 8 or G % 16):
+            raise ValueError(f"backward: pad {pad}, {T} tokens, {G} experts; expected multiples of 8, 8 and 16")
         self.topk, self.pad, self.coef, self.eps = topk, pad, balance_coef, eps
         self.gate_mode, self.branch_scale, self.res_scale = gate_mode, branch_scale, res_scale
         self.plan = B.RoutePlan(T, G, topk, pad, loss=balance_coef is not None, dev=dev)
         self.moe = MoeNvfp4(T, H, G, inter, self.plan, dev, keep_h=False)
         self.n, self.logits, self.out = _bf16((T, H), dev), _f32((T, G), dev), _bf16((T, H), dev)
         self.rstd_pre, self.rstd_post = _f32((T,), dev), _f32((T,), dev)
-        if backward:                                               # needs pad % 8 == tokens % 8 == experts % 16 == 0
+        if backward:
             self.bwd = MoeDequantBackward(self.moe)
             self.d_y, self.d_o, self.d_w = _f32((T, H), dev), _bf16((self.plan.slots, H), dev), _f32((T, topk), dev)
             self.dw_post = _f32((H,), dev)

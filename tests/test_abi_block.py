@@ -186,3 +186,31 @@ def test_a_plan_keeps_no_loss_of_another_call():
         B.moe_route(torch.zeros(4, 8), 2, out=plan)
     with pytest.raises(ValueError, match="GPU tensor"):      # with a coefficient, even zero, it is written
         B.moe_route(torch.zeros(4, 8), 2, out=plan, balance_coef=0.0)
+
+
+def test_backward_refuses_slots_that_its_weight_gradients_would_leave_out():
+    """The weight gradients' GEMMs reduce over slots that begin at multiples of 8; at any other offset
+    they write nothing, so such a block, or such a routing from the host, is refused when it is made."""
+    from types import SimpleNamespace
+
+    import numpy as np
+
+    from microscaling_precision_quantization_amd import inputs, pipeline
+    make = lambda T=192, G=16, pad=32: pipeline.MoeBlockNvfp4(T, 64, G, 32, 3, "cpu", pad=pad, backward=True)
+    for kw in (dict(pad=1), dict(pad=4), dict(pad=12), dict(T=190), dict(G=24)):
+        with pytest.raises(ValueError, match="expected multiples of 8, 8 and 16"):
+            make(**kw)
+    logits = np.random.default_rng(0).standard_normal((64, 16)).astype(np.float32)
+    fwd = lambda r: SimpleNamespace(r=r, dev="cpu", G=16, H=64, I=32, S=r.slots)
+    for pad in (1, 4, 12):                                   # 12: some offset is no multiple of 8
+        r = pipeline.MoeRoutingDevice(inputs.route_topk(logits, 3, pad=pad), "cpu")
+        assert any(int(v) % 8 for v in r.offsets)
+        with pytest.raises(ValueError, match="multiple of 8"):
+            pipeline.MoeDequantBackward(fwd(r))
+        with pytest.raises(ValueError, match="multiple of 8"):
+            pipeline.MoeDequantBackward(fwd(B.RoutePlan(64, 16, 3, pad, dev="cpu")))
+    for pad in (8, 32):
+        r = pipeline.MoeRoutingDevice(inputs.route_topk(logits, 3, pad=pad), "cpu")
+        assert pipeline.MoeDequantBackward(fwd(r)).dw_d.shape == (16, 64, 32)
+        assert make(pad=pad).bwd.dw_gu.shape == (16, 64, 64)
+    assert pipeline.MoeBlockNvfp4(5, 64, 3, 32, 2, "cpu").plan.pad == 1           # forward only: any sizes
