@@ -214,3 +214,12 @@ def test_backward_refuses_slots_that_its_weight_gradients_would_leave_out():
         assert pipeline.MoeDequantBackward(fwd(r)).dw_d.shape == (16, 64, 32)
         assert make(pad=pad).bwd.dw_gu.shape == (16, 64, 64)
     assert pipeline.MoeBlockNvfp4(5, 64, 3, 32, 2, "cpu").plan.pad == 1           # forward only: any sizes
+
+
+def test_combine_backward_without_choices_or_slots():
+    """topk = 0 takes no dy, slot_of or weights, whatever the tokens; the slots' own buffers are
+    still required."""
+    f = lambda S, o=P, row=P, d_o=P, T=4: B.lib().moe_combine_backward(None, F32, o, S, T, 0, 64, None, None, row, d_o,
+                                                                       None, None)
+    assert f(0) == 0 and f(0, T=0) == 0
+    assert f(8, o=None) == 1 and f(8, row=None) == 1 and f(8, d_o=None) == 1

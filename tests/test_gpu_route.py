@@ -325,3 +325,22 @@ def test_route_where_the_blocks_change_size(T, G, k):
     valid = inputs.rng(318, T + G).uniform(size=T) < 0.8
     plan = B.moe_route(dev(z), k, pad=8, valid=dev(valid), balance_coef=COEF)
     _check_plan(plan, z, k, 8, valid, True, f"{T}x{G}")
+
+
+def test_combine_backward_without_choices_reads_no_gradient():
+    """topk = 0: the C ABI takes a null dy then, and only the padding slots are cleared."""
+    S, H = 70, 2048
+    row_index = torch.zeros(S, dtype=torch.int32, device="cuda")
+    row_index[::3] = -1
+    o = torch.ones((S, H), device="cuda")
+    d_o = torch.full((S + 2, H), 85.0, dtype=torch.bfloat16, device="cuda")
+    for tokens in (0, 5):
+        d_o.fill_(85.0)
+        status = B.lib().moe_combine_backward(None, B.OUT_F32, B._ptr(o), S, tokens, 0, H, None, None, B._ptr(row_index),
+                                              B._ptr(d_o[1:-1]), None, B._stream(o.device))
+        assert status == 0
+        assert bool((d_o[1:-1][row_index < 0] == 0).all()) and bool((d_o[1:-1][row_index >= 0] == 85).all())
+        assert bool((d_o[0] == 85).all()) and bool((d_o[-1] == 85).all())
+    out = B.moe_combine_backward(torch.ones((5, H), device="cuda"), o, torch.empty((5, 0), dtype=torch.int64, device="cuda"),
+                                 torch.empty((5, 0), device="cuda"), row_index, out=(d_o[1:-1], torch.empty((5, 0), device="cuda")))
+    assert out[1].shape == (5, 0)
