@@ -788,7 +788,7 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
       total_slots > kMaxGridBlocks / 2)
     return MXQ_ERR_SHAPE;
   if (topk == 0) tokens = 0;                       // no choices: dy is not read, the padding slots are cleared
-  if (tokens == 0 && total_slots == 0) return MXQ_OK;
+  if (tokens == 0 && (total_slots == 0 || hidden == 0)) return MXQ_OK;
   if ((tokens > 0 && (!dy || !slot_of || !weights || !d_weights)) ||
       (total_slots > 0 && hidden > 0 && (!o_slots || !row_index || !d_o_bf16)))
     return MXQ_ERR_NULL;

@@ -870,7 +870,8 @@ hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int6
   using std::integral_constant;
   const bool large = total * hidden * 2 > kStreamBytes;
   // a grid holds fewer than 2^32 threads (1024 to a token at most): more tokens take more launches,
-  // and the last one clears the padding slots
+  // and the last one clears the padding slots (rows of no elements: none, row_index is not read)
+  const int64_t clearing = hidden > 0 ? (total + 63) / 64 : 0;
   constexpr int64_t kLaunchTokens = (int64_t)1 << 21;
   auto go = [&](auto D, auto N, auto V) {
     constexpr int W = decltype(N)::value, NV = decltype(V)::value;
@@ -880,7 +881,7 @@ hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int6
     do {
       const bool last = tokens - t0 <= kLaunchTokens;
       const int64_t some = last ? tokens - t0 : kLaunchTokens;
-      const dim3 grid((unsigned)(some + (last ? (total + 63) / 64 : 0)));
+      const dim3 grid((unsigned)(some + (last ? clearing : 0)));
       hipLaunchKernelGGL(kernel, grid, dim3(W * 64), 0, st, (const uint8_t*)dy + t0 * hidden * (DF ? 4 : 2), o, total,
                          some, (int)topk, hidden, slot_of + t0 * topk, weights + t0 * topk, row_index,
                          (uint16_t*)d_o, d_weights + t0 * topk);

@@ -223,3 +223,10 @@ def test_combine_backward_without_choices_or_slots():
                                                                        None, None)
     assert f(0) == 0 and f(0, T=0) == 0
     assert f(8, o=None) == 1 and f(8, row=None) == 1 and f(8, d_o=None) == 1
+
+
+def test_combine_backward_of_rows_without_elements():
+    """hidden = 0 takes no slot buffers, and without tokens there is nothing to launch."""
+    f = lambda T, k, dy=P: B.lib().moe_combine_backward(dy, F32, None, 8, T, k, 0, P, P, None, None, P, None)
+    assert f(0, 2) == 0 and f(4, 0) == 0
+    assert f(4, 2, dy=None) == 1

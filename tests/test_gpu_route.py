@@ -344,3 +344,13 @@ def test_combine_backward_without_choices_reads_no_gradient():
     out = B.moe_combine_backward(torch.ones((5, H), device="cuda"), o, torch.empty((5, 0), dtype=torch.int64, device="cuda"),
                                  torch.empty((5, 0), device="cuda"), row_index, out=(d_o[1:-1], torch.empty((5, 0), device="cuda")))
     assert out[1].shape == (5, 0)
+
+
+def test_combine_backward_of_rows_without_elements():
+    """hidden = 0: the C ABI takes null slot buffers then; the weights' gradients are sums of nothing."""
+    slot_of = torch.zeros((5, 2), dtype=torch.int64, device="cuda")
+    w, d_w, dy = torch.ones((5, 2), device="cuda"), torch.full((7, 2), 85.0, device="cuda"), torch.ones(8, device="cuda")
+    status = B.lib().moe_combine_backward(B._ptr(dy), B.OUT_F32, None, 300, 5, 2, 0, B._ptr(slot_of), B._ptr(w), None,
+                                          None, B._ptr(d_w[1:-1]), B._stream(dy.device))
+    assert status == 0
+    assert bool((d_w[1:-1] == 0).all()) and bool((d_w[0] == 85).all()) and bool((d_w[-1] == 85).all())
