@@ -114,10 +114,11 @@ size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols) {
 
 int64_t mxq_route_slots(int64_t tokens, int64_t experts, int64_t topk, int64_t pad) {
   if (tokens < 0 || experts < 1 || topk < 1 || pad < 1 || tokens > kMaxRouteTokens || topk > kMaxTopk ||
-      experts > kMaxExperts || pad > kMaxGridBlocks)
+      topk > experts || experts > kMaxExperts || pad > kMaxGridBlocks)
     return -1;
   const int64_t n = tokens * topk, used = n < experts ? n : experts;
-  return (n + used * (pad - 1)) / pad * pad;
+  const int64_t least = (n + used * (pad - 1)) / pad * pad;
+  return least > kMaxGridBlocks ? -1 : least;
 }
 
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {

@@ -230,3 +230,18 @@ def test_combine_backward_of_rows_without_elements():
     f = lambda T, k, dy=P: B.lib().moe_combine_backward(dy, F32, None, 8, T, k, 0, P, P, None, None, P, None)
     assert f(0, 2) == 0 and f(4, 0) == 0
     assert f(4, 2, dy=None) == 1
+
+
+def test_route_slots_of_sizes_that_the_router_refuses():
+    """-1 for every size that moe_route answers with a shape error, whatever total it is given, and a
+    plan of such a size is not made."""
+    f = B.lib().mxq_route_slots
+    for T, G, k, pad in ((4, 8, 9, 1), (10, 4, 8, 1), (4, 8, 0, 1), (4, 0, 1, 1), (4, 2000, 2, 1), (-1, 8, 2, 1),
+                         (4, 8, 2, 0), ((1 << 22) + 1, 8, 2, 1), (4, 64, 33, 1),
+                         (1 << 20, 1024, 2, 1 << 21), (8, 8, 1, 1 << 30)):    # the last two: 2^31 slots and more
+        assert f(T, G, k, pad) == -1, (T, G, k, pad)
+        total = (1 << 31) - 1 - ((1 << 31) - 1) % max(pad, 1)
+        assert B.lib().moe_route(P, None, T, G, max(G, 1), k, pad, total, 0.1, P, P, P, P, P, P, P, P, 1 << 40, None) == 2
+        with pytest.raises(ValueError, match="no routing"):
+            B.RoutePlan(T, G, k, pad, dev="cpu")
+    assert f(4, 8, 8, 1) == 32 and f(0, 8, 8, 4) == 0 and f(1, 1, 1, 0x7FFFFFFF) == 0x7FFFFFFF
