@@ -624,7 +624,8 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
  *   rstd   : FP32 (rows), r rounded, NULL = not written.
  *   Requires eps > 0 (MXQ_ERR_FORMAT), cols % 32 == 0 (MXFP8, MXFP4), % 16 (NVFP4), % 8
  *   (BF16), and cols <= 16384 (a row is held in the registers of one workgroup). Outputs must
- *   not overlap x.
+ *   not overlap x. Here and in the three calls below, rows = 0 or cols = 0 writes no row's output
+ *   (a row without elements has no mean).
  * ------------------------------------------------------------------------- */
 mxq_status rmsnorm_quantize(mxq_format fmt, const void* x, mxq_out_dtype x_dtype, int64_t rows, int64_t cols,
                             int64_t ld_x, const float* weight, double eps, void* n_bf16, void* q, void* s, float* t,

@@ -737,6 +737,8 @@ def _float_dtype(t, name: str) -> int:
         raise ValueError(f"{name}: expected a bfloat16 or float32 tensor")
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D tensor (rows, cols)")
+    if t.shape[1] == 0:                                      # the mean over a row is undefined
+        raise ValueError(f"{name}: rows without elements")
     return OUT_F32 if t.dtype == torch.float32 else OUT_BF16
 
 

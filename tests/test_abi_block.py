@@ -245,3 +245,15 @@ def test_route_slots_of_sizes_that_the_router_refuses():
         with pytest.raises(ValueError, match="no routing"):
             B.RoutePlan(T, G, k, pad, dev="cpu")
     assert f(4, 8, 8, 1) == 32 and f(0, 8, 8, 4) == 0 and f(1, 1, 1, 0x7FFFFFFF) == 0x7FFFFFFF
+
+
+def test_rows_without_elements_are_refused():
+    """They have no mean: no statistic, and no gradient of a token's gate, is handed back for them."""
+    x, y, one = torch.zeros((4, 0), dtype=torch.bfloat16), torch.zeros((4, 0)), torch.zeros(4)
+    empty = torch.zeros(0)
+    for call in (lambda: B.rmsnorm_quantize(x, fmt=B.BF16), lambda: B.rmsnorm_backward(y, x, one, empty),
+                 lambda: B.rmsnorm_gate_residual(x, y), lambda: B.rmsnorm_gate_residual_backward(x, y, one, None, one, "token"),
+                 lambda: B.moe_combine_backward(y, y, torch.zeros((4, 1), dtype=torch.int64), torch.zeros((4, 1)),
+                                                torch.zeros(4, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="rows without elements"):
+            call()
