@@ -622,7 +622,8 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
  *   n_bf16 : BF16 (rows, cols), NULL = not written (required for MXQ_BF16).
  *   q, s, t: as the format's row quantizer writes them (t: MXQ_NVFP4 only).
  *   rstd   : FP32 (rows), r rounded, NULL = not written.
- *   Requires eps > 0 (MXQ_ERR_FORMAT), cols % 32 == 0 (MXFP8, MXFP4), % 16 (NVFP4), % 8
+ *   Requires eps > 0, with rstd eps >= 2^-252 so that no row's r passes the binary32 range
+ *   (MXQ_ERR_FORMAT), cols % 32 == 0 (MXFP8, MXFP4), % 16 (NVFP4), % 8
  *   (BF16), and cols <= 16384 (a row is held in the registers of one workgroup). Outputs must
  *   not overlap x. Here and in the three calls below, rows = 0 or cols = 0 writes no row's output
  *   (a row without elements has no mean).
@@ -657,7 +658,8 @@ mxq_status rmsnorm_backward(const void* dn, const void* dn2, mxq_out_dtype dn_dt
  *   out = res_scale x + branch_scale gate (y r w), in binary32, rounded once to x_dtype.
  *   x, out : (rows, cols) x_dtype; y: (rows, cols) y_dtype; weight: FP32 (cols), NULL = ones.
  *   gate   : FP32, laid out as gate_mode says (NULL with MXQ_GATE_NONE).
- *   rstd   : FP32 (rows), NULL = not written. Requires eps > 0, cols % 8 == 0, cols <= 16384.
+ *   rstd   : FP32 (rows), NULL = not written. Requires eps >= 2^-252 (MXQ_ERR_FORMAT),
+ *   cols % 8 == 0, cols <= 16384.
  *   out must not overlap an input.
  * ------------------------------------------------------------------------- */
 mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const void* y, mxq_out_dtype y_dtype,

@@ -643,6 +643,9 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
 namespace {
 inline bool is_dtype(mxq_out_dtype d) { return d == MXQ_OUT_BF16 || d == MXQ_OUT_F32; }
 inline bool positive(double v) { return v > 0.0 && v <= 1.79769313486231570815e308; }   // finite, not NaN
+// From here on (mean + eps)^(-1/2) <= 2^126 is a binary32 number whatever the row: an infinite one
+// would turn a row of zeros into NaN.
+constexpr double kLeastEps = 0x1p-252;
 
 mxq_status gate_check(const float* gate, mxq_gate_mode mode) {
   if (mode != MXQ_GATE_NONE && mode != MXQ_GATE_TOKEN && mode != MXQ_GATE_CHANNEL && mode != MXQ_GATE_FULL)
@@ -664,7 +667,7 @@ mxq_status rmsnorm_quantize(mxq_format fmt, const void* x, mxq_out_dtype x_dtype
                             float* rstd, void* stream) {
   if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
   if ((fmt != MXQ_MXFP8 && fmt != MXQ_NVFP4 && fmt != MXQ_BF16 && fmt != MXQ_MXFP4) || !is_dtype(x_dtype) ||
-      !positive(eps))
+      !positive(eps) || (rstd && eps < kLeastEps))
     return MXQ_ERR_FORMAT;
   if (rows == 0 || cols == 0) return MXQ_OK;
   if (!x || (fmt == MXQ_BF16 ? !n_bf16 : !q || !s) || (fmt == MXQ_NVFP4 && !t)) return MXQ_ERR_NULL;
@@ -702,7 +705,7 @@ mxq_status rmsnorm_gate_residual(const void* x, mxq_out_dtype x_dtype, const voi
                                  float branch_scale, float res_scale, int64_t rows, int64_t cols, void* out,
                                  float* rstd, void* stream) {
   if (rows < 0 || cols < 0) return MXQ_ERR_SHAPE;
-  if (!is_dtype(x_dtype) || !is_dtype(y_dtype) || !positive(eps)) return MXQ_ERR_FORMAT;
+  if (!is_dtype(x_dtype) || !is_dtype(y_dtype) || !positive(eps) || eps < kLeastEps) return MXQ_ERR_FORMAT;
   if (rows == 0 || cols == 0) return MXQ_OK;
   const mxq_status g = gate_check(gate, gate_mode);
   if (g != MXQ_OK) return g;

@@ -257,3 +257,12 @@ def test_rows_without_elements_are_refused():
                                                 torch.zeros(4, dtype=torch.int32))):
         with pytest.raises(ValueError, match="rows without elements"):
             call()
+
+
+def test_eps_that_would_leave_the_binary32_range():
+    """Below 2^-252 the statistic of a row of zeros passes the binary32 range: refused wherever it is
+    held in binary32."""
+    for eps, status in ((2.0 ** -253, 4), (1e-80, 4), (5e-324, 4), (2.0 ** -252, 1), (1e-30, 1)):     # 1: x is null
+        assert B.lib().rmsnorm_quantize(B.BF16, None, BF, 4, 64, 64, P, eps, P, None, None, None, P, None) == status
+        assert B.lib().rmsnorm_gate_residual(None, BF, P, F32, P, None, 0, eps, 1.0, 1.0, 4, 64, P, P, None) == status
+    assert B.lib().rmsnorm_quantize(B.BF16, None, BF, 4, 64, 64, P, 1e-80, P, None, None, None, None, None) == 1

@@ -428,3 +428,23 @@ def test_norm_quantize_where_a_binary32_product_underflows(log_w, dtype):
         n, q, s, t, _ = B.rmsnorm_quantize(x, dev(w), eps=EPS, fmt=B.NVFP4)
         assert_bytes_equal(host(n), exp, "n beside NVFP4")
         _check_quantized(B.NVFP4, exp, q, s, t, "underflow")
+
+
+def test_rows_of_zeros_at_the_smallest_eps():
+    """eps = 2^-252: r = 2^126 for a row of zeros, whose normed row is zero and whose gradients are
+    those of the formula; a smaller eps only without a row statistic."""
+    eps, cols = 2.0 ** -252, 64
+    x, y = torch.full((3, cols), 3.0, device="cuda"), torch.zeros((3, cols), device="cuda")
+    y[1, 0] = 1.0
+    w = torch.full((cols,), 2.0, device="cuda")
+    out, rstd = B.rmsnorm_gate_residual(x, y, w, eps=eps)
+    want = x.clone()
+    want[1, 0] += 16.0                                       # 1 / sqrt(1 / 64) times the weight
+    assert torch.equal(out, want) and rstd.tolist() == [2.0 ** 126, 8.0, 2.0 ** 126]
+    n, _, _, _, rstd = B.rmsnorm_quantize(y, w, eps=eps, fmt=B.BF16)
+    assert torch.equal(n, (want - x).bfloat16()) and rstd.tolist() == [2.0 ** 126, 8.0, 2.0 ** 126]
+    dx, dw = B.rmsnorm_backward(torch.full_like(y, 2.0 ** -100), y, rstd, w)
+    assert bool((dx[0] == 2.0 ** 27).all()) and bool(torch.isfinite(dx).all()) and dw[1] == 0
+    none = torch.empty((3, cols), dtype=torch.bfloat16, device="cuda")
+    B.rmsnorm_quantize(y, w, eps=1e-200, fmt=B.BF16, out=(none, None, None, None, None))
+    assert torch.equal(none, n)
