@@ -137,7 +137,7 @@ def _stream(dev):
 
 def _call(fn: str, dev, *args):
     """One C-ABI call on dev's current stream (the last argument), with dev the current device:
-    a kernel is launched on the device that is current, whatever its stream."""
+    a kernel is launched on the device that is current, whatever its stream. dev: a tensor's."""
     if dev.index == torch._C._cuda_getDevice():
         _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
     else:
@@ -250,8 +250,7 @@ def quantize_mxfp8(x: torch.Tensor, rowwise: bool = True, colwise: bool = True, 
         s_row = _u8((R, C // 32), dev) if rowwise else None
         q_col = _u8((C, R), dev) if colwise else None
         s_col = _u8((C, R // 32), dev) if colwise else None
-    _check("quantize_mxfp8", lib().quantize_mxfp8(_ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row),
-                                                  _ptr(q_col), _ptr(s_col), _stream(dev)))
+    _call("quantize_mxfp8", dev, _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col))
     return q_row, s_row, q_col, s_col
 
 
@@ -271,8 +270,7 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = True, 
         s_row = _u8((R, C // 32), dev) if rowwise else None
         q_col = _u8((C, R // 2), dev) if colwise else None
         s_col = _u8((C, R // 32), dev) if colwise else None
-    _check("quantize_mxfp4", lib().quantize_mxfp4(_ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row),
-                                                  _ptr(q_col), _ptr(s_col), _stream(dev)))
+    _call("quantize_mxfp4", dev, _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col))
     return q_row, s_row, q_col, s_col
 
 
@@ -289,8 +287,7 @@ def quantize_fp8_block_act(x: torch.Tensor, rowwise: bool = True, colwise: bool 
     else:
         q_row, s_row = (_u8((R, C), dev), f32(R, C // 128)) if rowwise else (None, None)
         q_col, s_col = (_u8((C, R), dev), f32(C, R // 128)) if colwise else (None, None)
-    _check("quantize_fp8_block_act", lib().quantize_fp8_block_act(
-        _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col), _stream(dev)))
+    _call("quantize_fp8_block_act", dev, _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col))
     return q_row, s_row, q_col, s_col
 
 
@@ -308,8 +305,8 @@ def quantize_fp8_block_weight(x: torch.Tensor, rowwise: bool = True, colwise: bo
         s_row = f32(R // 128, C // 128) if rowwise else None
         q_col = _u8((C, R), dev) if colwise else None
         s_col = f32(C // 128, R // 128) if colwise else None
-    _check("quantize_fp8_block_weight", lib().quantize_fp8_block_weight(
-        _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col), _stream(dev)))
+    _call("quantize_fp8_block_weight", dev, _ptr(x), R, C, x.stride(0), _ptr(q_row), _ptr(s_row), _ptr(q_col),
+          _ptr(s_col))
     return q_row, s_row, q_col, s_col
 
 
@@ -344,7 +341,7 @@ def _mx_multi(fn: str, xs, outs):
         q_row, s_row, q_col, s_col = o
         arr[i] = _Mxfp8Tensor(x.data_ptr(), x.shape[0], x.shape[1], x.stride(0),
                               *(None if t is None else t.data_ptr() for t in (q_row, s_row, q_col, s_col)))
-    _check(fn, getattr(lib(), fn)(ctypes.cast(arr, _c_void_p), n, _stream(xs[0].device)))
+    _call(fn, xs[0].device, ctypes.cast(arr, _c_void_p), n)
     return outs
 
 
@@ -367,8 +364,7 @@ def quantize_nvfp4_per_token(x: torch.Tensor):
     dev = x.device
     q, s = _u8((T, H // 2), dev), _u8((T, H // 16), dev)
     t = torch.empty(T, dtype=torch.float32, device=dev)
-    _check("quantize_nvfp4_per_token", lib().quantize_nvfp4_per_token(_ptr(x), T, H, x.stride(0), _ptr(q), _ptr(s),
-                                                                      _ptr(t), _stream(dev)))
+    _call("quantize_nvfp4_per_token", dev, _ptr(x), T, H, x.stride(0), _ptr(q), _ptr(s), _ptr(t))
     return q, s, t
 
 
@@ -393,13 +389,11 @@ def quantize_nvfp4(x: torch.Tensor, scope: str = "tensor", group_rows: int = 0, 
         workspace = _u8((ws_bytes,), dev)
     wsn = workspace.numel() if workspace is not None else 0
     if sr_seed is None:
-        _check("quantize_nvfp4", lib().quantize_nvfp4(_ptr(x), R, C, x.stride(0), sc, group_rows, int(transpose),
-                                                      signs, _ptr(q), _ptr(s), _ptr(t), _ptr(workspace), wsn,
-                                                      _stream(dev)))
+        _call("quantize_nvfp4", dev, _ptr(x), R, C, x.stride(0), sc, group_rows, int(transpose), signs, _ptr(q),
+              _ptr(s), _ptr(t), _ptr(workspace), wsn)
     else:
-        _check("quantize_nvfp4_stochastic", lib().quantize_nvfp4_stochastic(
-            _ptr(x), R, C, x.stride(0), sc, group_rows, int(transpose), signs, int(sr_seed), _ptr(q), _ptr(s), _ptr(t),
-            _ptr(workspace), wsn, _stream(dev)))
+        _call("quantize_nvfp4_stochastic", dev, _ptr(x), R, C, x.stride(0), sc, group_rows, int(transpose), signs,
+              int(sr_seed), _ptr(q), _ptr(s), _ptr(t), _ptr(workspace), wsn)
     return q, s, t
 
 
@@ -423,9 +417,8 @@ def quantize_nvfp4_2d(x: torch.Tensor, scope: str = "tensor", group_rows: int = 
     ws_bytes = lib().mxq_workspace_bytes(OP_QUANTIZE_NVFP4, R, C, n_scopes)
     if workspace is None:
         workspace = _u8((max(ws_bytes, 4),), dev)
-    _check("quantize_nvfp4_2d", lib().quantize_nvfp4_2d(_ptr(x), R, C, x.stride(0), SCOPE[scope], group_rows,
-                                                        _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col),
-                                                        _ptr(t), _ptr(workspace), workspace.numel(), _stream(dev)))
+    _call("quantize_nvfp4_2d", dev, _ptr(x), R, C, x.stride(0), SCOPE[scope], group_rows, _ptr(q_row), _ptr(s_row),
+          _ptr(q_col), _ptr(s_col), _ptr(t), _ptr(workspace), workspace.numel())
     return q_row, s_row, q_col, s_col, t
 
 
@@ -435,8 +428,7 @@ def dequantize(fmt: int, q: torch.Tensor, s: torch.Tensor, t: torch.Tensor | Non
     cols = q.shape[1] * (2 if fmt in _PACKED4 else 1)
     out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
     od = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
-    _check("dequantize", lib().dequantize(fmt, _ptr(q), _ptr(s), _ptr(t), SCOPE[t_scope], group_rows, rows, cols,
-                                          _ptr(out), od, _stream(q.device)))
+    _call("dequantize", q.device, fmt, _ptr(q), _ptr(s), _ptr(t), SCOPE[t_scope], group_rows, rows, cols, _ptr(out), od)
     return out
 
 
@@ -457,9 +449,8 @@ def dequantize_transposed(fmt: int, q: torch.Tensor, s=None, t=None, t_scope: st
           or out.shape[2] < out_cols or out.stride(-1) != 1 or out.stride(0) != cols * out.stride(1)
           or out.device != q.device):
         raise ValueError(f"out: expected BF16 (groups={groups}, cols={cols}, >= {out_cols}) rows on {q.device}")
-    _check("dequantize_transposed", lib().dequantize_transposed(
-        fmt, _ptr(q), _ptr(s), _ptr(t), SCOPE[t_scope], groups, group_rows, cols, _ptr(src_row), out_cols,
-        _ptr(out), out.stride(-2), _stream(q.device)))
+    _call("dequantize_transposed", q.device, fmt, _ptr(q), _ptr(s), _ptr(t), SCOPE[t_scope], groups, group_rows, cols,
+          _ptr(src_row), out_cols, _ptr(out), out.stride(-2))
     return out
 
 
@@ -492,9 +483,8 @@ def gemm_block_scaled(fmt: int, A, sA, B, sB, tA=None, tB=None, tA_scope="row", 
     M, N, K = _gemm_args(fmt, A, sA, B, sB, tA, tB, tA_scope, tB_scope, out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    _check("gemm_block_scaled", lib().gemm_block_scaled(fmt, M, N, K, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope],
-                                                        _ptr(B), _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out),
-                                                        out.stride(0), _stream(A.device)))
+    _call("gemm_block_scaled", A.device, fmt, M, N, K, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B),
+          _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out), out.stride(0))
     return out
 
 
@@ -520,7 +510,7 @@ def gemm_block_scaled_batch(fmt: int, problems):
         arr[i] = _GemmProblem(A.shape[0], B_.shape[0], K, A.data_ptr(), ptr(q.get("sA")), ptr(q.get("tA")),
                               SCOPE[q.get("tA_scope", "row")], B_.data_ptr(), ptr(q.get("sB")), ptr(q.get("tB")),
                               SCOPE[q.get("tB_scope", "tensor")], out.data_ptr(), out.stride(0))
-    _check("gemm_block_scaled_batch", lib().gemm_block_scaled_batch(fmt, ctypes.cast(arr, _c_void_p), n, _stream(dev)))
+    _call("gemm_block_scaled_batch", dev, fmt, ctypes.cast(arr, _c_void_p), n)
     return [q["out"] for q in problems]
 
 
@@ -544,8 +534,8 @@ def gemm_fp8_blockwise(A, sA, B, sB, b_blocks: bool = True, out=None):
     M, N, K = _fp8_block_args(A, sA, B, sB, b_blocks, out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    _check("gemm_fp8_blockwise", lib().gemm_fp8_blockwise(M, N, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), int(b_blocks),
-                                                          _ptr(out), out.stride(0), _stream(A.device)))
+    _call("gemm_fp8_blockwise", A.device, M, N, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), int(b_blocks), _ptr(out),
+          out.stride(0))
     return out
 
 
@@ -567,7 +557,7 @@ def gemm_fp8_blockwise_batch(problems):
         _fp8_block_args(A, q["sA"], B_, q["sB"], q["b_blocks"], out)
         arr[i] = _Fp8BlockProblem(A.shape[0], B_.shape[0], A.shape[1], A.data_ptr(), q["sA"].data_ptr(), B_.data_ptr(),
                                   q["sB"].data_ptr(), int(q["b_blocks"]), out.data_ptr(), out.stride(0))
-    _check("gemm_fp8_blockwise_batch", lib().gemm_fp8_blockwise_batch(ctypes.cast(arr, _c_void_p), n, _stream(dev)))
+    _call("gemm_fp8_blockwise_batch", dev, ctypes.cast(arr, _c_void_p), n)
     return [q["out"] for q in problems]
 
 
@@ -576,8 +566,7 @@ def gemm_mxfp8_matrix_core(A, sA, B, sB, out=None):
     M, N, K = _gemm_args(MXFP8, A, sA, B, sB, None, None, "row", "tensor", out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    _check("gemm_mxfp8_matrix_core", lib().gemm_mxfp8_matrix_core(M, N, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB),
-                                                                  _ptr(out), out.stride(0), _stream(A.device)))
+    _call("gemm_mxfp8_matrix_core", A.device, M, N, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(out), out.stride(0))
     return out
 
 
@@ -663,11 +652,10 @@ def grouped_gemm_block_scaled(fmt: int, offsets, A, B, N: int, K: int, sA=None, 
         workspace = _u8((max(ws_bytes, 1),), dev)
     elif workspace.numel() < ws_bytes:
         raise ValueError(f"workspace: {workspace.numel()} bytes, the call needs {ws_bytes}")
-    _check("grouped_gemm_block_scaled", lib().grouped_gemm_block_scaled(
-        fmt, groups, _ptr(offsets), int(vary_k), total, M, N, K, _ptr(a_row_index), a_rows if a_rows is not None
-        else (A.shape[0] if a_row_index is not None else 0), _ptr(A), _ptr(sA), _ptr(tA),
-        SCOPE[tA_scope], _ptr(B), _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out), _ptr(workspace),
-        workspace.numel(), _stream(dev)))
+    _call("grouped_gemm_block_scaled", dev, fmt, groups, _ptr(offsets), int(vary_k), total, M, N, K,
+          _ptr(a_row_index), a_rows if a_rows is not None else (A.shape[0] if a_row_index is not None else 0),
+          _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out),
+          _ptr(workspace), workspace.numel())
     return out
 
 
@@ -683,10 +671,10 @@ def grouped_gemm_block_scaled_noalloc(fmt: int, offsets, A, B, N: int, K: int, s
         raise ValueError("total: pass it explicitly (reading it from the device offsets would synchronize)")
     _grouped_args(fmt, offsets, A, B, N, K, sA, sB, tA, tB, tA_scope, tB_scope, a_row_index, vary_k, M, total,
                   a_rows, out)
-    _check("grouped_gemm_block_scaled_noalloc", lib().grouped_gemm_block_scaled_noalloc(
-        fmt, offsets.numel() - 1, _ptr(offsets), int(vary_k), total, M, N, K, _ptr(a_row_index),
-        a_rows if a_rows is not None else (A.shape[0] if a_row_index is not None else 0), _ptr(A), _ptr(sA), _ptr(tA),
-        SCOPE[tA_scope], _ptr(B), _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out), _stream(A.device)))
+    _call("grouped_gemm_block_scaled_noalloc", A.device, fmt, offsets.numel() - 1, _ptr(offsets), int(vary_k), total,
+          M, N, K, _ptr(a_row_index),
+          a_rows if a_rows is not None else (A.shape[0] if a_row_index is not None else 0), _ptr(A), _ptr(sA),
+          _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB), _ptr(tB), SCOPE[tB_scope], _ptr(out))
     return out
 
 
@@ -705,8 +693,7 @@ def moe_swiglu_quantize_nvfp4(gate_up: torch.Tensor, keep_h: bool = True):
     h = torch.empty((rows, inter), dtype=torch.bfloat16, device=dev) if keep_h else None
     q, s = _u8((rows, inter // 2), dev), _u8((rows, inter // 16), dev)
     t = torch.empty(rows, dtype=torch.float32, device=dev)
-    _check("moe_swiglu_quantize_nvfp4", lib().moe_swiglu_quantize_nvfp4(_ptr(gate_up), rows, inter, _ptr(h), _ptr(q),
-                                                                        _ptr(s), _ptr(t), _stream(dev)))
+    _call("moe_swiglu_quantize_nvfp4", dev, _ptr(gate_up), rows, inter, _ptr(h), _ptr(q), _ptr(s), _ptr(t))
     return h, q, s, t
 
 
@@ -721,9 +708,8 @@ def moe_combine(o_slots: torch.Tensor, slot_of: torch.Tensor, weights: torch.Ten
     c.done()
     if out is None:
         out = torch.empty((T, H), dtype=torch.float32, device=o_slots.device)
-    _check("moe_combine", lib().moe_combine(_ptr(o_slots), o_slots.shape[0], T, k, H, _ptr(slot_of), _ptr(weights),
-                                            _ptr(out),
-                                            _stream(o_slots.device)))
+    _call("moe_combine", o_slots.device, _ptr(o_slots), o_slots.shape[0], T, k, H, _ptr(slot_of), _ptr(weights),
+          _ptr(out))
     return out
 
 

@@ -187,9 +187,8 @@ class MoeNvfp4:
             self.wq_ws = _u8((B.lib().mxq_workspace_bytes(B.OP_QUANTIZE_NVFP4, 0, 0, G),), dev)
         for key, w, gr in (("gu", w_gu, 2 * I), ("d", w_d, H)):
             q, s, t = self.wq[key]
-            B._check("quantize_nvfp4", B.lib().quantize_nvfp4(
-                B._ptr(w), w.shape[0], w.shape[1], w.stride(0), B.SCOPE["group"], gr, 0, None, B._ptr(q),
-                B._ptr(s), B._ptr(t), B._ptr(self.wq_ws), self.wq_ws.numel(), B._stream(dev)))
+            B._call("quantize_nvfp4", w.device, B._ptr(w), w.shape[0], w.shape[1], w.stride(0), B.SCOPE["group"], gr, 0,
+                    None, B._ptr(q), B._ptr(s), B._ptr(t), B._ptr(self.wq_ws), self.wq_ws.numel())
         return self.wq
 
     def quantize_weights_2d(self, w_gu, w_d):
@@ -208,9 +207,8 @@ class MoeNvfp4:
         return self.wq2d
 
     def quantize_tokens(self, x):                                  # A3
-        B._check("quantize_nvfp4_per_token", B.lib().quantize_nvfp4_per_token(
-            B._ptr(x), self.T, self.H, x.stride(0), B._ptr(self.qx), B._ptr(self.sx), B._ptr(self.tx),
-            B._stream(x.device)))
+        B._call("quantize_nvfp4_per_token", x.device, B._ptr(x), self.T, self.H, x.stride(0), B._ptr(self.qx),
+                B._ptr(self.sx), B._ptr(self.tx))
 
     def gate_up(self):                                             # A9 + A10 (gather inside the GEMM)
         qw, sw, tw = self.wq["gu"]
@@ -220,9 +218,8 @@ class MoeNvfp4:
                                     workspace=self.ws)
 
     def swiglu(self):                                              # A11
-        B._check("moe_swiglu_quantize_nvfp4", B.lib().moe_swiglu_quantize_nvfp4(
-            B._ptr(self.gu), self.S, self.I, B._ptr(self.h), B._ptr(self.qh), B._ptr(self.sh), B._ptr(self.th),
-            B._stream(self.dev)))
+        B._call("moe_swiglu_quantize_nvfp4", self.gu.device, B._ptr(self.gu), self.S, self.I, B._ptr(self.h),
+                B._ptr(self.qh), B._ptr(self.sh), B._ptr(self.th))
 
     def down(self):                                                # A10
         qw, sw, tw = self.wq["d"]
@@ -442,9 +439,8 @@ class SharedExpertBf16:
     def forward(self, x, w_sgu, w_sd):
         B.gemm_block_scaled(B.BF16, x, None, w_sgu, None, out=self.gu)
         # SwiGLU to BF16 (the NVFP4 copy the same call emits is not used by this expert)
-        B._check("moe_swiglu_quantize_nvfp4", B.lib().moe_swiglu_quantize_nvfp4(
-            B._ptr(self.gu), self.T, self.I, B._ptr(self.h), B._ptr(self.qh), B._ptr(self.sh), B._ptr(self.th),
-            B._stream(self.dev)))
+        B._call("moe_swiglu_quantize_nvfp4", self.gu.device, B._ptr(self.gu), self.T, self.I, B._ptr(self.h),
+                B._ptr(self.qh), B._ptr(self.sh), B._ptr(self.th))
         B.gemm_block_scaled(B.BF16, self.h, None, w_sd, None, out=self.o)
 
     def transposes(self, x, w_sgu, w_sd, d_o, d_gu):
@@ -513,16 +509,14 @@ class StressStep:
     def quantize_rht(self, a, b):
         for k, x in (("a", a), ("b", b)):
             q, s, t = self.nv[k]
-            B._check("quantize_nvfp4", B.lib().quantize_nvfp4(
-                B._ptr(x), self.n, self.n, x.stride(0), B.SCOPE["tensor"], 0, 1, self._signs_c, B._ptr(q),
-                B._ptr(s), B._ptr(t), B._ptr(self.ws), self.ws.numel(), B._stream(self.dev)))
+            B._call("quantize_nvfp4", x.device, B._ptr(x), self.n, self.n, x.stride(0), B.SCOPE["tensor"], 0, 1,
+                    self._signs_c, B._ptr(q), B._ptr(s), B._ptr(t), B._ptr(self.ws), self.ws.numel())
 
     def quantize_rht_sr(self, a, seed: int):
         """The gradient operand A with stochastically rounded elements (gradients only)."""
         q, s, t = self.nv["a"]
-        B._check("quantize_nvfp4_stochastic", B.lib().quantize_nvfp4_stochastic(
-            B._ptr(a), self.n, self.n, a.stride(0), B.SCOPE["tensor"], 0, 1, self._signs_c, seed, B._ptr(q),
-            B._ptr(s), B._ptr(t), B._ptr(self.ws), self.ws.numel(), B._stream(self.dev)))
+        B._call("quantize_nvfp4_stochastic", a.device, B._ptr(a), self.n, self.n, a.stride(0), B.SCOPE["tensor"], 0,
+                1, self._signs_c, seed, B._ptr(q), B._ptr(s), B._ptr(t), B._ptr(self.ws), self.ws.numel())
 
     def quantize_mxfp4(self, a, b):
         """MXFP4 rowwise + columnwise copies of A and B (one launch)."""

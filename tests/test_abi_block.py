@@ -266,3 +266,42 @@ def test_eps_that_would_leave_the_binary32_range():
         assert B.lib().rmsnorm_quantize(B.BF16, None, BF, 4, 64, 64, P, eps, P, None, None, None, P, None) == status
         assert B.lib().rmsnorm_gate_residual(None, BF, P, F32, P, None, 0, eps, 1.0, 1.0, 4, 64, P, P, None) == status
     assert B.lib().rmsnorm_quantize(B.BF16, None, BF, 4, 64, 64, P, 1e-80, P, None, None, None, None, None) == 1
+
+
+def test_every_call_runs_on_the_device_of_its_tensors(monkeypatch):
+    """A kernel is launched on the device that is current, so a call makes its tensors' device the
+    current one around the launch and hands in that device's stream; every call of the library that
+    takes a stream goes this way."""
+    import inspect
+    import re
+
+    from microscaling_precision_quantization_amd import pipeline
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Lib:
+        def moe_combine(self, *args):
+            seen.append((current[0], args))
+            return 0
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    for index in (0, 1):
+        B._call("moe_combine", torch.device("cuda", index), 7)
+    assert seen == [(0, (7, 100)), (1, (7, 101))] and current == [0]
+    source = inspect.getsource(B) + inspect.getsource(pipeline)
+    assert len(re.findall(r"_stream\(", source)) == 3        # its definition and _call's two
+    assert len(re.findall(r"_check\(", source)) == 3
+    takes_stream = {n for n in B._SIGS if not n.startswith("mxq_")}
+    assert takes_stream - {"quantize_mxfp8_multi", "quantize_mxfp4_multi"} <= set(re.findall(r'_call\(\s*"(\w+)"', source))
