@@ -448,3 +448,50 @@ def test_rows_of_zeros_at_the_smallest_eps():
     none = torch.empty((3, cols), dtype=torch.bfloat16, device="cuda")
     B.rmsnorm_quantize(y, w, eps=1e-200, fmt=B.BF16, out=(none, None, None, None, None))
     assert torch.equal(none, n)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("rows,cols,xt,yt", [(1100, 2048, "bf16", "f32"), (1537, 2056, "f32", "bf16"),
+                                             (1030, 4104, "bf16", "bf16"), (1025, 8200, "f32", "f32")])
+def test_norm_backwards_where_a_workgroup_takes_several_rows(rows, cols, xt, yt, mode):
+    """512 workgroups of several waves, each with two to four rows in turn: the rows' sums meet in two
+    buffers of LDS by turns. Every row, dgate and both column sums against FP64, and bit for bit
+    against calls in which a workgroup has one row."""
+    y, yv = _values(rows, rows, cols, yt)
+    d, dv = _values(rows + 1, rows, cols, xt, 1e-3)
+    w = _weight(rows, cols)
+    gate, gb = _gate(rows, mode, rows, cols)
+    gt, wt = None if gate is None else dev(gate), dev(w)
+    rstd = norm.rstd(yv, EPS).astype(np.float32)
+    rt = dev(rstd)
+    dy, dw, dgate = B.rmsnorm_gate_residual_backward(d, y, rt, wt, gt, gate_mode=mode, branch_scale=0.625)
+    for a in range(0, rows, 512):
+        p = slice(a, min(a + 512, rows))
+        gp = gt if mode in ("none", "channel") else gt[p].clone()           # a gate of its own allocation
+        part = B.rmsnorm_gate_residual_backward(d[p], y[p], rt[p], wt, gp, gate_mode=mode, branch_scale=0.625)
+        assert torch.equal(dy[p], part[0])
+        if mode in ("token", "full"):
+            assert torch.equal(dgate[p], part[2])
+    r = rstd.astype(np.float64)[:, None]
+    yh, up = yv * r, 0.625 * dv.astype(np.float64)
+    dn = up if gb is None else up * gb
+    ref, ref_w = norm.backward(dn, yv, rstd, w)
+    got = inputs.bf16_bits_to_float(host(dy)) if yt == "bf16" else host(dy)
+    # as _dx_bound and the dgate bounds count them; rows of 8200 join sixteen waves: 15 joins, not 3
+    assert np.all(np.abs(got - ref) <= _dx_bound(dn * w, yh, r, np.abs(yh * r) * 12 * U * np.mean(np.abs(dn * w * yh), axis=1, keepdims=True),
+                                                 yt == "bf16", ref))
+    assert np.all(np.abs(host(dw) - ref_w) <= _dw_bound(dn * yh, rows))
+    terms = up * yh * w
+    if mode == "token":
+        assert np.all(np.abs(host(dgate) - terms.sum(1)) <= 96 * U * np.abs(terms).sum(1) + 1e-44)
+    elif mode == "channel":
+        assert np.all(np.abs(host(dgate) - terms.sum(0)) <= _dw_bound(terms, rows))
+    elif mode == "full":
+        assert np.all(np.abs(host(dgate) - terms) <= 6 * U * np.abs(terms) + 1e-44)
+    if mode == "none":                                       # the norm before a block: two gradients and a residual's
+        dn2, dr = _values(rows + 2, rows, cols, xt, 1e-3)[0], _values(rows + 3, rows, cols, yt, 1e-3)[0]
+        dx, dw = B.rmsnorm_backward(d, y, rt, wt, dn2=dn2, d_res=dr, res_scale=0.75)
+        for a in range(0, rows, 512):
+            p = slice(a, min(a + 512, rows))
+            part = B.rmsnorm_backward(d[p], y[p], rt[p], wt, dn2=dn2[p], d_res=dr[p], res_scale=0.75)
+            assert torch.equal(dx[p], part[0])

@@ -354,3 +354,41 @@ def test_combine_backward_of_rows_without_elements():
                                           None, B._ptr(d_w[1:-1]), B._stream(dy.device))
     assert status == 0
     assert bool((d_w[1:-1] == 0).all()) and bool((d_w[0] == 85).all()) and bool((d_w[-1] == 85).all())
+
+
+@pytest.mark.parametrize("T,G,k", [(8193, 60, 4), (8195, 130, 20), (16401, 250, 8), (16387, 257, 3), (24581, 7, 2)])
+def test_route_backward_where_a_wave_takes_several_tokens(T, G, k):
+    """Beyond 8192 tokens (2048 workgroups of four waves) a wave goes on to a next token: its logits
+    and choices are fetched ahead, and its row of LDS is used again. Masked tokens and short lists
+    among them; against FP64, and bit for bit against calls in which a wave has one token."""
+    g = inputs.rng(319, T)
+    z = _logits(T, T, G, dead=1)
+    z[5::11, 2:] = -np.inf                                   # at most two usable experts
+    z[7::13] = -np.inf                                       # none
+    valid = g.uniform(size=T) < 0.8
+    plan = B.moe_route(dev(z), k, valid=dev(valid))
+    idx, w, counts = host(plan.topk_idx), host(plan.weights), host(plan.counts)
+    d_w = (1e-2 * g.standard_normal((T, k))).astype(np.float32)
+    zt, dwt, d_loss = dev(z), dev(d_w), dev(np.float32([1.25]))
+    for dw, dl in ((dwt, d_loss), (dwt, None), (None, d_loss)):
+        got = B.moe_route_backward(zt, plan.topk_idx, plan.weights, plan.counts, dw, dl, COEF)
+        half = torch.empty((T, G), dtype=torch.bfloat16, device="cuda")
+        B.moe_route_backward(zt, plan.topk_idx, plan.weights, plan.counts, dw, dl, COEF, out=half)
+        for a in range(0, T, 8192):
+            p = slice(a, min(a + 8192, T))
+            part = B.moe_route_backward(zt[p], plan.topk_idx[p], plan.weights[p], plan.counts, None if dw is None else dw[p],
+                                        dl, COEF)
+            assert torch.equal(got[p], part) and torch.equal(half[p], part.bfloat16())
+        c32 = float(np.float32(COEF))
+        ref = router.backward(z, idx, w, counts, None if dw is None else d_w, None if dl is None else 1.25, c32)
+        bound = U * np.abs(ref) + 1e-44                      # as test_route_backward counts them
+        if dw is not None:
+            share = w * d_w * (idx >= 0)
+            b = 12 * U * w * (np.abs(d_w) + np.abs(share).sum(1, keepdims=True))
+            rows, at = np.nonzero(idx >= 0)
+            bound[rows, idx[rows, at]] += b[rows, at]
+        if dl is not None:
+            p = router.softmax(z, idx[:, 0] >= 0)
+            c = 1.25 * c32 * G * counts[:G] / (counts[:G].sum() * float(counts[G]))
+            bound += (3 * np.max(_far(z), axis=1, keepdims=True) + 80) * U * p * (c + (p @ c)[:, None])
+        assert np.all(np.abs(host(got) - ref) <= bound), float(np.max(np.abs(host(got) - ref) - bound))
