@@ -613,7 +613,7 @@ mxq_status moe_combine(const float* o_slots, int64_t total_slots, int64_t tokens
  *   r = (mean over the row of x^2 + eps)^(-1/2);  n = x r w, rounded once to BF16;  then the
  *   row quantizer of the format on that BF16 row: the bytes of quantize_mxfp8 /
  *   quantize_mxfp4 (rowwise copy) or quantize_nvfp4_per_token on n.
- *   n is evaluated in binary64 (relative error below 2^-50) and rounded to nearest even: the
+ *   n is evaluated in binary64 (relative error below 2^-48) and rounded to nearest even: the
  *   correctly rounded value unless the exact one lies that close to a rounding midpoint.
  *
  *   fmt    : MXQ_MXFP8, MXQ_MXFP4, MXQ_NVFP4 (per token), or MXQ_BF16 (n only; q, s, t unused).
@@ -721,7 +721,8 @@ mxq_status moe_route(const float* logits, const uint8_t* valid, int64_t tokens, 
  * logits (the counts are constants, as the choice is).
  *   d = w (dw - sum over the chosen of w dw) on the chosen experts, plus
  *   p (c - sum over e of p_e c_e) with c_e = d_loss balance_coef experts counts_e / (A N).
- *   topk_idx, weights, counts: from moe_route; a token that is not routed gets zeros.
+ *   topk_idx, weights, counts: from moe_route (the experts of a token differ); a token that is
+ *   not routed gets zeros.
  *   d_weights : FP32 (tokens, topk), NULL = none;  d_loss: FP32 (1) on the device, NULL = none.
  *   d_logits  : d_dtype (tokens, experts), contiguous; BF16 is what the router's own backward
  *               GEMMs read. Limits as moe_route.
@@ -740,7 +741,8 @@ mxq_status moe_route_backward(const float* logits, int64_t tokens, int64_t exper
  *   slot_of, weights, row_index: the plan of moe_route (a slot index outside
  *   [0, total_slots) contributes nothing and gets d_weights 0);
  *   d_o_bf16  : BF16 (total_slots, hidden);  d_weights: FP32 (tokens, topk).
- *   Requires hidden % 8 == 0, hidden <= 16384, topk <= 32.
+ *   Requires hidden % 8 == 0, hidden <= 16384, topk <= 32. With topk = 0 dy, slot_of, weights
+ *   and d_weights are not touched and may be NULL.
  * ------------------------------------------------------------------------- */
 mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const float* o_slots, int64_t total_slots,
                                 int64_t tokens, int64_t topk, int64_t hidden, const int64_t* slot_of,
@@ -764,7 +766,7 @@ size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
 
 /* Slots that hold every routing of `tokens` tokens over `experts` experts, topk each, with
  * every expert's range a multiple of pad (moe_route's smallest `total`); -1 for sizes that
- * moe_route refuses. */
+ * moe_route refuses, 2^31 slots and more among them. */
 int64_t mxq_route_slots(int64_t tokens, int64_t experts, int64_t topk, int64_t pad);
 
 const char* mxq_status_string(mxq_status s);

@@ -755,7 +755,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: f
                      keep_n: bool = True, out=None):
     """RMSNorm of BF16 or FP32 x (T, H), rounded to BF16 and quantized row by row in one pass:
     (n | None, q | None, s | None, t | None, rstd). fmt: MXFP8, MXFP4, NVFP4 (per token) or
-    BF16 (n only). `out` may supply preallocated (n, q, s, t, rstd); n None there = not written."""
+    BF16 (n only). x's rows may be strided (rmsnorm_backward takes dense ones). `out` may supply
+    preallocated (n, q, s, t, rstd); n or rstd None there = not written."""
     xd = _float_dtype(x, "x")
     if fmt not in (MXFP8, NVFP4, BF16, MXFP4):
         raise ValueError(f"unknown format {fmt}")

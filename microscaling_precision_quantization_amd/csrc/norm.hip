@@ -6,9 +6,10 @@
 //   dn -> g = dn w,  xh = x r,  dx = r (g - xh mean(g xh)),  dw = sum over rows of dn xh
 //   out = res_scale x + branch_scale gate (y r w)
 // The forward norm that feeds a quantizer is rounded once to BF16 from a value whose relative
-// error stays below 2^-50 (binary64 from the squares on; binary32 where its roundings cannot
-// change the result): the correctly rounded one unless the exact value lies that close to a
-// rounding midpoint. The quantized bytes are those of the library's quantizers on it.
+// error stays below 2^-48 (binary64 from the squares on, whose sum takes at most 16 additions in a
+// lane, 6 exchanges and 15 joins of waves, and the root halves its error; binary32 where its
+// roundings cannot change the result): the correctly rounded one unless the exact value lies that
+// close to a rounding midpoint. The quantized bytes are those of the library's quantizers on it.
 #include <type_traits>
 
 #include "common.h"
@@ -270,8 +271,9 @@ norm_quant_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ld
 
 // ---------------------------------------------------------------------------
 // Norm after a block: out = res_scale x + branch_scale gate (y r w), one workgroup per row. HBM
-// bounds it: 16384 x 7168, BF16 x, FP32 y 165 us, 5.7 TB/s (176 with E = 8; 172 with plain stores
-// and a new output each call); all FP32 178 (262 with E = 8); all BF16 106 (121 with E = 4).
+// bounds it: 16384 x 7168, channel gate, BF16 x, FP32 y 165 us, 5.7 TB/s (177 with E = 8; 172 with
+// plain stores and a new output each call); all FP32 234, 6.0 TB/s (294 with E = 8); all BF16 130, 5.4
+// TB/s (140 with E = 4). Every row's x, y and out lie in memory of their own.
 // GATE: 0 none, 1 one per row, 2 one per column, 3 one per element.
 // ---------------------------------------------------------------------------
 template <bool X32, bool Y32, int GATE, bool STREAM, int W, int NV, int E>
@@ -335,8 +337,11 @@ gate_residual_kernel(const void* __restrict__ x, const void* __restrict__ y, int
 // column is constant over the rows as the weight is, so it is multiplied into the weight (GATE 0)
 // and one sum, S = sum over the rows of scale d yh, gives both gradients: dw = gate S, dgate = w S.
 // HBM bounds it: 16381 x 7168 with two FP32 gradients and the residual's 300 us, 5.5 TB/s (317 us
-// with plain stores of dx); 8191 x 7168 after a block, FP32 y, 109 us, 5.4 TB/s (119 with E = 8, 117
-// with plain stores); all FP32, 16384 x 7168, 193 us (244 with E = 8).
+// with plain stores of dx); 8191 x 7168 after a block, FP32 y, 109 us, 5.4 TB/s (123 with E = 8, 117
+// with plain stores); all FP32, 16384 x 7168, 242 us, 5.8 TB/s (292 with E = 8); all BF16 123, 5.7 TB/s
+// (120 with E = 4, but at 16384 x 2048 52 against 58). With sixteen waves (rows beyond 8192) 128 registers
+// a lane are all there are, and up to 62 spill (FP32 rows, token gate); 8192 x 16384 still runs at the
+// copy's rate, 313 us of 315 for all FP32 and 250 of 262 with BF16 gradients.
 // ---------------------------------------------------------------------------
 struct NormGrad {
   const void *d, *d2, *y, *res;
@@ -520,6 +525,10 @@ void with_gate(int gate, F&& go) {
 // more launches.
 constexpr int64_t kLaunchRows = (int64_t)1 << 21;
 
+// Workgroups of a backward, each with its column sums: two a CU. (us with 256, 512, 1024 and 2048; two BF16
+// gradients of n, BF16 x and residual: 16381 x 7168 206, 215, 217, 220; 16384 x 4096 137, 123, 132, 135;
+// 4096 x 2048 31, 24, 25, 29; 16384 x 2048 100, 66, 63, 67. Narrower rows leave SIMDs without a wave and
+// would take more workgroups: 16384 x 1024 85, 52, 40, 40.)
 int64_t backward_parts(int64_t rows) { return rows < 512 ? rows : 512; }
 
 }  // namespace
