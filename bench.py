@@ -53,12 +53,16 @@ HBM_PEAK_GBPS = 8000.0
 MFMA_PEAK_TFLOPS = {"bf16": 2500.0, "fp16": 2500.0, "fp8": 5000.0, "fp4": 10100.0}
 METRIC = "quantize GB/s (% HBM peak) + block-scaled GEMM TFLOPS (% MFMA peak), 1 GPU"
 KERNEL_SOURCES = ["microscaling_precision_quantization_amd/csrc/gemm_exact.hip",
+                  "microscaling_precision_quantization_amd/csrc/gemm_swiglu.hip",
+                  "microscaling_precision_quantization_amd/csrc/gemv.hip",
                   "microscaling_precision_quantization_amd/csrc/quant_mxfp8.hip",
                   "microscaling_precision_quantization_amd/csrc/quant_fp8_block.hip",
                   "microscaling_precision_quantization_amd/csrc/quant_nvfp4.hip",
                   "microscaling_precision_quantization_amd/csrc/dequant_moe.hip",
                   "microscaling_precision_quantization_amd/csrc/norm.hip",
                   "microscaling_precision_quantization_amd/csrc/moe_route.hip",
+                  "microscaling_precision_quantization_amd/csrc/gemm_tile.h",
+                  "microscaling_precision_quantization_amd/csrc/swiglu.h",
                   "microscaling_precision_quantization_amd/csrc/common.h"]
 
 # algorithmic bytes per element

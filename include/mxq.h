@@ -750,6 +750,108 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
                                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * gemm_swiglu -- the two projections of a gated feed-forward block, the activation and the
+ * product in one kernel:
+ *   (g | u) = A_hat B_hat^T, sums as gemm_block_scaled's;  h = g sigma(g) u.
+ *   Defined by: SwiGLU blocks whose gate and up projections enter one fused GEMM ("Miles
+ *   Blackwell RL", remio.ai, section "Un Cuantizador Compartido ...").
+ *   The FP32 product is not stored: h, and (g | u) where the backward wants it, are each
+ *   rounded to BF16 once, from the FP32 sums (h: a binary32 evaluation within 2^-20 of the
+ *   exact function of the sums). moe_swiglu_quantize_nvfp4, on a stored FP32 product, rounds h
+ *   correctly instead.
+ *   fmt, A, sA, tA, sB, tB: as gemm_block_scaled, MXQ_MXFP8, MXQ_NVFP4 or MXQ_BF16 (tA, tB:
+ *             MXQ_NVFP4, scopes ROW or TENSOR). B: (2 inter, K), the gate rows, then the up rows.
+ *   h       : BF16 (M, inter);  gate_up: BF16 (M, 2 inter) = (g | u), NULL = not written.
+ *   Requires inter % 8 == 0, K % 32 == 0 (BF16: % 8), K <= 2^22, 2 inter rows of B below 2^31 bytes;
+ *   every pointer but tA and tB 16-byte aligned. Outputs must not overlap inputs.
+ * ------------------------------------------------------------------------- */
+mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
+                       const float* tA, mxq_scope tA_scope, const void* B, const void* sB, const float* tB,
+                       mxq_scope tB_scope, void* h, void* gate_up, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_swiglu_backward -- the gradient of the block's output through the down projection and
+ * SwiGLU to the two projections, in one kernel:
+ *   dh = A_hat B_hat^T, sums as gemm_block_scaled's (A: the output's gradient, B: W_d^T);
+ *   s = sigma(g);  dg = dh u s (1 + g (1 - s));  du = dh g s;  and h = g s u made again.
+ *   dh is not stored; each output is rounded to BF16 once.
+ *   fmt       : MXQ_BF16, or MXQ_MXFP8 (A the rowwise copy of the gradient, B the columnwise copy
+ *               of W_d). A (M, K), B (inter, K): K the block's output width.
+ *   gate_up   : (M, 2 inter) gu_dtype, BF16 as gemm_swiglu keeps it, or FP32.
+ *   d_gate_up : BF16 (M, 2 inter) = (dg | du), what the GEMMs for dX and dW_gu read;
+ *   h         : BF16 (M, inter), what the GEMM for dW_d reads; NULL = not wanted.
+ *   Limits as gemm_swiglu. Outputs must not overlap inputs.
+ * ------------------------------------------------------------------------- */
+mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
+                                const void* B, const void* sB, const void* gate_up, mxq_out_dtype gu_dtype,
+                                void* d_gate_up, void* h, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * grouped_gemm_swiglu, grouped_gemm_swiglu_backward -- the same per routed expert, scheduled on
+ * the device from the expert offsets (as grouped_gemm_block_scaled, vary_k = 0; its rules for
+ * offsets, total, a_row_index and a_rows hold, rejected offsets leave the outputs unwritten).
+ *   forward  : fmt MXQ_NVFP4 (tA ROW or TENSOR, tB GROUP -- one an expert -- or ROW) or MXQ_BF16; B: the
+ *              experts' (2 inter, K) stacked. h: BF16 (total, inter), gate_up: BF16 (total, 2 inter)
+ *              or NULL; a slot whose row index is out of range (padding) has zeros in both.
+ *   backward : fmt MXQ_BF16 (B: the experts' (inter, K) transposes of W_d stacked) or
+ *              MXQ_BF16_NVFP4T (B, sB, tB: the forward's NVFP4 W_d, (K, inter) an expert, read
+ *              transposed as grouped_gemm_block_scaled reads it; inter % 16 == 0,
+ *              K inter / 2 < 2^31). A: BF16 (total, K); the other tensors as gemm_swiglu_backward's,
+ *              `total` rows. sB and tB are unused with MXQ_BF16.
+ *   workspace: mxq_workspace_bytes(MXQ_OP_GROUPED_GEMM, groups, 0, 0) bytes, 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+mxq_status grouped_gemm_swiglu(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
+                               int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
+                               const float* tA, mxq_scope tA_scope, const void* B, const void* sB, const float* tB,
+                               mxq_scope tB_scope, void* h, void* gate_up, void* workspace, size_t workspace_bytes,
+                               void* stream);
+mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total,
+                                        int64_t inter, int64_t K, const void* A, const void* B, const void* sB,
+                                        const float* tB, const void* gate_up, mxq_out_dtype gu_dtype,
+                                        void* d_gate_up, void* h, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gemv_block_scaled, gemv_swiglu -- a few BF16 rows (a decoding step's tokens) against 4-bit
+ * weights as the quantizers store them; the rows are not quantized.
+ *   y[r, n] = t_n sum_k x[r, k] (q S)[n, k], products exact, sums FP32, rounded to y_dtype once;
+ *   gemv_swiglu: W (2 inter, K), gate rows, then up rows; h = silu(y gate) (y up), BF16.
+ *   Defined by: NVFP4 weights moving through memory can bind harder than arithmetic (remio.ai,
+ *   section "NVFP4 por token ..."); MXFP4: 7minutos.es, section "NVFP4 frente a MXFP4".
+ *   fmt : MXQ_NVFP4 (tW: TENSOR or ROW) or MXQ_MXFP4 (tW unused; scale codes s <= 252).
+ *   x   : BF16 (rows, K), row stride ld_x (a multiple of 8);  W (N, K/2), sW (N, K/16 or K/32).
+ *   y   : (rows, N) y_dtype, row stride ld_y >= N;  h: BF16 (rows, inter), row stride ld_h >= inter.
+ *   Requires rows <= 64 (more rows are the GEMMs'), K % 32 == 0, 32 <= K <= 2^22; x and W 16-byte
+ *   aligned, NVFP4 scales 2-byte aligned. A row of x reaches only its own row of the result.
+ * ------------------------------------------------------------------------- */
+mxq_status gemv_block_scaled(mxq_format fmt, int64_t rows, int64_t N, int64_t K, const void* x, int64_t ld_x,
+                             const void* W, const void* sW, const float* tW, mxq_scope tW_scope, void* y,
+                             mxq_out_dtype y_dtype, int64_t ld_y, void* stream);
+mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, const void* x, int64_t ld_x,
+                       const void* W, const void* sW, const float* tW, mxq_scope tW_scope, void* h, int64_t ld_h,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_decode_gate_up, moe_decode_down -- an expert layer for a decoding step: the few tokens
+ * through their chosen experts' 4-bit weights, each chosen expert's weight read once.
+ *   gate_up : h[t, j, :] = silu(x[t] Wg_e^T) (x[t] Wu_e^T), e = topk_idx[t, j]; BF16 (tokens, topk, inter).
+ *   down    : y[t, :] = sum over j of weights[t, j] (h[t, j] W_e^T), sums FP32, y_dtype (tokens, hidden).
+ *   topk_idx, weights: (tokens, topk) int32 and FP32, as moe_route writes them. A choice outside
+ *   [0, experts) is none: zeros in h, nothing in y (its h and weight are not read).
+ *   x: BF16 (tokens, K), row stride ld_x;  h of the down call: BF16 (tokens, topk, K), contiguous.
+ *   W : the experts' (2 inter, K) or (hidden, K) stacked;  fmt MXQ_NVFP4 (tW GROUP -- one an expert --
+ *   or ROW) or MXQ_MXFP4.
+ *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled.
+ * ------------------------------------------------------------------------- */
+mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
+                              const void* x, int64_t ld_x, const int32_t* topk_idx, const void* W, const void* sW,
+                              const float* tW, mxq_scope tW_scope, void* h, void* stream);
+mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t hidden, int64_t K,
+                           const void* h, const int32_t* topk_idx, const float* weights, const void* W,
+                           const void* sW, const float* tW, mxq_scope tW_scope, void* y, mxq_out_dtype y_dtype,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
  * Queries.
  * ------------------------------------------------------------------------- */
 /* Bytes of the scale matrix for a (rows, cols) tensor blocked along cols

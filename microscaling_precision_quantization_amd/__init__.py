@@ -10,4 +10,6 @@ from .binding import (BF16, BF16_NVFP4T, MXFP4, MXFP8, NVFP4, MxqError, RoutePla
                       moe_swiglu_quantize_nvfp4, quantize_mxfp4, quantize_mxfp4_multi, quantize_mxfp8, quantize_mxfp8_multi, quantize_nvfp4,
                       quantize_nvfp4_2d,
                       quantize_nvfp4_per_token, rmsnorm_backward, rmsnorm_gate_residual, rmsnorm_gate_residual_backward,
-                      rmsnorm_quantize, moe_combine_backward, moe_route, moe_route_backward, route_slots, scale_bytes)
+                      rmsnorm_quantize, moe_combine_backward, moe_route, moe_route_backward, route_slots, scale_bytes,
+                      gemm_swiglu, gemm_swiglu_backward, grouped_gemm_swiglu, grouped_gemm_swiglu_backward, gemv_block_scaled, gemv_swiglu,
+                      moe_decode_gate_up, moe_decode_down)

@@ -81,6 +81,23 @@ _SIGS = {
                            _f32, _c_void_p, _int, _c_void_p],
     "moe_combine_backward": [_c_void_p, _int, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                              _c_void_p, _c_void_p, _c_void_p],
+    "gemm_swiglu": [_int, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _int,
+                    _c_void_p, _c_void_p, _c_void_p],
+    "gemm_swiglu_backward": [_int, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _int,
+                             _c_void_p, _c_void_p, _c_void_p],
+    "grouped_gemm_swiglu": [_int, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
+                            _int, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _size,
+                            _c_void_p],
+    "grouped_gemm_swiglu_backward": [_int, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
+    "gemv_block_scaled": [_int, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _int,
+                          _i64, _c_void_p],
+    "gemv_swiglu": [_int, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _i64,
+                    _c_void_p],
+    "moe_decode_gate_up": [_int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
+                           _c_void_p, _int, _c_void_p, _c_void_p],
+    "moe_decode_down": [_int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                        _c_void_p, _int, _c_void_p, _int, _c_void_p],
     "mxq_route_slots": [_i64, _i64, _i64, _i64],
     "mxq_scale_bytes": [_int, _i64, _i64],
     "mxq_workspace_bytes": [_int, _i64, _i64, _i64],
@@ -710,6 +727,246 @@ def moe_combine(o_slots: torch.Tensor, slot_of: torch.Tensor, weights: torch.Ten
         out = torch.empty((T, H), dtype=torch.float32, device=o_slots.device)
     _call("moe_combine", o_slots.device, _ptr(o_slots), o_slots.shape[0], T, k, H, _ptr(slot_of), _ptr(weights),
           _ptr(out))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward block
+# ---------------------------------------------------------------------------
+
+def _gated_out(c, out, names, rows: int, inter: int, keep: bool, dev):
+    """(h, gate_up) or (d_gate_up, h) BF16: the caller's (the second may be None), or new ones.
+    names: which of them is 2 inter wide ends in "gate_up"."""
+    width = lambda n: 2 * inter if n.endswith("gate_up") else inter
+    if out is not None:
+        first, second = out
+        c.need(first, names[0], torch.bfloat16, (rows, width(names[0])))
+        c.opt(second, names[1], torch.bfloat16, (rows, width(names[1])))
+        c.done()
+        return first, second
+    c.done()
+    new = lambda n: torch.empty((rows, width(n)), dtype=torch.bfloat16, device=dev)
+    return new(names[0]), new(names[1]) if keep else None
+
+
+def _grouped_workspace(workspace, groups: int, dev):
+    need = lib().mxq_workspace_bytes(OP_GROUPED_GEMM, groups, 0, 0)
+    if workspace is None:
+        return _u8((max(need, 1),), dev)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace: expected contiguous uint8 memory on {dev}")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace: {workspace.numel()} bytes, the call needs {need}")
+    return workspace
+
+
+def _two_d(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
+    return t
+
+
+def gemm_swiglu(fmt: int, A, sA, B, sB, tA=None, tB=None, tA_scope="row", tB_scope="tensor", keep_gate_up: bool = False,
+                out=None):
+    """h = silu(g) u in BF16, (g | u) = A_hat B_hat^T, in one kernel: (h (M, inter), gate_up (M, 2 inter) | None).
+    fmt: MXFP8, NVFP4 or BF16; B (2 inter, K): the gate rows, then the up rows. `out` may supply
+    (h, gate_up); gate_up None there = not written."""
+    if fmt not in (MXFP8, NVFP4, BF16):
+        raise ValueError(f"gemm_swiglu: format {fmt} is not supported")
+    M, N, K = _gemm_args(fmt, _two_d(A, "A"), sA, _two_d(B, "B"), sB, tA, tB, tA_scope, tB_scope, None)
+    if N % 2:
+        raise ValueError(f"B: {N} rows, expected as many up rows as gate rows")
+    c = _Checks(A.device)
+    h, gate_up = _gated_out(c, out, ("h", "gate_up"), M, N // 2, keep_gate_up, A.device)
+    _call("gemm_swiglu", A.device, fmt, M, N // 2, K, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB),
+          _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up))
+    return h, gate_up
+
+
+def _gate_up_dtype(gate_up) -> int:
+    if not isinstance(gate_up, torch.Tensor) or gate_up.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("gate_up: expected a bfloat16 or float32 tensor")
+    return OUT_F32 if gate_up.dtype == torch.float32 else OUT_BF16
+
+
+def gemm_swiglu_backward(fmt: int, A, sA, B, sB, gate_up, keep_h: bool = True, out=None):
+    """The gradient A (M, K) of a gated block's output through W_d and SwiGLU: (d_gate_up BF16 (M, 2 inter),
+    h BF16 (M, inter) | None). B (inter, K): W_d^T, K-contiguous; fmt BF16 or MXFP8 (the columnwise copy
+    of W_d). gate_up: as gemm_swiglu kept it, or FP32. `out` may supply (d_gate_up, h)."""
+    if fmt not in (MXFP8, BF16):
+        raise ValueError(f"gemm_swiglu_backward: format {fmt} is not supported")
+    gd = _gate_up_dtype(gate_up)
+    M, inter, K = _gemm_args(fmt, _two_d(A, "A"), sA, _two_d(B, "B"), sB, None, None, "row", "tensor", None)
+    c = _Checks(A.device)
+    c.need(gate_up, "gate_up", gate_up.dtype, (M, 2 * inter))
+    d_gate_up, h = _gated_out(c, out, ("d_gate_up", "h"), M, inter, keep_h, A.device)
+    _call("gemm_swiglu_backward", A.device, fmt, M, inter, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(gate_up), gd,
+          _ptr(d_gate_up), _ptr(h))
+    return d_gate_up, h
+
+
+def grouped_gemm_swiglu(fmt: int, offsets, A, B, inter: int, K: int, sA=None, sB=None, tA=None, tB=None, tA_scope="row",
+                        tB_scope="group", a_row_index=None, total: int | None = None, keep_gate_up: bool = False,
+                        out=None, workspace=None):
+    """gemm_swiglu per expert: (h (total, inter), gate_up (total, 2 inter) | None), BF16. fmt: NVFP4 or BF16;
+    offsets, a_row_index, total and the operands as grouped_gemm_block_scaled's with N = 2 inter."""
+    if fmt not in (NVFP4, BF16):
+        raise ValueError(f"grouped_gemm_swiglu: format {fmt} is not supported")
+    if total is None:
+        total = int(offsets[-1].item())
+    _two_d(A, "A")
+    _grouped_args(fmt, offsets, A, B, 2 * inter, K, sA, sB, tA, tB, tA_scope, tB_scope, a_row_index, False, 0, total,
+                  None, None)
+    dev, groups = A.device, offsets.numel() - 1
+    c = _Checks(dev)
+    h, gate_up = _gated_out(c, out, ("h", "gate_up"), total, inter, keep_gate_up, dev)
+    ws = _grouped_workspace(workspace, groups, dev)
+    _call("grouped_gemm_swiglu", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(a_row_index),
+          A.shape[0] if a_row_index is not None else 0, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB),
+          _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up), _ptr(ws), ws.numel())
+    return h, gate_up
+
+
+def grouped_gemm_swiglu_backward(fmt: int, offsets, A, B, inter: int, K: int, gate_up, sB=None, tB=None,
+                                 total: int | None = None, keep_h: bool = True, out=None, workspace=None):
+    """gemm_swiglu_backward per expert: (d_gate_up (total, 2 inter), h (total, inter) | None), BF16. A BF16
+    (total, K); fmt BF16 (B: the experts' (inter, K) stacked) or BF16_NVFP4T (B, sB, tB: the forward's
+    NVFP4 W_d as it is, (experts K, inter / 2))."""
+    if fmt not in (BF16, BF16_NVFP4T):
+        raise ValueError(f"grouped_gemm_swiglu_backward: format {fmt} is not supported")
+    if total is None:
+        total = int(offsets[-1].item())
+    gd = _gate_up_dtype(gate_up)
+    _two_d(A, "A")
+    _grouped_args(fmt, offsets, A, B, inter, K, None, sB, None, tB, "row", "group", None, False, 0, total, None, None)
+    dev, groups = A.device, offsets.numel() - 1
+    c = _Checks(dev)
+    c.need(gate_up, "gate_up", gate_up.dtype, (total, 2 * inter))
+    d_gate_up, h = _gated_out(c, out, ("d_gate_up", "h"), total, inter, keep_h, dev)
+    ws = _grouped_workspace(workspace, groups, dev)
+    _call("grouped_gemm_swiglu_backward", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(A), _ptr(B), _ptr(sB),
+          _ptr(tB), _ptr(gate_up), gd, _ptr(d_gate_up), _ptr(h), _ptr(ws), ws.numel())
+    return d_gate_up, h
+
+
+# ---------------------------------------------------------------------------
+# Matrix-vector products with 4-bit weights
+# ---------------------------------------------------------------------------
+
+def _weights4(c, fmt: int, W, sW, tW, t_scope: str, rows: int, K: int, groups: int, wide: str):
+    """4-bit weights of `rows` rows in all; NVFP4: one FP32 scale a row, or (t_scope == wide) a group."""
+    if fmt not in _PACKED4:
+        raise ValueError(f"format {fmt}: expected NVFP4 or MXFP4 weights")
+    c.need(W, "W", torch.uint8, (rows, K // 2))
+    c.need(sW, "sW", torch.uint8, (rows, K // _scale_block(fmt)))
+    if fmt == NVFP4:
+        if t_scope not in ("row", wide):
+            raise ValueError(f"t_scope: {t_scope!r}, expected 'row' or {wide!r}")
+        if tW is None:
+            raise ValueError("tW: NVFP4 needs its FP32 scale")
+        c.need(tW, "tW", torch.float32, (rows if t_scope == "row" else groups,))
+
+
+def _decode_rows(x, name: str, dim: int):
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != dim:
+        raise ValueError(f"{name}: expected a {dim}-D bfloat16 tensor")
+    return x.shape
+
+
+def _gemv_args(fmt: int, x, W, sW, tW, t_scope: str, gated: bool, out_dtype, out):
+    """The output and the C call's arguments up to it."""
+    rows, K = _decode_rows(x, "x", 2)
+    N = _two_d(W, "W").shape[0]
+    if gated and N % 2:
+        raise ValueError(f"W: {N} rows, expected as many up rows as gate rows")
+    n = N // 2 if gated else N
+    dev = x.device
+    c = _Checks(dev)
+    c.need(x, "x", torch.bfloat16, (rows, K), ld=True)
+    _weights4(c, fmt, W, sW, tW, t_scope, N, K, 1, "tensor")
+    if out is not None:
+        c.need(out, "out", out.dtype if not gated and _float_dtype(out, "out") is not None else torch.bfloat16,
+               (rows, n), ld=True)
+    c.done()
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype, device=dev)
+    return out, (fmt, rows, n, K, _ptr(x), max(x.stride(0), K), _ptr(W), _ptr(sW), _ptr(tW), SCOPE[t_scope], _ptr(out))
+
+
+def gemv_block_scaled(fmt: int, x, W, sW, tW=None, t_scope: str = "tensor", out_dtype: torch.dtype = torch.float32,
+                      out=None):
+    """y = x W_hat^T of a few BF16 rows x (rows <= 64, K; rows may be strided) and 4-bit weights W (N, K/2):
+    (rows, N) in FP32 or BF16 (`out`'s type where given). fmt: NVFP4 (tW, t_scope "tensor" or "row") or MXFP4."""
+    if out is None and out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype: {out_dtype}, expected float32 or bfloat16")
+    out, args = _gemv_args(fmt, x, W, sW, tW, t_scope, False, out_dtype, out)
+    _call("gemv_block_scaled", x.device, *args, OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
+          max(out.stride(0), out.shape[1]))
+    return out
+
+
+def gemv_swiglu(fmt: int, x, W, sW, tW=None, t_scope: str = "tensor", out=None):
+    """h = silu(x Wg_hat^T) (x Wu_hat^T) in BF16 (rows, inter), W (2 inter, K/2): gate rows, then up rows;
+    otherwise as gemv_block_scaled."""
+    out, args = _gemv_args(fmt, x, W, sW, tW, t_scope, True, torch.bfloat16, out)
+    _call("gemv_swiglu", x.device, *args, max(out.stride(0), out.shape[1]))
+    return out
+
+
+def _stacked(W, experts: int) -> int:
+    """Rows an expert of a stacked weight (experts n, K/2)."""
+    rows = _two_d(W, "W").shape[0]
+    if experts < 1 or rows % experts:
+        raise ValueError(f"W: {rows} rows for {experts} experts")
+    return rows // experts
+
+
+def moe_decode_gate_up(fmt: int, x, topk_idx, W, sW, tW=None, experts: int = 0, t_scope: str = "group", out=None):
+    """h (tokens, topk, inter) BF16 of a decoding step: each token (x (tokens <= 64, K) BF16, rows may be
+    strided) through gate_up and SwiGLU of the experts topk_idx (tokens, topk) int32 names; zeros for a
+    choice of -1. W: (experts 2 inter, K/2), NVFP4 or MXFP4, as quantize_nvfp4(scope="group") and
+    quantize_mxfp4 store the stacked weights."""
+    T, K = _decode_rows(x, "x", 2)
+    n = _stacked(W, experts)
+    if n % 2:
+        raise ValueError(f"W: {n} rows an expert, expected as many up rows as gate rows")
+    dev = x.device
+    c = _Checks(dev)
+    c.need(x, "x", torch.bfloat16, (T, K), ld=True)
+    k = _two_d(topk_idx, "topk_idx").shape[1]
+    c.need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _weights4(c, fmt, W, sW, tW, t_scope, W.shape[0], K, experts, "group")
+    c.opt(out, "out", torch.bfloat16, (T, k, n // 2))
+    c.done()
+    if out is None:
+        out = torch.empty((T, k, n // 2), dtype=torch.bfloat16, device=dev)
+    _call("moe_decode_gate_up", dev, fmt, T, k, experts, n // 2, K, _ptr(x), max(x.stride(0), K), _ptr(topk_idx), _ptr(W),
+          _ptr(sW), _ptr(tW), SCOPE[t_scope], _ptr(out))
+    return out
+
+
+def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int = 0, t_scope: str = "group",
+                    out_dtype: torch.dtype = torch.float32, out=None):
+    """y (tokens, hidden) = sum over j of weights[t, j] (h[t, j] W_hat_e^T), FP32 or BF16 (`out`'s type where
+    given): the down projection and the combine of a decoding step. h (tokens, topk, inter) BF16 as
+    moe_decode_gate_up gives it, W: (experts hidden, inter / 2)."""
+    T, k, K = _decode_rows(h, "h", 3)
+    n = _stacked(W, experts)
+    if out is None and out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype: {out_dtype}, expected float32 or bfloat16")
+    dev = h.device
+    c = _Checks(dev)
+    c.need(h, "h", torch.bfloat16, (T, k, K))
+    c.need(topk_idx, "topk_idx", torch.int32, (T, k))
+    c.need(weights, "weights", torch.float32, (T, k))
+    _weights4(c, fmt, W, sW, tW, t_scope, W.shape[0], K, experts, "group")
+    if out is not None:
+        c.need(out, "out", torch.float32 if out.dtype == torch.float32 else torch.bfloat16, (T, n))
+    c.done()
+    if out is None:
+        out = torch.empty((T, n), dtype=out_dtype, device=dev)
+    _call("moe_decode_down", dev, fmt, T, k, experts, n, K, _ptr(h), _ptr(topk_idx), _ptr(weights), _ptr(W), _ptr(sW),
+          _ptr(tW), SCOPE[t_scope], _ptr(out), OUT_F32 if out.dtype == torch.float32 else OUT_BF16)
     return out
 
 

@@ -28,7 +28,7 @@ LIB = os.path.join(HERE, "libmxq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "quant_mxfp8.hip", "quant_nvfp4.hip", "quant_fp8_block.hip", "dequant_moe.hip", "norm.hip",
-           "moe_route.hip", "gemm_exact.hip"]
+           "moe_route.hip", "gemm_exact.hip", "gemm_swiglu.hip", "gemv.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -65,6 +65,28 @@ hipError_t launch_route_backward(const float* logits, int64_t tokens, int64_t ex
 hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int64_t total, int64_t tokens,
                                    int64_t topk, int64_t hidden, const int64_t* slot_of, const float* weights,
                                    const int32_t* row_index, void* d_o, float* d_weights, hipStream_t st);
+hipError_t launch_gemm_swiglu(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
+                              int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode, void* h,
+                              void* gate_up, hipStream_t st);
+hipError_t launch_gemm_swiglu_backward(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
+                                       const void* B, const void* sB, const void* gate_up, int gu32, void* d_gate_up,
+                                       void* h, hipStream_t st);
+hipError_t launch_grouped_gemm_swiglu(int fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
+                                      int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
+                                      const float* tA, int tA_mode, const void* B, const void* sB, const float* tB,
+                                      int tB_mode, void* h, void* gate_up, void* ws, hipStream_t st);
+hipError_t launch_grouped_gemm_swiglu_backward(int fmt, int64_t groups, const int64_t* offsets, int64_t total,
+                                               int64_t inter, int64_t K, const void* A, const void* B, const void* sB,
+                                               const float* tB, const void* gate_up, int gu32, void* d_gate_up, void* h,
+                                               void* ws, hipStream_t st);
+hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, const void* x, int64_t ld_x, const void* w,
+                       const void* s, const float* t, int t_mode, void* y, int64_t ld_y, int out32, hipStream_t st);
+hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
+                                 const void* x, int64_t ld_x, const int32_t* idx, const void* w, const void* s,
+                                 const float* t, int t_mode, void* h, hipStream_t st);
+hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t K, const void* h,
+                              const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
+                              int t_mode, void* y, int out32, hipStream_t st);
 }  // namespace mxq
 
 namespace {
@@ -76,6 +98,8 @@ constexpr int64_t kMaxRouteTokens = int64_t(1) << 22;  // router: 16 bits for th
 // GEMM operand reads use 32-bit buffer offsets: a 256-row tile of K-contiguous rows,
 // or (gather) the whole gathered operand, must span less than 2^31 bytes.
 constexpr int64_t kMaxGemmK = int64_t(1) << 22;
+constexpr int64_t kMaxGridTiles = (int64_t(1) << 24) - 1;   // of 256 threads: a grid holds fewer than 2^32
+constexpr int64_t kMaxDecodeRows = 64;                       // rows of a matrix-vector product
 inline int64_t gemm_row_bytes(mxq_format fmt, int64_t k) {
   return fmt == MXQ_BF16 ? 2 * k : fmt == MXQ_MXFP8 ? k : k / 2;   // NVFP4, MXFP4: two per byte
 }
@@ -801,6 +825,201 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
     return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_combine_backward(dy, dy_dtype == MXQ_OUT_F32, o_slots, total_slots, tokens, topk,
                                                  hidden, slot_of, weights, row_index, d_o_bf16, d_weights, S(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Gated feed-forward block
+// ---------------------------------------------------------------------------
+
+namespace {
+// 128 x 128 tiles of (rows, n), the most a launch can need (a group's last tile may be mostly padding)
+bool tiles_fit(int64_t rows, int64_t n, int64_t groups) {
+  const int64_t tm = (rows + 127) / 128 + groups, tn = (n + 127) / 128;
+  return tm <= kMaxGridTiles && tn <= kMaxGridTiles && tm * tn + 8 <= kMaxGridTiles;
+}
+
+// What the gated GEMMs ask of their operands; `n` rows of B (of a group).
+mxq_status gated_check(mxq_format fmt, int64_t rows, int64_t inter, int64_t n, int64_t K, const void* A, const void* sA,
+                       const void* B, const void* sB) {
+  if (!A || !B) return MXQ_ERR_NULL;
+  const bool scaled = fmt == MXQ_MXFP8 || fmt == MXQ_NVFP4;
+  if (scaled && (!sA || !sB)) return MXQ_ERR_NULL;
+  if (inter % 8 || K % (scaled ? 32 : 8) || K > kMaxGemmK) return MXQ_ERR_SHAPE;
+  // the rows of B that a tile reads, gate and up, lie within 32-bit offsets
+  if (inter > kMaxGridBlocks || (K > 0 && n > 0x7FFFFFFF / (gemm_row_bytes(fmt, K) > 0 ? gemm_row_bytes(fmt, K) : 1)))
+    return MXQ_ERR_SHAPE;
+  if (!al16(A) || !al16(B) || (scaled && (!al16(sA) || !al16(sB)))) return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+}  // namespace
+
+mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
+                       mxq_scope tA_scope, const void* B, const void* sB, const float* tB, mxq_scope tB_scope, void* h,
+                       void* gate_up, void* stream) {
+  if (M < 0 || inter < 0 || K < 0) return MXQ_ERR_SHAPE;
+  if (fmt != MXQ_MXFP8 && fmt != MXQ_NVFP4 && fmt != MXQ_BF16) return MXQ_ERR_FORMAT;
+  if (M == 0 || inter == 0) return MXQ_OK;
+  int ta = 0, tb = 0;
+  if (fmt == MXQ_NVFP4) {
+    if (!tA || !tB) return MXQ_ERR_NULL;
+    ta = scope_mode(tA_scope);
+    tb = scope_mode(tB_scope);
+    if ((ta != 0 && ta != 1) || (tb != 0 && tb != 1)) return MXQ_ERR_FORMAT;
+    if (!al4(tA) || !al4(tB)) return MXQ_ERR_ALIGN;
+  }
+  if (!h) return MXQ_ERR_NULL;
+  const mxq_status st = gated_check(fmt, M, inter, 2 * inter, K, A, sA, B, sB);
+  if (st != MXQ_OK) return st;
+  if (!tiles_fit(M, 2 * inter, 0)) return MXQ_ERR_SHAPE;
+  if (!al16(h) || !al16(gate_up)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_gemm_swiglu((int)fmt, M, inter, K, A, sA, tA, ta, B, sB, tB, tb, h, gate_up, S(stream)));
+}
+
+mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
+                                const void* B, const void* sB, const void* gate_up, mxq_out_dtype gu_dtype,
+                                void* d_gate_up, void* h, void* stream) {
+  if (M < 0 || inter < 0 || K < 0) return MXQ_ERR_SHAPE;
+  if ((fmt != MXQ_MXFP8 && fmt != MXQ_BF16) || !is_dtype(gu_dtype)) return MXQ_ERR_FORMAT;
+  if (M == 0 || inter == 0) return MXQ_OK;
+  if (!gate_up || !d_gate_up) return MXQ_ERR_NULL;
+  const mxq_status st = gated_check(fmt, M, inter, inter, K, A, sA, B, sB);
+  if (st != MXQ_OK) return st;
+  if (!tiles_fit(M, inter, 0)) return MXQ_ERR_SHAPE;
+  if (!al16(gate_up) || !al16(d_gate_up) || !al16(h)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_gemm_swiglu_backward((int)fmt, M, inter, K, A, sA, B, sB, gate_up,
+                                                     gu_dtype == MXQ_OUT_F32, d_gate_up, h, S(stream)));
+}
+
+mxq_status grouped_gemm_swiglu(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
+                               int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
+                               const float* tA, mxq_scope tA_scope, const void* B, const void* sB, const float* tB,
+                               mxq_scope tB_scope, void* h, void* gate_up, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (groups < 0 || total < 0 || inter < 0 || K < 0 || (a_row_index && a_rows < 0)) return MXQ_ERR_SHAPE;
+  if (fmt != MXQ_NVFP4 && fmt != MXQ_BF16) return MXQ_ERR_FORMAT;
+  if (groups == 0 || total == 0 || inter == 0) return MXQ_OK;
+  int ta = 0, tb = 0;
+  if (fmt == MXQ_NVFP4) {
+    if (!tA || !tB) return MXQ_ERR_NULL;
+    ta = scope_mode(tA_scope);
+    tb = scope_mode(tB_scope);
+    if ((ta != 0 && ta != 1) || (tb != 0 && tb != 2)) return MXQ_ERR_FORMAT;   // B: a row's scale, or an expert's
+    if (!al4(tA) || !al4(tB)) return MXQ_ERR_ALIGN;
+  }
+  if (!offsets || !h) return MXQ_ERR_NULL;
+  const mxq_status st = gated_check(fmt, total, inter, 2 * inter, K, A, sA, B, sB);
+  if (st != MXQ_OK) return st;
+  if (a_row_index && K > 0 && a_rows > 0x7FFFFFFF / gemm_row_bytes(fmt, K)) return MXQ_ERR_SHAPE;
+  if (!tiles_fit(total, 2 * inter, groups)) return MXQ_ERR_SHAPE;
+  if (!al8(offsets) || !al4(a_row_index) || !al16(h) || !al16(gate_up)) return MXQ_ERR_ALIGN;
+  if (!workspace || workspace_bytes < mxq::grouped_gemm_ws_bytes(groups)) return MXQ_ERR_WORKSPACE;
+  if (!al16(workspace)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_grouped_gemm_swiglu((int)fmt, groups, offsets, total, inter, K, a_row_index,
+                                                    a_row_index ? a_rows : total, A, sA, tA, ta, B, sB, tB, tb, h,
+                                                    gate_up, workspace, S(stream)));
+}
+
+mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total,
+                                        int64_t inter, int64_t K, const void* A, const void* B, const void* sB,
+                                        const float* tB, const void* gate_up, mxq_out_dtype gu_dtype, void* d_gate_up,
+                                        void* h, void* workspace, size_t workspace_bytes, void* stream) {
+  if (groups < 0 || total < 0 || inter < 0 || K < 0) return MXQ_ERR_SHAPE;
+  if ((fmt != MXQ_BF16_NVFP4T && fmt != MXQ_BF16) || !is_dtype(gu_dtype)) return MXQ_ERR_FORMAT;
+  if (groups == 0 || total == 0 || inter == 0) return MXQ_OK;
+  if (!offsets || !gate_up || !d_gate_up || (fmt == MXQ_BF16_NVFP4T && (!sB || !tB))) return MXQ_ERR_NULL;
+  const mxq_status st = gated_check(MXQ_BF16, total, inter, fmt == MXQ_BF16 ? inter : 0, K, A, nullptr, B, nullptr);
+  if (st != MXQ_OK) return st;
+  if (fmt == MXQ_BF16_NVFP4T && (inter % 16 || (inter > 0 && K / 2 > 0x7FFFFFFF / inter))) return MXQ_ERR_SHAPE;
+  if (!tiles_fit(total, inter, groups)) return MXQ_ERR_SHAPE;
+  if (!al8(offsets) || !al16(gate_up) || !al16(d_gate_up) || !al16(h) || (fmt == MXQ_BF16_NVFP4T && !al4(tB)))
+    return MXQ_ERR_ALIGN;
+  if (!workspace || workspace_bytes < mxq::grouped_gemm_ws_bytes(groups)) return MXQ_ERR_WORKSPACE;
+  if (!al16(workspace)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_grouped_gemm_swiglu_backward(fmt == MXQ_BF16 ? 3 : 7, groups, offsets, total, inter, K, A, B,
+                                                             sB, tB, gate_up, gu_dtype == MXQ_OUT_F32, d_gate_up, h,
+                                                             workspace, S(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Matrix-vector products with 4-bit weights
+// ---------------------------------------------------------------------------
+
+namespace {
+// Weights of `rows` rows in all, x or h rows of K elements.
+mxq_status gemv_check(mxq_format fmt, int64_t K, const void* x, int64_t ld_x, const void* w, const void* s,
+                      const float* t, mxq_scope scope, mxq_scope wide) {
+  if (!x || !w || !s || (fmt == MXQ_NVFP4 && !t)) return MXQ_ERR_NULL;
+  if (fmt == MXQ_NVFP4 && scope != MXQ_SCOPE_ROW && scope != wide) return MXQ_ERR_FORMAT;
+  if (K < 32 || K % 32 || K > kMaxGemmK || ld_x < K) return MXQ_ERR_SHAPE;
+  if (ld_x % 8 || !al16(x) || !al16(w) || (fmt == MXQ_NVFP4 && ((reinterpret_cast<uintptr_t>(s) & 1u) || !al4(t))))
+    return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+mxq_status gemv_any(mxq_format fmt, int gated, int64_t rows, int64_t n, int64_t K, const void* x, int64_t ld_x,
+                    const void* w, const void* s, const float* t, mxq_scope scope, void* y, int64_t ld_y, int out32,
+                    void* stream) {
+  if (rows < 0 || rows > kMaxDecodeRows || n < 0) return MXQ_ERR_SHAPE;
+  if (fmt != MXQ_NVFP4 && fmt != MXQ_MXFP4) return MXQ_ERR_FORMAT;
+  if (rows == 0 || n == 0) return MXQ_OK;
+  if (!y) return MXQ_ERR_NULL;
+  const mxq_status st = gemv_check(fmt, K, x, ld_x, w, s, t, scope, MXQ_SCOPE_TENSOR);
+  if (st != MXQ_OK) return st;
+  if (ld_y < n || (n + 15) / 16 > kMaxGridTiles / 4) return MXQ_ERR_SHAPE;
+  if (out32 ? !al4(y) : (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_gemv((int)fmt, gated, rows, n, K, x, ld_x, w, s, t, scope == MXQ_SCOPE_ROW ? 0 : 1, y, ld_y,
+                                     out32, S(stream)));
+}
+
+// The sizes of the two decode calls over experts; `n` product rows.
+bool decode_sizes(int64_t tokens, int64_t topk, int64_t experts, int64_t n) {
+  return tokens >= 0 && tokens <= kMaxDecodeRows && topk >= 0 && topk <= kMaxTopk && experts >= 0 &&
+         experts <= kMaxExperts && n >= 0 && (n + 15) / 16 <= kMaxGridTiles / 4096;
+}
+}  // namespace
+
+mxq_status gemv_block_scaled(mxq_format fmt, int64_t rows, int64_t N, int64_t K, const void* x, int64_t ld_x,
+                             const void* W, const void* sW, const float* tW, mxq_scope tW_scope, void* y,
+                             mxq_out_dtype y_dtype, int64_t ld_y, void* stream) {
+  if (!is_dtype(y_dtype)) return MXQ_ERR_FORMAT;
+  return gemv_any(fmt, 0, rows, N, K, x, ld_x, W, sW, tW, tW_scope, y, ld_y, y_dtype == MXQ_OUT_F32, stream);
+}
+
+mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, const void* x, int64_t ld_x, const void* W,
+                       const void* sW, const float* tW, mxq_scope tW_scope, void* h, int64_t ld_h, void* stream) {
+  return gemv_any(fmt, 1, rows, inter, K, x, ld_x, W, sW, tW, tW_scope, h, ld_h, 0, stream);
+}
+
+mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
+                              const void* x, int64_t ld_x, const int32_t* topk_idx, const void* W, const void* sW,
+                              const float* tW, mxq_scope tW_scope, void* h, void* stream) {
+  if (!decode_sizes(tokens, topk, experts, inter)) return MXQ_ERR_SHAPE;
+  if (fmt != MXQ_NVFP4 && fmt != MXQ_MXFP4) return MXQ_ERR_FORMAT;
+  if (tokens == 0 || topk == 0 || inter == 0) return MXQ_OK;
+  if (experts == 0) return MXQ_ERR_SHAPE;
+  if (!topk_idx || !h) return MXQ_ERR_NULL;
+  const mxq_status st = gemv_check(fmt, K, x, ld_x, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
+  if (st != MXQ_OK) return st;
+  if (!al4(topk_idx) || (reinterpret_cast<uintptr_t>(h) & 1u)) return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_decode_gate_up((int)fmt, tokens, topk, experts, inter, K, x, ld_x, topk_idx, W, sW, tW,
+                                               tW_scope == MXQ_SCOPE_ROW ? 0 : 1, h, S(stream)));
+}
+
+mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t hidden, int64_t K,
+                           const void* h, const int32_t* topk_idx, const float* weights, const void* W, const void* sW,
+                           const float* tW, mxq_scope tW_scope, void* y, mxq_out_dtype y_dtype, void* stream) {
+  if (!decode_sizes(tokens, topk, experts, hidden)) return MXQ_ERR_SHAPE;
+  if ((fmt != MXQ_NVFP4 && fmt != MXQ_MXFP4) || !is_dtype(y_dtype)) return MXQ_ERR_FORMAT;
+  if (tokens == 0 || hidden == 0) return MXQ_OK;
+  if (topk == 0 || experts == 0) return MXQ_ERR_SHAPE;
+  if (!topk_idx || !weights || !y) return MXQ_ERR_NULL;
+  const mxq_status st = gemv_check(fmt, K, h, K, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
+  if (st != MXQ_OK) return st;
+  if (!al4(topk_idx) || !al4(weights) ||
+      (y_dtype == MXQ_OUT_F32 ? !al4(y) : (reinterpret_cast<uintptr_t>(y) & 1u) != 0))
+    return MXQ_ERR_ALIGN;
+  return hip_status(mxq::launch_decode_down((int)fmt, tokens, topk, experts, hidden, K, h, topk_idx, weights, W, sW, tW,
+                                            tW_scope == MXQ_SCOPE_ROW ? 0 : 1, y, y_dtype == MXQ_OUT_F32, S(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,205 @@
+// Gated feed-forward block: both projections, SwiGLU and the product in one kernel, and the
+// gradient of that.
+//   forward   (g | u) = A_hat W_gu_hat^T;  h = g sigma(g) u, and (g | u) kept for the backward
+//   backward  dh = dO_hat W_d_hat;  d_gate = dh u sigma(g) (1 + g (1 - sigma(g)));  d_up = dh g sigma(g)
+// Dense and per expert. The product is the tile loop of gemm_tile.h; what is new is how a tile's
+// columns are chosen (a wave holds the gate and the up of the same h columns) and its epilogue:
+// the FP32 product never reaches memory, each output is rounded to BF16 once, from the FP32 sums.
+// SwiGLU experts whose gate and up projections enter one fused GEMM: remio.ai ("Miles Blackwell RL"),
+// section "Un Cuantizador Compartido Es el Mecanismo Real".
+#include "gemm_tile.h"
+
+namespace mxq {
+
+void launch_tile_prefix(const int64_t* offsets, int64_t groups, int64_t total, int64_t bm, int64_t tiles_n, int64_t* prefix,
+                        hipStream_t st);
+
+// h columns of a tile
+template <int BN, int EPI> constexpr int kTileCols = EPI == 1 ? BN / 2 : BN;
+
+template <int LD, int BT, int SM, bool WIDE, int EPI>
+__global__ void __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1)))
+gated_dense_kernel(ExactProblem p, GatedArgs ga, int64_t tiles_m, int64_t tiles_n) {
+  using C = gx::Cfg<LD, BT, BT, SM, 1, WIDE, EPI>;
+  MXQ_EXACT_LDS(C)
+  int64_t tm, tn;
+  if (!exact_map_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
+  exact_gemm_tile<LD, BT, BT, SM, 1, WIDE, false, false, EPI>(p, tm * BT, tn * kTileCols<BT, EPI>, lds0, lds1, lds2, lds3,
+                                                              ldsc, ga);
+}
+
+// Per expert: group g covers the slots [offsets[g], offsets[g + 1]); tile order as in
+// exact_grouped_kernel (each XCD a contiguous run, bands of row tiles down a weight slab).
+constexpr int kGatedBand = 4;
+template <int LD, int BM, int BN, int SM, int OCC, int EPI>
+__global__ void __launch_bounds__(256, OCC) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+gated_grouped_kernel(ExactProblem base, GatedArgs ga, const int64_t* __restrict__ offsets,
+                     const int64_t* __restrict__ tile_prefix, int64_t groups, int64_t tiles_n) {
+  using C = gx::Cfg<LD, BM, BN, SM, OCC, false, EPI>;
+  MXQ_EXACT_LDS(C)
+  const int64_t total = tile_prefix[groups];
+  const int64_t T8 = (total + 7) / 8;
+  if ((int64_t)blockIdx.x >= 8 * T8) return;              // the grid may exceed the tile count
+  const int64_t tile = (int64_t)blockIdx.x % 8 * T8 + blockIdx.x / 8;
+  if (tile >= total) return;
+  const int64_t g = find_group(tile_prefix, groups, tile);
+  const int64_t local = tile - tile_prefix[g];
+  const int64_t tiles_m = (tile_prefix[g + 1] - tile_prefix[g]) / tiles_n;
+  const int64_t band = local / (kGatedBand * tiles_n);
+  const int64_t rows_in_band = min((int64_t)kGatedBand, tiles_m - band * kGatedBand);
+  const int64_t idx = local - band * kGatedBand * tiles_n;
+  const int64_t tm = band * kGatedBand + idx % rows_in_band, tn = idx / rows_in_band;
+  ExactProblem p = base;
+  p.a_base = offsets[g];
+  p.m_valid = offsets[g + 1] - offsets[g];
+  const int64_t n = EPI == 1 ? 2 * ga.inter : ga.inter;   // rows of the expert's B
+  if constexpr (LD == 6) {                                // K rows of inter NVFP4 elements
+    const int64_t w_elems = g * base.k_end * base.ldb;
+    p.B = base.B + w_elems / 2;
+    p.sB = base.sB + w_elems / 16;
+    p.tB = base.tB + g;
+  } else {
+    const int64_t b_elems = g * n * base.ldb;
+    p.B = base.B + k_bytes<LD>(b_elems);
+    if constexpr (LD == 2) {
+      p.sB = base.sB + b_elems / 16;
+      if (base.tB_mode == 2) { p.tB = base.tB + g; p.tB_mode = 1; }
+      else p.tB = base.tB + g * n;
+    }
+  }
+  constexpr bool PART = LD == 2;                          // expert tails, as in exact_grouped_kernel
+  exact_gemm_tile<LD, BM, BN, SM, OCC, false, false, PART, EPI>(p, tm * BM, tn * kTileCols<BN, EPI>, lds0, lds1, lds2, lds3,
+                                                                ldsc, ga);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+static ExactProblem gated_problem(int64_t rows, int64_t n, int64_t K, const void* A, const void* sA, const float* tA,
+                                  int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode) {
+  ExactProblem p;
+  p.A = (const uint8_t*)A; p.sA = (const uint8_t*)sA; p.tA = tA; p.tA_mode = tA_mode;
+  p.a_idx = nullptr; p.a_rows = rows; p.a_base = 0; p.m_valid = rows; p.lda = K;
+  p.B = (const uint8_t*)B; p.sB = (const uint8_t*)sB; p.tB = tB; p.tB_mode = tB_mode; p.n_valid = n; p.ldb = K;
+  p.k_begin = 0; p.k_end = K; p.C = nullptr; p.ldc = 0;
+  return p;
+}
+
+// As the plain GEMMs choose: 2 where K fills whole stages and the scale rows start 16-byte aligned, 1
+// where K fills whole stages, else 0.
+static int gated_scale_mode(int ld, int64_t K) {
+  if (K % 64) return 0;
+  return ld == 1 && K % 512 == 0 ? 2 : ld == 2 && K % 256 == 0 ? 2 : 1;
+}
+
+template <int LD, int SM, int EPI>
+static void launch_gated_dense_t(const ExactProblem& p, const GatedArgs& ga, hipStream_t st) {
+  constexpr bool WIDE = SM == 2;
+  auto go = [&](auto BTC) {
+    constexpr int BT = decltype(BTC)::value;
+    const int64_t tm = (p.m_valid + BT - 1) / BT, tn = (ga.inter + kTileCols<BT, EPI> - 1) / kTileCols<BT, EPI>;
+    hipLaunchKernelGGL((gated_dense_kernel<LD, BT, SM, WIDE, EPI>), dim3((unsigned)((tm * tn + 7) / 8 * 8)), dim3(256), 0,
+                       st, p, ga, tm, tn);
+  };
+  // 256 x 256 unless that leaves most of the 256 CUs idle
+  const int64_t n = EPI == 1 ? 2 * ga.inter : ga.inter;
+  if (((p.m_valid + 255) / 256) * ((n + 255) / 256) >= 192) go(ic<256>{});
+  else go(ic<128>{});
+}
+
+template <int LD, int EPI>
+static void launch_gated_dense_ld(const ExactProblem& p, const GatedArgs& ga, hipStream_t st) {
+  const int sm = gated_scale_mode(LD, p.lda);
+  if constexpr (LD != 0) {
+    if (sm == 2) { launch_gated_dense_t<LD, 2, EPI>(p, ga, st); return; }
+  }
+  if (sm >= 1) launch_gated_dense_t<LD, 1, EPI>(p, ga, st);
+  else launch_gated_dense_t<LD, 0, EPI>(p, ga, st);
+}
+
+// fmt: 1 MXFP8, 2 NVFP4, 3 BF16
+hipError_t launch_gemm_swiglu(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
+                              int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode, void* h,
+                              void* gate_up, hipStream_t st) {
+  const ExactProblem p = gated_problem(M, inter, K, A, sA, tA, tA_mode, B, sB, tB, tB_mode);
+  const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)gate_up, nullptr, 0};
+  if (fmt == 1) launch_gated_dense_ld<1, 1>(p, ga, st);
+  else if (fmt == 2) launch_gated_dense_ld<2, 1>(p, ga, st);
+  else launch_gated_dense_ld<0, 1>(p, ga, st);
+  return hipGetLastError();
+}
+
+// fmt: 1 MXFP8, 3 BF16
+hipError_t launch_gemm_swiglu_backward(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
+                                       const void* B, const void* sB, const void* gate_up, int gu32, void* d_gate_up,
+                                       void* h, hipStream_t st) {
+  const ExactProblem p = gated_problem(M, inter, K, A, sA, nullptr, 0, B, sB, nullptr, 0);
+  const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)d_gate_up, gate_up, gu32};
+  if (fmt == 1) launch_gated_dense_ld<1, 2>(p, ga, st);
+  else launch_gated_dense_ld<0, 2>(p, ga, st);
+  return hipGetLastError();
+}
+
+template <int LD, int BM, int BN, int SM, int OCC, int EPI>
+static void launch_gated_grouped_t(const ExactProblem& p, const GatedArgs& ga, const int64_t* offsets, int64_t groups,
+                                   int64_t total, int64_t* prefix, hipStream_t st) {
+  const int64_t tn = (ga.inter + kTileCols<BN, EPI> - 1) / kTileCols<BN, EPI>;
+  launch_tile_prefix(offsets, groups, total, BM, tn, prefix, st);
+  // an upper bound on the tiles, a multiple of 8 so that the XCD order reaches every one
+  const int64_t tiles = (((total + BM - 1) / BM + groups) * tn + 7) / 8 * 8;
+  hipLaunchKernelGGL((gated_grouped_kernel<LD, BM, BN, SM, OCC, EPI>), dim3((unsigned)tiles), dim3(256), 0, st, p, ga,
+                     offsets, prefix, groups, tn);
+}
+
+template <int EPI>
+static void launch_gated_grouped_bf16(const ExactProblem& p, const GatedArgs& ga, const int64_t* offsets, int64_t groups,
+                                      int64_t total, int64_t* prefix, hipStream_t st) {
+  auto by_sm = [&](auto SMC) {
+    constexpr int SM = decltype(SMC)::value;
+    // experts of 384 rows and more on average fill 256-row tiles
+    if (total / groups >= 384) launch_gated_grouped_t<0, 256, 256, SM, 1, EPI>(p, ga, offsets, groups, total, prefix, st);
+    else launch_gated_grouped_t<0, 128, 128, SM, 2, EPI>(p, ga, offsets, groups, total, prefix, st);
+  };
+  if (gated_scale_mode(0, p.lda)) by_sm(ic<1>{});
+  else by_sm(ic<0>{});
+}
+
+// fmt: 2 NVFP4, 3 BF16
+hipError_t launch_grouped_gemm_swiglu(int fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
+                                      int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
+                                      const float* tA, int tA_mode, const void* B, const void* sB, const float* tB,
+                                      int tB_mode, void* h, void* gate_up, void* ws, hipStream_t st) {
+  ExactProblem p = gated_problem(0, inter, K, A, sA, tA, tA_mode, B, sB, tB, tB_mode);
+  p.a_idx = a_row_index; p.a_rows = a_rows;
+  const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)gate_up, nullptr, 0};
+  int64_t* prefix = (int64_t*)ws;
+  if (fmt == 2) {
+    const int sm = gated_scale_mode(2, K);
+    if (sm == 2) launch_gated_grouped_t<2, 128, 256, 2, 2, 1>(p, ga, offsets, groups, total, prefix, st);
+    else if (sm == 1) launch_gated_grouped_t<2, 128, 128, 1, 2, 1>(p, ga, offsets, groups, total, prefix, st);
+    else launch_gated_grouped_t<2, 128, 128, 0, 2, 1>(p, ga, offsets, groups, total, prefix, st);
+  } else {
+    launch_gated_grouped_bf16<1>(p, ga, offsets, groups, total, prefix, st);
+  }
+  return hipGetLastError();
+}
+
+// fmt: 3 BF16 (B the stacked (inter, K) transposes of W_d), 7 BF16 A x the stacked NVFP4 W_d (K, inter)
+hipError_t launch_grouped_gemm_swiglu_backward(int fmt, int64_t groups, const int64_t* offsets, int64_t total,
+                                               int64_t inter, int64_t K, const void* A, const void* B, const void* sB,
+                                               const float* tB, const void* gate_up, int gu32, void* d_gate_up, void* h,
+                                               void* ws, hipStream_t st) {
+  ExactProblem p = gated_problem(0, inter, K, A, nullptr, nullptr, 0, B, sB, tB, 0);
+  const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)d_gate_up, gate_up, gu32};
+  int64_t* prefix = (int64_t*)ws;
+  if (fmt == 7) {
+    p.ldb = inter;
+    launch_gated_grouped_t<6, 256, 256, 0, 1, 2>(p, ga, offsets, groups, total, prefix, st);
+  } else {
+    launch_gated_grouped_bf16<2>(p, ga, offsets, groups, total, prefix, st);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mxq

@@ -1,0 +1,36 @@
+// SwiGLU and its gradient in binary32, for the epilogues that round the result to BF16.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace mxq {
+
+// e = e^-|g| <= 1 never overflows; with r = 1 / (1 + e): sigma(g) = r (g >= 0) or e r, 1 - sigma(g) = e r
+// or r, neither by cancellation. Binary32: expf and the reciprocal are good to an ulp or two each, so
+// every value below is within 2^-20 of the exact one, far inside the BF16 rounding that follows. A gate
+// so far out that sigma is 0 gives 0 (also at -Inf, where g sigma would be a NaN).
+__device__ __forceinline__ void sigmoid_pair(float g, float& s, float& c) {
+  const float e = expf(-fabsf(g));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  const float er = e * r;
+  s = g < 0.0f ? er : r;
+  c = g < 0.0f ? r : er;
+  if (g != g) s = c = g;
+}
+// h = g sigma(g) u
+__device__ __forceinline__ float swiglu_forward(float g, float u) {
+  float s, c;
+  sigmoid_pair(g, s, c);
+  return (s == 0.0f ? 0.0f : g * s) * u;
+}
+// dg = dh u sigma (1 + g (1 - sigma)), du = dh g sigma, h = g sigma u
+__device__ __forceinline__ void swiglu_backward(float dh, float g, float u, float& dg, float& du, float& h) {
+  float s, c;
+  sigmoid_pair(g, s, c);
+  const float si = s == 0.0f ? 0.0f : g * s;
+  const float ds = s == 0.0f ? 0.0f : c == 0.0f ? s : s * (1.0f + g * c);
+  dg = dh * u * ds;
+  du = dh * si;
+  h = si * u;
+}
+
+}  // namespace mxq
