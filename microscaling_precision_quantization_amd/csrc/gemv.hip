@@ -63,6 +63,17 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* s) {
   else return *s;
 }
 
+// ... as what multiplies the lane's first and second 16 K.
+template <int FMT>
+__device__ __forceinline__ void scales_of(uint32_t codes, float (&S)[2]) {
+  if constexpr (FMT == 2) {
+    S[0] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 0);
+    S[1] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 1);
+  } else {
+    S[0] = S[1] = __uint_as_float(codes << 23);
+  }
+}
+
 // acc[nt][tt] += the products of NT row tiles and TT column tiles over chunks [c0, c1). wp, sp: the lane's
 // row (bytes, scales) at its 32 K of chunk 0; xp: its x row there; on[tt]: the lane's column exists.
 template <int FMT, int NT, int TT>
@@ -84,7 +95,7 @@ __device__ __forceinline__ void dot(const uint8_t* const (&wp)[NT], const uint8_
         w[u][n] = make_uint4(0, 0, 0, 0);
         s[u][n] = 0;
         if (in) {
-          w[u][n] = load_stream16(wp[n] + (int64_t)(c + u) * (kChunk / 2));
+          w[u][n] = *reinterpret_cast<const uint4*>(wp[n] + (int64_t)(c + u) * (kChunk / 2));
           s[u][n] = load_codes<FMT>(sp[n] + (int64_t)(c + u) * SB);
         }
       }
@@ -102,12 +113,7 @@ __device__ __forceinline__ void dot(const uint8_t* const (&wp)[NT], const uint8_
       for (int n = 0; n < NT; ++n) {
         const uint32_t d[4] = {w[u][n].x, w[u][n].y, w[u][n].z, w[u][n].w};
         float S[2];
-        if constexpr (FMT == 2) {
-          S[0] = __builtin_amdgcn_cvt_f32_fp8((int)s[u][n], 0);
-          S[1] = __builtin_amdgcn_cvt_f32_fp8((int)s[u][n], 1);
-        } else {
-          S[0] = S[1] = __uint_as_float(s[u][n] << 23);
-        }
+        scales_of<FMT>(s[u][n], S);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const v8bf a = weights8<FMT>(d[i], S[i / 2]);
@@ -119,6 +125,70 @@ __device__ __forceinline__ void dot(const uint8_t* const (&wp)[NT], const uint8_
   }
 }
 
+// The same for at most four x rows, where a column tile of 16 would be mostly empty and cost four loads of x
+// for each of weights: the free columns split K further. MFMA row i = (weight row i / 4 of four, K segment i % 4),
+// column j = (x row j / 4, segment j % 4), a lane's segment 32 K; only where both segments agree is a
+// product of the row and the column, so of a lane's four accumulators one counts, and the four lanes of a
+// quad hold the segments' sums. A chunk is 512 K of 16 weight rows: four loads of weights, 64 consecutive
+// bytes of a row to four lanes, and four of x.
+constexpr int kWide = 512;
+template <int FMT, int NT>
+__device__ __forceinline__ void dot4(const uint8_t* const (&wp)[NT], const uint8_t* const (&sp)[NT], int64_t row_bytes,
+                                     int64_t row_scales, const int (&step)[4], const uint16_t* xp, bool on, int K, int c0,
+                                     int c1, v4f (&acc)[NT][4]) {
+  constexpr int SB = FMT == 2 ? 32 : 16;                  // scale bytes of a row and chunk
+  const int lane = threadIdx.x & 63;
+  const int at = 128 * (lane >> 4) + 32 * (lane & 3);     // the lane's K of a chunk
+  for (int c = c0; c < c1; ++c) {
+    uint4 w[NT][4], x[4];
+    uint32_t s[NT][4];
+    const bool in = c * kWide + at < K;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        w[n][r] = make_uint4(0, 0, 0, 0);
+        if (in) w[n][r] = *reinterpret_cast<const uint4*>(wp[n] + step[r] * row_bytes + (int64_t)c * (kWide / 2));
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[n][r] = 0;
+        if (in) s[n][r] = load_codes<FMT>(sp[n] + step[r] * row_scales + (int64_t)c * SB);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (in && on) x[i] = *reinterpret_cast<const uint4*>(xp + (int64_t)c * kWide + 8 * i);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t d[4] = {w[n][r].x, w[n][r].y, w[n][r].z, w[n][r].w};
+        float S[2];
+        scales_of<FMT>(s[n][r], S);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[n][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<FMT>(d[i], S[i / 2]), as_bf(x[i]), acc[n][r], 0, 0, 0);
+      }
+  }
+}
+// Lane l's result: weight row 4 (l % 4) + l / 16 of the tile, x row (l % 16) / 4.
+__device__ __forceinline__ float gather4(const v4f (&acc)[4]) {
+  const int seg = threadIdx.x & 3;
+  float out = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    float v = seg == 0 ? acc[r][0] : seg == 1 ? acc[r][1] : seg == 2 ? acc[r][2] : acc[r][3];
+    v += __uint_as_float(dpp_xor1(__float_as_uint(v)));
+    v += __uint_as_float(dpp_xor2(__float_as_uint(v)));
+    if (seg == r) out = v;
+  }
+  return out;
+}
+
 // The wave's share of a row tile's chunks.
 __device__ __forceinline__ void share(int chunks, int part, int parts, int& c0, int& c1) {
   const int per = (chunks + parts - 1) / parts;
@@ -126,24 +196,39 @@ __device__ __forceinline__ void share(int chunks, int part, int parts, int& c0, 
   c1 = min(c0 + per, chunks);
 }
 
-// Choices of expert e, in order: lane l gets the (first + l % 16)-th, or -1; the return value is how many
-// there are in all. `col`: 16 ints of LDS of the wave's own.
+// Choices of expert e, in order: the lane gets the (first + q)-th, q = lane % 16 / 4 its x row, or -1; the return
+// value is how many there are in all. `col`: four ints of LDS of the wave's own.
 __device__ __forceinline__ int choices_of(const int32_t* idx, int n, int e, int first, int* col, int& mine) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, q = (lane >> 2) & 3;
   int seen = 0;
   for (int b = 0; b < n; b += 64) {
     const bool hit = b + lane < n && idx[b + lane] == e;
     const uint64_t m = __ballot(hit);
     const int at = seen + __popcll(m & ((1ull << lane) - 1)) - first;
-    if (hit && at >= 0 && at < kTile) col[at] = b + lane;
+    if (hit && at >= 0 && at < 4) col[at] = b + lane;
     seen += __popcll(m);
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0)
   __builtin_amdgcn_wave_barrier();
-  mine = first + lane % kTile < seen ? col[lane % kTile] : -1;
+  mine = first + q < seen ? col[q] : -1;
   __builtin_amdgcn_s_waitcnt(0xC07F);
   __builtin_amdgcn_wave_barrier();
   return seen;
+}
+
+// The lane's weight pointers for dot4: rows 4 r + (l % 16) / 4 of the tile at row0 + n0, step[r] rows on from
+// the first; rows past the end (n rows) are the last one again, and what they give is not stored.
+template <int FMT>
+__device__ __forceinline__ void rows4(const uint8_t* w, const uint8_t* s, int64_t row0, int64_t n0, int64_t n, int K,
+                                      const uint8_t*& wp, const uint8_t*& sp, int (&step)[4]) {
+  const int lane = threadIdx.x & 63, q = (lane >> 2) & 3, seg = 4 * (lane >> 4) + (lane & 3);
+  const int left = (int)min((int64_t)kTile, n - n0) - 1;
+  const int at = min(q, left);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) step[r] = min(4 * r + q, left) - at;
+  const int64_t row = row0 + n0 + at;
+  wp = w + row * (K / 2) + 16 * seg;
+  sp = s + row * (K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * seg;
 }
 
 }  // namespace gv
@@ -167,19 +252,80 @@ struct GemvArgs {
 };
 
 // A workgroup: one tile of 16 rows of the product (gated: the tile's gates and ups), K split over its WV
-// waves. Dense: TT column tiles hold all x rows. Experts: blockIdx.y names the expert, either as itself or
-// (by_choice) as the choice that names it first; its choices come in column tiles of 16, one after another.
-template <int FMT, bool GATED, int TT, bool MOE, int WV>
+// waves; TT column tiles hold all x rows.
+template <int FMT, bool GATED, int TT, int WV>
 __global__ void __launch_bounds__(64 * WV)
-gemv_kernel(GemvArgs a, int by_choice) {
+gemv_kernel(GemvArgs a) {
   using namespace gv;
   constexpr int NT = GATED ? 2 : 1;
   __shared__ float part[WV][NT][TT][4][64];
-  __shared__ int col[WV][kTile];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * kTile;
-  const int64_t all = GATED ? 2 * a.n : a.n;              // weight rows (of an expert)
+  const uint8_t *wp[NT], *sp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // rows past the end read the last one's bytes; what they give is not stored
+    const int64_t row = n * a.n + min(n0 + lane % kTile, a.n - 1);
+    wp[n] = a.w + row * (a.K / 2) + 16 * g;
+    sp[n] = a.s + row * (a.K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * g;
+  }
+  int c0, c1;
+  share((a.K + kChunk - 1) / kChunk, wave, WV, c0, c1);
+  const uint16_t* xp[TT];
+  bool on[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int r = t * kTile + lane % kTile;
+    on[t] = r < a.rows;
+    xp[t] = a.x + (on[t] ? r : 0) * a.ld_x + 32 * g;
+  }
+  v4f acc[NT][TT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  dot<FMT, NT, TT>(wp, sp, xp, on, a.K, c0, c1, acc);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[wave][n][t][r][lane] = acc[n][t][r];
+  __syncthreads();
+  // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
+  for (int o = tid; o < TT * 256; o += 64 * WV) {
+    const int t = o >> 8, n = o & 15, c = (o >> 4) & 15;
+    const int l = 16 * (n >> 2) + c, r = n & 3, at = t * kTile + c;
+    if (at >= a.rows || n0 + n >= a.n) continue;
+    float y[NT];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      float v = part[0][k][t][r][l];
+#pragma unroll
+      for (int w = 1; w < WV; ++w) v += part[w][k][t][r][l];
+      if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? k * a.n + n0 + n : 0];
+      y[k] = v;
+    }
+    const int64_t to = at * a.ld_y + n0 + n;
+    if constexpr (GATED) ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(swiglu_forward(y[0], y[1]));
+    else if (a.out32) ((float*)a.y)[to] = y[0];
+    else ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(y[0]);
+  }
+}
+
+// At most four x rows at a time (dot4). Dense: all of them. Experts: blockIdx.y names the expert, either as
+// itself or (by_choice) as the choice that names it first; its choices come four by four.
+template <int FMT, bool GATED, bool MOE, int WV>
+__global__ void __launch_bounds__(64 * WV)
+gemv4_kernel(GemvArgs a, int by_choice) {
+  using namespace gv;
+  constexpr int NT = GATED ? 2 : 1;
+  __shared__ float part[2][WV][NT][64];
+  __shared__ int col[WV][4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kTile;
   int64_t base = 0;                                       // the expert's first weight row
   int e = 0;
   if constexpr (MOE) {
@@ -198,70 +344,48 @@ gemv_kernel(GemvArgs a, int by_choice) {
       if (tid < kTile && n0 + tid < a.n) ((uint16_t*)a.y)[c * a.ld_y + n0 + tid] = 0;
     }
     if ((unsigned)e >= (unsigned)a.experts) return;
-    base = (int64_t)e * all;
+    base = (int64_t)e * (GATED ? 2 : 1) * a.n;
   }
   const uint8_t *wp[NT], *sp[NT];
+  int step[4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    // rows past the end read the last one's bytes; what they give is not stored
-    const int64_t row = base + n * a.n + min(n0 + lane % kTile, a.n - 1);
-    wp[n] = a.w + row * (a.K / 2) + 16 * g;
-    sp[n] = a.s + row * (a.K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * g;
-  }
+  for (int n = 0; n < NT; ++n) rows4<FMT>(a.w, a.s, base + n * a.n, n0, a.n, a.K, wp[n], sp[n], step);
   int c0, c1;
-  share((a.K + kChunk - 1) / kChunk, wave, WV, c0, c1);
+  share((a.K + kWide - 1) / kWide, wave, WV, c0, c1);
+  const int q = (lane >> 2) & 3, n = 4 * (lane & 3) + (lane >> 4);   // the lane's x row and result row
   int seen = a.rows;
-  for (int first = 0; first < seen; first += kTile * TT) {
-    const uint16_t* xp[TT];
-    bool on[TT];
-    int mine = -1;
+  for (int first = 0, buf = 0; first < seen; first += 4, buf ^= 1) {
+    int mine = first + q < seen ? first + q : -1;
     if constexpr (MOE) {
       seen = choices_of(a.idx, a.rows, e, first, col[wave], mine);
       if (seen == 0) return;                              // an expert nobody chose (all waves alike)
-      on[0] = mine >= 0;
-      xp[0] = a.x + (on[0] ? mine / a.topk : 0) * a.ld_x + 32 * g;
-    } else {
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int r = first + t * kTile + lane % kTile;
-        on[t] = r < a.rows;
-        xp[t] = a.x + (on[t] ? r : 0) * a.ld_x + 32 * g;
-      }
     }
-    v4f acc[NT][TT];
+    const bool on = mine >= 0;
+    const uint16_t* xp = a.x + (on ? (MOE ? mine / a.topk : mine) : 0) * a.ld_x + 128 * (lane >> 4) + 32 * (lane & 3);
+    v4f acc[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int k = 0; k < NT; ++k)
 #pragma unroll
-      for (int t = 0; t < TT; ++t) acc[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    dot<FMT, NT, TT>(wp, sp, xp, on, a.K, c0, c1, acc);
+      for (int r = 0; r < 4; ++r) acc[k][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    dot4<FMT, NT>(wp, sp, a.K / 2, a.K / (FMT == 2 ? 16 : 32), step, xp, on, a.K, c0, c1, acc);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) part[wave][n][t][r][lane] = acc[n][t][r];
-    __syncthreads();
-    // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
-    for (int o = tid; o < TT * 256; o += 64 * WV) {
-      const int t = o >> 8, n = o & 15, c = (o >> 4) & 15;
-      const int l = 16 * (n >> 2) + c, r = n & 3;
-      const int at = first + t * kTile + c;
-      if (at >= seen || n0 + n >= a.n) continue;
+    for (int k = 0; k < NT; ++k) part[buf][wave][k][lane] = gather4(acc[k]);
+    __syncthreads();                                      // two buffers: the next pass writes the other one
+    if (wave == 0 && on && n0 + n < a.n) {
       float y[NT];
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        float v = part[0][k][t][r][l];
+        float v = part[buf][0][k][lane];
 #pragma unroll
-        for (int w = 1; w < WV; ++w) v += part[w][k][t][r][l];
+        for (int w = 1; w < WV; ++w) v += part[buf][w][k][lane];
         if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? base + k * a.n + n0 + n : MOE ? e : 0];
         y[k] = v;
       }
-      const int64_t to = (MOE ? col[0][c] : at) * a.ld_y + n0 + n;
+      const int64_t to = mine * a.ld_y + n0 + n;
       if constexpr (GATED) ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(swiglu_forward(y[0], y[1]));
       else if (a.out32) ((float*)a.y)[to] = y[0];
       else ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(y[0]);
     }
-    __syncthreads();                                      // part and col are free again
   }
 }
 
@@ -292,8 +416,8 @@ decode_down_kernel(DownArgs a, int kparts) {
   __shared__ float sum[WV][TCAP][kTile];
   __shared__ int first_of[kMaxDecodeExperts];
   __shared__ int list[kMaxDecodeExperts];                 // the chosen experts, by first choice
-  __shared__ int col[WV][kTile], found[WV];
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
+  __shared__ int col[WV][4], found[WV];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * kTile;
   const int S = a.tokens * a.topk;
@@ -322,33 +446,30 @@ decode_down_kernel(DownArgs a, int kparts) {
     experts += here;
     __syncthreads();
   }
-  const int chunks = (a.K + kChunk - 1) / kChunk;
+  const int chunks = (a.K + kWide - 1) / kWide;
+  const int n = 4 * (lane & 3) + (lane >> 4);             // the lane's result row
   for (int item = wave; item < experts * kparts; item += WV) {
     const int e = __builtin_amdgcn_readfirstlane(list[item / kparts]);
-    int c0, c1;
+    int c0, c1, step[4];
     share(chunks, item % kparts, kparts, c0, c1);
-    const int64_t row = (int64_t)e * a.n + min(n0 + lane % kTile, a.n - 1);
-    const uint8_t* const wp[1] = {a.w + row * (a.K / 2) + 16 * g};
-    const uint8_t* const sp[1] = {a.s + row * (a.K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * g};
+    const uint8_t *wp[1], *sp[1];
+    rows4<FMT>(a.w, a.s, (int64_t)e * a.n, n0, a.n, a.K, wp[0], sp[0], step);
+    float tw = 1.0f;
+    if constexpr (FMT == 2) tw = a.t[a.t_mode == 0 ? (int64_t)e * a.n + min(n0 + n, a.n - 1) : e];
     int seen = 1;
-    for (int first = 0; first < seen; first += kTile) {
+    for (int first = 0; first < seen; first += 4) {
       int mine;
       seen = choices_of(a.idx, S, e, first, col[wave], mine);
-      const bool on[1] = {mine >= 0};
-      const uint16_t* const xp[1] = {a.h + (int64_t)(on[0] ? mine : 0) * a.K + 32 * g};
-      v4f acc[1][1] = {{v4f{0.0f, 0.0f, 0.0f, 0.0f}}};
-      dot<FMT, 1, 1>(wp, sp, xp, on, a.K, c0, c1, acc);
-      if (on[0]) {
-        const float wt = a.weights[mine];
-        float* to = &sum[wave][mine / a.topk][4 * g];
+      const bool on = mine >= 0;
+      const uint16_t* xp = a.h + (int64_t)(on ? mine : 0) * a.K + 128 * (lane >> 4) + 32 * (lane & 3);
+      const float wt = on ? a.weights[mine] : 0.0f;
+      v4f acc[1][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v = acc[0][0][r];
-          if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? (int64_t)e * a.n + min(n0 + 4 * g + r, a.n - 1) : e];
-          // an add in LDS: two lanes meet here where a token names an expert twice
-          atomicAdd(&to[r], wt * v);
-        }
-      }
+      for (int r = 0; r < 4; ++r) acc[0][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      dot4<FMT, 1>(wp, sp, a.K / 2, a.K / (FMT == 2 ? 16 : 32), step, xp, on, a.K, c0, c1, acc);
+      const float v = gather4(acc[0]) * tw;
+      // an add in LDS: two lanes meet here where a token names an expert twice
+      if (on) atomicAdd(&sum[wave][mine / a.topk][n], wt * v);
     }
   }
   __syncthreads();
@@ -381,18 +502,20 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
                    (int)K, y, ld_y, out32};
   const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile));
   by_format(fmt, [&](auto F) {
-    auto go = [&](auto G, auto T) {
+    constexpr int FMT = decltype(F)::value;
+    auto go = [&](auto G) {
+      constexpr bool GATED = decltype(G)::value != 0;
       constexpr int WV = 8;
-      hipLaunchKernelGGL((gemv_kernel<decltype(F)::value, decltype(G)::value != 0, decltype(T)::value, false, WV>), grid,
-                         dim3(64 * WV), 0, st, a, 0);
+      if (rows <= 4) {
+        if (K <= 4 * gv::kWide) hipLaunchKernelGGL((gemv4_kernel<FMT, GATED, false, 4>), grid, dim3(64 * 4), 0, st, a, 0);
+        else hipLaunchKernelGGL((gemv4_kernel<FMT, GATED, false, 8>), grid, dim3(64 * 8), 0, st, a, 0);
+      }
+      else if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, WV>), grid, dim3(64 * WV), 0, st, a);
+      else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, WV>), grid, dim3(64 * WV), 0, st, a);
+      else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, WV>), grid, dim3(64 * WV), 0, st, a);
     };
-    auto by_rows = [&](auto G) {
-      if (rows <= 16) go(G, ic<1>{});
-      else if (rows <= 32) go(G, ic<2>{});
-      else go(G, ic<4>{});
-    };
-    if (gated) by_rows(ic<1>{});
-    else by_rows(ic<0>{});
+    if (gated) go(ic<1>{});
+    else go(ic<0>{});
   });
   return hipGetLastError();
 }
@@ -407,8 +530,9 @@ hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t 
   const int by_choice = S < experts;
   const dim3 grid((unsigned)((inter + gv::kTile - 1) / gv::kTile), (unsigned)(by_choice ? S : experts));
   by_format(fmt, [&](auto F) {
-    constexpr int WV = 8;
-    hipLaunchKernelGGL((gemv_kernel<decltype(F)::value, true, 1, true, WV>), grid, dim3(64 * WV), 0, st, a, by_choice);
+    constexpr int FMT = decltype(F)::value;
+    if (K <= 4 * gv::kWide) hipLaunchKernelGGL((gemv4_kernel<FMT, true, true, 4>), grid, dim3(64 * 4), 0, st, a, by_choice);
+    else hipLaunchKernelGGL((gemv4_kernel<FMT, true, true, 8>), grid, dim3(64 * 8), 0, st, a, by_choice);
   });
   return hipGetLastError();
 }
@@ -420,7 +544,7 @@ hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t exp
                    (const uint8_t*)s, t, t_mode, n, (int)K, y, out32};
   constexpr int WV = 16;
   // parts of K so that a few choices still give every wave one
-  const int64_t S = tokens * topk, chunks = (K + gv::kChunk - 1) / gv::kChunk;
+  const int64_t S = tokens * topk, chunks = (K + gv::kWide - 1) / gv::kWide;
   int kparts = 1;
   while (S * kparts < WV && 2 * kparts <= chunks) kparts *= 2;
   const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile));
