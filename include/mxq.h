@@ -821,8 +821,9 @@ mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const in
  *   fmt : MXQ_NVFP4 (tW: TENSOR or ROW) or MXQ_MXFP4 (tW unused; scale codes s <= 252).
  *   x   : BF16 (rows, K), row stride ld_x (a multiple of 8);  W (N, K/2), sW (N, K/16 or K/32).
  *   y   : (rows, N) y_dtype, row stride ld_y >= N;  h: BF16 (rows, inter), row stride ld_h >= inter.
- *   Requires rows <= 64 (more rows are the GEMMs'), K % 32 == 0, 32 <= K <= 2^22; x and W 16-byte
- *   aligned, NVFP4 scales 2-byte aligned. A row of x reaches only its own row of the result.
+ *   Requires rows <= 64 (more rows are the GEMMs'), K % 32 == 0, 32 <= K <= 2^22, inter K < 2^31, x below
+ *   2^31 bytes from its first row to its last; x and W 16-byte aligned, NVFP4 scales 2-byte aligned.
+ *   A row of x reaches only its own row of the result.
  * ------------------------------------------------------------------------- */
 mxq_status gemv_block_scaled(mxq_format fmt, int64_t rows, int64_t N, int64_t K, const void* x, int64_t ld_x,
                              const void* W, const void* sW, const float* tW, mxq_scope tW_scope, void* y,
@@ -841,7 +842,10 @@ mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, c
  *   x: BF16 (tokens, K), row stride ld_x;  h of the down call: BF16 (tokens, topk, K), contiguous.
  *   W : the experts' (2 inter, K) or (hidden, K) stacked;  fmt MXQ_NVFP4 (tW GROUP -- one an expert --
  *   or ROW) or MXQ_MXFP4.
- *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled.
+ *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled; x (or h) below
+ *   2^31 bytes from its first row to its last.
+ *   workspace (down): mxq_workspace_bytes(MXQ_OP_DECODE_DOWN, tokens, hidden, 0) bytes, 4-byte aligned;
+ *   NULL where that is 0. Calls that may overlap need their own.
  * ------------------------------------------------------------------------- */
 mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
                               const void* x, int64_t ld_x, const int32_t* topk_idx, const void* W, const void* sW,
@@ -849,7 +853,7 @@ mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int6
 mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t hidden, int64_t K,
                            const void* h, const int32_t* topk_idx, const float* weights, const void* W,
                            const void* sW, const float* tW, mxq_scope tW_scope, void* y, mxq_out_dtype y_dtype,
-                           void* stream);
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Queries.
@@ -858,12 +862,14 @@ mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t
  * (MXFP8, MXFP4: rows * cols/32, NVFP4: rows * cols/16); 0 for BF16 or bad shapes. */
 size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols);
 
-enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD = 3, MXQ_OP_ROUTE = 4 };
+enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD = 3, MXQ_OP_ROUTE = 4,
+       MXQ_OP_DECODE_DOWN = 5 };
 /* Workspace bytes for an op:
  *   MXQ_OP_QUANTIZE_NVFP4 (a = rows, b = cols, c = number of FP32 scales);
  *   MXQ_OP_GROUPED_GEMM   (a = groups);
  *   MXQ_OP_NORM_BACKWARD  (a = rows, b = cols);
- *   MXQ_OP_ROUTE          (a = tokens, b = experts). */
+ *   MXQ_OP_ROUTE          (a = tokens, b = experts);
+ *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden). */
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
 
 /* Slots that hold every routing of `tokens` tokens over `experts` experts, topk each, with

@@ -24,7 +24,7 @@ BF16_NVFP4T = 5                    # grouped only: BF16 A x stacked NVFP4 weight
 _PACKED4 = (NVFP4, MXFP4)          # formats with two elements per byte
 OUT_BF16, OUT_F32 = 0, 1
 SCOPE = {"row": 0, "token": 0, "tensor": 1, "group": 2}
-OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE = 1, 2, 3, 4
+OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE, OP_DECODE_DOWN = 1, 2, 3, 4, 5
 GATE = {"none": 0, "token": 1, "channel": 2, "full": 3}
 
 _c_void_p = ctypes.c_void_p
@@ -97,7 +97,7 @@ _SIGS = {
     "moe_decode_gate_up": [_int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
                            _c_void_p, _int, _c_void_p, _c_void_p],
     "moe_decode_down": [_int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
-                        _c_void_p, _int, _c_void_p, _int, _c_void_p],
+                        _c_void_p, _int, _c_void_p, _int, _c_void_p, _size, _c_void_p],
     "mxq_route_slots": [_i64, _i64, _i64, _i64],
     "mxq_scale_bytes": [_int, _i64, _i64],
     "mxq_workspace_bytes": [_int, _i64, _i64, _i64],
@@ -946,7 +946,7 @@ def moe_decode_gate_up(fmt: int, x, topk_idx, W, sW, tW=None, experts: int = 0, 
 
 
 def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int = 0, t_scope: str = "group",
-                    out_dtype: torch.dtype = torch.float32, out=None):
+                    out_dtype: torch.dtype = torch.float32, out=None, workspace=None):
     """y (tokens, hidden) = sum over j of weights[t, j] (h[t, j] W_hat_e^T), FP32 or BF16 (`out`'s type where
     given): the down projection and the combine of a decoding step. h (tokens, topk, inter) BF16 as
     moe_decode_gate_up gives it, W: (experts hidden, inter / 2)."""
@@ -965,8 +965,9 @@ def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int
     c.done()
     if out is None:
         out = torch.empty((T, n), dtype=out_dtype, device=dev)
+    ws = _workspace(OP_DECODE_DOWN, T, n, workspace, dev)
     _call("moe_decode_down", dev, fmt, T, k, experts, n, K, _ptr(h), _ptr(topk_idx), _ptr(weights), _ptr(W), _ptr(sW),
-          _ptr(tW), SCOPE[t_scope], _ptr(out), OUT_F32 if out.dtype == torch.float32 else OUT_BF16)
+          _ptr(tW), SCOPE[t_scope], _ptr(out), OUT_F32 if out.dtype == torch.float32 else OUT_BF16, _ptr(ws), ws.numel())
     return out
 
 

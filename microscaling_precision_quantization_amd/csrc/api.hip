@@ -86,7 +86,8 @@ hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t 
                                  const float* t, int t_mode, void* h, hipStream_t st);
 hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t K, const void* h,
                               const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
-                              int t_mode, void* y, int out32, hipStream_t st);
+                              int t_mode, void* y, int out32, void* ws, hipStream_t st);
+size_t decode_down_ws_bytes(int64_t tokens, int64_t n);
 }  // namespace mxq
 
 namespace {
@@ -150,6 +151,7 @@ size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {
   if (op == MXQ_OP_GROUPED_GEMM) return a > 0 ? mxq::grouped_gemm_ws_bytes(a) : 0;
   if (op == MXQ_OP_NORM_BACKWARD) return a > 0 && b > 0 ? mxq::norm_backward_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_ROUTE) return a > 0 && b > 0 ? mxq::route_ws_bytes(a, b) : 0;
+  if (op == MXQ_OP_DECODE_DOWN) return a > 0 && b > 0 ? mxq::decode_down_ws_bytes(a, b) : 0;
   return 0;
 }
 
@@ -945,12 +947,13 @@ mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const in
 // ---------------------------------------------------------------------------
 
 namespace {
-// Weights of `rows` rows in all, x or h rows of K elements.
-mxq_status gemv_check(mxq_format fmt, int64_t K, const void* x, int64_t ld_x, const void* w, const void* s,
+// `rows` rows of x or h, ld_x apart, of K elements; weights of K elements a row.
+mxq_status gemv_check(mxq_format fmt, int64_t rows, int64_t K, const void* x, int64_t ld_x, const void* w, const void* s,
                       const float* t, mxq_scope scope, mxq_scope wide) {
   if (!x || !w || !s || (fmt == MXQ_NVFP4 && !t)) return MXQ_ERR_NULL;
   if (fmt == MXQ_NVFP4 && scope != MXQ_SCOPE_ROW && scope != wide) return MXQ_ERR_FORMAT;
   if (K < 32 || K % 32 || K > kMaxGemmK || ld_x < K) return MXQ_ERR_SHAPE;
+  if (rows > 1 && ld_x > (0x7FFFFFFF / 2 - K) / (rows - 1)) return MXQ_ERR_SHAPE;    // 32-bit offsets into x
   if (ld_x % 8 || !al16(x) || !al16(w) || (fmt == MXQ_NVFP4 && ((reinterpret_cast<uintptr_t>(s) & 1u) || !al4(t))))
     return MXQ_ERR_ALIGN;
   return MXQ_OK;
@@ -963,8 +966,9 @@ mxq_status gemv_any(mxq_format fmt, int gated, int64_t rows, int64_t n, int64_t 
   if (fmt != MXQ_NVFP4 && fmt != MXQ_MXFP4) return MXQ_ERR_FORMAT;
   if (rows == 0 || n == 0) return MXQ_OK;
   if (!y) return MXQ_ERR_NULL;
-  const mxq_status st = gemv_check(fmt, K, x, ld_x, w, s, t, scope, MXQ_SCOPE_TENSOR);
+  const mxq_status st = gemv_check(fmt, rows, K, x, ld_x, w, s, t, scope, MXQ_SCOPE_TENSOR);
   if (st != MXQ_OK) return st;
+  if (gated && n > 0x7FFFFFFF / K) return MXQ_ERR_SHAPE;                 // gate and up rows within 32-bit offsets
   if (ld_y < n || (n + 15) / 16 > kMaxGridTiles / 4) return MXQ_ERR_SHAPE;
   if (out32 ? !al4(y) : (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_gemv((int)fmt, gated, rows, n, K, x, ld_x, w, s, t, scope == MXQ_SCOPE_ROW ? 0 : 1, y, ld_y,
@@ -998,7 +1002,7 @@ mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int6
   if (tokens == 0 || topk == 0 || inter == 0) return MXQ_OK;
   if (experts == 0) return MXQ_ERR_SHAPE;
   if (!topk_idx || !h) return MXQ_ERR_NULL;
-  const mxq_status st = gemv_check(fmt, K, x, ld_x, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
+  const mxq_status st = gemv_check(fmt, tokens, K, x, ld_x, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
   if (st != MXQ_OK) return st;
   if (!al4(topk_idx) || (reinterpret_cast<uintptr_t>(h) & 1u)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_decode_gate_up((int)fmt, tokens, topk, experts, inter, K, x, ld_x, topk_idx, W, sW, tW,
@@ -1007,19 +1011,24 @@ mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int6
 
 mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t hidden, int64_t K,
                            const void* h, const int32_t* topk_idx, const float* weights, const void* W, const void* sW,
-                           const float* tW, mxq_scope tW_scope, void* y, mxq_out_dtype y_dtype, void* stream) {
+                           const float* tW, mxq_scope tW_scope, void* y, mxq_out_dtype y_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
   if (!decode_sizes(tokens, topk, experts, hidden)) return MXQ_ERR_SHAPE;
   if ((fmt != MXQ_NVFP4 && fmt != MXQ_MXFP4) || !is_dtype(y_dtype)) return MXQ_ERR_FORMAT;
   if (tokens == 0 || hidden == 0) return MXQ_OK;
   if (topk == 0 || experts == 0) return MXQ_ERR_SHAPE;
   if (!topk_idx || !weights || !y) return MXQ_ERR_NULL;
-  const mxq_status st = gemv_check(fmt, K, h, K, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
+  const mxq_status st = gemv_check(fmt, tokens * topk, K, h, K, W, sW, tW, tW_scope, MXQ_SCOPE_GROUP);
   if (st != MXQ_OK) return st;
   if (!al4(topk_idx) || !al4(weights) ||
       (y_dtype == MXQ_OUT_F32 ? !al4(y) : (reinterpret_cast<uintptr_t>(y) & 1u) != 0))
     return MXQ_ERR_ALIGN;
+  const size_t need = mxq::decode_down_ws_bytes(tokens, hidden);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERR_WORKSPACE;
+  if (need > 0 && !al4(workspace)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_decode_down((int)fmt, tokens, topk, experts, hidden, K, h, topk_idx, weights, W, sW, tW,
-                                            tW_scope == MXQ_SCOPE_ROW ? 0 : 1, y, y_dtype == MXQ_OUT_F32, S(stream)));
+                                            tW_scope == MXQ_SCOPE_ROW ? 0 : 1, y, y_dtype == MXQ_OUT_F32, workspace,
+                                            S(stream)));
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@
 // Element-wise 4-bit weights under group scales: remio.ai ("Miles Blackwell RL"), section "La
 // Compatibilidad ..."; moving expert weights through memory can bind harder than arithmetic: same page,
 // section "NVFP4 por token ...".
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -36,34 +37,32 @@ __device__ __forceinline__ v8bf as_bf(const uint4& v) {
   return r;
 }
 
-// Eight E2M1 codes (a dword) times their block scale -> BF16, exact. MXFP4: `s` is the E8M0 code, whose
-// power of two the convert applies; NVFP4: S in binary32, multiplied there.
+// Eight E2M1 codes (a dword) times a power of two -> BF16, exact.
+__device__ __forceinline__ v8bf codes8(uint32_t w, float p2) {
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p2, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p2, 1);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p2, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p2, 3);
+  v8bf r;
+  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1]; r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+  return r;
+}
+// ... times their block scale: MXFP4, the E8M0 code's power of two; NVFP4: S, multiplied in binary32.
 template <int FMT>
 __device__ __forceinline__ v8bf weights8(uint32_t w, float S) {
-  uint32_t p[4];
   if constexpr (FMT == 4) {
-    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, S, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, S, 1);
-    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, S, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, S, 3);
-    __builtin_memcpy(&p[0], &a, 4); __builtin_memcpy(&p[1], &b, 4);
-    __builtin_memcpy(&p[2], &c, 4); __builtin_memcpy(&p[3], &d, 4);
+    return codes8(w, S);
   } else {
+    uint32_t p[4];
     const v2f_t a = e2m1x2_to_f32<0>(w), b = e2m1x2_to_f32<1>(w), c = e2m1x2_to_f32<2>(w), d = e2m1x2_to_f32<3>(w);
     p[0] = bf16x2_rne(a.x * S, a.y * S);
     p[1] = bf16x2_rne(b.x * S, b.y * S);
     p[2] = bf16x2_rne(c.x * S, c.y * S);
     p[3] = bf16x2_rne(d.x * S, d.y * S);
+    return as_bf(make_uint4(p[0], p[1], p[2], p[3]));
   }
-  return as_bf(make_uint4(p[0], p[1], p[2], p[3]));
 }
 
-// The scale codes of a lane's 32 K of a chunk: two E4M3 bytes (NVFP4) or one E8M0 byte (MXFP4).
-template <int FMT>
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* s) {
-  if constexpr (FMT == 2) return *reinterpret_cast<const uint16_t*>(s);
-  else return *s;
-}
-
-// ... as what multiplies the lane's first and second 16 K.
+// ... the scale codes of a lane's 32 K of a chunk (two E4M3 bytes, or one E8M0 byte) as what multiplies its
+// first and second 16 K.
 template <int FMT>
 __device__ __forceinline__ void scales_of(uint32_t codes, float (&S)[2]) {
   if constexpr (FMT == 2) {
@@ -74,120 +73,177 @@ __device__ __forceinline__ void scales_of(uint32_t codes, float (&S)[2]) {
   }
 }
 
-// acc[nt][tt] += the products of NT row tiles and TT column tiles over chunks [c0, c1). wp, sp: the lane's
-// row (bytes, scales) at its 32 K of chunk 0; xp: its x row there; on[tt]: the lane's column exists.
-template <int FMT, int NT, int TT>
-__device__ __forceinline__ void dot(const uint8_t* const (&wp)[NT], const uint8_t* const (&sp)[NT],
-                                    const uint16_t* const (&xp)[TT], const bool (&on)[TT], int K, int c0, int c1,
-                                    v4f (&acc)[NT][TT]) {
-  constexpr int U = TT == 1 ? 4 : TT == 2 ? 2 : 1;        // chunks whose loads go out together
-  constexpr int SB = FMT == 2 ? 8 : 4;                    // scale bytes of a row and chunk
-  const int g = (threadIdx.x & 63) >> 4;
+// Loads go through buffer descriptors: what lies past their end, or is switched off by kOff, reads zeros, so
+// rows past the last, K past the end and absent x rows need no branch.
+constexpr uint32_t kOff = 0x80000000u;
+constexpr uint32_t kMaxRecords = 0x7FFFFFFFu;
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)min(bytes, (int64_t)kMaxRecords), 0x00020000);
+}
+__device__ __forceinline__ uint4 load16(Rsrc r, uint32_t voff, uint32_t soff) {
+  typedef unsigned int v4u_t __attribute__((ext_vector_type(4)));
+  const v4u_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t load_codes(Rsrc r, uint32_t voff, uint32_t soff) {
+  if constexpr (FMT == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)voff, (int)soff, 0);
+  else return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)voff, (int)soff, 0);
+}
+template <int FMT> constexpr int kScaleK = FMT == 2 ? 16 : 32;      // K of a scale
+template <int FMT> constexpr int kCodes = FMT == 2 ? 2 : 1;         // codes of a lane's 32 K
+
+// ---------------------------------------------------------------------------
+// More than four x rows: a column tile of 16 is 16 x rows
+// ---------------------------------------------------------------------------
+// acc[t] += the products of one row tile and TT column tiles over chunks [c0, c1). wo, so: the lane's row at its
+// 32 K of chunk 0; xo[t]: its x row there.
+template <int FMT, int TT>
+__device__ __forceinline__ void dot16(Rsrc rw, Rsrc rs, Rsrc rx, uint32_t wo, uint32_t so, const uint32_t (&xo)[TT], int K,
+                                      int c0, int c1, v4f (&acc)[TT]) {
+  constexpr int U = 4;                                    // chunks whose weights' loads go out together
+  const int k0 = 32 * ((threadIdx.x & 63) >> 4);
   for (int c = c0; c < c1; c += U) {
-    uint4 w[U][NT], x[U][TT][4];
-    uint32_t s[U][NT];
+    uint4 w[U];
+    uint32_t s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // chunks past the wave's share and a last chunk's K past the end multiply zeros
-      const bool in = c + u < c1 && (c + u) * kChunk + 32 * g < K;
+      const bool in = c + u < c1 && (c + u) * kChunk + k0 < K;
+      w[u] = load16(rw, in ? wo : kOff, (uint32_t)(c + u) * (kChunk / 2));
+      s[u] = load_codes<FMT>(rs, in ? so : kOff, (uint32_t)(c + u) * (kChunk / kScaleK<FMT>));
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        w[u][n] = make_uint4(0, 0, 0, 0);
-        s[u][n] = 0;
-        if (in) {
-          w[u][n] = *reinterpret_cast<const uint4*>(wp[n] + (int64_t)(c + u) * (kChunk / 2));
-          s[u][n] = load_codes<FMT>(sp[n] + (int64_t)(c + u) * SB);
-        }
-      }
+    for (int u = 0; u < U; ++u) {
+      if (c + u >= c1) break;
+      const bool in = (c + u) * kChunk + k0 < K;
+      uint4 x[TT][4];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[u][t][i] = make_uint4(0, 0, 0, 0);
-          if (in && on[t]) x[u][t][i] = *reinterpret_cast<const uint4*>(xp[t] + (int64_t)(c + u) * kChunk + 8 * i);
-        }
-    }
+        for (int i = 0; i < 4; ++i) x[t][i] = load16(rx, (in ? xo[t] : kOff) + 16 * i, (uint32_t)(c + u) * (2 * kChunk));
+      const uint32_t d[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      float S[2];
+      scales_of<FMT>(s[u], S);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int i = 0; i < 4; ++i) {
+        const v8bf a = weights8<FMT>(d[i], S[i / 2]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t d[4] = {w[u][n].x, w[u][n].y, w[u][n].z, w[u][n].w};
-        float S[2];
-        scales_of<FMT>(s[u][n], S);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const v8bf a = weights8<FMT>(d[i], S[i / 2]);
-#pragma unroll
-          for (int t = 0; t < TT; ++t)
-            acc[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(x[u][t][i]), acc[n][t], 0, 0, 0);
-        }
+        for (int t = 0; t < TT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(x[t][i]), acc[t], 0, 0, 0);
       }
+    }
   }
 }
 
-// The same for at most four x rows, where a column tile of 16 would be mostly empty and cost four loads of x
-// for each of weights: the free columns split K further. MFMA row i = (weight row i / 4 of four, K segment i % 4),
-// column j = (x row j / 4, segment j % 4), a lane's segment 32 K; only where both segments agree is a
-// product of the row and the column, so of a lane's four accumulators one counts, and the four lanes of a
-// quad hold the segments' sums. A chunk is 512 K of 16 weight rows: four loads of weights, 64 consecutive
-// bytes of a row to four lanes, and four of x.
+// ---------------------------------------------------------------------------
+// At most four x rows
+// ---------------------------------------------------------------------------
+// A column tile of 16 x rows would be mostly empty, so the 4x4x4 MFMA takes over, which is sixteen independent
+// 4 x 4 products: block b = l / 4 is a K segment of 32, its four lanes four weight rows of A and four x
+// rows of B, and each instruction advances every block by four K. A chunk is 512 K of the tile's 16 weight
+// rows: four loads of weights (lane l: row 4 r + l % 4, 16 bytes), and four of x (x row l % 4). As no sum crosses
+// lanes before the end, NVFP4's block scale can follow the products: the codes go to BF16 as they are
+// (one convert a pair), 16 K sum up in the matrix core, and one FMA a weight row, its scale read from the
+// lane of the quad that holds the row, adds them: 0.75 vector instructions a weight against 2 for scaled
+// BF16 operands.
 constexpr int kWide = 512;
-template <int FMT, int NT>
-__device__ __forceinline__ void dot4(const uint8_t* const (&wp)[NT], const uint8_t* const (&sp)[NT], int64_t row_bytes,
-                                     int64_t row_scales, const int (&step)[4], const uint16_t* xp, bool on, int K, int c0,
-                                     int c1, v4f (&acc)[NT][4]) {
-  constexpr int SB = FMT == 2 ? 32 : 16;                  // scale bytes of a row and chunk
-  const int lane = threadIdx.x & 63;
-  const int at = 128 * (lane >> 4) + 32 * (lane & 3);     // the lane's K of a chunk
+typedef short v4s __attribute__((ext_vector_type(4)));
+// The lane's part of the tile: two descriptors (rows 0 .. 7 and 8 .. 15), its offsets within each.
+struct Rows4 {
+  Rsrc w[2], s[2];
+  uint32_t wo, so, w4, s4;                                // w4, s4: four rows on
+};
+// first[h]: the weight row that half h of the tile begins with, rows[h] (at most 8) how many it has
+template <int FMT>
+__device__ __forceinline__ Rows4 rows4(const uint8_t* w, const uint8_t* s, const int64_t (&first)[2],
+                                       const int64_t (&rows)[2], int K) {
+  const int lane = threadIdx.x & 63, i = lane & 3, seg = lane >> 2;
+  const int64_t wb = K / 2, sb = K / kScaleK<FMT>;
+  Rows4 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    r.w[h] = rsrc(w + first[h] * wb, rows[h] * wb);
+    r.s[h] = rsrc(s + first[h] * sb, rows[h] * sb);
+  }
+  r.wo = (uint32_t)(i * wb) + 16 * seg;
+  r.so = (uint32_t)(i * sb) + kCodes<FMT> * seg;
+  r.w4 = (uint32_t)(4 * wb);
+  r.s4 = (uint32_t)(4 * sb);
+  return r;
+}
+__device__ __forceinline__ v4s half8(const v8bf& v, int h) {
+  v4s r;
+  __builtin_memcpy(&r, reinterpret_cast<const char*>(&v) + 8 * h, 8);
+  return r;
+}
+template <int R>
+__device__ __forceinline__ float quad_lane(float v) {      // lane R of the quad's
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), R * 0x55, 0xF, 0xF, true));
+}
+// acc[r][i] += the lane's segment of weight row 4 r + i times x row l % 4, over chunks [c0, c1). x_of() is asked for
+// the lane's x row at its K of chunk 0 (or kOff), with the first weights on their way.
+template <int FMT, typename F>
+__device__ __forceinline__ void dot4(const Rows4& rows, Rsrc rx, F&& x_of, int K, int c0, int c1, v4f (&acc)[4]) {
+  const int at = 32 * ((threadIdx.x & 63) >> 2);          // the lane's K of a chunk
+  uint32_t xo = kOff;
   for (int c = c0; c < c1; ++c) {
-    uint4 w[NT][4], x[4];
-    uint32_t s[NT][4];
+    uint4 w[4], x[4];
+    uint32_t s[4];
     const bool in = c * kWide + at < K;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 4; ++r)
+      w[r] = load16(rows.w[r / 2], in ? rows.wo + r % 2 * rows.w4 : kOff, (uint32_t)c * (kWide / 2));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        w[n][r] = make_uint4(0, 0, 0, 0);
-        if (in) w[n][r] = *reinterpret_cast<const uint4*>(wp[n] + step[r] * row_bytes + (int64_t)c * (kWide / 2));
+    for (int r = 0; r < 4; ++r)
+      s[r] = load_codes<FMT>(rows.s[r / 2], in ? rows.so + r % 2 * rows.s4 : kOff, (uint32_t)c * (kWide / kScaleK<FMT>));
+    if (c == c0) xo = x_of();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = load16(rx, (in ? xo : kOff) + 16 * i, (uint32_t)c * (2 * kWide));
+    __builtin_amdgcn_sched_barrier(0);                    // all of them in flight: the scheduler would sink some
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t d[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+      float S[2];
+      scales_of<FMT>(s[r], S);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                       // the lane's first and second 16 K
+        v4f sum = FMT == 4 ? acc[r] : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 2 * h; i < 2 * h + 2; ++i) {
+          const v8bf q = codes8(d[i], FMT == 4 ? S[h] : 1.0f), xi = as_bf(x[i]);
+          sum = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(half8(q, 0), half8(xi, 0), sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(half8(q, 1), half8(xi, 1), sum, 0, 0, 0);
+        }
+        if constexpr (FMT == 4) {
+          acc[r] = sum;
+        } else {
+          acc[r][0] = __builtin_fmaf(quad_lane<0>(S[h]), sum[0], acc[r][0]);
+          acc[r][1] = __builtin_fmaf(quad_lane<1>(S[h]), sum[1], acc[r][1]);
+          acc[r][2] = __builtin_fmaf(quad_lane<2>(S[h]), sum[2], acc[r][2]);
+          acc[r][3] = __builtin_fmaf(quad_lane<3>(S[h]), sum[3], acc[r][3]);
+        }
       }
+    }
+  }
+}
+// The sums over the four segments of each row of 16 lanes: lane l of it is left with weight rows 4 (l / 4) + (0 .. 3)
+// of the tile, x row l % 4.
+__device__ __forceinline__ float4 gather4(v4f (&acc)[4]) {
+  const int quad = (threadIdx.x >> 2) & 3;
+  float out[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[n][r] = 0;
-        if (in) s[n][r] = load_codes<FMT>(sp[n] + step[r] * row_scales + (int64_t)c * SB);
-      }
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (in && on) x[i] = *reinterpret_cast<const uint4*>(xp + (int64_t)c * kWide + 8 * i);
+      float v = acc[r][i];
+      v += dpp_f32<0x124, 0xF>(v);                        // rotations by 4 and 8 lanes
+      v += dpp_f32<0x128, 0xF>(v);
+      if (r == 0) out[i] = v;
+      else out[i] = quad == r ? v : out[i];
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t d[4] = {w[n][r].x, w[n][r].y, w[n][r].z, w[n][r].w};
-        float S[2];
-        scales_of<FMT>(s[n][r], S);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[n][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<FMT>(d[i], S[i / 2]), as_bf(x[i]), acc[n][r], 0, 0, 0);
-      }
-  }
+  return make_float4(out[0], out[1], out[2], out[3]);
 }
-// Lane l's result: weight row 4 (l % 4) + l / 16 of the tile, x row (l % 16) / 4.
-__device__ __forceinline__ float gather4(const v4f (&acc)[4]) {
-  const int seg = threadIdx.x & 3;
-  float out = 0.0f;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    float v = seg == 0 ? acc[r][0] : seg == 1 ? acc[r][1] : seg == 2 ? acc[r][2] : acc[r][3];
-    v += __uint_as_float(dpp_xor1(__float_as_uint(v)));
-    v += __uint_as_float(dpp_xor2(__float_as_uint(v)));
-    if (seg == r) out = v;
-  }
-  return out;
-}
+__device__ __forceinline__ uint32_t x_off4() { return 64 * ((threadIdx.x & 63) >> 2); }
 
 // The wave's share of a row tile's chunks.
 __device__ __forceinline__ void share(int chunks, int part, int parts, int& c0, int& c1) {
@@ -196,17 +252,50 @@ __device__ __forceinline__ void share(int chunks, int part, int parts, int& c0, 
   c1 = min(c0 + per, chunks);
 }
 
-// Choices of expert e, in order: the lane gets the (first + q)-th, q = lane % 16 / 4 its x row, or -1; the return
+// Choices as bits, 64 a word.
+template <int NB>
+struct Who {
+  uint64_t m[NB];
+  __device__ __forceinline__ int count() const {
+    int n = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) n += __popcll(m[b]);
+    return n;
+  }
+  // the lane's: the (first + q)-th, q = lane % 4 its x row, or -1
+  __device__ __forceinline__ int pick(int first) const {
+    int left = first + (threadIdx.x & 3), at = -1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = __popcll(m[b]);
+      if (at < 0 && left < n) {
+        uint64_t w = m[b];
+        for (; left > 0; --left) w &= w - 1;
+        at = 64 * b + __builtin_ctzll(w);
+      }
+      left -= n;
+    }
+    return at;
+  }
+};
+
+// Choices of expert e, in order: the lane gets the (first + q)-th, q = lane % 4 its x row, or -1; the return
 // value is how many there are in all. `col`: four ints of LDS of the wave's own.
 __device__ __forceinline__ int choices_of(const int32_t* idx, int n, int e, int first, int* col, int& mine) {
-  const int lane = threadIdx.x & 63, q = (lane >> 2) & 3;
+  const int lane = threadIdx.x & 63, q = lane & 3;
   int seen = 0;
-  for (int b = 0; b < n; b += 64) {
-    const bool hit = b + lane < n && idx[b + lane] == e;
-    const uint64_t m = __ballot(hit);
-    const int at = seen + __popcll(m & ((1ull << lane) - 1)) - first;
-    if (hit && at >= 0 && at < 4) col[at] = b + lane;
-    seen += __popcll(m);
+  for (int b = 0; b < n; b += 256) {                      // four loads in flight
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = b + 64 * i + lane < n ? idx[b + 64 * i + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool hit = v[i] == e;                         // e >= 0
+      const uint64_t m = __ballot(hit);
+      const int at = seen + __popcll(m & ((1ull << lane) - 1)) - first;
+      if (hit && at >= 0 && at < 4) col[at] = b + 64 * i + lane;
+      seen += __popcll(m);
+    }
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);                     // lgkmcnt(0)
   __builtin_amdgcn_wave_barrier();
@@ -214,21 +303,6 @@ __device__ __forceinline__ int choices_of(const int32_t* idx, int n, int e, int 
   __builtin_amdgcn_s_waitcnt(0xC07F);
   __builtin_amdgcn_wave_barrier();
   return seen;
-}
-
-// The lane's weight pointers for dot4: rows 4 r + (l % 16) / 4 of the tile at row0 + n0, step[r] rows on from
-// the first; rows past the end (n rows) are the last one again, and what they give is not stored.
-template <int FMT>
-__device__ __forceinline__ void rows4(const uint8_t* w, const uint8_t* s, int64_t row0, int64_t n0, int64_t n, int K,
-                                      const uint8_t*& wp, const uint8_t*& sp, int (&step)[4]) {
-  const int lane = threadIdx.x & 63, q = (lane >> 2) & 3, seg = 4 * (lane >> 4) + (lane & 3);
-  const int left = (int)min((int64_t)kTile, n - n0) - 1;
-  const int at = min(q, left);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) step[r] = min(4 * r + q, left) - at;
-  const int64_t row = row0 + n0 + at;
-  wp = w + row * (K / 2) + 16 * seg;
-  sp = s + row * (K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * seg;
 }
 
 }  // namespace gv
@@ -244,147 +318,187 @@ struct GemvArgs {
   const uint8_t* s;
   const float* t;          // NVFP4
   int t_mode;              // 0 a row, 1 one (of an expert)
-  int64_t n;               // rows of the product, gated: inter
+  int64_t n;               // columns of the result: rows of the product, gated: inter
   int K;
   void* y;                 // (rows, n): BF16 (gated, out32 = 0) or FP32
   int64_t ld_y;
   int out32;
 };
 
-// A workgroup: one tile of 16 rows of the product (gated: the tile's gates and ups), K split over its WV
-// waves; TT column tiles hold all x rows.
+// A workgroup has one tile of 16 weight rows: 16 columns of the result, or (gated) 8, their gates and their ups.
+template <bool GATED> constexpr int kTileOut = GATED ? 8 : 16;
+
+__device__ __forceinline__ void store_y(void* y, int64_t at, float v, int f32) {
+  if (f32) ((float*)y)[at] = v;
+  else ((uint16_t*)y)[at] = (uint16_t)f32_to_bf16_rne(v);
+}
+
+// K split over the workgroup's WV waves; TT column tiles hold all x rows. (Gated: 2 n K / 2 < 2^31 bytes of weights.)
 template <int FMT, bool GATED, int TT, int WV>
 __global__ void __launch_bounds__(64 * WV)
 gemv_kernel(GemvArgs a) {
   using namespace gv;
-  constexpr int NT = GATED ? 2 : 1;
-  __shared__ float part[WV][NT][TT][4][64];
+  constexpr int NO = kTileOut<GATED>;
+  __shared__ float part[WV][TT][4][64];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * kTile;
-  const uint8_t *wp[NT], *sp[NT];
+  const int64_t n0 = (int64_t)blockIdx.x * NO;
+  const int64_t wb = a.K / 2, sb = a.K / kScaleK<FMT>;
+  const int64_t rows = (GATED ? 2 * a.n : min(a.n, n0 + kTile)) - n0;   // gate rows past n read ups, not stored
+  const Rsrc rw = rsrc(a.w + n0 * wb, rows * wb), rs = rsrc(a.s + n0 * sb, rows * sb);
+  const int m = lane % kTile;
+  const int64_t row = GATED && m >= 8 ? a.n + m - 8 : m;
+  const uint32_t wo = (uint32_t)(row * wb) + 16 * g, so = (uint32_t)(row * sb) + kCodes<FMT> * g;
+  const Rsrc rx = rsrc(a.x, ((a.rows - 1) * a.ld_x + a.K) * 2);
+  uint32_t xo[TT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    // rows past the end read the last one's bytes; what they give is not stored
-    const int64_t row = n * a.n + min(n0 + lane % kTile, a.n - 1);
-    wp[n] = a.w + row * (a.K / 2) + 16 * g;
-    sp[n] = a.s + row * (a.K / (FMT == 2 ? 16 : 32)) + (FMT == 2 ? 2 : 1) * g;
+  for (int t = 0; t < TT; ++t) {
+    const int r = t * kTile + m;
+    xo[t] = r < a.rows ? (uint32_t)(r * a.ld_x + 32 * g) * 2 : kOff;
   }
   int c0, c1;
   share((a.K + kChunk - 1) / kChunk, wave, WV, c0, c1);
-  const uint16_t* xp[TT];
-  bool on[TT];
+  v4f acc[TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int r = t * kTile + lane % kTile;
-    on[t] = r < a.rows;
-    xp[t] = a.x + (on[t] ? r : 0) * a.ld_x + 32 * g;
-  }
-  v4f acc[NT][TT];
+  for (int t = 0; t < TT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  dot16<FMT, TT>(rw, rs, rx, wo, so, xo, a.K, c0, c1, acc);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  dot<FMT, NT, TT>(wp, sp, xp, on, a.K, c0, c1, acc);
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][n][t][r][lane] = acc[n][t][r];
+    for (int r = 0; r < 4; ++r) part[wave][t][r][lane] = acc[t][r];
   __syncthreads();
   // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
-  for (int o = tid; o < TT * 256; o += 64 * WV) {
-    const int t = o >> 8, n = o & 15, c = (o >> 4) & 15;
-    const int l = 16 * (n >> 2) + c, r = n & 3, at = t * kTile + c;
+  for (int o = tid; o < TT * 16 * NO; o += 64 * WV) {
+    const int t = o / (16 * NO), n = o % NO, c = o / NO % 16, at = t * kTile + c;
     if (at >= a.rows || n0 + n >= a.n) continue;
-    float y[NT];
+    float y[2];
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      float v = part[0][k][t][r][l];
+    for (int k = 0; k < (GATED ? 2 : 1); ++k) {
+      const int i = n + 8 * k, l = 16 * (i >> 2) + c;
+      float v = part[0][t][i & 3][l];
 #pragma unroll
-      for (int w = 1; w < WV; ++w) v += part[w][k][t][r][l];
+      for (int w = 1; w < WV; ++w) v += part[w][t][i & 3][l];
       if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? k * a.n + n0 + n : 0];
       y[k] = v;
     }
-    const int64_t to = at * a.ld_y + n0 + n;
-    if constexpr (GATED) ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(swiglu_forward(y[0], y[1]));
-    else if (a.out32) ((float*)a.y)[to] = y[0];
-    else ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(y[0]);
+    store_y(a.y, at * a.ld_y + n0 + n, GATED ? swiglu_forward(y[0], y[1]) : y[0], !GATED && a.out32);
   }
 }
 
-// At most four x rows at a time (dot4). Dense: all of them. Experts: blockIdx.y names the expert, either as
-// itself or (by_choice) as the choice that names it first; its choices come four by four.
-template <int FMT, bool GATED, bool MOE, int WV>
-__global__ void __launch_bounds__(64 * WV)
+// At most four x rows at a time (dot4). Dense: all of them. Experts: the choices of one expert, four by four.
+// Up to 512 choices are looked at by every wave at once and kept as bits (NB words of 64); NB = 0 finds them
+// through LDS, pass by pass. blockIdx.y is a choice, which works for its expert if it is the first to name
+// it, or (by_choice = 0) the expert.
+constexpr int kDense = -1;
+// KS waves share a tile's K; a workgroup has at least four waves, so 4 / KS tiles.
+template <int FMT, bool GATED, int NB, int KS>
+__global__ void __launch_bounds__(64 * (KS < 4 ? 4 : KS)) __attribute__((amdgpu_waves_per_eu(NB == 1 ? 6 : NB == kDense ? 4 : 5)))
 gemv4_kernel(GemvArgs a, int by_choice) {
   using namespace gv;
-  constexpr int NT = GATED ? 2 : 1;
-  __shared__ float part[2][WV][NT][64];
-  __shared__ int col[WV][4];
+  constexpr int WV = KS < 4 ? 4 : KS, TILES = WV / KS;
+  constexpr bool MOE = NB != kDense;
+  constexpr int NO = kTileOut<GATED>;
+  __shared__ __attribute__((aligned(16))) float part[2][4 * WV][64];
+  __shared__ int col[NB == 0 ? WV : 1][4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * kTile;
+  const int64_t n0 = ((int64_t)blockIdx.x * TILES + wave / KS) * NO;     // a tile past the end: no rows, no stores
+  const int64_t b0 = (int64_t)blockIdx.x * TILES * NO;                   // the workgroup's first column
   int64_t base = 0;                                       // the expert's first weight row
-  int e = 0;
+  int e = 0, seen = a.rows;
+  Who<(NB > 0 ? NB : 1)> who;
   if constexpr (MOE) {
-    if (by_choice) {
-      e = a.idx[blockIdx.y];
+    const int y = blockIdx.y;
+    auto none = [&](int i) { return (unsigned)i >= (unsigned)a.experts; };
+    auto zero_row = [&](int c) {                          // by one thread: the choice c has no expert
+      for (int i = 0; i < TILES * NO && b0 + i < a.n; ++i) ((uint16_t*)a.y)[c * a.ld_y + b0 + i] = 0;
+    };
+    if constexpr (NB > 0) {
+      int v[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) v[b] = 64 * b + lane < a.rows ? a.idx[64 * b + lane] : -1;
+      e = y;
+      if (by_choice) {
+        e = __builtin_amdgcn_readfirstlane(a.idx[y]);
+        if (none(e)) {
+          if (tid == 0) zero_row(y);
+          return;
+        }
+      } else if (y == 0) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (wave == b % WV && 64 * b + lane < a.rows && none(v[b])) zero_row(64 * b + lane);
+      }
       bool earlier = false;
-      for (int b = 0; b < (int)blockIdx.y; b += 64)
-        earlier = earlier || __ballot(b + lane < (int)blockIdx.y && a.idx[b + lane] == e) != 0;
-      if ((unsigned)e < (unsigned)a.experts && earlier) return;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        who.m[b] = __ballot(v[b] == e);
+        const int before = y - 64 * b;                    // choices of this word ahead of y
+        if (before > 0) earlier = earlier || (who.m[b] << (before < 64 ? 64 - before : 0)) != 0;
+      }
+      seen = who.count();
+      if (seen == 0 || (by_choice && earlier)) return;
     } else {
-      e = blockIdx.y;
+      if (by_choice) {
+        e = __builtin_amdgcn_readfirstlane(a.idx[y]);
+        if (none(e)) {
+          if (tid == 0) zero_row(y);
+          return;
+        }
+        for (int b = 0; b < y; b += 64)
+          if (__ballot(b + lane < y && a.idx[b + lane] == e)) return;
+      } else {
+        e = y;
+        if (y == 0)
+          for (int c = tid; c < a.rows; c += 64 * WV)
+            if (none(a.idx[c])) zero_row(c);
+      }
     }
-    // the rows of choices without an expert: zeros
-    for (int c = by_choice ? (int)blockIdx.y : 0; c < (by_choice ? (int)blockIdx.y + 1 : blockIdx.y ? 0 : a.rows); ++c) {
-      if ((unsigned)a.idx[c] < (unsigned)a.experts) continue;
-      if (tid < kTile && n0 + tid < a.n) ((uint16_t*)a.y)[c * a.ld_y + n0 + tid] = 0;
-    }
-    if ((unsigned)e >= (unsigned)a.experts) return;
     base = (int64_t)e * (GATED ? 2 : 1) * a.n;
   }
-  const uint8_t *wp[NT], *sp[NT];
-  int step[4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) rows4<FMT>(a.w, a.s, base + n * a.n, n0, a.n, a.K, wp[n], sp[n], step);
+  const int64_t second = GATED ? a.n + n0 : n0 + 8;       // the tile's second half: the ups, or eight rows on
+  const Rows4 rows = rows4<FMT>(a.w, a.s, {base + n0, base + second},
+                                {max(min(a.n - n0, (int64_t)8), (int64_t)0),
+                                 max(min((GATED ? 2 : 1) * a.n - second, (int64_t)8), (int64_t)0)},
+                                a.K);
+  const Rsrc rx = rsrc(a.x, (((MOE ? a.rows / a.topk : a.rows) - 1) * a.ld_x + a.K) * 2);
   int c0, c1;
-  share((a.K + kWide - 1) / kWide, wave, WV, c0, c1);
-  const int q = (lane >> 2) & 3, n = 4 * (lane & 3) + (lane >> 4);   // the lane's x row and result row
-  int seen = a.rows;
+  share((a.K + kWide - 1) / kWide, wave % KS, KS, c0, c1);
+  // lane l of the tile's first wave joins the sums of x row l % 4, product row l / 4
+  const int i = lane >> 2, n = GATED ? i % 8 : i;
+  float t = 1.0f;
+  if (FMT == 2 && wave % KS == 0 && n0 + n < a.n) t = a.t[a.t_mode == 0 ? base + (GATED ? i / 8 * a.n : 0) + n0 + n : MOE ? e : 0];
   for (int first = 0, buf = 0; first < seen; first += 4, buf ^= 1) {
-    int mine = first + q < seen ? first + q : -1;
-    if constexpr (MOE) {
+    int mine = -1;                                        // the lane's x row, or choice
+    if constexpr (NB == 0) {
       seen = choices_of(a.idx, a.rows, e, first, col[wave], mine);
       if (seen == 0) return;                              // an expert nobody chose (all waves alike)
     }
-    const bool on = mine >= 0;
-    const uint16_t* xp = a.x + (on ? (MOE ? mine / a.topk : mine) : 0) * a.ld_x + 128 * (lane >> 4) + 32 * (lane & 3);
-    v4f acc[NT][4];
+    auto x_of = [&]() -> uint32_t {
+      if constexpr (NB > 0) mine = who.pick(first);
+      if constexpr (NB == kDense) mine = first + lane % 4 < seen ? first + lane % 4 : -1;
+      return mine >= 0 ? (uint32_t)((MOE ? mine / a.topk : mine) * a.ld_x * 2) + x_off4() : kOff;
+    };
+    v4f acc[4];
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int r = 0; r < 4; ++r) acc[r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    dot4<FMT>(rows, rx, x_of, a.K, c0, c1, acc);
+    *reinterpret_cast<float4*>(&part[buf][wave * 4 + lane / 16][4 * (lane % 16)]) = gather4(acc);
+    if constexpr (KS > 1) __syncthreads();                // two buffers: the next pass writes the other one
+    else __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the wave's own
+    if (wave % KS == 0) {
+      const float* p = &part[buf][4 * wave][16 * (i / 4) + 4 * (lane % 4) + i % 4];
+      float v = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[k][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    dot4<FMT, NT>(wp, sp, a.K / 2, a.K / (FMT == 2 ? 16 : 32), step, xp, on, a.K, c0, c1, acc);
-#pragma unroll
-    for (int k = 0; k < NT; ++k) part[buf][wave][k][lane] = gather4(acc[k]);
-    __syncthreads();                                      // two buffers: the next pass writes the other one
-    if (wave == 0 && on && n0 + n < a.n) {
-      float y[NT];
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        float v = part[buf][0][k][lane];
-#pragma unroll
-        for (int w = 1; w < WV; ++w) v += part[buf][w][k][lane];
-        if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? base + k * a.n + n0 + n : MOE ? e : 0];
-        y[k] = v;
+      for (int w = 0; w < 4 * KS; ++w) v += p[64 * w];
+      if constexpr (FMT == 2) v *= t;
+      const bool store = mine >= 0 && n0 + n < a.n;
+      if constexpr (GATED) {                              // the up of lane l's gate is 32 lanes on
+        const float up = __shfl_xor(v, 32, 64);
+        if (store && i < 8) store_y(a.y, mine * a.ld_y + n0 + n, swiglu_forward(v, up), 0);
+      } else {
+        if (store) store_y(a.y, mine * a.ld_y + n0 + n, v, a.out32);
       }
-      const int64_t to = mine * a.ld_y + n0 + n;
-      if constexpr (GATED) ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(swiglu_forward(y[0], y[1]));
-      else if (a.out32) ((float*)a.y)[to] = y[0];
-      else ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(y[0]);
     }
   }
 }
@@ -403,86 +517,130 @@ struct DownArgs {
   int K;
   void* y;                 // (tokens, n)
   int out32;
+  float* parts;            // gridDim.y > 1: FP32 (parts, tokens, n)
 };
 
-// y[t] = sum over the choices j of t of weights[t, j] (W_e h[t, j]): a workgroup has one tile of 16 rows of
-// y; its waves share out the chosen experts (and, with few of them, parts of K), each adding to an own
-// copy of the tile's (tokens, 16) sums in LDS; the copies meet in wave order.
-constexpr int kMaxDecodeExperts = 1024;
-template <int FMT, int TCAP, int WV>
-__global__ void __launch_bounds__(64 * WV)
+// y[t] = sum over the choices j of t of weights[t, j] (W_e h[t, j]): a workgroup has a tile of 16 rows of y and
+// (blockIdx.y) one of gridDim.y shares of the chosen experts; its waves share those out (and, with few of
+// them, parts of K), each adding to an own copy of the tile's (tokens, 16) sums in LDS. The copies meet in
+// wave order, the shares in theirs (decode_join_kernel).
+// MANY: more than 64 choices, found through LDS; else each wave holds them in its lanes.
+constexpr int kMaxDecodeExperts = 1024, kMaxChoices = 2048;
+template <int FMT, int TCAP, bool MANY, int WV>
+__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4)))
 decode_down_kernel(DownArgs a, int kparts) {
   using namespace gv;
   __shared__ float sum[WV][TCAP][kTile];
-  __shared__ int first_of[kMaxDecodeExperts];
-  __shared__ int list[kMaxDecodeExperts];                 // the chosen experts, by first choice
-  __shared__ int col[WV][4], found[WV];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * kTile;
   const int S = a.tokens * a.topk;
-  for (int i = tid; i < a.experts; i += 64 * WV) first_of[i] = 0x7FFFFFFF;
-  for (int i = lane; i < TCAP * kTile; i += 64) (&sum[wave][0][0])[i] = 0.0f;
-  __syncthreads();
-  for (int c = tid; c < S; c += 64 * WV) {
-    const int e = a.idx[c];
-    if ((unsigned)e < (unsigned)a.experts) atomicMin(&first_of[e], c);
-  }
-  __syncthreads();
-  int experts = 0;
-  for (int b = 0; b < S; b += 64 * WV) {                  // compacted in the order of the choices
-    const int c = b + tid;
-    const int e = c < S ? a.idx[c] : -1;
-    const bool lead = (unsigned)e < (unsigned)a.experts && first_of[e] == c;
-    const uint64_t m = __ballot(lead);
-    if (lane == 0) found[wave] = __popcll(m);
-    __syncthreads();
-    int before = experts, here = 0;
-    for (int w = 0; w < WV; ++w) {
-      before += w < wave ? found[w] : 0;
-      here += found[w];
-    }
-    if (lead) list[before + __popcll(m & ((1ull << lane) - 1))] = e;
-    experts += here;
-    __syncthreads();
-  }
   const int chunks = (a.K + kWide - 1) / kWide;
-  const int n = 4 * (lane & 3) + (lane >> 4);             // the lane's result row
-  for (int item = wave; item < experts * kparts; item += WV) {
-    const int e = __builtin_amdgcn_readfirstlane(list[item / kparts]);
-    int c0, c1, step[4];
-    share(chunks, item % kparts, kparts, c0, c1);
-    const uint8_t *wp[1], *sp[1];
-    rows4<FMT>(a.w, a.s, (int64_t)e * a.n, n0, a.n, a.K, wp[0], sp[0], step);
-    float tw = 1.0f;
-    if constexpr (FMT == 2) tw = a.t[a.t_mode == 0 ? (int64_t)e * a.n + min(n0 + n, a.n - 1) : e];
+  const Rsrc rx = rsrc(a.h, (int64_t)S * a.K * 2);
+  for (int i = lane; i < a.tokens * kTile; i += 64) (&sum[wave][0][0])[i] = 0.0f;
+  // choice `mine` (or -1) of expert e, K part `part`
+  auto add = [&](int e, int part, auto&& choice) {
+    int c0, c1;
+    share(chunks, part, kparts, c0, c1);
+    const int64_t row = (int64_t)e * a.n + n0, left = min(a.n - n0, (int64_t)kTile);
+    const Rows4 rows = rows4<FMT>(a.w, a.s, {row, row + 8}, {min(left, (int64_t)8), max(left - 8, (int64_t)0)}, a.K);
+    const int n = 4 * ((lane >> 2) & 3);                   // the first of the lane's four rows
+    float tw[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if constexpr (FMT == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tw[i] = a.t[a.t_mode == 0 ? (int64_t)e * a.n + min(n0 + n + i, a.n - 1) : e];
+    }
     int seen = 1;
     for (int first = 0; first < seen; first += 4) {
       int mine;
-      seen = choices_of(a.idx, S, e, first, col[wave], mine);
-      const bool on = mine >= 0;
-      const uint16_t* xp = a.h + (int64_t)(on ? mine : 0) * a.K + 128 * (lane >> 4) + 32 * (lane & 3);
-      const float wt = on ? a.weights[mine] : 0.0f;
-      v4f acc[1][4];
+      seen = choice(first, mine);
+      const float wt = mine >= 0 ? a.weights[mine] : 0.0f;
+      v4f acc[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[0][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      dot4<FMT, 1>(wp, sp, a.K / 2, a.K / (FMT == 2 ? 16 : 32), step, xp, on, a.K, c0, c1, acc);
-      const float v = gather4(acc[0]) * tw;
-      // an add in LDS: two lanes meet here where a token names an expert twice
-      if (on) atomicAdd(&sum[wave][mine / a.topk][n], wt * v);
+      for (int r = 0; r < 4; ++r) acc[r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      dot4<FMT>(rows, rx, [&]() { return mine >= 0 ? (uint32_t)mine * (2 * a.K) + x_off4() : kOff; }, a.K, c0, c1, acc);
+      const float4 p = gather4(acc);
+      float v[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                       // the four rows of 16 lanes
+        v[i] += __shfl_xor(v[i], 16, 64);
+        v[i] += __shfl_xor(v[i], 32, 64);
+      }
+      // adds in LDS: two lanes meet here where a token names an expert twice
+      if (mine >= 0 && lane < 16) {
+        float* to = &sum[wave][mine / a.topk][n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) atomicAdd(&to[i], wt * (v[i] * tw[i]));
+      }
+    }
+  };
+  const int stride = WV * gridDim.y, me = blockIdx.y * WV + wave;
+  if constexpr (MANY) {
+    __shared__ int first_of[kMaxDecodeExperts], list[kMaxDecodeExperts], idx[kMaxChoices];
+    __shared__ int col[WV][4], found[WV];
+    for (int i = tid; i < a.experts; i += 64 * WV) first_of[i] = 0x7FFFFFFF;
+    for (int c = tid; c < S; c += 64 * WV) idx[c] = a.idx[c];
+    __syncthreads();
+    for (int c = tid; c < S; c += 64 * WV)
+      if ((unsigned)idx[c] < (unsigned)a.experts) atomicMin(&first_of[idx[c]], c);
+    __syncthreads();
+    int experts = 0;
+    for (int b = 0; b < S; b += 64 * WV) {                // the chosen experts in the order of the choices
+      const int c = b + tid;
+      const int e = c < S ? idx[c] : -1;
+      const bool lead = (unsigned)e < (unsigned)a.experts && first_of[e] == c;
+      const uint64_t m = __ballot(lead);
+      if (lane == 0) found[wave] = __popcll(m);
+      __syncthreads();
+      int before = experts, here = 0;
+      for (int w = 0; w < WV; ++w) {
+        before += w < wave ? found[w] : 0;
+        here += found[w];
+      }
+      if (lead) list[before + __popcll(m & ((1ull << lane) - 1))] = e;
+      experts += here;
+      __syncthreads();
+    }
+    for (int item = me; item < experts * kparts; item += stride) {
+      const int e = __builtin_amdgcn_readfirstlane(list[item / kparts]);
+      add(e, item % kparts, [&](int first, int& mine) { return choices_of(idx, S, e, first, col[wave], mine); });
+    }
+  } else {
+    const int mine_e = lane < S ? a.idx[lane] : -1;
+    uint64_t todo = __ballot((unsigned)mine_e < (unsigned)a.experts);
+    for (int i = 0; todo; ++i) {
+      const int e = __builtin_amdgcn_readlane(mine_e, __builtin_ctzll(todo));
+      const Who<1> who{{__ballot(mine_e == e)}};
+      todo &= ~who.m[0];
+      for (int p = 0; p < kparts; ++p) {
+        if ((i * kparts + p) % stride != me) continue;
+        add(e, p, [&](int first, int& mine) {
+          mine = who.pick(first);
+          return who.count();
+        });
+      }
     }
   }
   __syncthreads();
+  const bool whole = gridDim.y == 1;
   for (int o = tid; o < a.tokens * kTile; o += 64 * WV) {
-    const int t = o >> 4, n = o & 15;
-    if (n0 + n >= a.n) continue;
-    float v = sum[0][t][n];
+    const int t = o >> 4, i = o & 15;
+    if (n0 + i >= a.n) continue;
+    float v = sum[0][t][i];
 #pragma unroll
-    for (int w = 1; w < WV; ++w) v += sum[w][t][n];
-    const int64_t to = (int64_t)t * a.n + n0 + n;
-    if (a.out32) ((float*)a.y)[to] = v;
-    else ((uint16_t*)a.y)[to] = (uint16_t)f32_to_bf16_rne(v);
+    for (int w = 1; w < WV; ++w) v += sum[w][t][i];
+    if (whole) store_y(a.y, t * a.n + n0 + i, v, a.out32);
+    else a.parts[((int64_t)blockIdx.y * a.tokens + t) * a.n + n0 + i] = v;
   }
+}
+
+__global__ void __launch_bounds__(256)
+decode_join_kernel(const float* __restrict__ parts, int n_parts, int64_t n, void* __restrict__ y, int out32) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= n) return;
+  float v = parts[at];
+  for (int p = 1; p < n_parts; ++p) v += parts[p * n + at];
+  store_y(y, at, v, out32);
 }
 
 // ---------------------------------------------------------------------------
@@ -496,23 +654,46 @@ static void by_format(int fmt, F&& go) {
   else go(ic<4>{});
 }
 
+// `each` workgroups in y. K is split over as few waves as give the CUs some 20 each (a wave's fixed work is
+// worth one to two chunks).
+template <int FMT, bool GATED, int NB>
+static void launch_gemv4(const GemvArgs& a, int64_t tiles, int64_t each, int by_choice, hipStream_t st) {
+  const int64_t chunks = (a.K + gv::kWide - 1) / gv::kWide, waves = tiles * each;
+  auto go = [&](auto KSC) {
+    constexpr int KS = decltype(KSC)::value, TILES = KS < 4 ? 4 / KS : 1;
+    hipLaunchKernelGGL((gemv4_kernel<FMT, GATED, NB, KS>), dim3((unsigned)((tiles + TILES - 1) / TILES), (unsigned)each),
+                       dim3(64 * (KS < 4 ? 4 : KS)), 0, st, a, by_choice);
+  };
+  int ks = 1;
+  while (ks < 8 && 2 * ks <= chunks && waves * ks < 16384) ks *= 2;
+  if (ks == 1) go(ic<1>{});
+  else if (ks == 2) go(ic<2>{});
+  else if (ks == 4) go(ic<4>{});
+  else go(ic<8>{});
+}
+
 hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, const void* x, int64_t ld_x, const void* w,
                        const void* s, const float* t, int t_mode, void* y, int64_t ld_y, int out32, hipStream_t st) {
   const GemvArgs a{(const uint16_t*)x, ld_x, (int)rows, 1, nullptr, 1, (const uint8_t*)w, (const uint8_t*)s, t, t_mode, n,
                    (int)K, y, ld_y, out32};
-  const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile));
+  const int64_t tile = gated ? kTileOut<true> : kTileOut<false>, tiles = (n + tile - 1) / tile;
+  const dim3 grid((unsigned)tiles);
   by_format(fmt, [&](auto F) {
     constexpr int FMT = decltype(F)::value;
     auto go = [&](auto G) {
       constexpr bool GATED = decltype(G)::value != 0;
-      constexpr int WV = 8;
       if (rows <= 4) {
-        if (K <= 4 * gv::kWide) hipLaunchKernelGGL((gemv4_kernel<FMT, GATED, false, 4>), grid, dim3(64 * 4), 0, st, a, 0);
-        else hipLaunchKernelGGL((gemv4_kernel<FMT, GATED, false, 8>), grid, dim3(64 * 8), 0, st, a, 0);
+        launch_gemv4<FMT, GATED, kDense>(a, tiles, 1, 0, st);
+        return;
       }
-      else if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, WV>), grid, dim3(64 * WV), 0, st, a);
-      else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, WV>), grid, dim3(64 * WV), 0, st, a);
-      else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, WV>), grid, dim3(64 * WV), 0, st, a);
+      auto by_rows = [&](auto W) {
+        constexpr int WV = decltype(W)::value;
+        if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, WV>), grid, dim3(64 * WV), 0, st, a);
+        else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, WV>), grid, dim3(64 * WV), 0, st, a);
+        else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, WV>), grid, dim3(64 * WV), 0, st, a);
+      };
+      if (K > 16 * gv::kChunk) by_rows(ic<16>{});
+      else by_rows(ic<8>{});
     };
     if (gated) go(ic<1>{});
     else go(ic<0>{});
@@ -528,32 +709,53 @@ hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t 
                    t_mode, inter, (int)K, h, inter, 0};
   // one row of workgroups per expert that can be named: the choices, or the experts where those are fewer
   const int by_choice = S < experts;
-  const dim3 grid((unsigned)((inter + gv::kTile - 1) / gv::kTile), (unsigned)(by_choice ? S : experts));
+  const int64_t tiles = (inter + kTileOut<true> - 1) / kTileOut<true>, each = by_choice ? S : experts;
   by_format(fmt, [&](auto F) {
     constexpr int FMT = decltype(F)::value;
-    if (K <= 4 * gv::kWide) hipLaunchKernelGGL((gemv4_kernel<FMT, true, true, 4>), grid, dim3(64 * 4), 0, st, a, by_choice);
-    else hipLaunchKernelGGL((gemv4_kernel<FMT, true, true, 8>), grid, dim3(64 * 8), 0, st, a, by_choice);
+    if (S <= 64) launch_gemv4<FMT, true, 1>(a, tiles, each, by_choice, st);
+    else if (S <= 256) launch_gemv4<FMT, true, 4>(a, tiles, each, by_choice, st);
+    else if (S <= 512) launch_gemv4<FMT, true, 8>(a, tiles, each, by_choice, st);
+    else launch_gemv4<FMT, true, 0>(a, tiles, each, by_choice, st);
   });
   return hipGetLastError();
 }
 
+// Shares of the chosen experts that the down call may be cut into: tiles of 16 rows alone fill the CUs
+// twice from 8192 rows on.
+static int64_t down_shares(int64_t n) {
+  const int64_t tiles = (n + gv::kTile - 1) / gv::kTile;
+  return std::max<int64_t>(1, std::min<int64_t>(8, 512 / tiles));
+}
+size_t decode_down_ws_bytes(int64_t tokens, int64_t n) {
+  const int64_t p = down_shares(n);
+  return p == 1 ? 0 : (size_t)((p * tokens * n * 4 + 255) / 256 * 256);
+}
+
 hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t K, const void* h,
                               const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
-                              int t_mode, void* y, int out32, hipStream_t st) {
+                              int t_mode, void* y, int out32, void* ws, hipStream_t st) {
   const DownArgs a{(const uint16_t*)h, (int)tokens, (int)topk, idx, weights, (int)experts, (const uint8_t*)w,
-                   (const uint8_t*)s, t, t_mode, n, (int)K, y, out32};
-  constexpr int WV = 16;
-  // parts of K so that a few choices still give every wave one
-  const int64_t S = tokens * topk, chunks = (K + gv::kWide - 1) / gv::kWide;
+                   (const uint8_t*)s, t, t_mode, n, (int)K, y, out32, (float*)ws};
+  constexpr int WV = 8;
+  const int64_t S = tokens * topk, chunks = (K + gv::kWide - 1) / gv::kWide, most = std::min(S, experts);
+  // shares: as long as every wave is left four chunks; parts of K so that a few choices still give every wave one
+  const int64_t shares = std::max<int64_t>(1, std::min(down_shares(n), most * chunks / (4 * WV)));
   int kparts = 1;
-  while (S * kparts < WV && 2 * kparts <= chunks) kparts *= 2;
-  const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile));
+  while (most * kparts < WV * shares && 2 * kparts <= chunks) kparts *= 2;
+  const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile), (unsigned)shares);
   by_format(fmt, [&](auto F) {
-    if (tokens <= 16)
-      hipLaunchKernelGGL((decode_down_kernel<decltype(F)::value, 16, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
-    else
-      hipLaunchKernelGGL((decode_down_kernel<decltype(F)::value, 64, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
+    constexpr int FMT = decltype(F)::value;
+    auto go = [&](auto T) {
+      constexpr int TCAP = decltype(T)::value;
+      if (S <= 64) hipLaunchKernelGGL((decode_down_kernel<FMT, TCAP, false, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
+      else hipLaunchKernelGGL((decode_down_kernel<FMT, TCAP, true, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
+    };
+    if (tokens <= 16) go(ic<16>{});
+    else go(ic<64>{});
   });
+  if (shares > 1)
+    hipLaunchKernelGGL(decode_join_kernel, dim3((unsigned)((tokens * n + 255) / 256)), dim3(256), 0, st, (const float*)ws,
+                       (int)shares, tokens * n, y, out32);
   return hipGetLastError();
 }
 

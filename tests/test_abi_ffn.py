@@ -100,6 +100,7 @@ def test_gemv_validation():
     def g(fmt=B.NVFP4, rows=4, N=16, K=64, x=P, ld=64, W=P, s=P, t=P, sc=TENSOR, y=P, ldy=16):
         return B.lib().gemv_swiglu(fmt, rows, N, K, x, ld, W, s, t, sc, y, ldy, None)
 
+    assert g(N=1 << 20, K=1 << 12, ld=1 << 12, ldy=1 << 20) == 2            # gate and up rows: 2^32 bytes
     assert f(yd=2) == 4 and f(y=P + 2) == 3 and f(y=P + 1, yd=BF) == 3
     for q in (f, g):
         assert q(rows=-1) == 2 and q(rows=65) == 2 and q(N=-1) == 2
@@ -109,7 +110,7 @@ def test_gemv_validation():
         assert q(x=None) == 1 and q(W=None) == 1 and q(s=None) == 1 and q(t=None) == 1 and q(y=None) == 1
         assert q(sc=GROUP) == 4
         assert q(K=0, ld=64) == 2 and q(K=48) == 2 and q(ld=32) == 2 and q(ldy=8) == 2 and q(K=1 << 23, ld=1 << 23) == 2
-        assert q(N=1 << 40, ldy=1 << 40) == 2
+        assert q(N=1 << 40, ldy=1 << 40) == 2 and q(ld=1 << 29) == 2
         assert q(x=MIS) == 3 and q(W=MIS) == 3 and q(s=P + 1) == 3 and q(t=P + 2) == 3 and q(ld=68) == 3 and q(y=P + 1) == 3
 
 
@@ -117,8 +118,15 @@ def test_moe_decode_validation():
     def f(fmt=B.MXFP4, T=4, k=2, E=8, n=16, K=64, x=P, ld=64, idx=P, W=P, s=P, t=None, sc=GROUP, h=P):
         return B.lib().moe_decode_gate_up(fmt, T, k, E, n, K, x, ld, idx, W, s, t, sc, h, None)
 
-    def g(fmt=B.MXFP4, T=4, k=2, E=8, n=16, K=64, x=P, idx=P, w=P, W=P, s=P, t=None, sc=GROUP, h=P, yd=F32):
-        return B.lib().moe_decode_down(fmt, T, k, E, n, K, x, idx, w, W, s, t, sc, h, yd, None)
+    need = B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 4, 16, 0)
+    assert need > 0 and B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 4, 8192, 0) == 0
+    assert B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 0, 16, 0) == 0
+
+    def g(fmt=B.MXFP4, T=4, k=2, E=8, n=16, K=64, x=P, idx=P, w=P, W=P, s=P, t=None, sc=GROUP, h=P, yd=F32, ws=P, wsn=need):
+        return B.lib().moe_decode_down(fmt, T, k, E, n, K, x, idx, w, W, s, t, sc, h, yd, ws, wsn, None)
+
+    assert g(ws=None) == 5 and g(wsn=need - 1) == 5 and g(ws=P + 2) == 3
+    assert g(T=64, k=32, E=64, K=1 << 20, wsn=1 << 20) == 2                 # h of 2^32 bytes
 
     for q in (f, g):
         assert q(T=-1) == 2 and q(T=65) == 2 and q(k=-1) == 2 and q(k=33) == 2 and q(E=-1) == 2 and q(E=1025) == 2
