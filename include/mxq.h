@@ -756,13 +756,13 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
  *   Defined by: SwiGLU blocks whose gate and up projections enter one fused GEMM ("Miles
  *   Blackwell RL", remio.ai, section "Un Cuantizador Compartido ...").
  *   The FP32 product is not stored: h, and (g | u) where the backward wants it, are each
- *   rounded to BF16 once, from the FP32 sums (h: a binary32 evaluation within 2^-20 of the
- *   exact function of the sums). moe_swiglu_quantize_nvfp4, on a stored FP32 product, rounds h
+ *   rounded to BF16 once, from the FP32 sums (h: a binary32 evaluation within 2^-17 of the
+ *   exact function of the sums, plus 2^-126 |g u|). moe_swiglu_quantize_nvfp4, on a stored FP32 product, rounds h
  *   correctly instead.
  *   fmt, A, sA, tA, sB, tB: as gemm_block_scaled, MXQ_MXFP8, MXQ_NVFP4 or MXQ_BF16 (tA, tB:
  *             MXQ_NVFP4, scopes ROW or TENSOR). B: (2 inter, K), the gate rows, then the up rows.
  *   h       : BF16 (M, inter);  gate_up: BF16 (M, 2 inter) = (g | u), NULL = not written.
- *   Requires inter % 8 == 0, K % 32 == 0 (BF16: % 8), K <= 2^22, 2 inter rows of B below 2^31 bytes;
+ *   Requires inter % 8 == 0, K % 32 == 0 (BF16: % 8), both <= 2^22, 2 inter rows of B below 2^31 bytes;
  *   every pointer but tA and tB 16-byte aligned. Outputs must not overlap inputs.
  * ------------------------------------------------------------------------- */
 mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,

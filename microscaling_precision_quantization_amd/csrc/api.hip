@@ -100,6 +100,7 @@ constexpr int64_t kMaxRouteTokens = int64_t(1) << 22;  // router: 16 bits for th
 // or (gather) the whole gathered operand, must span less than 2^31 bytes.
 constexpr int64_t kMaxGemmK = int64_t(1) << 22;
 constexpr int64_t kMaxGridTiles = (int64_t(1) << 24) - 1;   // of 256 threads: a grid holds fewer than 2^32
+constexpr int64_t kMaxInter = int64_t(1) << 22;              // 32 rows of (g | u) within 32-bit offsets
 constexpr int64_t kMaxDecodeRows = 64;                       // rows of a matrix-vector product
 inline int64_t gemm_row_bytes(mxq_format fmt, int64_t k) {
   return fmt == MXQ_BF16 ? 2 * k : fmt == MXQ_MXFP8 ? k : k / 2;   // NVFP4, MXFP4: two per byte
@@ -846,10 +847,9 @@ mxq_status gated_check(mxq_format fmt, int64_t rows, int64_t inter, int64_t n, i
   if (!A || !B) return MXQ_ERR_NULL;
   const bool scaled = fmt == MXQ_MXFP8 || fmt == MXQ_NVFP4;
   if (scaled && (!sA || !sB)) return MXQ_ERR_NULL;
-  if (inter % 8 || K % (scaled ? 32 : 8) || K > kMaxGemmK) return MXQ_ERR_SHAPE;
+  if (inter % 8 || K % (scaled ? 32 : 8) || K > kMaxGemmK || inter > kMaxInter) return MXQ_ERR_SHAPE;
   // the rows of B that a tile reads, gate and up, lie within 32-bit offsets
-  if (inter > kMaxGridBlocks || (K > 0 && n > 0x7FFFFFFF / (gemm_row_bytes(fmt, K) > 0 ? gemm_row_bytes(fmt, K) : 1)))
-    return MXQ_ERR_SHAPE;
+  if (K > 0 && n > 0x7FFFFFFF / gemm_row_bytes(fmt, K)) return MXQ_ERR_SHAPE;
   if (!al16(A) || !al16(B) || (scaled && (!al16(sA) || !al16(sB)))) return MXQ_ERR_ALIGN;
   return MXQ_OK;
 }

@@ -77,7 +77,8 @@ struct Cfg {
   static constexpr int EPI_PITCH = BN / 2 + 8;
   static constexpr int EPI_BYTES = EPI_STAGED ? 4 * 32 * EPI_PITCH * 4 : 0;
   static constexpr int LDS_MAIN = NS * STAGE + (CH ? 2 * CH_HALF : 0);
-  static constexpr int LDS_TOTAL = LDS_MAIN > EPI_BYTES ? LDS_MAIN : EPI_BYTES;
+  // (SwiGLU on NVFP4: tA of the tile's rows behind all of it)
+  static constexpr int LDS_TOTAL = (LDS_MAIN > EPI_BYTES ? LDS_MAIN : EPI_BYTES) + (LD == 2 && EPI != 0 ? BM * 4 : 0);
   static_assert(A_BYTES % 4096 == 0 && B_BYTES % 4096 == 0, "tile must split into 1 KiB wave loads");
   // chunk c + 1 is issued at stage SPC c ahead of that stage's loads (tile SPC c + NS - 1);
   // the wait for tile SPC (c + 1) must cover it
@@ -303,33 +304,34 @@ __device__ __forceinline__ void static_for(F&& f) {
 // ---------------------------------------------------------------------------
 // SwiGLU in the epilogue
 // ---------------------------------------------------------------------------
-// Eight consecutive values of an FP32 or BF16 row.
-__device__ __forceinline__ void load8(const void* p, int64_t at, int f32, float* v) {
-  if (f32) {
-    const float4* q = reinterpret_cast<const float4*>((const float*)p + at);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>((const uint16_t*)p + at), v);
-  }
+// Rows of a wave's strip as a buffer: reads past them give zeros, writes past them are dropped, so that no
+// access needs a branch (columns past the end take an offset past it).
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t strip_rsrc(const void* base, int64_t row, int64_t rows, int64_t row_bytes) {
+  const int64_t bytes = rows > 0 ? rows * row_bytes : 0;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)base + (rows > 0 ? row * row_bytes : 0)), (short)0, (int)bytes,
+                                           0x00020000);
 }
-__device__ __forceinline__ uint4 pack8_bf16(const float* v) {
-  return make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+constexpr int kNonTemporal = 2;                           // the cache policy of the streaming stores
+__device__ __forceinline__ void store8_bf16(__amdgpu_buffer_rsrc_t rs, const float* v, uint32_t off) {
+  const v4u p = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+  __builtin_amdgcn_raw_buffer_store_b128(p, rs, (int)off, 0, kNonTemporal);
 }
 
-// Each 32-row strip of the wave's accumulators (NVFP4: times tA tB) goes to LDS as FP32; a lane then takes
-// 8 consecutive h columns of a row, so that every access to memory is 16 bytes and a row's segments
-// are whole lines.
-template <int LD, int BM, int BN, int TI, int TJ, int P, int EPI, typename Acc>
+// Each 32-row strip of the wave's accumulators (NVFP4: times tB) goes to LDS as FP32; a lane then takes 8
+// consecutive h columns of a row (NVFP4: times the row's tA, which the tile's prologue has put into LDS), so
+// that every access to memory is 16 bytes and a row's segments are whole lines. The backward's reads of
+// (g | u) of the next strip are on their way while one is worked on.
+template <int LD, int BM, int BN, int TI, int TJ, int P, int EPI, bool GU32, typename Acc>
 __device__ __forceinline__ void gated_epilogue(const ExactProblem& p, const GatedArgs& ga, int64_t m0, int64_t n0,
-                                               const Acc& acc, uint8_t* lds) {
+                                               const Acc& acc, uint8_t* lds, const float* lds_ta) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int h = lane >> 5, lr = lane & 31;
   constexpr int W = EPI == 1 ? BN / 4 : BN / 2;           // h columns of the wave
-  constexpr int CPR = W / 8, RPI = 64 / CPR;              // chunks of 8 columns a row, rows a pass
-  __syncthreads();                                        // every wave is done with the stage buffers
+  constexpr int CPR = W / 8, RPI = 64 / CPR, KP = 32 / RPI;   // chunks of 8 columns a row, rows a pass, passes
+  constexpr int ES = GU32 ? 4 : 2;
   float* stg = reinterpret_cast<float*>(lds) + wave * 32 * P;
   const int64_t I = ga.inter, col0 = n0 + wn * W, col = col0 + 8 * (lane % CPR);
   float tb[TJ];
@@ -341,53 +343,91 @@ __device__ __forceinline__ void gated_epilogue(const ExactProblem& p, const Gate
       tb[j] = c < I ? (p.tB_mode == 0 ? p.tB[row] : p.tB[0]) : 0.0f;
     }
   }
+  // offsets of the lane's chunk in a row of I (h) and, for the row of pass k, in the strip
+  const uint32_t rl0 = lane / CPR;
+  const bool in = col < I;
+  // the backward's reads run one unit ahead: a strip of BF16, half a strip of FP32 (64 registers either way)
+  constexpr int NU = EPI == 2 && GU32 ? 2 : 1, UP = KP / NU, NQ = GU32 ? 4 : 2;
+  v4u gu[EPI == 2 ? 2 : 1][UP][NQ];                       // per pass g (first half of NQ), u
+  auto fetch = [&](int unit, auto B) {
+    if constexpr (EPI == 2) {
+      const int64_t r0 = m0 + wm * (BM / 2) + unit / NU * 32;
+      const auto rs = strip_rsrc(ga.gu_in, p.a_base + r0, min((int64_t)32, p.m_valid - r0), 2 * I * ES);
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int64_t rbase = m0 + wm * (BM / 2) + i * 32;
+      for (int k = 0; k < UP; ++k) {
+        const uint32_t o = in ? (uint32_t)((rl0 + (unit % NU * UP + k) * RPI) * 2 * I + col) * ES : kOutOfRange;
+#pragma unroll
+        for (int q = 0; q < NQ / 2; ++q) {
+          gu[decltype(B)::value][k][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(o + 16 * q), 0, kNonTemporal);
+          gu[decltype(B)::value][k][NQ / 2 + q] =
+              __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(o + 16 * q), (int)(I * ES), kNonTemporal);
+        }
+      }
+    }
+  };
+  fetch(0, ic<0>{});
+  __syncthreads();                                        // every wave is done with the stage buffers
+  static_for<0, TI>([&](auto IC) {
+    constexpr int i = decltype(IC)::value;
+    const int64_t r0 = m0 + wm * (BM / 2) + i * 32, rows = min((int64_t)32, p.m_valid - r0);
+    const auto rsh = strip_rsrc(ga.h, p.a_base + r0, ga.h ? rows : 0, I * 2);
+    const auto rsg = strip_rsrc(ga.gu, p.a_base + r0, ga.gu ? rows : 0, I * 4);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int rl = (r / 4) * 8 + h * 4 + (r % 4);
-      float ta = 1.0f;
-      if constexpr (LD == 2) {
-        const int64_t row = rbase + rl;
-        const int64_t arow = row < p.m_valid ? exact_src_row(p, row) : -1;
-        ta = arow < 0 ? 0.0f : p.tA_mode == 0 ? p.tA[arow] : p.tA[0];
-      }
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) stg[rl * P + j * 32 + lr] = LD == 2 ? (acc[i][j][r] * ta) * tb[j] : acc[i][j][r];
+      for (int j = 0; j < TJ; ++j) stg[rl * P + j * 32 + lr] = LD == 2 ? acc[i][j][r] * tb[j] : acc[i][j][r];
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0): this wave's LDS writes landed
-#pragma unroll
-    for (int k = 0; k < 32 / RPI; ++k) {
-      const int rl = k * RPI + lane / CPR;
-      const int64_t row = rbase + rl;
+    static_for<0, KP>([&](auto KC) {
+      constexpr int k = decltype(KC)::value, unit = i * NU + k / UP, B = EPI == 2 ? unit % 2 : 0;
+      if constexpr (EPI == 2 && k % UP == 0 && unit + 1 < TI * NU) fetch(unit + 1, ic<(unit + 1) % 2>{});
+      const uint32_t rl = rl0 + k * RPI;
       const float* src = stg + rl * P + 8 * (lane % CPR);
-      float a[8], b[8], dg[8], du[8], hv[8];
-      load8(src, 0, 1, a);
-      if constexpr (EPI == 1) load8(src + W, 0, 1, b);
-      if (row >= p.m_valid || col >= I) continue;
-      const int64_t at = p.a_base + row;                  // row of the outputs
+      const float ta = LD == 2 ? lds_ta[wm * (BM / 2) + i * 32 + rl] : 1.0f;
+      float a[8], b[8], hv[8];
+      auto row8 = [&](const float* q, float* v) {
+        const float4 x = reinterpret_cast<const float4*>(q)[0], y = reinterpret_cast<const float4*>(q)[1];
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        if constexpr (LD == 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= ta;
+        }
+      };
+      const uint32_t oh = in ? (uint32_t)(rl * I + col) * 2 : kOutOfRange;
+      const uint32_t og = in ? (uint32_t)(rl * 2 * I + col) * 2 : kOutOfRange;
+      row8(src, a);
       if constexpr (EPI == 1) {
+        row8(src + W, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) hv[e] = swiglu_forward(a[e], b[e]);
-        store16<true>(ga.h + at * I + col, pack8_bf16(hv));
+        store8_bf16(rsh, hv, oh);
         if (ga.gu) {
-          store16<true>(ga.gu + at * 2 * I + col, pack8_bf16(a));
-          store16<true>(ga.gu + at * 2 * I + I + col, pack8_bf16(b));
+          store8_bf16(rsg, a, og);
+          store8_bf16(rsg, b, in ? og + (uint32_t)(2 * I) : kOutOfRange);
         }
       } else {
-        float g[8], u[8];
-        load8(ga.gu_in, at * 2 * I + col, ga.gu32, g);
-        load8(ga.gu_in, at * 2 * I + I + col, ga.gu32, u);
+        float dg[8], du[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) swiglu_backward(a[e], g[e], u[e], dg[e], du[e], hv[e]);
-        store16<true>(ga.gu + at * 2 * I + col, pack8_bf16(dg));
-        store16<true>(ga.gu + at * 2 * I + I + col, pack8_bf16(du));
-        if (ga.h) store16<true>(ga.h + at * I + col, pack8_bf16(hv));
+        for (int e = 0; e < 8; ++e) {
+          float g, u;
+          if constexpr (GU32) {
+            g = __uint_as_float(gu[B][k % UP][e / 4][e % 4]);
+            u = __uint_as_float(gu[B][k % UP][2 + e / 4][e % 4]);
+          } else {
+            const uint32_t gw = gu[B][k % UP][0][e / 2], uw = gu[B][k % UP][1][e / 2];
+            g = e % 2 ? bf16_hi(gw) : bf16_lo(gw);
+            u = e % 2 ? bf16_hi(uw) : bf16_lo(uw);
+          }
+          swiglu_backward(a[e], g, u, dg[e], du[e], hv[e]);
+        }
+        store8_bf16(rsg, dg, og);
+        store8_bf16(rsg, du, in ? og + (uint32_t)(2 * I) : kOutOfRange);
+        if (ga.h) store8_bf16(rsh, hv, oh);
       }
-    }
+    });
     __builtin_amdgcn_s_waitcnt(0xC07F);                   // reads done before the next strip overwrites
-  }
+  });
 }
 
 // Tile of BM x BN outputs over K in [k_begin, k_end); 4 waves in a 2 x 2 grid,
@@ -1098,6 +1138,14 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
     promote4();
   };
 
+  if constexpr (LD == 2 && EPI != 0) {                    // the epilogue's row scales, out of its way
+    if (threadIdx.x < BM) {
+      const int64_t row = m0 + threadIdx.x;
+      const int64_t src = row < p.m_valid ? exact_src_row(p, row) : -1;
+      reinterpret_cast<float*>(lds0 + C::LDS_TOTAL - BM * 4)[threadIdx.x] =
+          src < 0 ? 0.0f : p.tA_mode == 0 ? p.tA[src] : p.tA[0];
+    }
+  }
   // prologue: scale chunk 0, tiles 0 .. NS-2 in flight, then the first sub-block's fragments
   issue_chunk(0);
   static_for<0, NS - 1>([&](auto T) { issue_range(tile_k(T.value), T, ic<0>{}, ic<UNITS>{}); });
@@ -1151,7 +1199,9 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
   exact_drain();
 
   if constexpr (EPI != 0) {
-    gated_epilogue<LD, BM, BN, TI, TJ, C::EPI_PITCH, EPI>(p, ga, m0, n0, acc, lds0);
+    const float* ta = reinterpret_cast<const float*>(lds0 + C::LDS_TOTAL - (LD == 2 ? BM * 4 : 0));
+    if (EPI == 2 && ga.gu32) gated_epilogue<LD, BM, BN, TI, TJ, C::EPI_PITCH, EPI, true>(p, ga, m0, n0, acc, lds0, ta);
+    else gated_epilogue<LD, BM, BN, TI, TJ, C::EPI_PITCH, EPI, false>(p, ga, m0, n0, acc, lds0, ta);
   } else if constexpr (C::EPI_STAGED) {
     // NVFP4: C = tA tB acc. Each 32-row strip of the wave's block is scaled into LDS, then
     // leaves as 16-byte row segments (measured: 12-40% faster dense NVFP4 GEMMs than

@@ -3,13 +3,15 @@ may be off by. Plain torch on FP64 tensors (any device).
 
 Bounds. A binary32 sum of K exact products is within K 2^-24 S of the exact sum in any order, S the sum
 of the products' magnitudes; SUM doubles that for the matrix core's inner steps. A rounding to BF16 is
-within 2^-8 of the value (2^-134 below its normal numbers), one to binary32 within 2^-24. sigma and what
-it is made of are within EVAL of exact; sigma below binary32's normal numbers is off by up to 2^-148."""
+within 2^-8 of the value (2^-134 below its normal numbers), one to binary32 within 2^-24. sigma: its
+exponential's argument, rounded in binary32, is off by 2^-24 relative, so e^-|g| by |g| 2^-24, at most
+87.4 2^-24 < 2^-17.5 where it is not 0; with an ulp or two for each further step, EVAL = 2^-17 holds for sigma,
+1 - sigma and what is made of them. Where e^-|g| is below 2^-126 it is 0: off by up to 2^-126."""
 
 import torch
 
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0)
-BF16, F32, EVAL, TINY = 2.0 ** -8, 2.0 ** -24, 2.0 ** -20, 2.0 ** -134
+BF16, F32, EVAL, TINY, SUB = 2.0 ** -8, 2.0 ** -24, 2.0 ** -17, 2.0 ** -134, 2.0 ** -125
 SUM = 2.0 * F32
 
 
@@ -42,7 +44,7 @@ def gated(y, err):
     eg, eu = err.chunk(2, -1)
     s = torch.sigmoid(g)
     h = g * s * u
-    off = 1.1 * (eg * (u.abs() + eu)) + (g * s).abs() * eu + EVAL * h.abs() + 2.0 ** -148 * (g * u).abs()
+    off = 1.1 * (eg * (u.abs() + eu)) + (g * s).abs() * eu + EVAL * h.abs() + SUB * (g * u).abs()
     return h, (1 + BF16) * off + half_step(h), (1 + BF16) * err + half_step(y)
 
 
@@ -52,7 +54,7 @@ def through(dh, err, gate_up):
     s, c = torch.sigmoid(g), torch.sigmoid(-g)
     dg, du, h = dh * u * s * (1 + g * c), dh * g * s, g * s * u
     ds = s * (1 + g.abs() * c)                              # the size of what is added up in the derivative
-    sub = 2.0 ** -148 * (1 + g.abs())
+    sub = SUB * (1 + g.abs())
     eg = u.abs() * ((dh.abs() + err) * (EVAL * ds + sub) + err * ds)
     eu = (dh.abs() + err) * (EVAL * (g * s).abs() + sub) + err * (g * s).abs()
     eh = EVAL * h.abs() + sub * u.abs()
