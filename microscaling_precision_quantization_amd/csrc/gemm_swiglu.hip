@@ -14,18 +14,20 @@ namespace mxq {
 void launch_tile_prefix(const int64_t* offsets, int64_t groups, int64_t total, int64_t bm, int64_t tiles_n, int64_t* prefix,
                         hipStream_t st);
 
+template <int LD, int BN> constexpr bool kShort = LD == 0 && BN == 256;
+
 // h columns of a tile
 template <int BN, int EPI> constexpr int kTileCols = EPI == 1 ? BN / 2 : BN;
 
-template <int LD, int BT, int SM, bool WIDE, int EPI>
-__global__ void __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <int LD, int BM, int BN, int SM, int OCC, bool WIDE, int EPI>
+__global__ void __launch_bounds__(256, OCC) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 gated_dense_kernel(ExactProblem p, GatedArgs ga, int64_t tiles_m, int64_t tiles_n) {
-  using C = gx::Cfg<LD, BT, BT, SM, 1, WIDE, EPI>;
+  using C = gx::Cfg<LD, BM, BN, SM, OCC, WIDE, EPI, kShort<LD, BN>>;
   MXQ_EXACT_LDS(C)
   int64_t tm, tn;
   if (!exact_map_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
-  exact_gemm_tile<LD, BT, BT, SM, 1, WIDE, false, false, EPI>(p, tm * BT, tn * kTileCols<BT, EPI>, lds0, lds1, lds2, lds3,
-                                                              ldsc, ga);
+  exact_gemm_tile<LD, BM, BN, SM, OCC, WIDE, false, false, EPI, kShort<LD, BN>>(p, tm * BM, tn * kTileCols<BN, EPI>, lds0, lds1,
+                                                                               lds2, lds3, ldsc, ga);
 }
 
 // Per expert: group g covers the slots [offsets[g], offsets[g + 1]); tile order as in
@@ -67,7 +69,9 @@ gated_grouped_kernel(ExactProblem base, GatedArgs ga, const int64_t* __restrict_
       else p.tB = base.tB + g * n;
     }
   }
-  constexpr bool PART = LD == 2;                          // expert tails, as in exact_grouped_kernel
+  // expert tails (waves with no or few valid rows skip their matrix work): NVFP4 as in exact_grouped_kernel;
+  // against the transposed NVFP4 weights 2% with experts of 263 rows, nothing for BF16
+  constexpr bool PART = LD == 2 || LD == 6;
   exact_gemm_tile<LD, BM, BN, SM, OCC, false, false, PART, EPI>(p, tm * BM, tn * kTileCols<BN, EPI>, lds0, lds1, lds2, lds3,
                                                                 ldsc, ga);
 }
@@ -95,17 +99,20 @@ static int gated_scale_mode(int ld, int64_t K) {
 
 template <int LD, int SM, int EPI>
 static void launch_gated_dense_t(const ExactProblem& p, const GatedArgs& ga, hipStream_t st) {
-  constexpr bool WIDE = SM == 2;
-  auto go = [&](auto BTC) {
-    constexpr int BT = decltype(BTC)::value;
-    const int64_t tm = (p.m_valid + BT - 1) / BT, tn = (ga.inter + kTileCols<BT, EPI> - 1) / kTileCols<BT, EPI>;
-    hipLaunchKernelGGL((gated_dense_kernel<LD, BT, SM, WIDE, EPI>), dim3((unsigned)((tm * tn + 7) / 8 * 8)), dim3(256), 0,
-                       st, p, ga, tm, tn);
+  auto go = [&](auto BMC, auto BNC, auto OC) {
+    constexpr int BM = decltype(BMC)::value, BN = decltype(BNC)::value, OCC = decltype(OC)::value;
+    const int64_t tm = (p.m_valid + BM - 1) / BM, tn = (ga.inter + kTileCols<BN, EPI> - 1) / kTileCols<BN, EPI>;
+    hipLaunchKernelGGL((gated_dense_kernel<LD, BM, BN, SM, OCC, SM == 2 && OCC == 1, EPI>), dim3((unsigned)((tm * tn + 7) / 8 * 8)), dim3(256),
+                       0, st, p, ga, tm, tn);
   };
   // 256 x 256 unless that leaves most of the 256 CUs idle
   const int64_t n = EPI == 1 ? 2 * ga.inter : ga.inter;
-  if (((p.m_valid + 255) / 256) * ((n + 255) / 256) >= 192) go(ic<256>{});
-  else go(ic<128>{});
+  if (((p.m_valid + 255) / 256) * ((n + 255) / 256) >= 192) go(ic<256>{}, ic<256>{}, ic<1>{});
+  // small tiles, more than one a CU: two share it, one's epilogue beside the other's main loop (4096 x 2048 -> 2 x 768
+  // BF16 43 -> 36 us, backward 2011 x 2048 of 4096 MXFP8 52 -> 49); one a CU keeps all of LDS for its stages (1024 x
+  // 7168 -> 2 x 2048 BF16 72 against 103)
+  else if (((p.m_valid + 127) / 128) * ((n + 127) / 128) > 256) go(ic<128>{}, ic<128>{}, ic<2>{});
+  else go(ic<128>{}, ic<128>{}, ic<1>{});
 }
 
 template <int LD, int EPI>
@@ -195,7 +202,12 @@ hipError_t launch_grouped_gemm_swiglu_backward(int fmt, int64_t groups, const in
   int64_t* prefix = (int64_t*)ws;
   if (fmt == 7) {
     p.ldb = inter;
-    launch_gated_grouped_t<6, 256, 256, 0, 1, 2>(p, ga, offsets, groups, total, prefix, st);
+    // 256-row tiles where the experts fill them and the CUs get one each (1024 rows x 16 experts x 2048 columns
+    // 680 us against 753); else 128 rows (263 rows x 128 experts x 768 columns 250 against 263-272, 512 x 8 x 1024
+    // 96 against 140)
+    const bool tall = total / groups >= 384 && (total + 255) / 256 * ((inter + 255) / 256) >= 192;
+    if (tall) launch_gated_grouped_t<6, 256, 256, 0, 1, 2>(p, ga, offsets, groups, total, prefix, st);
+    else launch_gated_grouped_t<6, 128, 256, 0, 1, 2>(p, ga, offsets, groups, total, prefix, st);
   } else {
     launch_gated_grouped_bf16<2>(p, ga, offsets, groups, total, prefix, st);
   }

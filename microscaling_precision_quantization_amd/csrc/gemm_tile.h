@@ -46,10 +46,13 @@ template <int LD, int SM> struct ScaleDma {
 // OCC = workgroups meant to share one CU: the LDS budget of a workgroup is 1 / OCC of it.
 // WIDE (chunked-scale mode only): 128 bytes per row and stage for every format (MXFP8 128 K,
 // NVFP4 256 K per stage), i.e. fewer barriers and larger loads per stage.
-// EPI: what the tile ends with (see exact_gemm_tile).
-template <int LD, int BM, int BN, int SM, int OCC = 1, bool WIDE = false, int EPI = 0>
+// EPI: what the tile ends with (see exact_gemm_tile). SHORT (BF16): stages of 32 K, four in LDS, their loads
+// one at a time between the matrix instructions.
+template <int LD, int BM, int BN, int SM, int OCC = 1, bool WIDE = false, int EPI = 0, bool SHORT = false>
 struct Cfg {
-  static constexpr int RB = (WIDE && LD != 0) ? 128 : RowBytes<LD>::v;
+  static_assert(!SHORT || LD == 0, "short stages: BF16");
+  static constexpr int RB = SHORT ? 64 : (WIDE && LD != 0) ? 128 : RowBytes<LD>::v;
+  static constexpr int GS = SHORT ? 1 : 4;                // direct loads a unit (one M0 write)
   static constexpr int BK = (LD == 0 || LD == 6) ? RB / 2 : (LD == 1 || LD == 4 || LD == 5) ? RB : 2 * RB;   // K per stage
   static constexpr int SBS = LD == 5 ? RB / 64 : RB / 32;                 // sub-blocks per stage
   static_assert(!WIDE || SM == 2, "wide stages need chunked scales");
@@ -66,7 +69,7 @@ struct Cfg {
   static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
   static constexpr int FREE = kLdsBytes / OCC - 2 * CH_HALF;
   static constexpr int NS_LDS = (4 * STAGE <= FREE) ? 4 : (3 * STAGE <= FREE ? 3 : 2);
-  static constexpr int NS = (CH && NS_LDS > SPC + 1) ? SPC + 1 : NS_LDS;
+  static constexpr int NS = LD == 6 ? 2 : (CH && NS_LDS > SPC + 1) ? SPC + 1 : NS_LDS;   // (LD 6: see its B buffers)
   // 1 KiB wave instructions per wave (LD 6 builds its B tile through registers instead)
   static constexpr int IA = A_BYTES / 4096, IB = LD == 6 ? 0 : B_BYTES / 4096;
   static constexpr int IS = SU * (BM + BN) / 256;                 // 64-row scale loads per wave
@@ -446,11 +449,13 @@ __device__ __forceinline__ void gated_epilogue(const ExactProblem& p, const Gate
 // the tile covers BN / 2 of them, each wave BN / 4, its first BN / 4 product columns the gates and the
 // others the ups of the same h columns, so that both meet in one wave's accumulators. EPI 2 (SwiGLU
 // backward): the product is dh. Both write what swiglu_forward / swiglu_backward say.
-template <int LD, int BM, int BN, int SM, int OCC = 1, bool WIDE = false, bool AKM = false, bool PART = false, int EPI = 0>
+template <int LD, int BM, int BN, int SM, int OCC = 1, bool WIDE = false, bool AKM = false, bool PART = false, int EPI = 0,
+          bool SHORT = false>
 __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m0, int64_t n0, uint8_t* lds0,
                                                 uint8_t* lds1, uint8_t* lds2, uint8_t* lds3, uint8_t* ldsc,
                                                 const GatedArgs& ga = GatedArgs{}) {
-  using C = gx::Cfg<LD, BM, BN, SM, OCC, WIDE, EPI>;
+  using C = gx::Cfg<LD, BM, BN, SM, OCC, WIDE, EPI, SHORT>;
+  constexpr int GS = C::GS;
   constexpr bool PAIR = EPI == 1;
   constexpr bool AL = SM >= 1;                            // every K tile full and 64-aligned
   constexpr bool CH = C::CH;
@@ -515,14 +520,14 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
         o = src >= 0 ? (uint32_t)(src * ldA + lc * 16) : kOutOfRange;
       }
     }
-    voA[j] = o - 1024u * (uint32_t)(j % 4);                // see buf_dma16_group
+    voA[j] = o - 1024u * (uint32_t)(j % GS);               // see buf_dma16_group
   }
 #pragma unroll
   for (int j = 0; j < IB; ++j) {
     const int pos = (wave * IB + j) * 1024 + lane * 16;
     const int row = pos / RB;
     const int lc = ((pos % RB) / 16) ^ swz<RB>(row);
-    voB[j] = (uint32_t)(b_row(row) * ldB + lc * 16) - 1024u * (uint32_t)(j % 4);
+    voB[j] = (uint32_t)(b_row(row) * ldB + lc * 16) - 1024u * (uint32_t)(j % GS);
   }
   // Scales: load q of IS per wave covers 64 consecutive items of the [A rows | B rows]
   // list of unit u (SU units per stage); each lands in a 4-byte LDS slot per row.
@@ -605,7 +610,7 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
   const int kb_ = (int)p.k_begin;
   const int nk_ = ((int)p.k_end - kb_ + C::BK - 1) / C::BK;
   constexpr bool NVT = LD == 6;
-  static_assert(!NVT || (BN == 256 && C::BK == 64 && C::SBS == 4 && TJ / 2 - 1 == 1 && C::IA == 8),
+  static_assert(!NVT || (BN == 256 && C::BK == 64 && C::SBS == 4 && TJ / 2 - 1 == 1 && (C::IA == 8 || C::IA == 4)),
                 "the NVFP4-transposed B path is laid out for 256 x 64 stages of four sub-blocks");
   constexpr int BROW6 = 2 * BN;                           // bytes of one K-major B row in LDS
   constexpr int NB6 = 6;                                  // B loads per lane and stage
@@ -718,7 +723,7 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
   };
   // DMA unit d of a tile into slot S: units 0 .. GA-1 are groups of up to 4 A loads,
   // GA .. GA+GB-1 groups of B loads, then the IS scale loads.
-  constexpr int GA = (IA + 3) / 4, GB = (IB + 3) / 4, UNITS = GA + GB + IS;
+  constexpr int GA = (IA + GS - 1) / GS, GB = (IB + GS - 1) / GS, UNITS = GA + GB + IS;
   auto issue_unit = [&](const TileK& tk, auto SLOT, auto D) {
     constexpr int S = decltype(SLOT)::value, d = decltype(D)::value;
     const uint32_t lb = lbase[S];
@@ -726,11 +731,11 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
       constexpr bool isA = d < GA;
       constexpr int g = isA ? d : d - GA;
       constexpr int NI = isA ? IA : IB;
-      constexpr int N = (NI - 4 * g) < 4 ? NI - 4 * g : 4;
+      constexpr int N = (NI - GS * g) < GS ? NI - GS * g : GS;
       uint32_t vo[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int j = 4 * g + n;
+        const int j = GS * g + n;
         vo[n] = isA ? voA[j] : voB[j];
         if constexpr (!AL && !(AKM && isA)) {
           if (tk.tail) {
@@ -740,7 +745,7 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
           }
         }
       }
-      const uint32_t m0v = lb + (isA ? 0 : C::A_BYTES) + (uint32_t)(wave * NI + 4 * g) * 1024u;
+      const uint32_t m0v = lb + (isA ? 0 : C::A_BYTES) + (uint32_t)(wave * NI + GS * g) * 1024u;
       if constexpr (AKM && isA) buf_dma16_group<N>(tk.rsa, vo, 0u, m0v);
       else buf_dma16_group<N>(isA ? rsA : rsB, vo, tk.sod, m0v);
     } else if constexpr (IS > 0) {
@@ -1062,7 +1067,9 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
   // The loads of tile t + NS - 1 are spread over the first PJ B-fragment steps of
   // sub-block 0; the barrier comes after B fragment BJ of the last sub-block.
   constexpr int BJ = TJ / 2 - 1;
-  constexpr int PJ = SBS == 1 ? BJ + 1 : TJ;
+  // SHORT: over all steps up to the barrier, so that the address path keeps up with four waves' loads
+  // (all in sub-block 0 they take it twice as long as that sub-block's matrix work)
+  constexpr int PJ = SHORT ? (SBS - 1) * TJ + BJ + 1 : SBS == 1 ? BJ + 1 : TJ;
 
   // Loads issued after tile t+1's data (issued in stage t+2-NS): the data of the
   // NS-2 later tiles, plus the chunk loads of chunk-start stages among the last NS-2
@@ -1108,9 +1115,10 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
         // the barrier. Tile kt + 1's A loads and the B register loads of tile kt + 4 go out
         // during sub-block 0.
         if constexpr (NVT && jj == 0) __builtin_amdgcn_sched_barrier(0);
-        if constexpr (b == 0 && jj < PJ) {
+        constexpr int step = b * TJ + jj;
+        if constexpr ((SHORT || b == 0) && step < PJ) {
           __builtin_amdgcn_sched_barrier(0);
-          issue_range(tk, ic<SL>{}, ic<(UNITS * jj) / PJ>{}, ic<(UNITS * (jj + 1)) / PJ>{});
+          issue_range(tk, ic<SL>{}, ic<(UNITS * step) / PJ>{}, ic<(UNITS * (step + 1)) / PJ>{});
           if constexpr (NVT && jj == PJ - 1) nvt_issue(kt + 4, ic<ri % 4>{});
           __builtin_amdgcn_sched_barrier(0);
         }

@@ -54,11 +54,14 @@ DENSE = [("bf16", 1, 8, 8), ("bf16", 5, 16, 40), ("bf16", 127, 72, 64), ("bf16",
          ("nvfp4", 1, 8, 32), ("nvfp4", 129, 72, 96), ("nvfp4", 200, 264, 64), ("nvfp4", 130, 136, 256),
          ("nvfp4", 64, 128, 1280)]
 # enough 256 x 256 tiles for the large tile: 11 x 19 and more
+# more 128 x 128 tiles than CUs, fewer 256 x 256 than 192
+MANY = [(f, 1300, 1672, k) for f, k in (("bf16", 72), ("bf16", 64), ("mxfp8", 96), ("mxfp8", 128), ("mxfp8", 512), ("nvfp4", 96),
+                                        ("nvfp4", 128), ("nvfp4", 256))]
 LARGE = [("bf16", 2601, 2408, 72), ("bf16", 2601, 2408, 128), ("mxfp8", 2601, 2408, 96), ("mxfp8", 2601, 2408, 128),
          ("mxfp8", 2601, 2408, 512), ("nvfp4", 2601, 2408, 96), ("nvfp4", 2601, 2408, 128), ("nvfp4", 2601, 2408, 256)]
 
 
-@pytest.mark.parametrize("fmt,M,I,K", DENSE + LARGE)
+@pytest.mark.parametrize("fmt,M,I,K", DENSE + MANY + LARGE)
 def test_gemm_swiglu(fmt, M, I, K):
     g = gen(M * 7 + I + K)
     x, w = randn(g, M, K).to(BF), randn(g, 2 * I, K, scale=2.0 / K ** 0.5).to(BF)
@@ -113,7 +116,8 @@ def test_gates_far_out_give_zeros_and_no_nan():
     R.check(h2, hh, htol, "h")
 
 
-BACK = [c for c in DENSE + LARGE if c[0] != "nvfp4"] + [("bf16", 3200, 4104, 72), ("bf16", 3200, 4104, 64),
+BACK = [c for c in DENSE + LARGE if c[0] != "nvfp4"] + [("bf16", 2600, 1672, 72), ("mxfp8", 2600, 1672, 96), ("mxfp8", 2600, 1672, 512),
+                                                        ("bf16", 3200, 4104, 72), ("bf16", 3200, 4104, 64),
                                                         ("mxfp8", 3200, 4104, 512)]
 
 
@@ -170,6 +174,8 @@ def slots(counts, pads, tokens, seed):
 
 
 EXPERTS = [([3, 0, 1, 130, 0, 40, 0], [0, 0, 2, 5, 3, 0, 0]), ([1], [0]), ([0, 700, 520, 385], [0, 4, 0, 7])]
+# experts that fill 256-row tiles, and enough of those
+TALL = [([0, 1800, 1100, 1500], [0, 8, 0, 5])]
 
 
 @pytest.mark.parametrize("counts,pads", EXPERTS)
@@ -229,6 +235,12 @@ def test_grouped_gemm_swiglu_backward(fmt, I, K, counts, pads, f32):
         R.check(h[at], hw, htol, f"h of expert {e}")
     end(), h_end()
     assert not bool(dgu[row < 0].any()) and not bool(h[row < 0].any())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_grouped_gemm_swiglu_backward_of_tall_experts(fmt, f32):
+    test_grouped_gemm_swiglu_backward(fmt, 3088, 72, *TALL[0], f32)
 
 
 def test_rejected_offsets_leave_the_outputs_unwritten():
