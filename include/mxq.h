@@ -764,10 +764,13 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
  *   h       : BF16 (M, inter);  gate_up: BF16 (M, 2 inter) = (g | u), NULL = not written.
  *   Requires inter % 8 == 0, K % 32 == 0 (BF16: % 8), both <= 2^22, 2 inter rows of B below 2^31 bytes;
  *   every pointer but tA and tB 16-byte aligned. Outputs must not overlap inputs.
+ *   workspace : mxq_workspace_bytes(MXQ_OP_GEMM_SWIGLU, M, 2 inter, K) bytes, 16-byte aligned; NULL where
+ *             that is 0 (it is not for few rows and a long K, which is then split).
  * ------------------------------------------------------------------------- */
 mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
                        const float* tA, mxq_scope tA_scope, const void* B, const void* sB, const float* tB,
-                       mxq_scope tB_scope, void* h, void* gate_up, void* stream);
+                       mxq_scope tB_scope, void* h, void* gate_up, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* ---------------------------------------------------------------------------
  * gemm_swiglu_backward -- the gradient of the block's output through the down projection and
@@ -780,11 +783,11 @@ mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, cons
  *   gate_up   : (M, 2 inter) gu_dtype, BF16 as gemm_swiglu keeps it, or FP32.
  *   d_gate_up : BF16 (M, 2 inter) = (dg | du), what the GEMMs for dX and dW_gu read;
  *   h         : BF16 (M, inter), what the GEMM for dW_d reads; NULL = not wanted.
- *   Limits as gemm_swiglu. Outputs must not overlap inputs.
+ *   Limits as gemm_swiglu. Outputs must not overlap inputs. workspace: as there, with (M, inter, K).
  * ------------------------------------------------------------------------- */
 mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
                                 const void* B, const void* sB, const void* gate_up, mxq_out_dtype gu_dtype,
-                                void* d_gate_up, void* h, void* stream);
+                                void* d_gate_up, void* h, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * grouped_gemm_swiglu, grouped_gemm_swiglu_backward -- the same per routed expert, scheduled on
@@ -863,13 +866,14 @@ mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t
 size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols);
 
 enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD = 3, MXQ_OP_ROUTE = 4,
-       MXQ_OP_DECODE_DOWN = 5 };
+       MXQ_OP_DECODE_DOWN = 5, MXQ_OP_GEMM_SWIGLU = 6 };
 /* Workspace bytes for an op:
  *   MXQ_OP_QUANTIZE_NVFP4 (a = rows, b = cols, c = number of FP32 scales);
  *   MXQ_OP_GROUPED_GEMM   (a = groups);
  *   MXQ_OP_NORM_BACKWARD  (a = rows, b = cols);
  *   MXQ_OP_ROUTE          (a = tokens, b = experts);
- *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden). */
+ *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden);
+ *   MXQ_OP_GEMM_SWIGLU    (a = M, b = columns of the product: 2 inter forward, inter backward; c = K). */
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
 
 /* Slots that hold every routing of `tokens` tokens over `experts` experts, topk each, with

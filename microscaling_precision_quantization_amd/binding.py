@@ -24,7 +24,7 @@ BF16_NVFP4T = 5                    # grouped only: BF16 A x stacked NVFP4 weight
 _PACKED4 = (NVFP4, MXFP4)          # formats with two elements per byte
 OUT_BF16, OUT_F32 = 0, 1
 SCOPE = {"row": 0, "token": 0, "tensor": 1, "group": 2}
-OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE, OP_DECODE_DOWN = 1, 2, 3, 4, 5
+OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE, OP_DECODE_DOWN, OP_GEMM_SWIGLU = 1, 2, 3, 4, 5, 6
 GATE = {"none": 0, "token": 1, "channel": 2, "full": 3}
 
 _c_void_p = ctypes.c_void_p
@@ -82,9 +82,9 @@ _SIGS = {
     "moe_combine_backward": [_c_void_p, _int, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                              _c_void_p, _c_void_p, _c_void_p],
     "gemm_swiglu": [_int, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _int,
-                    _c_void_p, _c_void_p, _c_void_p],
+                    _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
     "gemm_swiglu_backward": [_int, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _int,
-                             _c_void_p, _c_void_p, _c_void_p],
+                             _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p],
     "grouped_gemm_swiglu": [_int, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
                             _int, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p, _size,
                             _c_void_p],
@@ -749,17 +749,6 @@ def _gated_out(c, out, names, rows: int, inter: int, keep: bool, dev):
     return new(names[0]), new(names[1]) if keep else None
 
 
-def _grouped_workspace(workspace, groups: int, dev):
-    need = lib().mxq_workspace_bytes(OP_GROUPED_GEMM, groups, 0, 0)
-    if workspace is None:
-        return _u8((max(need, 1),), dev)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace: expected contiguous uint8 memory on {dev}")
-    if workspace.numel() < need:
-        raise ValueError(f"workspace: {workspace.numel()} bytes, the call needs {need}")
-    return workspace
-
-
 def _two_d(t, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
@@ -767,7 +756,7 @@ def _two_d(t, name: str):
 
 
 def gemm_swiglu(fmt: int, A, sA, B, sB, tA=None, tB=None, tA_scope="row", tB_scope="tensor", keep_gate_up: bool = False,
-                out=None):
+                out=None, workspace=None):
     """h = silu(g) u in BF16, (g | u) = A_hat B_hat^T, in one kernel: (h (M, inter), gate_up (M, 2 inter) | None).
     fmt: MXFP8, NVFP4 or BF16; B (2 inter, K): the gate rows, then the up rows. `out` may supply
     (h, gate_up); gate_up None there = not written."""
@@ -778,8 +767,9 @@ def gemm_swiglu(fmt: int, A, sA, B, sB, tA=None, tB=None, tA_scope="row", tB_sco
         raise ValueError(f"B: {N} rows, expected as many up rows as gate rows")
     c = _Checks(A.device)
     h, gate_up = _gated_out(c, out, ("h", "gate_up"), M, N // 2, keep_gate_up, A.device)
+    ws = _workspace(OP_GEMM_SWIGLU, M, N, workspace, A.device, K)
     _call("gemm_swiglu", A.device, fmt, M, N // 2, K, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB),
-          _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up))
+          _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up), _ptr(ws), ws.numel())
     return h, gate_up
 
 
@@ -789,7 +779,7 @@ def _gate_up_dtype(gate_up) -> int:
     return OUT_F32 if gate_up.dtype == torch.float32 else OUT_BF16
 
 
-def gemm_swiglu_backward(fmt: int, A, sA, B, sB, gate_up, keep_h: bool = True, out=None):
+def gemm_swiglu_backward(fmt: int, A, sA, B, sB, gate_up, keep_h: bool = True, out=None, workspace=None):
     """The gradient A (M, K) of a gated block's output through W_d and SwiGLU: (d_gate_up BF16 (M, 2 inter),
     h BF16 (M, inter) | None). B (inter, K): W_d^T, K-contiguous; fmt BF16 or MXFP8 (the columnwise copy
     of W_d). gate_up: as gemm_swiglu kept it, or FP32. `out` may supply (d_gate_up, h)."""
@@ -800,8 +790,9 @@ def gemm_swiglu_backward(fmt: int, A, sA, B, sB, gate_up, keep_h: bool = True, o
     c = _Checks(A.device)
     c.need(gate_up, "gate_up", gate_up.dtype, (M, 2 * inter))
     d_gate_up, h = _gated_out(c, out, ("d_gate_up", "h"), M, inter, keep_h, A.device)
+    ws = _workspace(OP_GEMM_SWIGLU, M, inter, workspace, A.device, K)
     _call("gemm_swiglu_backward", A.device, fmt, M, inter, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(gate_up), gd,
-          _ptr(d_gate_up), _ptr(h))
+          _ptr(d_gate_up), _ptr(h), _ptr(ws), ws.numel())
     return d_gate_up, h
 
 
@@ -820,7 +811,7 @@ def grouped_gemm_swiglu(fmt: int, offsets, A, B, inter: int, K: int, sA=None, sB
     dev, groups = A.device, offsets.numel() - 1
     c = _Checks(dev)
     h, gate_up = _gated_out(c, out, ("h", "gate_up"), total, inter, keep_gate_up, dev)
-    ws = _grouped_workspace(workspace, groups, dev)
+    ws = _workspace(OP_GROUPED_GEMM, groups, 0, workspace, dev)
     _call("grouped_gemm_swiglu", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(a_row_index),
           A.shape[0] if a_row_index is not None else 0, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB),
           _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up), _ptr(ws), ws.numel())
@@ -843,7 +834,7 @@ def grouped_gemm_swiglu_backward(fmt: int, offsets, A, B, inter: int, K: int, ga
     c = _Checks(dev)
     c.need(gate_up, "gate_up", gate_up.dtype, (total, 2 * inter))
     d_gate_up, h = _gated_out(c, out, ("d_gate_up", "h"), total, inter, keep_h, dev)
-    ws = _grouped_workspace(workspace, groups, dev)
+    ws = _workspace(OP_GROUPED_GEMM, groups, 0, workspace, dev)
     _call("grouped_gemm_swiglu_backward", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(A), _ptr(B), _ptr(sB),
           _ptr(tB), _ptr(gate_up), gd, _ptr(d_gate_up), _ptr(h), _ptr(ws), ws.numel())
     return d_gate_up, h
@@ -997,9 +988,9 @@ def _need_gate(c, gate, gate_mode: str, name: str, rows: int, cols: int) -> int:
     return mode
 
 
-def _workspace(op: int, a: int, b: int, workspace, dev):
+def _workspace(op: int, a: int, b: int, workspace, dev, c: int = 0):
     """The call's scratch: allocated here, or the caller's, checked for size and device."""
-    need = lib().mxq_workspace_bytes(op, a, b, 0)
+    need = lib().mxq_workspace_bytes(op, a, b, c)
     if workspace is None:
         return _u8((need,), dev)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:

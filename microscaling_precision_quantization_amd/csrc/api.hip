@@ -67,10 +67,11 @@ hipError_t launch_combine_backward(const void* dy, int d32, const float* o, int6
                                    const int32_t* row_index, void* d_o, float* d_weights, hipStream_t st);
 hipError_t launch_gemm_swiglu(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
                               int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode, void* h,
-                              void* gate_up, hipStream_t st);
+                              void* gate_up, void* ws, hipStream_t st);
+size_t gated_ws_bytes(int64_t M, int64_t n, int64_t K);
 hipError_t launch_gemm_swiglu_backward(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
                                        const void* B, const void* sB, const void* gate_up, int gu32, void* d_gate_up,
-                                       void* h, hipStream_t st);
+                                       void* h, void* ws, hipStream_t st);
 hipError_t launch_grouped_gemm_swiglu(int fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
                                       int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
                                       const float* tA, int tA_mode, const void* B, const void* sB, const float* tB,
@@ -152,6 +153,7 @@ size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {
   if (op == MXQ_OP_GROUPED_GEMM) return a > 0 ? mxq::grouped_gemm_ws_bytes(a) : 0;
   if (op == MXQ_OP_NORM_BACKWARD) return a > 0 && b > 0 ? mxq::norm_backward_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_ROUTE) return a > 0 && b > 0 ? mxq::route_ws_bytes(a, b) : 0;
+  if (op == MXQ_OP_GEMM_SWIGLU) return a > 0 && b > 0 && c > 0 ? mxq::gated_ws_bytes(a, b, c) : 0;
   if (op == MXQ_OP_DECODE_DOWN) return a > 0 && b > 0 ? mxq::decode_down_ws_bytes(a, b) : 0;
   return 0;
 }
@@ -841,6 +843,14 @@ bool tiles_fit(int64_t rows, int64_t n, int64_t groups) {
   return tm <= kMaxGridTiles && tn <= kMaxGridTiles && tm * tn + 8 <= kMaxGridTiles;
 }
 
+// The dense ones' scratch: none for most sizes.
+mxq_status gated_workspace(int64_t M, int64_t n, int64_t K, void* workspace, size_t bytes) {
+  const size_t need = mxq::gated_ws_bytes(M, n, K);
+  if (need == 0) return MXQ_OK;
+  if (!workspace || bytes < need) return MXQ_ERR_WORKSPACE;
+  return al16(workspace) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+
 // What the gated GEMMs ask of their operands; `n` rows of B (of a group).
 mxq_status gated_check(mxq_format fmt, int64_t rows, int64_t inter, int64_t n, int64_t K, const void* A, const void* sA,
                        const void* B, const void* sB) {
@@ -857,7 +867,7 @@ mxq_status gated_check(mxq_format fmt, int64_t rows, int64_t inter, int64_t n, i
 
 mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
                        mxq_scope tA_scope, const void* B, const void* sB, const float* tB, mxq_scope tB_scope, void* h,
-                       void* gate_up, void* stream) {
+                       void* gate_up, void* workspace, size_t workspace_bytes, void* stream) {
   if (M < 0 || inter < 0 || K < 0) return MXQ_ERR_SHAPE;
   if (fmt != MXQ_MXFP8 && fmt != MXQ_NVFP4 && fmt != MXQ_BF16) return MXQ_ERR_FORMAT;
   if (M == 0 || inter == 0) return MXQ_OK;
@@ -874,12 +884,15 @@ mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, cons
   if (st != MXQ_OK) return st;
   if (!tiles_fit(M, 2 * inter, 0)) return MXQ_ERR_SHAPE;
   if (!al16(h) || !al16(gate_up)) return MXQ_ERR_ALIGN;
-  return hip_status(mxq::launch_gemm_swiglu((int)fmt, M, inter, K, A, sA, tA, ta, B, sB, tB, tb, h, gate_up, S(stream)));
+  const mxq_status ws = gated_workspace(M, 2 * inter, K, workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
+  return hip_status(mxq::launch_gemm_swiglu((int)fmt, M, inter, K, A, sA, tA, ta, B, sB, tB, tb, h, gate_up, workspace,
+                                            S(stream)));
 }
 
 mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
                                 const void* B, const void* sB, const void* gate_up, mxq_out_dtype gu_dtype,
-                                void* d_gate_up, void* h, void* stream) {
+                                void* d_gate_up, void* h, void* workspace, size_t workspace_bytes, void* stream) {
   if (M < 0 || inter < 0 || K < 0) return MXQ_ERR_SHAPE;
   if ((fmt != MXQ_MXFP8 && fmt != MXQ_BF16) || !is_dtype(gu_dtype)) return MXQ_ERR_FORMAT;
   if (M == 0 || inter == 0) return MXQ_OK;
@@ -888,8 +901,10 @@ mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_
   if (st != MXQ_OK) return st;
   if (!tiles_fit(M, inter, 0)) return MXQ_ERR_SHAPE;
   if (!al16(gate_up) || !al16(d_gate_up) || !al16(h)) return MXQ_ERR_ALIGN;
+  const mxq_status ws = gated_workspace(M, inter, K, workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
   return hip_status(mxq::launch_gemm_swiglu_backward((int)fmt, M, inter, K, A, sA, B, sB, gate_up,
-                                                     gu_dtype == MXQ_OUT_F32, d_gate_up, h, S(stream)));
+                                                     gu_dtype == MXQ_OUT_F32, d_gate_up, h, workspace, S(stream)));
 }
 
 mxq_status grouped_gemm_swiglu(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,

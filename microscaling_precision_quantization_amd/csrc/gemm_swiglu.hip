@@ -125,26 +125,158 @@ static void launch_gated_dense_ld(const ExactProblem& p, const GatedArgs& ga, hi
   else launch_gated_dense_t<LD, 0, EPI>(p, ga, st);
 }
 
+// ---------------------------------------------------------------------------
+// Few tiles: K split over them, the parts joined by a second kernel
+// ---------------------------------------------------------------------------
+// A tile walks K at some 0.45 us per 64, whatever else runs; with fewer tiles than half the CUs that walk is the
+// call's time (64 x 7168 -> 2 x 2048 BF16: 58 us against 12 for its bytes). Parts of 512 K and more each leave
+// their FP32 product in the workspace; the join adds them in order and ends as the epilogue does (25 us there).
+// The parts double as long as the walk saved is longer than writing and reading the products that come
+// with it, at 5 TB/s, and at first the second launch: 512 x 2048 -> 2 x 2048 MXFP8 stays whole (18 us against 22).
+constexpr int64_t kPartK = 512;                           // a part's K is a multiple: whole stages and scale chunks
+static int64_t gated_parts(int64_t M, int64_t n, int64_t K) {
+  const int64_t tiles = ((M + 127) / 128) * ((n + 127) / 128);
+  int64_t parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= 256 && K >= 2 * parts * kPartK) {
+    const int64_t saved_ns = K / (2 * parts) * 7, product_ns = M * n * 8 / 5000;
+    if (saved_ns <= (parts == 1 ? 2 * product_ns + 2500 : parts * product_ns)) break;
+    parts *= 2;
+  }
+  return parts;
+}
+size_t gated_ws_bytes(int64_t M, int64_t n, int64_t K) {
+  const int64_t parts = gated_parts(M, n, K);
+  return parts == 1 ? 0 : (size_t)((parts * M * n * 4 + 255) / 256 * 256);
+}
+
+template <int LD, int SM>
+__global__ void __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1)))
+gated_part_kernel(ExactProblem p, int64_t part_k, int64_t tiles_m, int64_t tiles_n) {
+  constexpr bool WIDE = SM == 2;
+  using C = gx::Cfg<LD, 128, 128, SM, 1, WIDE>;
+  MXQ_EXACT_LDS(C)
+  int64_t tm, tn;
+  if (!exact_map_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
+  // the part's operands begin at its first K (rows keep their stride)
+  const int64_t k0 = (int64_t)blockIdx.y * part_k;
+  constexpr int BS = LD == 2 ? 16 : 32;
+  p.A += k_bytes<LD>(k0);
+  p.B += k_bytes<LD>(k0);
+  if constexpr (LD != 0) {
+    p.sA += k0 / BS;
+    p.sB += k0 / BS;
+  }
+  p.k_end = min(part_k, p.lda - k0);
+  p.C += (int64_t)blockIdx.y * p.m_valid * p.ldc;
+  exact_gemm_tile<LD, 128, 128, SM, 1, WIDE>(p, tm * 128, tn * 128, lds0, lds1, lds2, lds3, ldsc);
+}
+
+// One thread: 8 h columns of a row.
+template <int EPI, bool GU32>
+__global__ void __launch_bounds__(256) gated_join_kernel(const float* __restrict__ parts, int n_parts, int64_t M, GatedArgs ga) {
+  const int64_t I = ga.inter, n = EPI == 1 ? 2 * I : I, per_row = I / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= M * per_row) return;
+  const int64_t row = at / per_row, col = at % per_row * 8;
+  auto row8 = [&](const float* q, float* v) {
+    const float4 x = reinterpret_cast<const float4*>(q)[0], y = reinterpret_cast<const float4*>(q)[1];
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  };
+  auto sum8 = [&](int64_t c, float* v) {
+    const float* q = parts + row * n + c;
+    row8(q, v);
+    for (int s = 1; s < n_parts; ++s) {
+      float w[8];
+      row8(q + s * M * n, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
+    }
+  };
+  auto put8 = [](uint16_t* to, const float* v) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                                               bf16x2_rne(v[6], v[7]));
+  };
+  float a[8], b[8], h[8];
+  sum8(col, a);
+  if constexpr (EPI == 1) {
+    sum8(I + col, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = swiglu_forward(a[e], b[e]);
+    put8(ga.h + row * I + col, h);
+    if (ga.gu) {
+      put8(ga.gu + row * 2 * I + col, a);
+      put8(ga.gu + row * 2 * I + I + col, b);
+    }
+  } else {
+    float g[8], u[8], dg[8], du[8];
+    if constexpr (GU32) {
+      row8((const float*)ga.gu_in + row * 2 * I + col, g);
+      row8((const float*)ga.gu_in + row * 2 * I + I + col, u);
+    } else {
+      unpack8(*reinterpret_cast<const uint4*>((const uint16_t*)ga.gu_in + row * 2 * I + col), g);
+      unpack8(*reinterpret_cast<const uint4*>((const uint16_t*)ga.gu_in + row * 2 * I + I + col), u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) swiglu_backward(a[e], g[e], u[e], dg[e], du[e], h[e]);
+    put8(ga.gu + row * 2 * I + col, dg);
+    put8(ga.gu + row * 2 * I + I + col, du);
+    if (ga.h) put8(ga.h + row * I + col, h);
+  }
+}
+
+template <int LD, int EPI>
+static void launch_gated_parts(ExactProblem p, const GatedArgs& ga, int64_t parts, void* ws, hipStream_t st) {
+  const int64_t M = p.m_valid, n = EPI == 1 ? 2 * ga.inter : ga.inter, K = p.lda;
+  const int64_t part_k = (K + parts * kPartK - 1) / (parts * kPartK) * kPartK, used = (K + part_k - 1) / part_k;
+  p.n_valid = n;
+  p.C = (float*)ws;
+  p.ldc = n;
+  const int64_t tm = (M + 127) / 128, tn = (n + 127) / 128;
+  const dim3 grid((unsigned)((tm * tn + 7) / 8 * 8), (unsigned)used);
+  auto go = [&](auto SMC) {
+    hipLaunchKernelGGL((gated_part_kernel<LD, decltype(SMC)::value>), grid, dim3(256), 0, st, p, part_k, tm, tn);
+  };
+  const int sm = gated_scale_mode(LD, K);
+  if constexpr (LD != 0) {
+    if (sm == 2) go(ic<2>{});
+  }
+  if (LD == 0 || sm != 2) {
+    if (sm >= 1) go(ic<1>{});
+    else go(ic<0>{});
+  }
+  const dim3 join((unsigned)((M * (ga.inter / 8) + 255) / 256));
+  if (EPI == 2 && ga.gu32)
+    hipLaunchKernelGGL((gated_join_kernel<EPI, true>), join, dim3(256), 0, st, (const float*)ws, (int)used, M, ga);
+  else hipLaunchKernelGGL((gated_join_kernel<EPI, false>), join, dim3(256), 0, st, (const float*)ws, (int)used, M, ga);
+}
+
+template <int LD, int EPI>
+static void launch_gated_any(const ExactProblem& p, const GatedArgs& ga, void* ws, hipStream_t st) {
+  const int64_t parts = gated_parts(p.m_valid, EPI == 1 ? 2 * ga.inter : ga.inter, p.lda);
+  if (parts > 1) launch_gated_parts<LD, EPI>(p, ga, parts, ws, st);
+  else launch_gated_dense_ld<LD, EPI>(p, ga, st);
+}
+
 // fmt: 1 MXFP8, 2 NVFP4, 3 BF16
 hipError_t launch_gemm_swiglu(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA, const float* tA,
                               int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode, void* h,
-                              void* gate_up, hipStream_t st) {
+                              void* gate_up, void* ws, hipStream_t st) {
   const ExactProblem p = gated_problem(M, inter, K, A, sA, tA, tA_mode, B, sB, tB, tB_mode);
   const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)gate_up, nullptr, 0};
-  if (fmt == 1) launch_gated_dense_ld<1, 1>(p, ga, st);
-  else if (fmt == 2) launch_gated_dense_ld<2, 1>(p, ga, st);
-  else launch_gated_dense_ld<0, 1>(p, ga, st);
+  if (fmt == 1) launch_gated_any<1, 1>(p, ga, ws, st);
+  else if (fmt == 2) launch_gated_any<2, 1>(p, ga, ws, st);
+  else launch_gated_any<0, 1>(p, ga, ws, st);
   return hipGetLastError();
 }
 
 // fmt: 1 MXFP8, 3 BF16
 hipError_t launch_gemm_swiglu_backward(int fmt, int64_t M, int64_t inter, int64_t K, const void* A, const void* sA,
                                        const void* B, const void* sB, const void* gate_up, int gu32, void* d_gate_up,
-                                       void* h, hipStream_t st) {
+                                       void* h, void* ws, hipStream_t st) {
   const ExactProblem p = gated_problem(M, inter, K, A, sA, nullptr, 0, B, sB, nullptr, 0);
   const GatedArgs ga{inter, (uint16_t*)h, (uint16_t*)d_gate_up, gate_up, gu32};
-  if (fmt == 1) launch_gated_dense_ld<1, 2>(p, ga, st);
-  else launch_gated_dense_ld<0, 2>(p, ga, st);
+  if (fmt == 1) launch_gated_any<1, 2>(p, ga, ws, st);
+  else launch_gated_any<0, 2>(p, ga, ws, st);
   return hipGetLastError();
 }
 

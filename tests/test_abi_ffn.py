@@ -14,8 +14,15 @@ BIG = 1 << 31
 
 
 def test_gemm_swiglu_validation():
-    def f(fmt=B.BF16, M=4, I=16, K=64, A=P, sA=P, tA=P, ta=ROW, W=P, sB=P, tB=P, tb=TENSOR, h=P, gu=P):
-        return B.lib().gemm_swiglu(fmt, M, I, K, A, sA, tA, ta, W, sB, tB, tb, h, gu, None)
+    def f(fmt=B.BF16, M=4, I=16, K=64, A=P, sA=P, tA=P, ta=ROW, W=P, sB=P, tB=P, tb=TENSOR, h=P, gu=P, ws=P,
+          wsn=1 << 30):
+        return B.lib().gemm_swiglu(fmt, M, I, K, A, sA, tA, ta, W, sB, tB, tb, h, gu, ws, wsn, None)
+
+    need = B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, 4, 32, 4096)
+    assert need == 8 * 4 * 32 * 4 and B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, 4, 32, 512) == 0
+    assert B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, 0, 32, 4096) == 0
+    assert B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, 16384, 4096, 7168) == 0
+    assert f(K=4096, ws=None) == 5 and f(K=4096, wsn=need - 1) == 5 and f(K=4096, ws=MIS) == 3
 
     assert f(M=-1) == 2 and f(I=-8) == 2 and f(K=-8) == 2
     for fmt in (0, B.MXFP4, B.BF16_NVFP4T, 9):
@@ -35,8 +42,11 @@ def test_gemm_swiglu_validation():
 
 
 def test_gemm_swiglu_backward_validation():
-    def f(fmt=B.BF16, M=4, I=16, K=64, A=P, sA=P, W=P, sB=P, gu=P, gd=BF, d=P, h=P):
-        return B.lib().gemm_swiglu_backward(fmt, M, I, K, A, sA, W, sB, gu, gd, d, h, None)
+    def f(fmt=B.BF16, M=4, I=16, K=64, A=P, sA=P, W=P, sB=P, gu=P, gd=BF, d=P, h=P, ws=P, wsn=1 << 30):
+        return B.lib().gemm_swiglu_backward(fmt, M, I, K, A, sA, W, sB, gu, gd, d, h, ws, wsn, None)
+
+    need = B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, 4, 16, 4096)
+    assert f(K=4096, ws=None) == 5 and f(K=4096, wsn=need - 1) == 5 and f(K=4096, ws=MIS) == 3
 
     assert f(M=-1) == 2 and f(I=-8) == 2 and f(K=-8) == 2
     for fmt in (B.NVFP4, B.MXFP4, B.BF16_NVFP4T, 0):

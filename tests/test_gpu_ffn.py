@@ -54,6 +54,10 @@ DENSE = [("bf16", 1, 8, 8), ("bf16", 5, 16, 40), ("bf16", 127, 72, 64), ("bf16",
          ("nvfp4", 1, 8, 32), ("nvfp4", 129, 72, 96), ("nvfp4", 200, 264, 64), ("nvfp4", 130, 136, 256),
          ("nvfp4", 64, 128, 1280)]
 # enough 256 x 256 tiles for the large tile: 11 x 19 and more
+# few tiles and a long K: split, in even and uneven parts, the last one short
+LONG = [("bf16", 3, 24, 1032), ("bf16", 130, 72, 7168), ("bf16", 1, 8, 5128), ("mxfp8", 5, 40, 1056), ("mxfp8", 140, 136, 2048),
+        ("mxfp8", 64, 256, 7168), ("mxfp8", 9, 8, 1664), ("nvfp4", 5, 40, 1056), ("nvfp4", 140, 136, 2048),
+        ("nvfp4", 64, 256, 7168), ("nvfp4", 9, 8, 1664)]
 # more 128 x 128 tiles than CUs, fewer 256 x 256 than 192
 MANY = [(f, 1300, 1672, k) for f, k in (("bf16", 72), ("bf16", 64), ("mxfp8", 96), ("mxfp8", 128), ("mxfp8", 512), ("nvfp4", 96),
                                         ("nvfp4", 128), ("nvfp4", 256))]
@@ -61,7 +65,7 @@ LARGE = [("bf16", 2601, 2408, 72), ("bf16", 2601, 2408, 128), ("mxfp8", 2601, 24
          ("mxfp8", 2601, 2408, 512), ("nvfp4", 2601, 2408, 96), ("nvfp4", 2601, 2408, 128), ("nvfp4", 2601, 2408, 256)]
 
 
-@pytest.mark.parametrize("fmt,M,I,K", DENSE + MANY + LARGE)
+@pytest.mark.parametrize("fmt,M,I,K", DENSE + LONG + MANY + LARGE)
 def test_gemm_swiglu(fmt, M, I, K):
     g = gen(M * 7 + I + K)
     x, w = randn(g, M, K).to(BF), randn(g, 2 * I, K, scale=2.0 / K ** 0.5).to(BF)
@@ -116,7 +120,7 @@ def test_gates_far_out_give_zeros_and_no_nan():
     R.check(h2, hh, htol, "h")
 
 
-BACK = [c for c in DENSE + LARGE if c[0] != "nvfp4"] + [("bf16", 2600, 1672, 72), ("mxfp8", 2600, 1672, 96), ("mxfp8", 2600, 1672, 512),
+BACK = [c for c in DENSE + LONG + LARGE if c[0] != "nvfp4"] + [("bf16", 2600, 1672, 72), ("mxfp8", 2600, 1672, 96), ("mxfp8", 2600, 1672, 512),
                                                         ("bf16", 3200, 4104, 72), ("bf16", 3200, 4104, 64),
                                                         ("mxfp8", 3200, 4104, 512)]
 
