@@ -162,15 +162,18 @@ class MoeNvfp4:
 
     X is quantized per token once, before the gather (a token's bits do not depend on
     the batch); the SwiGLU output is requantized per slot row; the expert weights carry
-    one FP32 scale per expert matrix (gate and up share one)."""
+    one FP32 scale per expert matrix (gate and up share one). fused=True puts SwiGLU into the
+    gate_up GEMM: GU is kept in BF16 (half the memory) and h is rounded from the FP32 sums, a
+    last-bit difference to the correctly rounded SwiGLU of the stored GU."""
 
     def __init__(self, tokens: int, hidden: int, experts: int, inter: int, routing: MoeRoutingDevice, dev,
-                 keep_h: bool = False):
+                 keep_h: bool = False, fused: bool = False):
         T, H, G, I, S = tokens, hidden, experts, inter, routing.slots
         self.T, self.H, self.G, self.I, self.S, self.dev, self.r = T, H, G, I, S, dev, routing
+        self.fused = fused
         self.qx, self.sx, self.tx = _u8((T, H // 2), dev), _u8((T, H // 16), dev), _f32((T,), dev)
-        self.gu = _f32((S, 2 * I), dev)
-        self.h = _bf16((S, I), dev) if keep_h else None
+        self.gu = (_bf16 if fused else _f32)((S, 2 * I), dev)
+        self.h = _bf16((S, I), dev) if keep_h or fused else None
         self.qh, self.sh, self.th = _u8((S, I // 2), dev), _u8((S, I // 16), dev), _f32((S,), dev)
         self.o = _f32((S, H), dev)
         self.y = _f32((T, H), dev)
@@ -212,12 +215,21 @@ class MoeNvfp4:
 
     def gate_up(self):                                             # A9 + A10 (gather inside the GEMM)
         qw, sw, tw = self.wq["gu"]
+        if self.fused:                                             # ... + A11's SwiGLU
+            B.grouped_gemm_swiglu(B.NVFP4, self.r.offsets, self.qx, qw, inter=self.I, K=self.H, sA=self.sx, sB=sw,
+                                  tA=self.tx, tB=tw, a_row_index=self.r.row_index, total=self.S, out=(self.h, self.gu),
+                                  workspace=self.ws)
+            return
         B.grouped_gemm_block_scaled(B.NVFP4, self.r.offsets, self.qx, qw, N=2 * self.I, K=self.H, sA=self.sx,
                                     sB=sw, tA=self.tx, tB=tw, tA_scope="row", tB_scope="group",
                                     a_row_index=self.r.row_index, total=self.S, a_rows=self.T, out=self.gu,
                                     workspace=self.ws)
 
     def swiglu(self):                                              # A11
+        if self.fused:
+            B._call("quantize_nvfp4_per_token", self.h.device, B._ptr(self.h), self.S, self.I, self.I, B._ptr(self.qh),
+                    B._ptr(self.sh), B._ptr(self.th))
+            return
         B._call("moe_swiglu_quantize_nvfp4", self.gu.device, B._ptr(self.gu), self.S, self.I, B._ptr(self.h),
                 B._ptr(self.qh), B._ptr(self.sh), B._ptr(self.th))
 
@@ -244,10 +256,28 @@ class MoeNvfp4:
         return {"gate_up": 2 * live * 2 * self.I * self.H, "down": 2 * live * self.H * self.I}
 
 
+class MoeDecodeNvfp4:
+    """A decoding step of the routed experts: at most 64 tokens, BF16 as they are (not quantized),
+    against the same NVFP4 expert weights (`wq`, as MoeNvfp4.quantize_weights gives them), each chosen
+    expert's weight read once:
+        h[t, j] = silu(x[t] Wg_e^T) (x[t] Wu_e^T),  e = topk_idx[t, j];   y[t] = sum_j w[t, j] h[t, j] W_d,e^T."""
+
+    def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, wq):
+        self.G, self.wq = experts, wq
+        self.h, self.y = _bf16((tokens, topk, inter), dev), _f32((tokens, hidden), dev)
+        self.ws = _u8((B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, tokens, hidden, 0),), dev)
+
+    def forward(self, x, topk_idx, weights):
+        B.moe_decode_gate_up(B.NVFP4, x, topk_idx, *self.wq["gu"], experts=self.G, out=self.h)
+        return B.moe_decode_down(B.NVFP4, self.h, topk_idx, weights, *self.wq["d"], experts=self.G, out=self.y,
+                                 workspace=self.ws)
+
+
 class MoeDequantBackward:
     """Dequantized backward of the routed experts (BF16 GEMMs on BF16 dequantizations
     of the exact forward operands), given upstream gradients dO (S, H) of the down
-    outputs and dGU (S, 2I) of the gate_up outputs (padding slots zero):
+    outputs and dGU (S, 2I) of the gate_up outputs (padding slots zero); through_swiglu=True
+    makes dGU itself, from dO and the forward's GU, in the down dgrad's own kernel:
         down:    dh = dO W_d,g          dW_d,g = dO_g^T h_hat_g
         gate_up: dX = dGU W_gu,g        dW_gu,g = dGU_g^T X_hat_g
     dgrad GEMMs vary M per expert; wgrad GEMMs vary K (the slots). The dgrads read the
@@ -258,7 +288,7 @@ class MoeDequantBackward:
     activations, are dequantized into K-contiguous BF16 transposes by dequantize_transposed.
     Every expert's slots begin at a multiple of 8 (16 bytes of BF16 along K)."""
 
-    def __init__(self, fwd: MoeNvfp4, fused_weights: bool = True):
+    def __init__(self, fwd: MoeNvfp4, fused_weights: bool = True, through_swiglu: bool = False):
         f = fwd
         # the weight-gradient GEMMs see the offsets on the device only, and leave dW as it was where
         # one is not a multiple of 8
@@ -272,7 +302,10 @@ class MoeDequantBackward:
             self.w_guT = _bf16((G, H, 2 * I), dev) # W_hat_gu,g^T
         self.hT = _bf16((1, I, S), dev)            # h_hat^T (slots along K)
         self.xT = _bf16((1, H, S), dev)            # X_hat gathered into slots, transposed
-        self.dh = _f32((S, I), dev)
+        if through_swiglu:
+            self.d_gu = _bf16((S, 2 * I), dev)
+        else:
+            self.d_gu, self.dh = None, _f32((S, I), dev)
         self.dx = _f32((S, H), dev)
         self.dw_d = _f32((G, H, I), dev)
         self.dw_gu = _f32((G, 2 * I, H), dev)
@@ -299,7 +332,9 @@ class MoeDequantBackward:
     def gemms(self, d_o, d_gu):                                    # A13
         f = self.f
         off = f.r.offsets
-        if self.fused:
+        if d_gu is self.d_gu:
+            pass                                                   # dh went into dGU
+        elif self.fused:
             qw, sw, tw = f.wq["d"]
             B.grouped_gemm_block_scaled(B.BF16_NVFP4T, off, d_o, qw, N=f.I, K=f.H, sB=sw, tB=tw, tB_scope="group",
                                         total=f.S, out=self.dh, workspace=f.ws)
@@ -318,7 +353,26 @@ class MoeDequantBackward:
         B.grouped_gemm_block_scaled(B.BF16, off, d_gu, self.xT[0], N=f.H, K=0, vary_k=2, M=2 * f.I,
                                     total=f.S, out=self.dw_gu, workspace=f.ws)
 
-    def backward(self, d_o, d_gu):
+    def swiglu_grad(self, d_o):
+        """dGU from dO: the down dgrad with the gradient of SwiGLU behind it."""
+        if self.d_gu is None:
+            raise ValueError("d_gu: not given, and the backward was not made with through_swiglu=True")
+        f = self.f
+        if self.fused:
+            qw, sw, tw = f.wq["d"]
+            B.grouped_gemm_swiglu_backward(B.BF16_NVFP4T, f.r.offsets, d_o, qw, inter=f.I, K=f.H, gate_up=f.gu, sB=sw,
+                                           tB=tw, total=f.S, out=(self.d_gu, None), workspace=f.ws)
+        else:
+            B.grouped_gemm_swiglu_backward(B.BF16, f.r.offsets, d_o, self.w_dT, inter=f.I, K=f.H, gate_up=f.gu,
+                                           total=f.S, out=(self.d_gu, None), workspace=f.ws)
+        return self.d_gu
+
+    def backward(self, d_o, d_gu=None):
+        """d_gu None: through SwiGLU (through_swiglu=True)."""
+        if d_gu is None:
+            d_gu = self.swiglu_grad(d_o)
+        elif self.d_gu is not None:
+            raise ValueError("d_gu: the backward was made with through_swiglu=True")
         self.dequantize_activations(d_o, d_gu)
         self.gemms(d_o, d_gu)
 
@@ -338,22 +392,24 @@ class MoeBlockNvfp4:
     The plan's slots are a fixed number (every expert's range padded to `pad`, the rest dealt
     out), so nothing waits for the counts and a step can be captured in a HIP graph. backward=True
     needs pad and tokens to be multiples of 8 and experts of 16 (they are reduction axes of its
-    weight gradients and of the router's GEMMs)."""
+    weight gradients and of the router's GEMMs). fused: SwiGLU in the gate_up GEMM (MoeNvfp4);
+    through_swiglu: the backward makes the gate_up outputs' gradient itself (MoeDequantBackward)."""
 
     def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, pad: int = 1,
                  balance_coef: float | None = None, gate_mode: str = "none", branch_scale: float = 1.0,
-                 res_scale: float = 1.0, eps: float = 1e-6, backward: bool = False):
+                 res_scale: float = 1.0, eps: float = 1e-6, backward: bool = False, fused: bool = False,
+                 through_swiglu: bool = False):
         T, H, G = tokens, hidden, experts
         if backward and (pad % 8 or T % 8 or G % 16):
             raise ValueError(f"backward: pad {pad}, {T} tokens, {G} experts; expected multiples of 8, 8 and 16")
         self.topk, self.pad, self.coef, self.eps = topk, pad, balance_coef, eps
         self.gate_mode, self.branch_scale, self.res_scale = gate_mode, branch_scale, res_scale
         self.plan = B.RoutePlan(T, G, topk, pad, loss=balance_coef is not None, dev=dev)
-        self.moe = MoeNvfp4(T, H, G, inter, self.plan, dev, keep_h=False)
+        self.moe = MoeNvfp4(T, H, G, inter, self.plan, dev, keep_h=False, fused=fused)
         self.n, self.logits, self.out = _bf16((T, H), dev), _f32((T, G), dev), _bf16((T, H), dev)
         self.rstd_pre, self.rstd_post = _f32((T,), dev), _f32((T,), dev)
         if backward:
-            self.bwd = MoeDequantBackward(self.moe)
+            self.bwd = MoeDequantBackward(self.moe, through_swiglu=through_swiglu)
             self.d_y, self.d_o, self.d_w = _f32((T, H), dev), _bf16((self.plan.slots, H), dev), _f32((T, topk), dev)
             self.dw_post = _f32((H,), dev)
             shape = {"none": None, "token": (T,), "channel": (H,), "full": (T, H)}[gate_mode]
@@ -405,7 +461,7 @@ class MoeBlockNvfp4:
 
     def backward(self, x, d_out, d_gu, w_pre, w_router, w_post, gate=None, d_loss=None):
         """All of it, given the upstream gradient dGU (slots, 2I) of the gate_up outputs, as
-        MoeDequantBackward is."""
+        MoeDequantBackward is, or None with through_swiglu."""
         self.backward_out(d_out, w_post, gate)
         self.bwd.backward(self.d_o, d_gu)
         self.backward_in(x, d_out, w_pre, w_router, d_loss)
@@ -464,6 +520,73 @@ class SharedExpertBf16:
     def gemm_flops(self) -> dict:
         T, H, I = self.T, self.H, self.I
         return {"fwd": 2 * T * H * 2 * I + 2 * T * I * H, "bwd": 2 * (2 * T * H * I + 2 * T * H * 2 * I)}
+
+
+class MoeBlockDecodeNvfp4:
+    """MoeBlockNvfp4's forward for a decoding step of at most 64 tokens: the same norm, router and
+    residual around MoeDecodeNvfp4. `wq`: the NVFP4 expert weights (MoeNvfp4.quantize_weights)."""
+
+    def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, wq, gate_mode: str = "none",
+                 branch_scale: float = 1.0, res_scale: float = 1.0, eps: float = 1e-6):
+        T, H, G = tokens, hidden, experts
+        self.topk, self.eps = topk, eps
+        self.gate_mode, self.branch_scale, self.res_scale = gate_mode, branch_scale, res_scale
+        self.plan = B.RoutePlan(T, G, topk, 1, dev=dev)
+        self.moe = MoeDecodeNvfp4(T, H, G, inter, topk, dev, wq)
+        self.n, self.logits, self.out = _bf16((T, H), dev), _f32((T, G), dev), _bf16((T, H), dev)
+        self.rstd_post = _f32((T,), dev)
+
+    def forward(self, x, w_pre, w_router, w_post, gate=None, valid=None):
+        B.rmsnorm_quantize(x, w_pre, self.eps, B.BF16, out=(self.n, None, None, None, None))
+        B.gemm_block_scaled(B.BF16, self.n, None, w_router, None, out=self.logits)
+        B.moe_route(self.logits, self.topk, 1, valid=valid, out=self.plan)
+        self.moe.forward(self.n, self.plan.topk_idx, self.plan.weights)
+        B.rmsnorm_gate_residual(x, self.moe.y, w_post, gate, self.gate_mode, self.eps, self.branch_scale, self.res_scale,
+                                out=(self.out, self.rstd_post))
+        return self.out
+
+
+class GatedFfnBf16:
+    """A gated feed-forward block in BF16 from its input to its gradients (the shared expert, SwiGLU
+    included): forward GU = X W_gu^T, h = silu(gate) up in one kernel, O = h W_d^T; backward dGU and
+    h from dO in one kernel, then dX = dGU W_gu, dW_gu = dGU^T X, dW_d = dO^T h. GU is kept in BF16.
+    tokens and inter multiples of 8 (16 bytes of BF16 along the reductions), hidden and inter of 16."""
+
+    def __init__(self, tokens: int, hidden: int, inter: int, dev):
+        T, H, I = tokens, hidden, inter
+        if T % 8 or H % 16 or I % 16:
+            raise ValueError(f"{T} tokens, hidden {H}, inter {I}: expected multiples of 8, 16 and 16")
+        self.T, self.H, self.I = T, H, I
+        self.h, self.gu, self.o = _bf16((T, I), dev), _bf16((T, 2 * I), dev), _f32((T, H), dev)
+        self.d_gu = _bf16((T, 2 * I), dev)
+        self.w_dT, self.w_guT = _bf16((1, I, H), dev), _bf16((1, H, 2 * I), dev)
+        self.hT, self.xT = _bf16((1, I, T), dev), _bf16((1, H, T), dev)
+        self.d_oT, self.d_guT = _bf16((1, H, T), dev), _bf16((1, 2 * I, T), dev)
+        self.dx, self.dw_d, self.dw_gu = _f32((T, H), dev), _f32((H, I), dev), _f32((2 * I, H), dev)
+        need = lambda n, k: B.lib().mxq_workspace_bytes(B.OP_GEMM_SWIGLU, T, n, k)
+        self.ws = _u8((max(need(2 * I, H), need(I, H)),), dev)
+
+    def forward(self, x, w_gu, w_d):
+        """x (T, H), w_gu (2I, H), w_d (H, I), BF16; O (T, H) FP32."""
+        B.gemm_swiglu(B.BF16, x, None, w_gu, None, out=(self.h, self.gu), workspace=self.ws)
+        return B.gemm_block_scaled(B.BF16, self.h, None, w_d, None, out=self.o)
+
+    def backward(self, x, w_gu, w_d, d_o):
+        """d_o (T, H) BF16, the gradient of O: dx, dw_gu, dw_d (FP32)."""
+        T, H, I = self.T, self.H, self.I
+        tr = lambda t, rows, cols, out: B.dequantize_transposed(B.BF16, t, groups=1, group_rows=rows, cols=cols, out=out)
+        tr(w_d, H, I, self.w_dT)
+        B.gemm_swiglu_backward(B.BF16, d_o, None, self.w_dT[0], None, self.gu, out=(self.d_gu, self.h), workspace=self.ws)
+        tr(w_gu, 2 * I, H, self.w_guT)
+        tr(self.h, T, I, self.hT)
+        tr(x, T, H, self.xT)
+        tr(d_o, T, H, self.d_oT)
+        tr(self.d_gu, T, 2 * I, self.d_guT)
+        B.gemm_block_scaled_batch(B.BF16, [
+            dict(A=self.d_oT[0], sA=None, B=self.hT[0], sB=None, out=self.dw_d),
+            dict(A=self.d_gu, sA=None, B=self.w_guT[0], sB=None, out=self.dx),
+            dict(A=self.d_guT[0], sA=None, B=self.xT[0], sB=None, out=self.dw_gu)])
+        return self.dx, self.dw_gu, self.dw_d
 
 
 # ---------------------------------------------------------------------------
