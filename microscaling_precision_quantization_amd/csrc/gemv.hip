@@ -97,39 +97,55 @@ template <int FMT> constexpr int kCodes = FMT == 2 ? 2 : 1;         // codes of 
 // ---------------------------------------------------------------------------
 // More than four x rows: a column tile of 16 is 16 x rows
 // ---------------------------------------------------------------------------
-// acc[t] += the products of one row tile and TT column tiles over chunks [c0, c1). wo, so: the lane's row at its
-// 32 K of chunk 0; xo[t]: its x row there.
-template <int FMT, int TT>
-__device__ __forceinline__ void dot16(Rsrc rw, Rsrc rs, Rsrc rx, uint32_t wo, uint32_t so, const uint32_t (&xo)[TT], int K,
-                                      int c0, int c1, v4f (&acc)[TT]) {
-  constexpr int U = 4;                                    // chunks whose weights' loads go out together
+// acc[r][t] += the products of RT row tiles and TT column tiles over chunks [c0, c1). rw, rs: the tiles' weights
+// and scales; wo, so: the lane's row at its 32 K of chunk 0; xo[t]: its x row there.
+template <int FMT, int RT, int TT, bool AHEAD>
+__device__ __forceinline__ void dot16(const Rsrc (&rw)[RT], const Rsrc (&rs)[RT], Rsrc rx, uint32_t wo, uint32_t so,
+                                      const uint32_t (&xo)[TT], int K, int c0, int c1, v4f (&acc)[RT][TT]) {
+  constexpr int U = RT * TT >= 4 ? 1 : RT * TT == 2 ? 2 : 4;   // chunks whose weights' loads go out together
   const int k0 = 32 * ((threadIdx.x & 63) >> 4);
   for (int c = c0; c < c1; c += U) {
-    uint4 w[U];
-    uint32_t s[U];
+    uint4 w[U][RT];
+    uint32_t s[U][RT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = c + u < c1 && (c + u) * kChunk + k0 < K;
-      w[u] = load16(rw, in ? wo : kOff, (uint32_t)(c + u) * (kChunk / 2));
-      s[u] = load_codes<FMT>(rs, in ? so : kOff, (uint32_t)(c + u) * (kChunk / kScaleK<FMT>));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        w[u][r] = load16(rw[r], in ? wo : kOff, (uint32_t)(c + u) * (kChunk / 2));
+        s[u][r] = load_codes<FMT>(rs[r], in ? so : kOff, (uint32_t)(c + u) * (kChunk / kScaleK<FMT>));
+      }
+    }
+    uint4 x[AHEAD ? U : 1][TT][4];
+    auto load_x = [&](int u) {
+      const bool in = c + u < c1 && (c + u) * kChunk + k0 < K;
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[AHEAD ? u : 0][t][i] = load16(rx, (in ? xo[t] : kOff) + 16 * i, (uint32_t)(c + u) * (2 * kChunk));
+    };
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_x(u);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (c + u >= c1) break;
-      const bool in = (c + u) * kChunk + k0 < K;
-      uint4 x[TT][4];
+      if constexpr (!AHEAD) load_x(u);
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t d[4] = {w[u][r].x, w[u][r].y, w[u][r].z, w[u][r].w};
+        float S[2];
+        scales_of<FMT>(s[u][r], S);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[t][i] = load16(rx, (in ? xo[t] : kOff) + 16 * i, (uint32_t)(c + u) * (2 * kChunk));
-      const uint32_t d[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      float S[2];
-      scales_of<FMT>(s[u], S);
+        for (int i = 0; i < 4; ++i) {
+          const v8bf a = weights8<FMT>(d[i], S[i / 2]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v8bf a = weights8<FMT>(d[i], S[i / 2]);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(x[t][i]), acc[t], 0, 0, 0);
+          for (int t = 0; t < TT; ++t)
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(x[AHEAD ? u : 0][t][i]), acc[r][t], 0, 0, 0);
+        }
       }
     }
   }
@@ -333,19 +349,32 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int f32) {
   else ((uint16_t*)y)[at] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// K split over the workgroup's WV waves; TT column tiles hold all x rows. (Gated: 2 n K / 2 < 2^31 bytes of weights.)
-template <int FMT, bool GATED, int TT, int WV>
+// TT column tiles hold all x rows. A workgroup has WV waves: KS of them share a tile's K, the others have tiles of
+// their own, RT each, and the same x at about the same time. The host has checked that the weights a descriptor
+// spans (gated: all 2 n rows from the tile on) stay below 2^31 bytes.
+// A tile needs all of x, 2 rows bytes for every 8 of its weights' bytes: past 16 rows the reads of x out of the L2
+// are what takes the time (2048 x 7168 gated, 16 rows 12.8 us, 32 20.4, 64 33.8; the weights alone 3.1), below it
+// the latency of three loads in turn. AH: x ahead of the products along with the weights (32 rows 23.0 -> 20.4);
+// short shares with one column tile lose by it (7168 x 2048 7.9 -> 9.0).
+template <int FMT, bool GATED, int TT, int RT, int KS, int WV>
 __global__ void __launch_bounds__(64 * WV)
 gemv_kernel(GemvArgs a) {
   using namespace gv;
-  constexpr int NO = kTileOut<GATED>;
-  __shared__ float part[WV][TT][4][64];
+  constexpr int NO = kTileOut<GATED>, NW = WV / KS;
+  constexpr bool AH = KS == 16 || TT >= 2;
+  __shared__ float part[WV][RT][TT][4][64];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * NO;
+  const int64_t b0 = (int64_t)blockIdx.x * (NW * RT * NO);
   const int64_t wb = a.K / 2, sb = a.K / kScaleK<FMT>;
-  const int64_t rows = (GATED ? 2 * a.n : min(a.n, n0 + kTile)) - n0;   // gate rows past n read ups, not stored
-  const Rsrc rw = rsrc(a.w + n0 * wb, rows * wb), rs = rsrc(a.s + n0 * sb, rows * sb);
+  Rsrc rw[RT], rs[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {                          // a tile past the end has no rows
+    const int64_t n0 = b0 + (wave / KS * RT + r) * NO;
+    const int64_t rows = n0 >= a.n ? 0 : (GATED ? 2 * a.n : min(a.n, n0 + kTile)) - n0;   // gates past n read ups, not stored
+    rw[r] = rsrc(a.w + n0 * wb, rows * wb);
+    rs[r] = rsrc(a.s + n0 * sb, rows * sb);
+  }
   const int m = lane % kTile;
   const int64_t row = GATED && m >= 8 ? a.n + m - 8 : m;
   const uint32_t wo = (uint32_t)(row * wb) + 16 * g, so = (uint32_t)(row * sb) + kCodes<FMT> * g;
@@ -357,31 +386,37 @@ gemv_kernel(GemvArgs a) {
     xo[t] = r < a.rows ? (uint32_t)(r * a.ld_x + 32 * g) * 2 : kOff;
   }
   int c0, c1;
-  share((a.K + kChunk - 1) / kChunk, wave, WV, c0, c1);
-  v4f acc[TT];
+  share((a.K + kChunk - 1) / kChunk, wave % KS, KS, c0, c1);
+  v4f acc[RT][TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  dot16<FMT, TT>(rw, rs, rx, wo, so, xo, a.K, c0, c1, acc);
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+    for (int t = 0; t < TT; ++t) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  dot16<FMT, RT, TT, AH>(rw, rs, rx, wo, so, xo, a.K, c0, c1, acc);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[wave][t][r][lane] = acc[t][r];
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][r][t][i][lane] = acc[r][t][i];
   __syncthreads();
   // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
-  for (int o = tid; o < TT * 16 * NO; o += 64 * WV) {
-    const int t = o / (16 * NO), n = o % NO, c = o / NO % 16, at = t * kTile + c;
-    if (at >= a.rows || n0 + n >= a.n) continue;
+  constexpr int PER = NW * RT * NO;                       // columns of the result
+  for (int o = tid; o < TT * 16 * PER; o += 64 * WV) {
+    const int n = o % PER, at = o / PER, tile = n / NO;
+    if (at >= a.rows || b0 + n >= a.n) continue;
     float y[2];
 #pragma unroll
     for (int k = 0; k < (GATED ? 2 : 1); ++k) {
-      const int i = n + 8 * k, l = 16 * (i >> 2) + c;
-      float v = part[0][t][i & 3][l];
+      const int i = n % NO + 8 * k, l = 16 * (i >> 2) + at % 16;
+      const float* q = &part[tile / RT * KS][tile % RT][at / 16][i & 3][l];
+      float v = q[0];
 #pragma unroll
-      for (int w = 1; w < WV; ++w) v += part[w][t][i & 3][l];
-      if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? k * a.n + n0 + n : 0];
+      for (int w = 1; w < KS; ++w) v += q[w * (RT * TT * 256)];
+      if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? k * a.n + b0 + n : 0];
       y[k] = v;
     }
-    store_y(a.y, at * a.ld_y + n0 + n, GATED ? swiglu_forward(y[0], y[1]) : y[0], !GATED && a.out32);
+    store_y(a.y, at * a.ld_y + b0 + n, GATED ? swiglu_forward(y[0], y[1]) : y[0], !GATED && a.out32);
   }
 }
 
@@ -654,8 +689,10 @@ static void by_format(int fmt, F&& go) {
   else go(ic<4>{});
 }
 
-// `each` workgroups in y. K is split over as few waves as give the CUs some 20 each (a wave's fixed work is
-// worth one to two chunks).
+// `each` workgroups in y. K is split over as few waves as make 16384, four times what the CUs hold at once: a wave's
+// fixed work (finding its choices, joining sums) is worth one to two chunks, but waves that end at different times
+// keep loads in flight. With 4096 / 8192 / 16384: 32 tokens, 8 of 128 experts, gate_up 51 / 51 / 46.5 us; one row
+// of x, 65536 x 4096 35.3 / 35.4 / 33.0, 129280 x 7168 115 / 112 / 108, 16384 x 4096 11.0 / 11.9 / 11.9.
 template <int FMT, bool GATED, int NB>
 static void launch_gemv4(const GemvArgs& a, int64_t tiles, int64_t each, int by_choice, hipStream_t st) {
   const int64_t chunks = (a.K + gv::kWide - 1) / gv::kWide, waves = tiles * each;
@@ -677,7 +714,6 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
   const GemvArgs a{(const uint16_t*)x, ld_x, (int)rows, 1, nullptr, 1, (const uint8_t*)w, (const uint8_t*)s, t, t_mode, n,
                    (int)K, y, ld_y, out32};
   const int64_t tile = gated ? kTileOut<true> : kTileOut<false>, tiles = (n + tile - 1) / tile;
-  const dim3 grid((unsigned)tiles);
   by_format(fmt, [&](auto F) {
     constexpr int FMT = decltype(F)::value;
     auto go = [&](auto G) {
@@ -686,14 +722,23 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
         launch_gemv4<FMT, GATED, kDense>(a, tiles, 1, 0, st);
         return;
       }
-      auto by_rows = [&](auto W) {
-        constexpr int WV = decltype(W)::value;
-        if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, WV>), grid, dim3(64 * WV), 0, st, a);
-        else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, WV>), grid, dim3(64 * WV), 0, st, a);
-        else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, WV>), grid, dim3(64 * WV), 0, st, a);
+      auto by_rows = [&](auto R, auto S, auto W) {
+        constexpr int RT = decltype(R)::value, KS = decltype(S)::value, WV = decltype(W)::value;
+        const int64_t per = WV / KS * RT;
+        const dim3 grid((unsigned)((tiles + per - 1) / per)), block(64 * WV);
+        if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, RT, KS, WV>), grid, block, 0, st, a);
+        else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, RT, KS, WV>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, RT, KS, WV>), grid, block, 0, st, a);
       };
-      if (K > 16 * gv::kChunk) by_rows(ic<16>{});
-      else by_rows(ic<8>{});
+      // Many tiles fill the CUs by themselves: a wave takes two over all of K and reads x once for both. Fewer share K
+      // until some 4096 to 8192 waves read at once. 7168 columns, 16 / 64 rows, us: 129280 rows of w two tiles a wave
+      // 245 / 527, one 307 / 916; 32768 x 4096 16 rows K in two 49, in four 52. 16384 x 4096 in two 25, whole 45;
+      // 8192 x 4096 in eight 15, in two 24, in sixteen 18. 2048 x 7168 gated in sixteen 12.8, in eight 13.6; short K
+      // is not cut further (7168 x 2048 in eight 7.9, in sixteen 12.9).
+      if (tiles >= 16 * 256) by_rows(ic<2>{}, ic<1>{}, ic<8>{});
+      else if (tiles >= 4 * 256) by_rows(ic<1>{}, ic<2>{}, ic<8>{});
+      else if (K <= 16 * gv::kChunk || tiles > 256) by_rows(ic<1>{}, ic<8>{}, ic<8>{});
+      else by_rows(ic<1>{}, ic<16>{}, ic<16>{});
     };
     if (gated) go(ic<1>{});
     else go(ic<0>{});
