@@ -354,14 +354,14 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int f32) {
 // spans (gated: all 2 n rows from the tile on) stay below 2^31 bytes.
 // A tile needs all of x, 2 rows bytes for every 8 of its weights' bytes: past 16 rows the reads of x out of the L2
 // are what takes the time (2048 x 7168 gated, 16 rows 12.8 us, 32 20.4, 64 33.8; the weights alone 3.1), below it
-// the latency of three loads in turn. AH: x ahead of the products along with the weights (32 rows 23.0 -> 20.4);
+// the latency of three loads in turn. AH: x ahead of the products along with the weights (32 rows 23.0 -> 20.4, 16 rows, 129280 x 7168 245 -> 205);
 // short shares with one column tile lose by it (7168 x 2048 7.9 -> 9.0).
 template <int FMT, bool GATED, int TT, int RT, int KS, int WV>
 __global__ void __launch_bounds__(64 * WV)
 gemv_kernel(GemvArgs a) {
   using namespace gv;
   constexpr int NO = kTileOut<GATED>, NW = WV / KS;
-  constexpr bool AH = KS == 16 || TT >= 2;
+  constexpr bool AH = KS == 16 || TT >= 2 || RT == 2;
   __shared__ float part[WV][RT][TT][4][64];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -732,7 +732,7 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
       };
       // Many tiles fill the CUs by themselves: a wave takes two over all of K and reads x once for both. Fewer share K
       // until some 4096 to 8192 waves read at once. 7168 columns, 16 / 64 rows, us: 129280 rows of w two tiles a wave
-      // 245 / 527, one 307 / 916; 32768 x 4096 16 rows K in two 49, in four 52. 16384 x 4096 in two 25, whole 45;
+      // 205 / 527, one 307 / 916; 32768 x 4096 16 rows K in two 49, in four 52. 16384 x 4096 in two 25, whole 45;
       // 8192 x 4096 in eight 15, in two 24, in sixteen 18. 2048 x 7168 gated in sixteen 12.8, in eight 13.6; short K
       // is not cut further (7168 x 2048 in eight 7.9, in sixteen 12.9).
       if (tiles >= 16 * 256) by_rows(ic<2>{}, ic<1>{}, ic<8>{});
