@@ -847,8 +847,8 @@ mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, c
  *   or ROW) or MXQ_MXFP4.
  *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled; x (or h) below
  *   2^31 bytes from its first row to its last.
- *   workspace (down): mxq_workspace_bytes(MXQ_OP_DECODE_DOWN, tokens, hidden, 0) bytes, 4-byte aligned;
- *   NULL where that is 0. Calls that may overlap need their own.
+ *   workspace (down): mxq_workspace_bytes(MXQ_OP_DECODE_DOWN, tokens, hidden, topk) bytes, 4-byte aligned.
+ *   Calls that may overlap need their own.
  * ------------------------------------------------------------------------- */
 mxq_status moe_decode_gate_up(mxq_format fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
                               const void* x, int64_t ld_x, const int32_t* topk_idx, const void* W, const void* sW,
@@ -872,7 +872,7 @@ enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD 
  *   MXQ_OP_GROUPED_GEMM   (a = groups);
  *   MXQ_OP_NORM_BACKWARD  (a = rows, b = cols);
  *   MXQ_OP_ROUTE          (a = tokens, b = experts);
- *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden);
+ *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden, c = topk);
  *   MXQ_OP_GEMM_SWIGLU    (a = M, b = columns of the product: 2 inter forward, inter backward; c = K). */
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
 

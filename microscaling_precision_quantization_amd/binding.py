@@ -956,7 +956,7 @@ def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int
     c.done()
     if out is None:
         out = torch.empty((T, n), dtype=out_dtype, device=dev)
-    ws = _workspace(OP_DECODE_DOWN, T, n, workspace, dev)
+    ws = _workspace(OP_DECODE_DOWN, T, n, workspace, dev, k)
     _call("moe_decode_down", dev, fmt, T, k, experts, n, K, _ptr(h), _ptr(topk_idx), _ptr(weights), _ptr(W), _ptr(sW),
           _ptr(tW), SCOPE[t_scope], _ptr(out), OUT_F32 if out.dtype == torch.float32 else OUT_BF16, _ptr(ws), ws.numel())
     return out

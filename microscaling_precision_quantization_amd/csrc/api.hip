@@ -88,7 +88,7 @@ hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t 
 hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t K, const void* h,
                               const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
                               int t_mode, void* y, int out32, void* ws, hipStream_t st);
-size_t decode_down_ws_bytes(int64_t tokens, int64_t n);
+size_t decode_down_ws_bytes(int64_t choices, int64_t n);
 }  // namespace mxq
 
 namespace {
@@ -154,7 +154,7 @@ size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {
   if (op == MXQ_OP_NORM_BACKWARD) return a > 0 && b > 0 ? mxq::norm_backward_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_ROUTE) return a > 0 && b > 0 ? mxq::route_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_GEMM_SWIGLU) return a > 0 && b > 0 && c > 0 ? mxq::gated_ws_bytes(a, b, c) : 0;
-  if (op == MXQ_OP_DECODE_DOWN) return a > 0 && b > 0 ? mxq::decode_down_ws_bytes(a, b) : 0;
+  if (op == MXQ_OP_DECODE_DOWN) return a > 0 && b > 0 && c > 0 ? mxq::decode_down_ws_bytes(a * c, b) : 0;
   return 0;
 }
 
@@ -1038,9 +1038,8 @@ mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t
   if (!al4(topk_idx) || !al4(weights) ||
       (y_dtype == MXQ_OUT_F32 ? !al4(y) : (reinterpret_cast<uintptr_t>(y) & 1u) != 0))
     return MXQ_ERR_ALIGN;
-  const size_t need = mxq::decode_down_ws_bytes(tokens, hidden);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERR_WORKSPACE;
-  if (need > 0 && !al4(workspace)) return MXQ_ERR_ALIGN;
+  if (!workspace || workspace_bytes < mxq::decode_down_ws_bytes(tokens * topk, hidden)) return MXQ_ERR_WORKSPACE;
+  if (!al4(workspace)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_decode_down((int)fmt, tokens, topk, experts, hidden, K, h, topk_idx, weights, W, sW, tW,
                                             tW_scope == MXQ_SCOPE_ROW ? 0 : 1, y, y_dtype == MXQ_OUT_F32, workspace,
                                             S(stream)));

@@ -6,13 +6,12 @@
 // read once, whatever the number of tokens that chose it (moe_decode_gate_up), the down projection with
 // the combine behind it (moe_decode_down).
 //
-// The weights' bytes are all that counts (4.5 or 4.25 bits a weight; one multiplication a weight and
-// token). A wave takes tiles of 16 weight rows in chunks of 128 K: lane (n = l % 16, g = l / 16) loads the
-// 16 bytes of row n that hold K [32 g, 32 g + 32) of the chunk, makes q S in BF16 from them -- exactly: at
-// most six significant bits -- and feeds four 16x16x32 BF16 MFMAs, the rows' x the other operand in the same
-// order of K (which order does not matter to a sum, as long as both agree). Sums are binary32; the
-// FP32 scale t multiplies the sum. K is split over the waves of a workgroup, whose partial sums meet in
-// LDS in a fixed order.
+// The weights' bytes are all that counts (4.5 or 4.25 bits a weight; one multiplication a weight and token), so
+// they go from memory straight into the registers that the matrix core reads, and nothing is staged: a wave has
+// a tile of 16 weight rows (gated: eight gates and their ups) and a share of K, its loads all issued before the
+// first product. q S is made in BF16 -- exactly: at most six significant bits -- or, up to four x rows, S follows
+// the products. Sums are binary32; the FP32 scale t multiplies the sum. The shares of K meet in LDS in a fixed order.
+// A GEMM's tile would be mostly empty and would have to quantize x; it starts to pay at more rows than are taken here.
 // Element-wise 4-bit weights under group scales: remio.ai ("Miles Blackwell RL"), section "La
 // Compatibilidad ..."; moving expert weights through memory can bind harder than arithmetic: same page,
 // section "NVFP4 por token ...".
@@ -422,8 +421,13 @@ gemv_kernel(GemvArgs a) {
 
 // At most four x rows at a time (dot4). Dense: all of them. Experts: the choices of one expert, four by four.
 // Up to 512 choices are looked at by every wave at once and kept as bits (NB words of 64); NB = 0 finds them
-// through LDS, pass by pass. blockIdx.y is a choice, which works for its expert if it is the first to name
-// it, or (by_choice = 0) the expert.
+// through LDS, pass by pass (one token, 8 of 256 experts: 38 us, as bits 30). blockIdx.y is a choice, which works
+// for its expert if it is the first to name it, or (by_choice = 0) the expert.
+// Bound by the weights' way from memory: one token, 8 of 256 experts, 2048 x 7168, gate_up 30.0 us = 4.4 TB/s (a
+// large copy 5.06), down 16 + 4 us for the combine; 32 tokens, 8 of 128, 768 x 2048, gate_up 46 us = 4.1 TB/s,
+// down 28 + 4 (its K of 768 leaves half of every second chunk empty). Small ones are latency: the launch, the
+// first loads, the join: 2048 x 7168, one row, 4.7 us for 1.6 us of bytes.
+// Waves a SIMD: as many as leave no spills (six at 64 choices, four where x rows are dense).
 constexpr int kDense = -1;
 // KS waves share a tile's K; a workgroup has at least four waves, so 4 / KS tiles.
 template <int FMT, bool GATED, int NB, int KS>
@@ -446,7 +450,8 @@ gemv4_kernel(GemvArgs a, int by_choice) {
     const int y = blockIdx.y;
     auto none = [&](int i) { return (unsigned)i >= (unsigned)a.experts; };
     auto zero_row = [&](int c) {                          // by one thread: the choice c has no expert
-      for (int i = 0; i < TILES * NO && b0 + i < a.n; ++i) ((uint16_t*)a.y)[c * a.ld_y + b0 + i] = 0;
+      if constexpr (GATED)                                // (the down call's join skips it)
+          for (int i = 0; i < TILES * NO && b0 + i < a.n; ++i) ((uint16_t*)a.y)[c * a.ld_y + b0 + i] = 0;
     };
     if constexpr (NB > 0) {
       int v[NB];
@@ -538,144 +543,32 @@ gemv4_kernel(GemvArgs a, int by_choice) {
   }
 }
 
-struct DownArgs {
-  const uint16_t* h;       // BF16 (tokens topk, K)
-  int tokens, topk;
-  const int32_t* idx;
-  const float* weights;
-  int experts;
-  const uint8_t* w;        // (experts, n, K / 2)
-  const uint8_t* s;
-  const float* t;
-  int t_mode;
-  int64_t n;
-  int K;
-  void* y;                 // (tokens, n)
-  int out32;
-  float* parts;            // gridDim.y > 1: FP32 (parts, tokens, n)
-};
-
-// y[t] = sum over the choices j of t of weights[t, j] (W_e h[t, j]): a workgroup has a tile of 16 rows of y and
-// (blockIdx.y) one of gridDim.y shares of the chosen experts; its waves share those out (and, with few of
-// them, parts of K), each adding to an own copy of the tile's (tokens, 16) sums in LDS. The copies meet in
-// wave order, the shares in theirs (decode_join_kernel).
-// MANY: more than 64 choices, found through LDS; else each wave holds them in its lanes.
-constexpr int kMaxDecodeExperts = 1024, kMaxChoices = 2048;
-template <int FMT, int TCAP, bool MANY, int WV>
-__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4)))
-decode_down_kernel(DownArgs a, int kparts) {
-  using namespace gv;
-  __shared__ float sum[WV][TCAP][kTile];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * kTile;
-  const int S = a.tokens * a.topk;
-  const int chunks = (a.K + kWide - 1) / kWide;
-  const Rsrc rx = rsrc(a.h, (int64_t)S * a.K * 2);
-  for (int i = lane; i < a.tokens * kTile; i += 64) (&sum[wave][0][0])[i] = 0.0f;
-  // choice `mine` (or -1) of expert e, K part `part`
-  auto add = [&](int e, int part, auto&& choice) {
-    int c0, c1;
-    share(chunks, part, kparts, c0, c1);
-    const int64_t row = (int64_t)e * a.n + n0, left = min(a.n - n0, (int64_t)kTile);
-    const Rows4 rows = rows4<FMT>(a.w, a.s, {row, row + 8}, {min(left, (int64_t)8), max(left - 8, (int64_t)0)}, a.K);
-    const int n = 4 * ((lane >> 2) & 3);                   // the first of the lane's four rows
-    float tw[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-    if constexpr (FMT == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tw[i] = a.t[a.t_mode == 0 ? (int64_t)e * a.n + min(n0 + n + i, a.n - 1) : e];
-    }
-    int seen = 1;
-    for (int first = 0; first < seen; first += 4) {
-      int mine;
-      seen = choice(first, mine);
-      const float wt = mine >= 0 ? a.weights[mine] : 0.0f;
-      v4f acc[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      dot4<FMT>(rows, rx, [&]() { return mine >= 0 ? (uint32_t)mine * (2 * a.K) + x_off4() : kOff; }, a.K, c0, c1, acc);
-      const float4 p = gather4(acc);
-      float v[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {                       // the four rows of 16 lanes
-        v[i] += __shfl_xor(v[i], 16, 64);
-        v[i] += __shfl_xor(v[i], 32, 64);
-      }
-      // adds in LDS: two lanes meet here where a token names an expert twice
-      if (mine >= 0 && lane < 16) {
-        float* to = &sum[wave][mine / a.topk][n];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) atomicAdd(&to[i], wt * (v[i] * tw[i]));
-      }
-    }
-  };
-  const int stride = WV * gridDim.y, me = blockIdx.y * WV + wave;
-  if constexpr (MANY) {
-    __shared__ int first_of[kMaxDecodeExperts], list[kMaxDecodeExperts], idx[kMaxChoices];
-    __shared__ int col[WV][4], found[WV];
-    for (int i = tid; i < a.experts; i += 64 * WV) first_of[i] = 0x7FFFFFFF;
-    for (int c = tid; c < S; c += 64 * WV) idx[c] = a.idx[c];
-    __syncthreads();
-    for (int c = tid; c < S; c += 64 * WV)
-      if ((unsigned)idx[c] < (unsigned)a.experts) atomicMin(&first_of[idx[c]], c);
-    __syncthreads();
-    int experts = 0;
-    for (int b = 0; b < S; b += 64 * WV) {                // the chosen experts in the order of the choices
-      const int c = b + tid;
-      const int e = c < S ? idx[c] : -1;
-      const bool lead = (unsigned)e < (unsigned)a.experts && first_of[e] == c;
-      const uint64_t m = __ballot(lead);
-      if (lane == 0) found[wave] = __popcll(m);
-      __syncthreads();
-      int before = experts, here = 0;
-      for (int w = 0; w < WV; ++w) {
-        before += w < wave ? found[w] : 0;
-        here += found[w];
-      }
-      if (lead) list[before + __popcll(m & ((1ull << lane) - 1))] = e;
-      experts += here;
-      __syncthreads();
-    }
-    for (int item = me; item < experts * kparts; item += stride) {
-      const int e = __builtin_amdgcn_readfirstlane(list[item / kparts]);
-      add(e, item % kparts, [&](int first, int& mine) { return choices_of(idx, S, e, first, col[wave], mine); });
-    }
-  } else {
-    const int mine_e = lane < S ? a.idx[lane] : -1;
-    uint64_t todo = __ballot((unsigned)mine_e < (unsigned)a.experts);
-    for (int i = 0; todo; ++i) {
-      const int e = __builtin_amdgcn_readlane(mine_e, __builtin_ctzll(todo));
-      const Who<1> who{{__ballot(mine_e == e)}};
-      todo &= ~who.m[0];
-      for (int p = 0; p < kparts; ++p) {
-        if ((i * kparts + p) % stride != me) continue;
-        add(e, p, [&](int first, int& mine) {
-          mine = who.pick(first);
-          return who.count();
-        });
-      }
-    }
-  }
-  __syncthreads();
-  const bool whole = gridDim.y == 1;
-  for (int o = tid; o < a.tokens * kTile; o += 64 * WV) {
-    const int t = o >> 4, i = o & 15;
-    if (n0 + i >= a.n) continue;
-    float v = sum[0][t][i];
-#pragma unroll
-    for (int w = 1; w < WV; ++w) v += sum[w][t][i];
-    if (whole) store_y(a.y, t * a.n + n0 + i, v, a.out32);
-    else a.parts[((int64_t)blockIdx.y * a.tokens + t) * a.n + n0 + i] = v;
-  }
-}
-
+// The combine of the down call: y[t, n] = sum over j of weights[t, j] parts[t topk + j, n], in the order of j, the
+// choices that name no expert left out (their rows of parts were not written: read, so that no load waits for
+// another's answer, but not used).
 __global__ void __launch_bounds__(256)
-decode_join_kernel(const float* __restrict__ parts, int n_parts, int64_t n, void* __restrict__ y, int out32) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= n) return;
-  float v = parts[at];
-  for (int p = 1; p < n_parts; ++p) v += parts[p * n + at];
-  store_y(y, at, v, out32);
+decode_join_kernel(const float* __restrict__ parts, const int32_t* __restrict__ idx, const float* __restrict__ weights,
+                   int topk, int experts, int64_t n, void* __restrict__ y, int out32) {
+  constexpr int U = 8;                                    // loads in flight
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int c0 = blockIdx.y * topk;
+  if (col >= n) return;
+  float v = 0.0f;
+  for (int j = 0; j < topk; j += U) {
+    float p[U], w[U];
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + min(j + u, topk - 1);
+      p[u] = parts[c * n + col];
+      e[u] = idx[c];
+      w[u] = weights[c];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j + u < topk && (unsigned)e[u] < (unsigned)experts) v = __builtin_fmaf(w[u], p[u], v);
+  }
+  store_y(y, blockIdx.y * n + col, v, out32);
 }
 
 // ---------------------------------------------------------------------------
@@ -746,61 +639,38 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
   return hipGetLastError();
 }
 
+// Over the experts that a.rows choices name: a row of workgroups per expert that can be named: the choices, or the
+// experts where those are fewer.
+template <bool GATED>
+static void launch_choices(int fmt, const GemvArgs& a, hipStream_t st) {
+  const int64_t S = a.rows, by_choice = S < a.experts, each = by_choice ? S : a.experts;
+  const int64_t tiles = (a.n + kTileOut<GATED> - 1) / kTileOut<GATED>;
+  by_format(fmt, [&](auto F) {
+    constexpr int FMT = decltype(F)::value;
+    if (S <= 64) launch_gemv4<FMT, GATED, 1>(a, tiles, each, by_choice, st);
+    else if (S <= 256) launch_gemv4<FMT, GATED, 4>(a, tiles, each, by_choice, st);
+    else if (S <= 512) launch_gemv4<FMT, GATED, 8>(a, tiles, each, by_choice, st);
+    else launch_gemv4<FMT, GATED, 0>(a, tiles, each, by_choice, st);
+  });
+}
+
 hipError_t launch_decode_gate_up(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t inter, int64_t K,
                                  const void* x, int64_t ld_x, const int32_t* idx, const void* w, const void* s,
                                  const float* t, int t_mode, void* h, hipStream_t st) {
-  const int64_t S = tokens * topk;
-  const GemvArgs a{(const uint16_t*)x, ld_x, (int)S, (int)topk, idx, (int)experts, (const uint8_t*)w, (const uint8_t*)s, t,
-                   t_mode, inter, (int)K, h, inter, 0};
-  // one row of workgroups per expert that can be named: the choices, or the experts where those are fewer
-  const int by_choice = S < experts;
-  const int64_t tiles = (inter + kTileOut<true> - 1) / kTileOut<true>, each = by_choice ? S : experts;
-  by_format(fmt, [&](auto F) {
-    constexpr int FMT = decltype(F)::value;
-    if (S <= 64) launch_gemv4<FMT, true, 1>(a, tiles, each, by_choice, st);
-    else if (S <= 256) launch_gemv4<FMT, true, 4>(a, tiles, each, by_choice, st);
-    else if (S <= 512) launch_gemv4<FMT, true, 8>(a, tiles, each, by_choice, st);
-    else launch_gemv4<FMT, true, 0>(a, tiles, each, by_choice, st);
-  });
+  launch_choices<true>(fmt, GemvArgs{(const uint16_t*)x, ld_x, (int)(tokens * topk), (int)topk, idx, (int)experts,
+                                     (const uint8_t*)w, (const uint8_t*)s, t, t_mode, inter, (int)K, h, inter, 0}, st);
   return hipGetLastError();
 }
 
-// Shares of the chosen experts that the down call may be cut into: tiles of 16 rows alone fill the CUs
-// twice from 8192 rows on.
-static int64_t down_shares(int64_t n) {
-  const int64_t tiles = (n + gv::kTile - 1) / gv::kTile;
-  return std::max<int64_t>(1, std::min<int64_t>(8, 512 / tiles));
-}
-size_t decode_down_ws_bytes(int64_t tokens, int64_t n) {
-  const int64_t p = down_shares(n);
-  return p == 1 ? 0 : (size_t)((p * tokens * n * 4 + 255) / 256 * 256);
-}
+size_t decode_down_ws_bytes(int64_t choices, int64_t n) { return (size_t)((choices * n * 4 + 255) / 256 * 256); }
 
 hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t K, const void* h,
                               const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
                               int t_mode, void* y, int out32, void* ws, hipStream_t st) {
-  const DownArgs a{(const uint16_t*)h, (int)tokens, (int)topk, idx, weights, (int)experts, (const uint8_t*)w,
-                   (const uint8_t*)s, t, t_mode, n, (int)K, y, out32, (float*)ws};
-  constexpr int WV = 8;
-  const int64_t S = tokens * topk, chunks = (K + gv::kWide - 1) / gv::kWide, most = std::min(S, experts);
-  // shares: as long as every wave is left four chunks; parts of K so that a few choices still give every wave one
-  const int64_t shares = std::max<int64_t>(1, std::min(down_shares(n), most * chunks / (4 * WV)));
-  int kparts = 1;
-  while (most * kparts < WV * shares && 2 * kparts <= chunks) kparts *= 2;
-  const dim3 grid((unsigned)((n + gv::kTile - 1) / gv::kTile), (unsigned)shares);
-  by_format(fmt, [&](auto F) {
-    constexpr int FMT = decltype(F)::value;
-    auto go = [&](auto T) {
-      constexpr int TCAP = decltype(T)::value;
-      if (S <= 64) hipLaunchKernelGGL((decode_down_kernel<FMT, TCAP, false, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
-      else hipLaunchKernelGGL((decode_down_kernel<FMT, TCAP, true, WV>), grid, dim3(64 * WV), 0, st, a, kparts);
-    };
-    if (tokens <= 16) go(ic<16>{});
-    else go(ic<64>{});
-  });
-  if (shares > 1)
-    hipLaunchKernelGGL(decode_join_kernel, dim3((unsigned)((tokens * n + 255) / 256)), dim3(256), 0, st, (const float*)ws,
-                       (int)shares, tokens * n, y, out32);
+  launch_choices<false>(fmt, GemvArgs{(const uint16_t*)h, K, (int)(tokens * topk), 1, idx, (int)experts, (const uint8_t*)w,
+                                      (const uint8_t*)s, t, t_mode, n, (int)K, ws, n, 1}, st);
+  hipLaunchKernelGGL(decode_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)tokens), dim3(256), 0, st,
+                     (const float*)ws, idx, weights, (int)topk, (int)experts, n, y, out32);
   return hipGetLastError();
 }
 

@@ -265,7 +265,7 @@ class MoeDecodeNvfp4:
     def __init__(self, tokens: int, hidden: int, experts: int, inter: int, topk: int, dev, wq):
         self.G, self.wq = experts, wq
         self.h, self.y = _bf16((tokens, topk, inter), dev), _f32((tokens, hidden), dev)
-        self.ws = _u8((B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, tokens, hidden, 0),), dev)
+        self.ws = _u8((B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, tokens, hidden, topk),), dev)
 
     def forward(self, x, topk_idx, weights):
         B.moe_decode_gate_up(B.NVFP4, x, topk_idx, *self.wq["gu"], experts=self.G, out=self.h)

@@ -128,9 +128,9 @@ def test_moe_decode_validation():
     def f(fmt=B.MXFP4, T=4, k=2, E=8, n=16, K=64, x=P, ld=64, idx=P, W=P, s=P, t=None, sc=GROUP, h=P):
         return B.lib().moe_decode_gate_up(fmt, T, k, E, n, K, x, ld, idx, W, s, t, sc, h, None)
 
-    need = B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 4, 16, 0)
-    assert need > 0 and B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 4, 8192, 0) == 0
-    assert B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 0, 16, 0) == 0
+    need = B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 4, 16, 2)
+    assert need == 4 * 2 * 16 * 4
+    assert B.lib().mxq_workspace_bytes(B.OP_DECODE_DOWN, 0, 16, 2) == 0
 
     def g(fmt=B.MXFP4, T=4, k=2, E=8, n=16, K=64, x=P, idx=P, w=P, W=P, s=P, t=None, sc=GROUP, h=P, yd=F32, ws=P, wsn=need):
         return B.lib().moe_decode_down(fmt, T, k, E, n, K, x, idx, w, W, s, t, sc, h, yd, ws, wsn, None)
