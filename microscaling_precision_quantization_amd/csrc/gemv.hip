@@ -355,67 +355,105 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int f32) {
 // are what takes the time (2048 x 7168 gated, 16 rows 12.8 us, 32 20.4, 64 33.8; the weights alone 3.1), below it
 // the latency of three loads in turn. AH: x ahead of the products along with the weights (32 rows 23.0 -> 20.4, 16 rows, 129280 x 7168 245 -> 205);
 // short shares with one column tile lose by it (7168 x 2048 7.9 -> 9.0).
-template <int FMT, bool GATED, int TT, int RT, int KS, int WV>
+// MOE: blockIdx.y is an expert, its choices are listed in LDS and taken 16 TT at a time.
+constexpr int kMaxChoices = 2048;
+template <int FMT, bool GATED, int TT, int RT, int KS, int WV, bool MOE>
 __global__ void __launch_bounds__(64 * WV)
 gemv_kernel(GemvArgs a) {
   using namespace gv;
   constexpr int NO = kTileOut<GATED>, NW = WV / KS;
   constexpr bool AH = KS == 16 || TT >= 2 || RT == 2;
+  constexpr int PER = NW * RT * NO;                       // columns of the result
   __shared__ float part[WV][RT][TT][4][64];
+  __shared__ uint16_t list[MOE ? kMaxChoices : 1];
+  __shared__ int hits[MOE ? kMaxChoices / 64 : 1];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t b0 = (int64_t)blockIdx.x * (NW * RT * NO);
+  const int64_t b0 = (int64_t)blockIdx.x * PER;
+  int64_t base = 0;                                       // the expert's first weight row
+  int e = 0, seen = a.rows;
+  if constexpr (MOE) {
+    e = blockIdx.y;
+    base = (int64_t)e * (GATED ? 2 : 1) * a.n;
+    if (GATED && e == 0) {                                // choices without an expert
+      for (int c = tid; c < a.rows; c += 64 * WV)
+        if ((unsigned)a.idx[c] >= (unsigned)a.experts)
+          for (int i = 0; i < PER && b0 + i < a.n; ++i) ((uint16_t*)a.y)[c * a.ld_y + b0 + i] = 0;
+    }
+    constexpr int W = kMaxChoices / 64 / WV;              // words of 64 choices a wave
+    uint64_t m[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int c = 64 * (i * WV + wave) + lane;
+      m[i] = __ballot(c < a.rows && a.idx[c] == e);
+      if (lane == 0) hits[i * WV + wave] = __popcll(m[i]);
+    }
+    __syncthreads();
+    seen = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      for (int w = 0; w < WV; ++w) {
+        if (w == wave && (m[i] >> lane & 1)) list[seen + __popcll(m[i] & ((1ull << lane) - 1))] = 64 * (i * WV + w) + lane;
+        seen += hits[i * WV + w];
+      }
+    if (seen == 0) return;                                // all waves alike
+    __syncthreads();
+  }
   const int64_t wb = a.K / 2, sb = a.K / kScaleK<FMT>;
   Rsrc rw[RT], rs[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {                          // a tile past the end has no rows
     const int64_t n0 = b0 + (wave / KS * RT + r) * NO;
     const int64_t rows = n0 >= a.n ? 0 : (GATED ? 2 * a.n : min(a.n, n0 + kTile)) - n0;   // gates past n read ups, not stored
-    rw[r] = rsrc(a.w + n0 * wb, rows * wb);
-    rs[r] = rsrc(a.s + n0 * sb, rows * sb);
+    rw[r] = rsrc(a.w + (base + n0) * wb, rows * wb);
+    rs[r] = rsrc(a.s + (base + n0) * sb, rows * sb);
   }
   const int m = lane % kTile;
   const int64_t row = GATED && m >= 8 ? a.n + m - 8 : m;
   const uint32_t wo = (uint32_t)(row * wb) + 16 * g, so = (uint32_t)(row * sb) + kCodes<FMT> * g;
-  const Rsrc rx = rsrc(a.x, ((a.rows - 1) * a.ld_x + a.K) * 2);
-  uint32_t xo[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int r = t * kTile + m;
-    xo[t] = r < a.rows ? (uint32_t)(r * a.ld_x + 32 * g) * 2 : kOff;
-  }
+  const Rsrc rx = rsrc(a.x, (((MOE ? a.rows / a.topk : a.rows) - 1) * a.ld_x + a.K) * 2);
   int c0, c1;
   share((a.K + kChunk - 1) / kChunk, wave % KS, KS, c0, c1);
-  v4f acc[RT][TT];
+  for (int first = 0; first < seen; first += 16 * TT) {
+    uint32_t xo[TT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  dot16<FMT, RT, TT, AH>(rw, rs, rx, wo, so, xo, a.K, c0, c1, acc);
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][r][t][i][lane] = acc[r][t][i];
-  __syncthreads();
-  // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
-  constexpr int PER = NW * RT * NO;                       // columns of the result
-  for (int o = tid; o < TT * 16 * PER; o += 64 * WV) {
-    const int n = o % PER, at = o / PER, tile = n / NO;
-    if (at >= a.rows || b0 + n >= a.n) continue;
-    float y[2];
-#pragma unroll
-    for (int k = 0; k < (GATED ? 2 : 1); ++k) {
-      const int i = n % NO + 8 * k, l = 16 * (i >> 2) + at % 16;
-      const float* q = &part[tile / RT * KS][tile % RT][at / 16][i & 3][l];
-      float v = q[0];
-#pragma unroll
-      for (int w = 1; w < KS; ++w) v += q[w * (RT * TT * 256)];
-      if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? k * a.n + b0 + n : 0];
-      y[k] = v;
+    for (int t = 0; t < TT; ++t) {
+      const int r = first + t * kTile + m;
+      xo[t] = r < seen ? (uint32_t)((MOE ? list[r] / a.topk : r) * a.ld_x + 32 * g) * 2 : kOff;
     }
-    store_y(a.y, at * a.ld_y + b0 + n, GATED ? swiglu_forward(y[0], y[1]) : y[0], !GATED && a.out32);
+    v4f acc[RT][TT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    dot16<FMT, RT, TT, AH>(rw, rs, rx, wo, so, xo, a.K, c0, c1, acc);
+    if (MOE && first) __syncthreads();                    // part has been read
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[wave][r][t][i][lane] = acc[r][t][i];
+    __syncthreads();
+    // accumulator r of lane l is (row 4 (l / 16) + r, column l % 16) of the tile
+    for (int o = tid; o < TT * 16 * PER; o += 64 * WV) {
+      const int n = o % PER, at = o / PER, tile = n / NO;
+      if (first + at >= seen || b0 + n >= a.n) continue;
+      float y[2];
+#pragma unroll
+      for (int k = 0; k < (GATED ? 2 : 1); ++k) {
+        const int i = n % NO + 8 * k, l = 16 * (i >> 2) + at % 16;
+        const float* q = &part[tile / RT * KS][tile % RT][at / 16][i & 3][l];
+        float v = q[0];
+#pragma unroll
+        for (int w = 1; w < KS; ++w) v += q[w * (RT * TT * 256)];
+        if constexpr (FMT == 2) v *= a.t[a.t_mode == 0 ? base + k * a.n + b0 + n : e];
+        y[k] = v;
+      }
+      const int to = MOE ? list[first + at] : at;
+      store_y(a.y, to * a.ld_y + b0 + n, GATED ? swiglu_forward(y[0], y[1]) : y[0], !GATED && a.out32);
+    }
+    if (!MOE) return;                                     // dense: 16 TT hold all rows
   }
 }
 
@@ -619,9 +657,9 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
         constexpr int RT = decltype(R)::value, KS = decltype(S)::value, WV = decltype(W)::value;
         const int64_t per = WV / KS * RT;
         const dim3 grid((unsigned)((tiles + per - 1) / per)), block(64 * WV);
-        if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, RT, KS, WV>), grid, block, 0, st, a);
-        else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, RT, KS, WV>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, RT, KS, WV>), grid, block, 0, st, a);
+        if (rows <= 16) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 1, RT, KS, WV, false>), grid, block, 0, st, a);
+        else if (rows <= 32) hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, RT, KS, WV, false>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 4, RT, KS, WV, false>), grid, block, 0, st, a);
       };
       // Many tiles fill the CUs by themselves: a wave takes two over all of K and reads x once for both. Fewer share K
       // until some 4096 to 8192 waves read at once. 7168 columns, 16 / 64 rows, us: 129280 rows of w two tiles a wave
@@ -639,14 +677,27 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
   return hipGetLastError();
 }
 
-// Over the experts that a.rows choices name: a row of workgroups per expert that can be named: the choices, or the
-// experts where those are fewer.
+// Over the experts that a.rows choices name. Up to six choices an expert, four by four: a row of workgroups per
+// expert that can be named: the choices, or the experts where those are fewer. More: 32 by 32, two tiles a wave,
+// the other way 64 tokens, 2 of 8 experts, 2048 x 4096 take 90 / 49 us (gate_up / down) against 50 / 34, 8 of 64,
+// 768 x 2048 71 / 51 against 59 / 37, but with four an expert (8 of 128) 83 / 54 against 93 / 54. K in four
+// where there are few tiles: 64 tokens, 2 of 8, in two 62 / 40; 4 of 32, 1024 x 4096, down in four 50, in two 45.
 template <bool GATED>
 static void launch_choices(int fmt, const GemvArgs& a, hipStream_t st) {
   const int64_t S = a.rows, by_choice = S < a.experts, each = by_choice ? S : a.experts;
   const int64_t tiles = (a.n + kTileOut<GATED> - 1) / kTileOut<GATED>;
   by_format(fmt, [&](auto F) {
     constexpr int FMT = decltype(F)::value;
+    if (S >= 6 * a.experts) {
+      auto many = [&](auto KSC) {
+        constexpr int KS = decltype(KSC)::value, PER = 8 / KS * 2;
+        hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, 2, KS, 8, true>),
+                           dim3((unsigned)((tiles + PER - 1) / PER), (unsigned)a.experts), dim3(512), 0, st, a);
+      };
+      if (tiles * a.experts <= 4096) many(ic<4>{});
+      else many(ic<2>{});
+      return;
+    }
     if (S <= 64) launch_gemv4<FMT, GATED, 1>(a, tiles, each, by_choice, st);
     else if (S <= 256) launch_gemv4<FMT, GATED, 4>(a, tiles, each, by_choice, st);
     else if (S <= 512) launch_gemv4<FMT, GATED, 8>(a, tiles, each, by_choice, st);

@@ -322,7 +322,8 @@ def test_gemv_strided_rows_row_scales_and_strange_rows():
 
 
 DECODE = [(1, 1, 4, 16, 32), (1, 8, 64, 40, 256), (3, 2, 5, 24, 96), (17, 8, 16, 72, 160), (33, 4, 40, 16, 128),
-          (64, 6, 9, 33, 64), (64, 32, 32, 16, 32), (2, 3, 1024, 8, 32), (5, 2, 1, 20, 64)]
+          (64, 6, 9, 33, 64), (64, 32, 32, 16, 32), (2, 3, 1024, 8, 32), (5, 2, 1, 20, 64),
+          (64, 8, 96, 16, 160), (64, 16, 200, 24, 64), (21, 2, 4, 16424, 160)]   # 512 and 1024 choices, many tiles
 
 
 def choices(T, k, E, seed, dead):
