@@ -157,16 +157,8 @@ gated_part_kernel(ExactProblem p, int64_t part_k, int64_t tiles_m, int64_t tiles
   MXQ_EXACT_LDS(C)
   int64_t tm, tn;
   if (!exact_map_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
-  // the part's operands begin at its first K (rows keep their stride)
-  const int64_t k0 = (int64_t)blockIdx.y * part_k;
-  constexpr int BS = LD == 2 ? 16 : 32;
-  p.A += k_bytes<LD>(k0);
-  p.B += k_bytes<LD>(k0);
-  if constexpr (LD != 0) {
-    p.sA += k0 / BS;
-    p.sB += k0 / BS;
-  }
-  p.k_end = min(part_k, p.lda - k0);
+  p.k_begin = (int64_t)blockIdx.y * part_k;
+  p.k_end = min(p.k_begin + part_k, p.lda);
   p.C += (int64_t)blockIdx.y * p.m_valid * p.ldc;
   exact_gemm_tile<LD, 128, 128, SM, 1, WIDE>(p, tm * 128, tn * 128, lds0, lds1, lds2, lds3, ldsc);
 }

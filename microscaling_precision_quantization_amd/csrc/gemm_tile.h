@@ -763,10 +763,10 @@ __device__ __forceinline__ void exact_gemm_tile(const ExactProblem& p, int64_t m
   auto issue_range = [&](const TileK& tk, auto SLOT, auto LO, auto HI) {
     static_for<decltype(LO)::value, decltype(HI)::value>([&](auto D) { issue_unit(tk, SLOT, D); });
   };
-  // scale chunk c (stages [SPC c, SPC c + SPC)) into chunk buffer c % 2
+  // scale chunk c (stages [SPC c, SPC c + SPC)) into chunk buffer c % 2 (k_begin is a multiple of a chunk's K)
   auto issue_chunk = [&](int c) {
     if constexpr (CH) {
-      const uint32_t so = c * SPC < nk ? (uint32_t)(16 * c) : kOutOfRange;
+      const uint32_t so = c * SPC < nk ? (uint32_t)(kb / BS + 16 * c) : kOutOfRange;
       const uint32_t m0v = lbase_c + (uint32_t)(c & 1) * C::CH_HALF + (uint32_t)(wave * XS) * 1024u;
       buf_dma16_group<XS>(rsX, voX, so, m0v);
     }

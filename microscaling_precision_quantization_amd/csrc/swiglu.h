@@ -7,7 +7,7 @@ namespace mxq {
 // e = e^-|g| <= 1 never overflows; with r = 1 / (1 + e): sigma(g) = r (g >= 0) or e r, 1 - sigma(g) = e r
 // or r, neither by cancellation. e is 2^(-|g| log2 e) by the hardware's exponential: the rounded
 // argument puts it off by |g| 2^-24 relative, and below 2^-126 (|g| > 87) it is 0. So sigma is within 2^-17 of
-// exact plus 2^-126, and so is everything below, far inside the BF16 rounding that follows (2^-9); the
+// exact plus 2^-126, and so is everything below, far inside the BF16 rounding that follows (2^-8); the
 // library's expf, good to an ulp, took a third more instructions in an epilogue that is bound by them.
 // A gate so far out that sigma is 0 gives 0 (also at -Inf, where g sigma would be a NaN).
 __device__ __forceinline__ void sigmoid_pair(float g, float& s, float& c) {
