@@ -1,6 +1,7 @@
 """The gated feed-forward block (gemm_swiglu and its backward, dense and per expert) and the 4-bit
 matrix-vector products against FP64, with the bounds of tests/ffn_ref.py: formats, ragged sizes, empty
-and padded experts, gates far out, rows behind the outputs, streams and graphs."""
+and padded experts, gates far out, rows behind the outputs, streams and graphs,
+long K and tensors past 2^31 bytes."""
 
 import pytest
 import torch
@@ -53,7 +54,6 @@ DENSE = [("bf16", 1, 8, 8), ("bf16", 5, 16, 40), ("bf16", 127, 72, 64), ("bf16",
          ("mxfp8", 64, 128, 1536),
          ("nvfp4", 1, 8, 32), ("nvfp4", 129, 72, 96), ("nvfp4", 200, 264, 64), ("nvfp4", 130, 136, 256),
          ("nvfp4", 64, 128, 1280)]
-# enough 256 x 256 tiles for the large tile: 11 x 19 and more
 # few tiles and a long K: split, in even and uneven parts, the last one short
 LONG = [("bf16", 3, 24, 1032), ("bf16", 130, 72, 7168), ("bf16", 1, 8, 5128), ("mxfp8", 5, 40, 1056), ("mxfp8", 140, 136, 2048),
         ("mxfp8", 64, 256, 7168), ("mxfp8", 9, 8, 1664), ("nvfp4", 5, 40, 1056), ("nvfp4", 140, 136, 2048),
@@ -61,6 +61,7 @@ LONG = [("bf16", 3, 24, 1032), ("bf16", 130, 72, 7168), ("bf16", 1, 8, 5128), ("
 # more 128 x 128 tiles than CUs, fewer 256 x 256 than 192
 MANY = [(f, 1300, 1672, k) for f, k in (("bf16", 72), ("bf16", 64), ("mxfp8", 96), ("mxfp8", 128), ("mxfp8", 512), ("nvfp4", 96),
                                         ("nvfp4", 128), ("nvfp4", 256))]
+# enough 256 x 256 tiles for the large tile: 11 x 19 and more
 LARGE = [("bf16", 2601, 2408, 72), ("bf16", 2601, 2408, 128), ("mxfp8", 2601, 2408, 96), ("mxfp8", 2601, 2408, 128),
          ("mxfp8", 2601, 2408, 512), ("nvfp4", 2601, 2408, 96), ("nvfp4", 2601, 2408, 128), ("nvfp4", 2601, 2408, 256)]
 
@@ -456,6 +457,104 @@ def test_calls_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(replayed, eager)):
             assert torch.equal(a, b), (seed, i)
+
+
+def two_calls(seed):
+    """Two calls that need a workspace, and one that does not: a function of their inputs."""
+    g = gen(seed)
+    T, k, E, I, H = 9, 4, 6, 96, 512
+    d = weights4("nvfp4", randn(g, E * H, I, scale=0.1).to(BF), E)
+    idx, wt = choices(T, k, E, seed, False)
+    h, x, wgu = randn(g, T, k, I).to(BF), randn(g, T, 7168).to(BF), randn(g, 48, 7168, scale=0.02).to(BF)
+    one = weights4("mxfp4", randn(g, 304, k * I, scale=0.1).to(BF))
+
+    def call():
+        return (mxq.moe_decode_down(B.NVFP4, h, idx, wt, *d, experts=E), mxq.gemm_swiglu(B.BF16, x, None, wgu, None)[0],
+                mxq.gemv_block_scaled(B.MXFP4, h.view(T, k * I), *one))
+    return call, (h, x, wt)
+
+
+def test_two_streams_at_once():
+    calls = [two_calls(31)[0], two_calls(32)[0]]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+def test_two_graphs_and_eager_calls_between_them():
+    calls, inputs = zip(two_calls(41), two_calls(42))
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for c, gr in zip(calls, graphs):
+        with torch.cuda.graph(gr):
+            outs.append(c())
+    for turn in range(3):
+        for t in inputs:
+            for v in t:
+                v.mul_(0.5 if turn % 2 else -2.0)
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        replayed = [[v.clone() for v in o] for o in outs]
+        for c, o in zip(calls, replayed):
+            assert all(torch.equal(a, b) for a, b in zip(c(), o)), turn
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_gemv_with_a_long_k(rows):
+    g = gen(rows)
+    N, K = 24, 1 << 20
+    x, t = randn(g, rows, K).to(BF), torch.full((1,), 2.0 ** -10, device="cuda")
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(0x28, 0x40, (N, K // 16), generator=g, device="cuda", dtype=torch.uint8)
+    want, err = R.product(x.double(), R.wide("nvfp4", q, s, t))
+    R.check(mxq.gemv_block_scaled(B.NVFP4, x, q, s, t), want, err + 2 * R.F32 * want.abs(), "y")
+
+
+@pytest.mark.parametrize("rows", [2, 16, 40])
+def test_gemv_with_weights_past_32_bits(rows):
+    """2.2 GB of weights: the last rows lie past 2^31 bytes."""
+    g = gen(rows)
+    N, K = 66003, 65536
+    x = randn(g, rows, K).to(BF)
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(110, 118, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    assert q.numel() > 2 ** 31
+    y = mxq.gemv_block_scaled(B.MXFP4, x, q, s)
+    for rows_of in (slice(0, 40), slice(N - 700, N)):
+        want, err = R.product(x.double(), R.wide("mxfp4", q[rows_of], s[rows_of]))
+        R.check(y[:, rows_of], want, err, "y")
+
+
+def test_gated_outputs_past_32_bits():
+    """(g | u) and its gradient of 2.2 GB."""
+    g = gen(5)
+    M, I, K = 270_000, 2048, 16
+    x, w = randn(g, M, K).to(BF), randn(g, 2 * I, K, scale=0.5).to(BF)
+    h, gu = mxq.gemm_swiglu(B.BF16, x, None, w, None, keep_gate_up=True)
+    assert gu.numel() * 2 > 2 ** 31
+    dy, wT = randn(g, M, K).to(BF), randn(g, I, K, scale=0.5).to(BF)
+    dgu, h2 = mxq.gemm_swiglu_backward(B.BF16, dy, None, wT, None, gu)
+    for at in (slice(0, 64), slice(M - 200, M)):
+        y, err = R.product(x[at].double(), w.double())
+        want, tol, gu_tol = R.gated(y, err)
+        R.check(gu[at], y, gu_tol, "gate_up")
+        R.check(h[at], want, tol, "h")
+        (dg, dtol), (hb, htol) = R.through(*R.product(dy[at].double(), wT.double()), gu[at])
+        R.check(dgu[at], dg, dtol, "d_gate_up")
+        if h2 is not None:
+            R.check(h2[at], hb, htol, "h made again")
 
 
 def test_empty_calls():

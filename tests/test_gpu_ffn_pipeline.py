@@ -39,9 +39,10 @@ def test_gated_ffn_from_its_input_to_its_gradients(T, H, I):
     R.check(dx, *R.product(f.d_gu.double(), w_gu.double().T), "dx")
     R.check(dw_gu, *R.product(f.d_gu.double().T, x.double().T), "dw_gu")
     R.check(dw_d, *R.product(d_o.double().T, f.h.double().T), "dw_d")
-    # the whole chain against autograd: h, (g | u) and dGU are rounded to BF16 (2^-9 relative each, half a
-    # step), and the factors of dGU, made from a rounded g and u, move by at most some 3 2^-9 (g sigma' and g^2
-    # sigma'' stay below 1); independent errors add up in the products' norms to no more than the sum
+    # the whole chain against autograd: h, (g | u) and dGU are rounded to BF16 (half a step, at most 2^-8 of a value;
+    # in the norm of many 0.38 of that: a uniform error of 2^-8 / sqrt(3) over values of 1 .. 2, 1.53 in the mean
+    # square; so below 2^-9 each), and the factors of dGU, made from a rounded g and u, move by at most some 3 2^-9
+    # (g sigma' and g^2 sigma'' stay below 1); independent errors add up in the products' norms to no more than the sum
     xs, a, b = (v.double().requires_grad_() for v in (x, w_gu, w_d))
     gg, u = (xs @ a.T).chunk(2, 1)
     ((gg * torch.sigmoid(gg) * u) @ b.T * d_o.double()).sum().backward()
