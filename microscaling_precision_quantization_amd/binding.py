@@ -148,7 +148,8 @@ def _ptr(t):
 def _stream(dev):
     """The raw handle of dev's current stream (20 times cheaper than building a Stream object); dev
     as torch names devices: a torch.device, a string or an index."""
-    dev = torch.device(dev)
+    if type(dev) is not torch.device:
+        dev = torch.device(dev)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
@@ -745,7 +746,7 @@ def _gated_out(c, out, names, rows: int, inter: int, keep: bool, dev):
         c.done()
         return first, second
     c.done()
-    new = lambda n: torch.empty((rows, width(n)), dtype=torch.bfloat16, device=dev)
+    new = lambda n: torch.empty(rows, width(n), dtype=torch.bfloat16, device=dev)
     return new(names[0]), new(names[1]) if keep else None
 
 
@@ -880,7 +881,7 @@ def _gemv_args(fmt: int, x, W, sW, tW, t_scope: str, gated: bool, out_dtype, out
                (rows, n), ld=True)
     c.done()
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype, device=dev)
+        out = torch.empty(rows, n, dtype=out_dtype, device=dev)
     return out, (fmt, rows, n, K, _ptr(x), max(x.stride(0), K), _ptr(W), _ptr(sW), _ptr(tW), SCOPE[t_scope], _ptr(out))
 
 
@@ -930,7 +931,7 @@ def moe_decode_gate_up(fmt: int, x, topk_idx, W, sW, tW=None, experts: int = 0, 
     c.opt(out, "out", torch.bfloat16, (T, k, n // 2))
     c.done()
     if out is None:
-        out = torch.empty((T, k, n // 2), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(T, k, n // 2, dtype=torch.bfloat16, device=dev)
     _call("moe_decode_gate_up", dev, fmt, T, k, experts, n // 2, K, _ptr(x), max(x.stride(0), K), _ptr(topk_idx), _ptr(W),
           _ptr(sW), _ptr(tW), SCOPE[t_scope], _ptr(out))
     return out
@@ -955,7 +956,7 @@ def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int
         c.need(out, "out", torch.float32 if out.dtype == torch.float32 else torch.bfloat16, (T, n))
     c.done()
     if out is None:
-        out = torch.empty((T, n), dtype=out_dtype, device=dev)
+        out = torch.empty(T, n, dtype=out_dtype, device=dev)
     ws = _workspace(OP_DECODE_DOWN, T, n, workspace, dev, k)
     _call("moe_decode_down", dev, fmt, T, k, experts, n, K, _ptr(h), _ptr(topk_idx), _ptr(weights), _ptr(W), _ptr(sW),
           _ptr(tW), SCOPE[t_scope], _ptr(out), OUT_F32 if out.dtype == torch.float32 else OUT_BF16, _ptr(ws), ws.numel())
@@ -988,11 +989,14 @@ def _need_gate(c, gate, gate_mode: str, name: str, rows: int, cols: int) -> int:
     return mode
 
 
+_NOTHING = torch.empty(0, dtype=torch.uint8)              # NULL, no bytes: spares an allocation a call
+
+
 def _workspace(op: int, a: int, b: int, workspace, dev, c: int = 0):
     """The call's scratch: allocated here, or the caller's, checked for size and device."""
     need = lib().mxq_workspace_bytes(op, a, b, c)
     if workspace is None:
-        return _u8((need,), dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else _NOTHING
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError(f"workspace: expected contiguous uint8 memory on {dev}")
     if workspace.numel() < need:
