@@ -801,7 +801,8 @@ mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_
  *              transposed as grouped_gemm_block_scaled reads it; inter % 16 == 0,
  *              K inter / 2 < 2^31). A: BF16 (total, K); the other tensors as gemm_swiglu_backward's,
  *              `total` rows. sB and tB are unused with MXQ_BF16.
- *   workspace: mxq_workspace_bytes(MXQ_OP_GROUPED_GEMM, groups, 0, 0) bytes, 16-byte aligned.
+ *   workspace: mxq_workspace_bytes(MXQ_OP_GROUPED_SWIGLU, groups, 0, 0) bytes, 16-byte aligned; NULL where
+ *             that is 0 (up to 256 groups).
  * ------------------------------------------------------------------------- */
 mxq_status grouped_gemm_swiglu(mxq_format fmt, int64_t groups, const int64_t* offsets, int64_t total, int64_t inter,
                                int64_t K, const int32_t* a_row_index, int64_t a_rows, const void* A, const void* sA,
@@ -866,14 +867,15 @@ mxq_status moe_decode_down(mxq_format fmt, int64_t tokens, int64_t topk, int64_t
 size_t mxq_scale_bytes(mxq_format fmt, int64_t rows, int64_t cols);
 
 enum { MXQ_OP_QUANTIZE_NVFP4 = 1, MXQ_OP_GROUPED_GEMM = 2, MXQ_OP_NORM_BACKWARD = 3, MXQ_OP_ROUTE = 4,
-       MXQ_OP_DECODE_DOWN = 5, MXQ_OP_GEMM_SWIGLU = 6 };
+       MXQ_OP_DECODE_DOWN = 5, MXQ_OP_GEMM_SWIGLU = 6, MXQ_OP_GROUPED_SWIGLU = 7 };
 /* Workspace bytes for an op:
  *   MXQ_OP_QUANTIZE_NVFP4 (a = rows, b = cols, c = number of FP32 scales);
  *   MXQ_OP_GROUPED_GEMM   (a = groups);
  *   MXQ_OP_NORM_BACKWARD  (a = rows, b = cols);
  *   MXQ_OP_ROUTE          (a = tokens, b = experts);
  *   MXQ_OP_DECODE_DOWN    (a = tokens, b = hidden, c = topk);
- *   MXQ_OP_GEMM_SWIGLU    (a = M, b = columns of the product: 2 inter forward, inter backward; c = K). */
+ *   MXQ_OP_GEMM_SWIGLU    (a = M, b = columns of the product: 2 inter forward, inter backward; c = K);
+ *   MXQ_OP_GROUPED_SWIGLU (a = groups). */
 size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c);
 
 /* Slots that hold every routing of `tokens` tokens over `experts` experts, topk each, with

@@ -25,6 +25,7 @@ _PACKED4 = (NVFP4, MXFP4)          # formats with two elements per byte
 OUT_BF16, OUT_F32 = 0, 1
 SCOPE = {"row": 0, "token": 0, "tensor": 1, "group": 2}
 OP_QUANTIZE_NVFP4, OP_GROUPED_GEMM, OP_NORM_BACKWARD, OP_ROUTE, OP_DECODE_DOWN, OP_GEMM_SWIGLU = 1, 2, 3, 4, 5, 6
+OP_GROUPED_SWIGLU = 7
 GATE = {"none": 0, "token": 1, "channel": 2, "full": 3}
 
 _c_void_p = ctypes.c_void_p
@@ -812,7 +813,7 @@ def grouped_gemm_swiglu(fmt: int, offsets, A, B, inter: int, K: int, sA=None, sB
     dev, groups = A.device, offsets.numel() - 1
     c = _Checks(dev)
     h, gate_up = _gated_out(c, out, ("h", "gate_up"), total, inter, keep_gate_up, dev)
-    ws = _workspace(OP_GROUPED_GEMM, groups, 0, workspace, dev)
+    ws = _workspace(OP_GROUPED_SWIGLU, groups, 0, workspace, dev)
     _call("grouped_gemm_swiglu", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(a_row_index),
           A.shape[0] if a_row_index is not None else 0, _ptr(A), _ptr(sA), _ptr(tA), SCOPE[tA_scope], _ptr(B), _ptr(sB),
           _ptr(tB), SCOPE[tB_scope], _ptr(h), _ptr(gate_up), _ptr(ws), ws.numel())
@@ -835,7 +836,7 @@ def grouped_gemm_swiglu_backward(fmt: int, offsets, A, B, inter: int, K: int, ga
     c = _Checks(dev)
     c.need(gate_up, "gate_up", gate_up.dtype, (total, 2 * inter))
     d_gate_up, h = _gated_out(c, out, ("d_gate_up", "h"), total, inter, keep_h, dev)
-    ws = _workspace(OP_GROUPED_GEMM, groups, 0, workspace, dev)
+    ws = _workspace(OP_GROUPED_SWIGLU, groups, 0, workspace, dev)
     _call("grouped_gemm_swiglu_backward", dev, fmt, groups, _ptr(offsets), total, inter, K, _ptr(A), _ptr(B), _ptr(sB),
           _ptr(tB), _ptr(gate_up), gd, _ptr(d_gate_up), _ptr(h), _ptr(ws), ws.numel())
     return d_gate_up, h

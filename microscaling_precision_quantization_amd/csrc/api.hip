@@ -89,6 +89,7 @@ hipError_t launch_decode_down(int fmt, int64_t tokens, int64_t topk, int64_t exp
                               const int32_t* idx, const float* weights, const void* w, const void* s, const float* t,
                               int t_mode, void* y, int out32, void* ws, hipStream_t st);
 size_t decode_down_ws_bytes(int64_t choices, int64_t n);
+size_t gated_grouped_ws_bytes(int64_t groups);
 }  // namespace mxq
 
 namespace {
@@ -154,6 +155,7 @@ size_t mxq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c) {
   if (op == MXQ_OP_NORM_BACKWARD) return a > 0 && b > 0 ? mxq::norm_backward_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_ROUTE) return a > 0 && b > 0 ? mxq::route_ws_bytes(a, b) : 0;
   if (op == MXQ_OP_GEMM_SWIGLU) return a > 0 && b > 0 && c > 0 ? mxq::gated_ws_bytes(a, b, c) : 0;
+  if (op == MXQ_OP_GROUPED_SWIGLU) return a > 0 ? mxq::gated_grouped_ws_bytes(a) : 0;
   if (op == MXQ_OP_DECODE_DOWN) return a > 0 && b > 0 && c > 0 ? mxq::decode_down_ws_bytes(a * c, b) : 0;
   return 0;
 }
@@ -843,9 +845,8 @@ bool tiles_fit(int64_t rows, int64_t n, int64_t groups) {
   return tm <= kMaxGridTiles && tn <= kMaxGridTiles && tm * tn + 8 <= kMaxGridTiles;
 }
 
-// The dense ones' scratch: none for most sizes.
-mxq_status gated_workspace(int64_t M, int64_t n, int64_t K, void* workspace, size_t bytes) {
-  const size_t need = mxq::gated_ws_bytes(M, n, K);
+// Scratch that most sizes do not need.
+mxq_status workspace_for(size_t need, const void* workspace, size_t bytes) {
   if (need == 0) return MXQ_OK;
   if (!workspace || bytes < need) return MXQ_ERR_WORKSPACE;
   return al16(workspace) ? MXQ_OK : MXQ_ERR_ALIGN;
@@ -884,7 +885,7 @@ mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, cons
   if (st != MXQ_OK) return st;
   if (!tiles_fit(M, 2 * inter, 0)) return MXQ_ERR_SHAPE;
   if (!al16(h) || !al16(gate_up)) return MXQ_ERR_ALIGN;
-  const mxq_status ws = gated_workspace(M, 2 * inter, K, workspace, workspace_bytes);
+  const mxq_status ws = workspace_for(mxq::gated_ws_bytes(M, 2 * inter, K), workspace, workspace_bytes);
   if (ws != MXQ_OK) return ws;
   return hip_status(mxq::launch_gemm_swiglu((int)fmt, M, inter, K, A, sA, tA, ta, B, sB, tB, tb, h, gate_up, workspace,
                                             S(stream)));
@@ -901,7 +902,7 @@ mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_
   if (st != MXQ_OK) return st;
   if (!tiles_fit(M, inter, 0)) return MXQ_ERR_SHAPE;
   if (!al16(gate_up) || !al16(d_gate_up) || !al16(h)) return MXQ_ERR_ALIGN;
-  const mxq_status ws = gated_workspace(M, inter, K, workspace, workspace_bytes);
+  const mxq_status ws = workspace_for(mxq::gated_ws_bytes(M, inter, K), workspace, workspace_bytes);
   if (ws != MXQ_OK) return ws;
   return hip_status(mxq::launch_gemm_swiglu_backward((int)fmt, M, inter, K, A, sA, B, sB, gate_up,
                                                      gu_dtype == MXQ_OUT_F32, d_gate_up, h, workspace, S(stream)));
@@ -929,8 +930,8 @@ mxq_status grouped_gemm_swiglu(mxq_format fmt, int64_t groups, const int64_t* of
   if (a_row_index && K > 0 && a_rows > 0x7FFFFFFF / gemm_row_bytes(fmt, K)) return MXQ_ERR_SHAPE;
   if (!tiles_fit(total, 2 * inter, groups)) return MXQ_ERR_SHAPE;
   if (!al8(offsets) || !al4(a_row_index) || !al16(h) || !al16(gate_up)) return MXQ_ERR_ALIGN;
-  if (!workspace || workspace_bytes < mxq::grouped_gemm_ws_bytes(groups)) return MXQ_ERR_WORKSPACE;
-  if (!al16(workspace)) return MXQ_ERR_ALIGN;
+  const mxq_status ws = workspace_for(mxq::gated_grouped_ws_bytes(groups), workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
   return hip_status(mxq::launch_grouped_gemm_swiglu((int)fmt, groups, offsets, total, inter, K, a_row_index,
                                                     a_row_index ? a_rows : total, A, sA, tA, ta, B, sB, tB, tb, h,
                                                     gate_up, workspace, S(stream)));
@@ -950,8 +951,8 @@ mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const in
   if (!tiles_fit(total, inter, groups)) return MXQ_ERR_SHAPE;
   if (!al8(offsets) || !al16(gate_up) || !al16(d_gate_up) || !al16(h) || (fmt == MXQ_BF16_NVFP4T && !al4(tB)))
     return MXQ_ERR_ALIGN;
-  if (!workspace || workspace_bytes < mxq::grouped_gemm_ws_bytes(groups)) return MXQ_ERR_WORKSPACE;
-  if (!al16(workspace)) return MXQ_ERR_ALIGN;
+  const mxq_status ws = workspace_for(mxq::gated_grouped_ws_bytes(groups), workspace, workspace_bytes);
+  if (ws != MXQ_OK) return ws;
   return hip_status(mxq::launch_grouped_gemm_swiglu_backward(fmt == MXQ_BF16 ? 3 : 7, groups, offsets, total, inter, K, A, B,
                                                              sB, tB, gate_up, gu_dtype == MXQ_OUT_F32, d_gate_up, h,
                                                              workspace, S(stream)));

@@ -14,6 +14,8 @@ namespace mxq {
 void launch_tile_prefix(const int64_t* offsets, int64_t groups, int64_t total, int64_t bm, int64_t tiles_n, int64_t* prefix,
                         hipStream_t st);
 
+size_t grouped_gemm_ws_bytes(int64_t groups);
+
 template <int LD, int BN> constexpr bool kShort = LD == 0 && BN == 256;
 
 // h columns of a tile
@@ -30,30 +32,94 @@ gated_dense_kernel(ExactProblem p, GatedArgs ga, int64_t tiles_m, int64_t tiles_
                                                                                lds2, lds3, ldsc, ga);
 }
 
+// Up to kScanGroups groups are looked through by every wave, four a lane, so that no kernel has to run before to
+// lay out the tiles (MXQ-SCAN).
+constexpr int64_t kScanGroups = 256;
+struct GroupTile {
+  int64_t g, local, tiles_m, first_row, rows;
+};
+// The tile's group, its place in it and the group's rows; false: offsets that do not fit (no tile runs), or no tile.
+// Tiles in XCD order: dispatch order b goes to XCD b % 8, and each XCD takes a contiguous run of the tiles.
+template <int BM>
+__device__ __forceinline__ bool scan_groups(const int64_t* __restrict__ offsets, int64_t groups, int64_t rows,
+                                            int64_t tiles_n, GroupTile& at) {
+  const int lane = threadIdx.x & 63;
+  int64_t o[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) o[i] = offsets[min((int64_t)(4 * lane + i), groups)];
+  bool bad = (lane == 0 && o[0] != 0) || (lane == 63 && o[4] != rows);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad = bad || o[i + 1] < o[i];
+  if (__ballot(bad)) return false;
+  int n[4], sum = 0;                                      // row tiles: of all groups below 2^31
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum += n[i] = (int)((o[i + 1] - o[i] + BM - 1) / BM);
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += v;
+  }
+  const int64_t total = __builtin_amdgcn_readlane(upto, 63) * tiles_n, T8 = (total + 7) / 8;
+  if ((int64_t)blockIdx.x >= 8 * T8) return false;        // the grid may exceed the tile count
+  const int64_t tile = (int64_t)blockIdx.x % 8 * T8 + blockIdx.x / 8;
+  if (tile >= total) return false;
+  const int src = __builtin_ctzll(__ballot(tile < upto * tiles_n));
+  int64_t local = tile - __builtin_amdgcn_readlane(upto - sum, src) * tiles_n;
+  int i = 0;
+  int64_t tiles_m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {                           // among the lane's four
+    const int64_t t = __builtin_amdgcn_readlane(n[j], src);
+    if (i == j) {
+      tiles_m = t;
+      if (local >= t * tiles_n) {
+        local -= t * tiles_n;
+        ++i;
+      }
+    }
+  }
+  at.g = 4 * src + i;
+  at.local = local;
+  at.tiles_m = tiles_m;
+  at.first_row = offsets[at.g];
+  at.rows = offsets[at.g + 1] - at.first_row;
+  return true;
+}
+
 // Per expert: group g covers the slots [offsets[g], offsets[g + 1]); tile order as in
 // exact_grouped_kernel (each XCD a contiguous run, bands of row tiles down a weight slab).
+// tile_prefix: NULL up to kScanGroups groups.
 constexpr int kGatedBand = 4;
 template <int LD, int BM, int BN, int SM, int OCC, int EPI>
 __global__ void __launch_bounds__(256, OCC) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 gated_grouped_kernel(ExactProblem base, GatedArgs ga, const int64_t* __restrict__ offsets,
-                     const int64_t* __restrict__ tile_prefix, int64_t groups, int64_t tiles_n) {
+                     const int64_t* __restrict__ tile_prefix, int64_t groups, int64_t rows, int64_t tiles_n) {
   using C = gx::Cfg<LD, BM, BN, SM, OCC, false, EPI>;
   MXQ_EXACT_LDS(C)
-  const int64_t total = tile_prefix[groups];
-  const int64_t T8 = (total + 7) / 8;
-  if ((int64_t)blockIdx.x >= 8 * T8) return;              // the grid may exceed the tile count
-  const int64_t tile = (int64_t)blockIdx.x % 8 * T8 + blockIdx.x / 8;
-  if (tile >= total) return;
-  const int64_t g = find_group(tile_prefix, groups, tile);
-  const int64_t local = tile - tile_prefix[g];
-  const int64_t tiles_m = (tile_prefix[g + 1] - tile_prefix[g]) / tiles_n;
-  const int64_t band = local / (kGatedBand * tiles_n);
-  const int64_t rows_in_band = min((int64_t)kGatedBand, tiles_m - band * kGatedBand);
-  const int64_t idx = local - band * kGatedBand * tiles_n;
+  GroupTile at;
+  if (!tile_prefix) {
+    if (!scan_groups<BM>(offsets, groups, rows, tiles_n, at)) return;
+  } else {
+    const int64_t total = tile_prefix[groups];
+    const int64_t T8 = (total + 7) / 8;
+    if ((int64_t)blockIdx.x >= 8 * T8) return;            // the grid may exceed the tile count
+    const int64_t tile = (int64_t)blockIdx.x % 8 * T8 + blockIdx.x / 8;
+    if (tile >= total) return;
+    at.g = find_group(tile_prefix, groups, tile);
+    at.local = tile - tile_prefix[at.g];
+    at.tiles_m = (tile_prefix[at.g + 1] - tile_prefix[at.g]) / tiles_n;
+    at.first_row = offsets[at.g];
+    at.rows = offsets[at.g + 1] - at.first_row;
+  }
+  const int64_t g = at.g;
+  const int64_t band = at.local / (kGatedBand * tiles_n);
+  const int64_t rows_in_band = min((int64_t)kGatedBand, at.tiles_m - band * kGatedBand);
+  const int64_t idx = at.local - band * kGatedBand * tiles_n;
   const int64_t tm = band * kGatedBand + idx % rows_in_band, tn = idx / rows_in_band;
   ExactProblem p = base;
-  p.a_base = offsets[g];
-  p.m_valid = offsets[g + 1] - offsets[g];
+  p.a_base = at.first_row;
+  p.m_valid = at.rows;
   const int64_t n = EPI == 1 ? 2 * ga.inter : ga.inter;   // rows of the expert's B
   if constexpr (LD == 6) {                                // K rows of inter NVFP4 elements
     const int64_t w_elems = g * base.k_end * base.ldb;
@@ -79,6 +145,8 @@ gated_grouped_kernel(ExactProblem base, GatedArgs ga, const int64_t* __restrict_
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+
+size_t gated_grouped_ws_bytes(int64_t groups) { return groups <= kScanGroups ? 0 : grouped_gemm_ws_bytes(groups); }
 
 static ExactProblem gated_problem(int64_t rows, int64_t n, int64_t K, const void* A, const void* sA, const float* tA,
                                   int tA_mode, const void* B, const void* sB, const float* tB, int tB_mode) {
@@ -276,11 +344,12 @@ template <int LD, int BM, int BN, int SM, int OCC, int EPI>
 static void launch_gated_grouped_t(const ExactProblem& p, const GatedArgs& ga, const int64_t* offsets, int64_t groups,
                                    int64_t total, int64_t* prefix, hipStream_t st) {
   const int64_t tn = (ga.inter + kTileCols<BN, EPI> - 1) / kTileCols<BN, EPI>;
-  launch_tile_prefix(offsets, groups, total, BM, tn, prefix, st);
+  if (groups <= kScanGroups) prefix = nullptr;
+  else launch_tile_prefix(offsets, groups, total, BM, tn, prefix, st);
   // an upper bound on the tiles, a multiple of 8 so that the XCD order reaches every one
   const int64_t tiles = (((total + BM - 1) / BM + groups) * tn + 7) / 8 * 8;
   hipLaunchKernelGGL((gated_grouped_kernel<LD, BM, BN, SM, OCC, EPI>), dim3((unsigned)tiles), dim3(256), 0, st, p, ga,
-                     offsets, prefix, groups, tn);
+                     offsets, prefix, groups, total, tn);
 }
 
 template <int EPI>

@@ -62,7 +62,8 @@ def test_gemm_swiglu_backward_validation():
 
 
 def test_grouped_gemm_swiglu_validation():
-    need = B.lib().mxq_workspace_bytes(B.OP_GROUPED_GEMM, 3, 0, 0)
+    need = B.lib().mxq_workspace_bytes(B.OP_GROUPED_SWIGLU, 257, 0, 0)
+    assert need > 0 and B.lib().mxq_workspace_bytes(B.OP_GROUPED_SWIGLU, 256, 0, 0) == 0
 
     def f(fmt=B.NVFP4, G=3, off=P, total=8, I=16, K=64, idx=P, rows=8, A=P, sA=P, tA=P, ta=ROW, W=P, sB=P, tB=P, tb=GROUP,
           h=P, gu=P, ws=P, wsn=need):
@@ -80,11 +81,12 @@ def test_grouped_gemm_swiglu_validation():
     assert f(rows=BIG // 32) == 2 and f(fmt=B.BF16, rows=BIG // 128) == 2   # the gathered operand: 2^31 bytes
     assert f(I=1 << 25) == 2 and f(total=1 << 40) == 2 and f(G=1 << 40) == 2
     assert f(off=P + 4) == 3 and f(idx=P + 2) == 3 and f(h=MIS) == 3 and f(gu=MIS) == 3 and f(A=MIS) == 3 and f(W=MIS) == 3
-    assert f(ws=None) == 5 and f(wsn=need - 1) == 5 and f(ws=MIS) == 3
+    assert f(G=257, ws=None) == 5 and f(G=257, wsn=need - 1) == 5 and f(G=257, ws=MIS) == 3
 
 
 def test_grouped_gemm_swiglu_backward_validation():
-    need = B.lib().mxq_workspace_bytes(B.OP_GROUPED_GEMM, 3, 0, 0)
+    need = B.lib().mxq_workspace_bytes(B.OP_GROUPED_SWIGLU, 257, 0, 0)
+    assert need > 0 and B.lib().mxq_workspace_bytes(B.OP_GROUPED_SWIGLU, 256, 0, 0) == 0
 
     def f(fmt=B.BF16_NVFP4T, G=3, off=P, total=8, I=16, K=64, A=P, W=P, sB=P, tB=P, gu=P, gd=F32, d=P, h=P, ws=P,
           wsn=need):
@@ -100,7 +102,7 @@ def test_grouped_gemm_swiglu_backward_validation():
     assert f(I=24) == 2 and f(K=12) == 2 and f(I=1 << 20, K=1 << 12) == 2
     assert f(fmt=B.BF16, I=1 << 24) == 2 and f(total=1 << 40) == 2
     assert f(off=P + 4) == 3 and f(gu=MIS) == 3 and f(d=MIS) == 3 and f(h=MIS) == 3 and f(A=MIS) == 3 and f(tB=P + 2) == 3
-    assert f(ws=None) == 5 and f(wsn=need - 1) == 5 and f(ws=MIS) == 3
+    assert f(G=257, ws=None) == 5 and f(G=257, wsn=need - 1) == 5 and f(G=257, ws=MIS) == 3
 
 
 def test_gemv_validation():

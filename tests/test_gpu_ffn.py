@@ -248,13 +248,26 @@ def test_grouped_gemm_swiglu_backward_of_tall_experts(fmt, f32):
     test_grouped_gemm_swiglu_backward(fmt, 3088, 72, *TALL[0], f32)
 
 
-def test_rejected_offsets_leave_the_outputs_unwritten():
+@pytest.mark.parametrize("groups", [5, 64, 65, 255, 256, 257, 400])
+def test_many_groups(groups):
+    """Around the number of groups that a kernel looks through by itself; some empty, one of several tiles."""
+    g = torch.Generator().manual_seed(groups)
+    counts = torch.randint(0, 5, (groups,), generator=g).tolist()
+    counts[groups // 3] = 150
+    counts[-1] = groups % 2 * 3                             # the last one empty, or not
+    test_grouped_gemm_swiglu("bf16", 136, 40, counts, [0] * groups)
+    test_grouped_gemm_swiglu("nvfp4", 16, 32, counts, [0] * groups)
+    test_grouped_gemm_swiglu_backward("nvfp4", 272, 40, counts, [0] * groups, True)
+
+
+@pytest.mark.parametrize("groups", [2, 300])
+def test_rejected_offsets_leave_the_outputs_unwritten(groups):
     g = gen(8)
-    x, w = randn(g, 64, 64).to(BF), randn(g, 2 * 32, 64).to(BF)
-    for off in ([0, 40, 60], [0, 70, 64], [1, 30, 64]):
+    x, w = randn(g, 64, 64).to(BF), randn(g, groups * 32, 64).to(BF)
+    for off in ([0, 40, 60], [0, 70, 64], [1, 30, 64], [0, -8, 64]):
         h = torch.full((64, 16), 5.0, dtype=BF, device="cuda")
-        mxq.grouped_gemm_swiglu(B.BF16, torch.tensor(off, device="cuda"), x, w.view(2, 32, 64), inter=16, K=64, total=64,
-                                out=(h, None))
+        offsets = torch.tensor(off[:2] + off[2:] * (groups - 1), device="cuda")
+        mxq.grouped_gemm_swiglu(B.BF16, offsets, x, w.view(groups, 32, 64), inter=16, K=64, total=64, out=(h, None))
         assert bool((h == 5.0).all()), off
 
 
