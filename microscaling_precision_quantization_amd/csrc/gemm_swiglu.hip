@@ -33,7 +33,9 @@ gated_dense_kernel(ExactProblem p, GatedArgs ga, int64_t tiles_m, int64_t tiles_
 }
 
 // Up to kScanGroups groups are looked through by every wave, four a lane, so that no kernel has to run before to
-// lay out the tiles (MXQ-SCAN).
+// lay out the tiles: one load's latency and a scan over the lanes, against a launch and three loads in turn (BF16
+// 64 experts of 8 rows, 512 -> 2 x 128: 9.1 us against 11.4; 256 of 100, 512 -> 2 x 256: 36.7 against 40.0). More
+// groups would take more loads a lane; they get the prefix kernel of the plain grouped GEMMs.
 constexpr int64_t kScanGroups = 256;
 struct GroupTile {
   int64_t g, local, tiles_m, first_row, rows;
