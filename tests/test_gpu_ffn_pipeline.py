@@ -189,3 +189,18 @@ def test_decoding_step_of_an_expert_block(T):
         got = blk.out.clone()
         blk.forward(x, w_pre, w_r, w_post, gate, valid)
         assert torch.equal(blk.out, got)
+
+
+def test_decoding_on_the_weights_of_the_whole_block():
+    """The quantized weights that the block trains with serve the step: the same plan for the same tokens, and the
+    bits of a step on weights quantized on their own."""
+    c = Block(7, fused=True, through_swiglu=True)
+    c.step()
+    T, d = 40, c.x.device
+    own = {"gu": B.quantize_nvfp4(c.w_gu, scope="group", group_rows=2 * c.I), "d": B.quantize_nvfp4(c.w_d, scope="group", group_rows=c.H)}
+    outs = []
+    for wq in (c.b.moe.wq, own):
+        step = pipeline.MoeBlockDecodeNvfp4(T, c.H, c.G, c.I, c.K, d, wq, gate_mode="channel")
+        outs.append(step.forward(c.x[:T], c.w_pre, c.w_r, c.w_post, c.gate))
+        assert torch.equal(step.plan.topk_idx, c.b.plan.topk_idx[:T]) and torch.equal(step.plan.weights, c.b.plan.weights[:T])
+    assert torch.equal(*outs) and bool(torch.isfinite(outs[0]).all())
