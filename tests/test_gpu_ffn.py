@@ -248,6 +248,25 @@ def test_grouped_gemm_swiglu_backward_of_tall_experts(fmt, f32):
     test_grouped_gemm_swiglu_backward(fmt, 3088, 72, *TALL[0], f32)
 
 
+@pytest.mark.parametrize("tA_scope", ["row", "tensor"])
+def test_grouped_gemm_swiglu_with_a_scale_a_weight_row(tA_scope):
+    G, T, I, K = 3, 60, 72, 96
+    g = gen(12)
+    off, row = slots([20, 0, 37], [0, 3, 0], T, 3)
+    x, w = randn(g, T, K).to(BF), randn(g, G * 2 * I, K, scale=0.2).to(BF)
+    a, b = operand("nvfp4", x, tA_scope), mxq.quantize_nvfp4_per_token(w)
+    h, gu = mxq.grouped_gemm_swiglu(B.NVFP4, off, a[0], b[0], inter=I, K=K, sA=a[1], sB=b[1], tA=a[2], tB=b[2],
+                                    tA_scope=tA_scope, tB_scope="row", a_row_index=row, total=60, keep_gate_up=True)
+    xs = torch.where((row >= 0)[:, None], R.wide("nvfp4", *a)[row.long().clamp(min=0)], 0.0)
+    ws = R.wide("nvfp4", *b).view(G, 2 * I, K)
+    for e in range(G):
+        at = slice(int(off[e]), int(off[e + 1]))
+        y, err = R.product(xs[at], ws[e])
+        want, tol, gu_tol = R.gated(y, err)
+        R.check(gu[at], y, gu_tol, f"gate_up of expert {e}")
+        R.check(h[at], want, tol, f"h of expert {e}")
+
+
 @pytest.mark.parametrize("groups", [5, 64, 65, 255, 256, 257, 400])
 def test_many_groups(groups):
     """Around the number of groups that a kernel looks through by itself; some empty, one of several tiles."""
@@ -398,6 +417,31 @@ def test_moe_decode_down(fmt, T, k, E, N, K, dead, dtype):
     R.check(y, want, (1 + R.BF16) * tol + (R.half_step(want) if dtype == BF else 0.0), "y")
     end()
     assert torch.equal(mxq.moe_decode_down(FMT[fmt], h, idx, weights, q, s, t, experts=E, out_dtype=dtype), y)
+
+
+@pytest.mark.parametrize("T,k,E", [(3, 2, 5), (30, 3, 4)])
+def test_decoding_with_a_scale_a_weight_row(T, k, E):
+    """One FP32 scale a weight row, four choices at a time and 32; gemv_swiglu likewise. x inside a wider buffer."""
+    I, H = 40, 96
+    g = gen(T)
+    x, idx = randn(g, T, H + 8).to(BF)[:, :H], choices(T, k, E, 5, False)[0]
+    gu, d = (mxq.quantize_nvfp4_per_token(randn(g, E * n, c, scale=0.2).to(BF)) for n, c in ((2 * I, H), (H, I + 24)))
+    e = idx.long()
+    wide = R.wide("nvfp4", *gu).view(E, 2 * I, H)[e]
+    y = (wide @ x.double()[:, None, :, None]).squeeze(-1)
+    err = (R.SUM * H + 2 * R.F32) * (wide.abs() @ x.double().abs()[:, None, :, None]).squeeze(-1)
+    want, tol, _ = R.gated(y, err)
+    R.check(mxq.moe_decode_gate_up(B.NVFP4, x, idx, *gu, experts=E, t_scope="row"), want, tol, "h")
+    h, weights = randn(g, T, k, I + 24).to(BF), torch.rand((T, k), generator=g, device="cuda")
+    wide = R.wide("nvfp4", *d).view(E, H, I + 24)[e] * weights.double()[..., None, None]
+    want = (wide @ h.double()[..., None]).squeeze(-1).sum(1)
+    size = (wide.abs() @ h.double().abs()[..., None]).squeeze(-1).sum(1)
+    got = mxq.moe_decode_down(B.NVFP4, h, idx, weights, *d, experts=E, t_scope="row")
+    R.check(got, want, (R.SUM * (I + 24) + (k + 4) * R.F32) * size, "y")
+    one = tuple(v[:2 * I] for v in gu)
+    y, err = R.product(x.double(), R.wide("nvfp4", *one))
+    want, tol, _ = R.gated(y, err + 2 * R.F32 * y.abs())
+    R.check(mxq.gemv_swiglu(B.NVFP4, x, *one, t_scope="row"), want, tol, "gemv_swiglu")
 
 
 def test_a_token_that_names_an_expert_twice():
