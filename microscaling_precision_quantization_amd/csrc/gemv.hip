@@ -349,8 +349,8 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int f32) {
 }
 
 // TT column tiles hold all x rows. A workgroup has WV waves: KS of them share a tile's K, the others have tiles of
-// their own, RT each, and the same x at about the same time. The host has checked that the weights a descriptor
-// spans (gated: all 2 n rows from the tile on) stay below 2^31 bytes.
+// their own, RT each, and the same x at about the same time. The weights a descriptor spans (gated: all 2 n rows
+// from the tile on) are below 2^31 bytes: the dense calls refuse more, launch_choices sends it to gemv4_kernel.
 // A tile needs all of x, 2 rows bytes for every 8 of its weights' bytes: past 16 rows the reads of x out of the L2
 // are what takes the time (2048 x 7168 gated, 16 rows 12.8 us, 32 20.4, 64 33.8; the weights alone 3.1), below it
 // the latency of three loads in turn. AH: x ahead of the products along with the weights (32 rows 23.0 -> 20.4, 16 rows, 129280 x 7168 245 -> 205);
@@ -682,13 +682,16 @@ hipError_t launch_gemv(int fmt, int gated, int64_t rows, int64_t n, int64_t K, c
 // the other way 64 tokens, 2 of 8 experts, 2048 x 4096 take 90 / 49 us (gate_up / down) against 50 / 34, 8 of 64,
 // 768 x 2048 71 / 51 against 59 / 37, but with four an expert (8 of 128) 83 / 54 against 93 / 54. K in four
 // where there are few tiles: 64 tokens, 2 of 8, in two 62 / 40; 4 of 32, 1024 x 4096, down in four 50, in two 45.
+// Gated experts of 2^31 bytes and more go four by four whatever their choices: an up row lies too far behind its gate.
 template <bool GATED>
 static void launch_choices(int fmt, const GemvArgs& a, hipStream_t st) {
   const int64_t S = a.rows, by_choice = S < a.experts, each = by_choice ? S : a.experts;
   const int64_t tiles = (a.n + kTileOut<GATED> - 1) / kTileOut<GATED>;
+  // gates and ups behind one descriptor (gemv_kernel) or one of eight rows each
+  const bool one_descriptor = !GATED || a.n <= 0x7FFFFFFF / a.K;
   by_format(fmt, [&](auto F) {
     constexpr int FMT = decltype(F)::value;
-    if (S >= 6 * a.experts) {
+    if (S >= 6 * a.experts && one_descriptor) {
       auto many = [&](auto KSC) {
         constexpr int KS = decltype(KSC)::value, PER = 8 / KS * 2;
         hipLaunchKernelGGL((gemv_kernel<FMT, GATED, 2, 2, KS, 8, true>),
