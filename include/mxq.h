@@ -823,7 +823,8 @@ mxq_status grouped_gemm_swiglu_backward(mxq_format fmt, int64_t groups, const in
  *   Defined by: NVFP4 weights moving through memory can bind harder than arithmetic (remio.ai,
  *   section "NVFP4 por token ..."); MXFP4: 7minutos.es, section "NVFP4 frente a MXFP4".
  *   fmt : MXQ_NVFP4 (tW: TENSOR or ROW) or MXQ_MXFP4 (tW unused; scale codes s <= 252).
- *   x   : BF16 (rows, K), row stride ld_x (a multiple of 8);  W (N, K/2), sW (N, K/16 or K/32).
+ *   x   : BF16 (rows, K), row stride ld_x >= K (a multiple of 8; any for a single row);  W (N, K/2),
+ *         sW (N, K/16 or K/32).
  *   y   : (rows, N) y_dtype, row stride ld_y >= N;  h: BF16 (rows, inter), row stride ld_h >= inter.
  *   Requires rows <= 64 (more rows are the GEMMs'), K % 32 == 0, 32 <= K <= 2^22, inter K < 2^31, x below
  *   2^31 bytes from its first row to its last; x and W 16-byte aligned, NVFP4 scales 2-byte aligned.
@@ -843,7 +844,7 @@ mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, c
  *   down    : y[t, :] = sum over j of weights[t, j] (h[t, j] W_e^T), sums FP32, y_dtype (tokens, hidden).
  *   topk_idx, weights: (tokens, topk) int32 and FP32, as moe_route writes them. A choice outside
  *   [0, experts) is none: zeros in h, nothing in y (its h and weight are not read).
- *   x: BF16 (tokens, K), row stride ld_x;  h of the down call: BF16 (tokens, topk, K), contiguous.
+ *   x: BF16 (tokens, K), row stride ld_x as there;  h of the down call: BF16 (tokens, topk, K), contiguous.
  *   W : the experts' (2 inter, K) or (hidden, K) stacked;  fmt MXQ_NVFP4 (tW GROUP -- one an expert --
  *   or ROW) or MXQ_MXFP4.
  *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled; x (or h) below

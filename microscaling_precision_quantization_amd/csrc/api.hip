@@ -970,7 +970,7 @@ mxq_status gemv_check(mxq_format fmt, int64_t rows, int64_t K, const void* x, in
   if (fmt == MXQ_NVFP4 && scope != MXQ_SCOPE_ROW && scope != wide) return MXQ_ERR_FORMAT;
   if (K < 32 || K % 32 || K > kMaxGemmK || ld_x < K) return MXQ_ERR_SHAPE;
   if (rows > 1 && ld_x > (0x7FFFFFFF / 2 - K) / (rows - 1)) return MXQ_ERR_SHAPE;    // 32-bit offsets into x
-  if (ld_x % 8 || !al16(x) || !al16(w) || (fmt == MXQ_NVFP4 && ((reinterpret_cast<uintptr_t>(s) & 1u) || !al4(t))))
+  if ((rows > 1 && ld_x % 8) || !al16(x) || !al16(w) || (fmt == MXQ_NVFP4 && ((reinterpret_cast<uintptr_t>(s) & 1u) || !al4(t))))
     return MXQ_ERR_ALIGN;
   return MXQ_OK;
 }

@@ -204,3 +204,14 @@ def test_binding_refuses_what_does_not_fit():
     bad(B.moe_decode_down, B.NVFP4, h, idx, wt, q, s, t2, experts=2, out_dtype=torch.int32)
     bad(B.moe_decode_down, B.NVFP4, h, idx, wt, q, s, t2, experts=2, out=e(4, 15))
     bad(B.moe_decode_down, B.NVFP4, h, idx, wt, q, s, t2, experts=2)        # not on a GPU
+
+
+def test_a_single_row_may_have_any_stride():
+    """One row: nothing is addressed by its stride (the output's stride, looked at afterwards, is what is refused)."""
+    def f(fn, rows, ld, ldy):
+        tail = (F32, ldy, None) if fn == "gemv_block_scaled" else (ldy, None)
+        return getattr(B.lib(), fn)(B.NVFP4, rows, 16, 64, P, ld, P, P, P, TENSOR, P, *tail)
+
+    for fn in ("gemv_block_scaled", "gemv_swiglu"):
+        assert f(fn, 2, 68, 8) == 3 and f(fn, 1, 68, 8) == 2 and f(fn, 1, (1 << 40) + 1, 8) == 2
+        assert f(fn, 1, 63, 16) == 2                                        # a row stride below the row

@@ -1,5 +1,5 @@
 """Edges of the gated feed-forward block and of the 4-bit matrix-vector products on the GPU: expert weights
-past 32-bit offsets."""
+past 32-bit offsets, a single row out of a buffer of any width."""
 
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 import microscaling_precision_quantization_amd as mxq
 from microscaling_precision_quantization_amd import binding as B
 from tests import ffn_ref as R
-from tests.test_gpu_ffn import BF, gen, randn
+from tests.test_gpu_ffn import BF, FMT, gen, randn, weights4
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,26 @@ def test_decode_gate_up_of_an_expert_past_32_bits(tokens, I, K):
         y = x.double() @ R.wide("mxfp4", q[rows], s[rows]).T
         want, tol, _ = R.gated(y, torch.zeros_like(y))
         R.check(h[:, lo:lo + 40], want, tol, f"h from column {lo}")
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_a_single_row_of_a_buffer_of_any_width(fmt):
+    """One token's row: no second row is addressed, so the buffer's width does not matter."""
+    K, I, E = 96, 40, 3
+    g = gen(1)
+    x = randn(g, 5, K + 3).to(BF)[:1, :K]
+    assert x.stride(0) % 8
+    w = randn(g, E * 2 * I, K, scale=0.2).to(BF)
+    q, s, t = weights4(fmt, w, E)
+    one = weights4(fmt, w[:2 * I])
+    y, err = R.product(x.double(), R.wide(fmt, *one))
+    R.check(mxq.gemv_block_scaled(FMT[fmt], x, *one), y, err + 2 * R.F32 * y.abs(), "y")
+    want, tol, _ = R.gated(y, err + 2 * R.F32 * y.abs())
+    R.check(mxq.gemv_swiglu(FMT[fmt], x, *one), want, tol, "h")
+    for e in range(E):
+        idx = torch.full((1, 1), e, dtype=torch.int32, device="cuda")
+        got = mxq.moe_decode_gate_up(FMT[fmt], x, idx, q, s, t, experts=E)[:, 0]
+        at = slice(e * 2 * I, (e + 1) * 2 * I)
+        y, err = R.product(x.double(), R.wide(fmt, q[at], s[at], None if t is None else t[e:e + 1]))
+        want, tol, _ = R.gated(y, err + 2 * R.F32 * y.abs())
+        R.check(got, want, tol, f"h of expert {e}")
