@@ -847,8 +847,8 @@ mxq_status gemv_swiglu(mxq_format fmt, int64_t rows, int64_t inter, int64_t K, c
  *   x: BF16 (tokens, K), row stride ld_x as there;  h of the down call: BF16 (tokens, topk, K), contiguous.
  *   W : the experts' (2 inter, K) or (hidden, K) stacked;  fmt MXQ_NVFP4 (tW GROUP -- one an expert --
  *   or ROW) or MXQ_MXFP4.
- *   Requires tokens <= 64, topk <= 32, experts <= 1024, K and alignment as gemv_block_scaled; x (or h) below
- *   2^31 bytes from its first row to its last.
+ *   Requires tokens <= 64, topk <= 32, experts <= 1024, inter (or hidden) <= 65520, K and alignment as
+ *   gemv_block_scaled; x (or h) below 2^31 bytes from its first row to its last.
  *   workspace (down): mxq_workspace_bytes(MXQ_OP_DECODE_DOWN, tokens, hidden, topk) bytes, 4-byte aligned.
  *   Calls that may overlap need their own.
  * ------------------------------------------------------------------------- */

@@ -917,7 +917,7 @@ def _stacked(W, experts: int) -> int:
 def moe_decode_gate_up(fmt: int, x, topk_idx, W, sW, tW=None, experts: int = 0, t_scope: str = "group", out=None):
     """h (tokens, topk, inter) BF16 of a decoding step: each token (x (tokens <= 64, K) BF16, rows may be
     strided) through gate_up and SwiGLU of the experts topk_idx (tokens, topk) int32 names; zeros for a
-    choice of -1. W: (experts 2 inter, K/2), NVFP4 or MXFP4, as quantize_nvfp4(scope="group") and
+    choice of -1. W: (experts 2 inter, K/2), inter <= 65520, NVFP4 or MXFP4, as quantize_nvfp4(scope="group") and
     quantize_mxfp4 store the stacked weights."""
     T, K = _decode_rows(x, "x", 2)
     n = _stacked(W, experts)
@@ -942,7 +942,7 @@ def moe_decode_down(fmt: int, h, topk_idx, weights, W, sW, tW=None, experts: int
                     out_dtype: torch.dtype = torch.float32, out=None, workspace=None):
     """y (tokens, hidden) = sum over j of weights[t, j] (h[t, j] W_hat_e^T), FP32 or BF16 (`out`'s type where
     given): the down projection and the combine of a decoding step. h (tokens, topk, inter) BF16 as
-    moe_decode_gate_up gives it, W: (experts hidden, inter / 2)."""
+    moe_decode_gate_up gives it, W: (experts hidden, inter / 2), hidden <= 65520."""
     T, k, K = _decode_rows(h, "h", 3)
     n = _stacked(W, experts)
     if out is None and out_dtype not in (torch.float32, torch.bfloat16):

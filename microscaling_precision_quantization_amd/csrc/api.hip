@@ -104,6 +104,9 @@ constexpr int64_t kMaxGemmK = int64_t(1) << 22;
 constexpr int64_t kMaxGridTiles = (int64_t(1) << 24) - 1;   // of 256 threads: a grid holds fewer than 2^32
 constexpr int64_t kMaxInter = int64_t(1) << 22;              // 32 rows of (g | u) within 32-bit offsets
 constexpr int64_t kMaxDecodeRows = 64;                       // rows of a matrix-vector product
+// inter and hidden of the products over experts: their grid is (tiles of 8 or 16 columns, experts) workgroups of up
+// to 512 threads, and 65520 / 8 tiles x 1024 experts x 512 is the most that stays below 2^32 threads
+constexpr int64_t kMaxDecodeCols = 65520;
 inline int64_t gemm_row_bytes(mxq_format fmt, int64_t k) {
   return fmt == MXQ_BF16 ? 2 * k : fmt == MXQ_MXFP8 ? k : k / 2;   // NVFP4, MXFP4: two per byte
 }
@@ -994,7 +997,7 @@ mxq_status gemv_any(mxq_format fmt, int gated, int64_t rows, int64_t n, int64_t 
 // The sizes of the two decode calls over experts; `n` product rows.
 bool decode_sizes(int64_t tokens, int64_t topk, int64_t experts, int64_t n) {
   return tokens >= 0 && tokens <= kMaxDecodeRows && topk >= 0 && topk <= kMaxTopk && experts >= 0 &&
-         experts <= kMaxExperts && n >= 0 && (n + 15) / 16 <= kMaxGridTiles / 4096;
+         experts <= kMaxExperts && n >= 0 && n <= kMaxDecodeCols;
 }
 }  // namespace
 

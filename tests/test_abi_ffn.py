@@ -215,3 +215,15 @@ def test_a_single_row_may_have_any_stride():
     for fn in ("gemv_block_scaled", "gemv_swiglu"):
         assert f(fn, 2, 68, 8) == 3 and f(fn, 1, 68, 8) == 2 and f(fn, 1, (1 << 40) + 1, 8) == 2
         assert f(fn, 1, 63, 16) == 2                                        # a row stride below the row
+
+
+def test_moe_decode_width_limit():
+    """inter and hidden up to 65520: beyond it the size is what is refused, up to it the pointer."""
+    def gate_up(n):
+        return B.lib().moe_decode_gate_up(B.MXFP4, 4, 2, 8, n, 64, P, 64, P + 2, P, P, None, GROUP, P, None)
+
+    def down(n):
+        return B.lib().moe_decode_down(B.MXFP4, 4, 2, 8, n, 64, P, P + 2, P, P, P, None, GROUP, P, F32, P, 1 << 30, None)
+
+    for f in (gate_up, down):
+        assert f(65520) == 3 and f(65521) == 2 and f(65536) == 2
