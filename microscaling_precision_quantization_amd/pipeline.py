@@ -283,7 +283,8 @@ class MoeDequantBackward:
     dgrad GEMMs vary M per expert; wgrad GEMMs vary K (the slots). The dgrads read the
     forward's NVFP4 expert weights directly (fused_weights: the GEMM loader builds the
     transposed BF16 dequantization, the BF16_NVFP4T format); with fused_weights=False
-    they read BF16 transposes written by dequantize_transposed first. The wgrads read dO and
+    they read BF16 transposes, which dequantize_weights writes: to be called before the first backward
+    (which is refused without it) and again whenever the weights change. The wgrads read dO and
     dGU as they are (slot-major, K-major A, vary_k=2); their other operands, the NVFP4
     activations, are dequantized into K-contiguous BF16 transposes by dequantize_transposed.
     Every expert's slots begin at a multiple of 8 (16 bytes of BF16 along K)."""
@@ -297,6 +298,7 @@ class MoeDequantBackward:
         dev, G, H, I, S = f.dev, f.G, f.H, f.I, f.S
         self.f = f
         self.fused = fused_weights
+        self.have_weights = fused_weights          # transposes, where they are read
         if not fused_weights:
             self.w_dT = _bf16((G, I, H), dev)      # W_hat_d,g^T
             self.w_guT = _bf16((G, H, 2 * I), dev) # W_hat_gu,g^T
@@ -321,6 +323,11 @@ class MoeDequantBackward:
         qw, sw, tw = f.wq["gu"]
         B.dequantize_transposed(B.NVFP4, qw, sw, tw, t_scope="group", groups=f.G, group_rows=2 * f.I, cols=f.H,
                                 out=self.w_guT)
+        self.have_weights = True
+
+    def _need_weights(self):
+        if not self.have_weights:
+            raise ValueError("fused_weights=False: dequantize_weights() has not been called")
 
     def dequantize_activations(self, d_o, d_gu):                   # A6 + layout for wgrad
         f = self.f
@@ -330,6 +337,7 @@ class MoeDequantBackward:
                                 src_row=f.r.row_index, out_cols=f.S, out=self.xT)
 
     def gemms(self, d_o, d_gu):                                    # A13
+        self._need_weights()
         f = self.f
         off = f.r.offsets
         if d_gu is self.d_gu:
@@ -357,6 +365,7 @@ class MoeDequantBackward:
         """dGU from dO: the down dgrad with the gradient of SwiGLU behind it."""
         if self.d_gu is None:
             raise ValueError("d_gu: not given, and the backward was not made with through_swiglu=True")
+        self._need_weights()
         f = self.f
         if self.fused:
             qw, sw, tw = f.wq["d"]
