@@ -1,5 +1,6 @@
 """Edges of the gated feed-forward block and of the 4-bit matrix-vector products on the GPU: expert weights
-past 32-bit offsets, a single row out of a buffer of any width, the backward against BF16 weight transposes."""
+past 32-bit offsets, a single row out of a buffer of any width, sums over no K, the backward against BF16 weight
+transposes."""
 
 import pytest
 import torch
@@ -59,6 +60,47 @@ def test_a_single_row_of_a_buffer_of_any_width(fmt):
         y, err = R.product(x.double(), R.wide(fmt, q[at], s[at], None if t is None else t[e:e + 1]))
         want, tol, _ = R.gated(y, err + 2 * R.F32 * y.abs())
         R.check(got, want, tol, f"h of expert {e}")
+
+
+def k0_call(fn, dev, *args):
+    B._call(fn, dev, *args)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M,I", [(5, 24), (300, 272), (2601, 2416)])
+def test_sums_over_no_k(M, I):
+    """K = 0: h, (g | u) and dGU are zeros, h made again is silu(g) u. A call that hands buffers in, of which
+    nothing is read."""
+    buf = torch.full((4096,), float("nan"), dtype=BF, device="cuda")
+    one = torch.ones(max(M, 2 * I), device="cuda")
+    p, dev = buf.data_ptr(), buf.device
+    off = torch.tensor([0, 0, M // 2, M], device="cuda")
+    t = one.data_ptr()
+    gu = randn(gen(M), M, 2 * I).to(BF)
+    (_, _), (hw, htol) = R.through(torch.zeros(M, I, dtype=torch.float64, device="cuda"), 0.0, gu)
+    new = lambda n: torch.full((M, n), float("nan"), dtype=BF, device="cuda")
+    for fmt in (B.BF16, B.MXFP8, B.NVFP4):
+        h, y = new(I), new(2 * I)
+        k0_call("gemm_swiglu", dev, fmt, M, I, 0, p, p, t, 0, p, p, t, 1, h.data_ptr(), y.data_ptr(), None, 0)
+        assert bool((h == 0).all()) and bool((y == 0).all()), fmt
+    for fmt in (B.BF16, B.MXFP8):
+        d, h = new(2 * I), new(I)
+        k0_call("gemm_swiglu_backward", dev, fmt, M, I, 0, p, p, p, p, gu.data_ptr(), 0, d.data_ptr(), h.data_ptr(), None, 0)
+        assert bool((d == 0).all()), fmt
+        R.check(h, hw, htol, "h")
+    for fmt in (B.BF16, B.NVFP4):
+        h, y = new(I), new(2 * I)
+        k0_call("grouped_gemm_swiglu", dev, fmt, 3, off.data_ptr(), M, I, 0, None, 0, p, p, t, 0, p, p, t, 2, h.data_ptr(),
+                y.data_ptr(), None, 0)
+        assert bool((h == 0).all()) and bool((y == 0).all()), fmt
+    for fmt in (B.BF16, B.BF16_NVFP4T):
+        if fmt == B.BF16_NVFP4T and I % 16:
+            continue
+        d, h = new(2 * I), new(I)
+        k0_call("grouped_gemm_swiglu_backward", dev, fmt, 3, off.data_ptr(), M, I, 0, p, p, p, t, gu.data_ptr(), 0,
+                d.data_ptr(), h.data_ptr(), None, 0)
+        assert bool((d == 0).all()), fmt
+        R.check(h, hw, htol, "h")
 
 
 class Experts:
