@@ -764,7 +764,7 @@ mxq_status moe_combine_backward(const void* dy, mxq_out_dtype dy_dtype, const fl
  *   h       : BF16 (M, inter);  gate_up: BF16 (M, 2 inter) = (g | u), NULL = not written.
  *   Requires inter % 8 == 0, K % 32 == 0 (BF16: % 8), both <= 2^22, 2 inter rows of B below 2^31 bytes;
  *   every pointer but tA and tB 16-byte aligned. Outputs must not overlap inputs.
- *   K = 0: the sums are 0 (no pointer may be NULL for it).
+ *   K = 0: the sums are 0 (and no operand's pointer may be NULL, as for any other K).
  *   workspace : mxq_workspace_bytes(MXQ_OP_GEMM_SWIGLU, M, 2 inter, K) bytes, 16-byte aligned; NULL where
  *             that is 0 (it is not for few rows and a long K, which is then split).
  * ------------------------------------------------------------------------- */

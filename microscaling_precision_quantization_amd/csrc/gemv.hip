@@ -62,6 +62,8 @@ __device__ __forceinline__ v8bf weights8(uint32_t w, float S) {
 
 // ... the scale codes of a lane's 32 K of a chunk (two E4M3 bytes, or one E8M0 byte) as what multiplies its
 // first and second 16 K.
+// E8M0: the code becomes the exponent field of what the scaled convert takes, which reads that field alone, so that
+// code 0, a +0, is the scale 2^-127 and the weights are BF16 subnormals, which the MFMA keeps.
 template <int FMT>
 __device__ __forceinline__ void scales_of(uint32_t codes, float (&S)[2]) {
   if constexpr (FMT == 2) {

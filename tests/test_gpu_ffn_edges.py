@@ -1,6 +1,6 @@
 """Edges of the gated feed-forward block and of the 4-bit matrix-vector products on the GPU: expert weights
-past 32-bit offsets, a single row out of a buffer of any width, sums over no K, the backward against BF16 weight
-transposes."""
+past 32-bit offsets, a single row out of a buffer of any width, sums over no K, scale codes at the ends of
+their range, the backward against BF16 weight transposes."""
 
 import pytest
 import torch
@@ -101,6 +101,30 @@ def test_sums_over_no_k(M, I):
                 d.data_ptr(), h.data_ptr(), None, 0)
         assert bool((d == 0).all()), fmt
         R.check(h, hw, htol, "h")
+
+
+@pytest.mark.parametrize("code", [0, 1, 3, 252])
+@pytest.mark.parametrize("rows", [1, 5, 20, 40])
+def test_mxfp4_scale_codes_at_the_ends(code, rows):
+    """Weights of q 2^(code - 127) from BF16's subnormal range to its largest, x such that the sums are ordinary
+    numbers; plain, gated, over experts with few choices and with many, and down."""
+    K, I = 160, 40
+    g = gen(rows + code)
+    x = (randn(g, rows, K) * 2.0 ** (120 if code < 100 else -112)).to(BF)
+    assert bool(torch.isfinite(x).all())
+    q = torch.randint(0, 256, (2 * I, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.full((2 * I, K // 32), code, dtype=torch.uint8, device="cuda")
+    w = R.wide("mxfp4", q, s)
+    y, err = R.product(x.double(), w)
+    R.check(mxq.gemv_block_scaled(B.MXFP4, x, q, s), y, err + 2 * R.F32 * y.abs(), "y")
+    want, tol, _ = R.gated(y, err)
+    R.check(mxq.gemv_swiglu(B.MXFP4, x, q, s), want, tol, "h")
+    idx = torch.zeros((rows, 1), dtype=torch.int32, device="cuda")
+    got = mxq.moe_decode_gate_up(B.MXFP4, x, idx, q, s, experts=1)
+    R.check(got[:, 0], want, tol, "h of the expert")
+    wt = torch.full((rows, 1), 0.5, device="cuda")
+    o = mxq.moe_decode_down(B.MXFP4, x[:, None].contiguous(), idx, wt, q, s, experts=1)
+    R.check(o, 0.5 * y, err + 2 * R.F32 * y.abs(), "down")
 
 
 class Experts:
