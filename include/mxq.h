@@ -778,7 +778,10 @@ mxq_status gemm_swiglu(mxq_format fmt, int64_t M, int64_t inter, int64_t K, cons
  * SwiGLU to the two projections, in one kernel:
  *   dh = A_hat B_hat^T, sums as gemm_block_scaled's (A: the output's gradient, B: W_d^T);
  *   s = sigma(g);  dg = dh u s (1 + g (1 - s));  du = dh g s;  and h = g s u made again.
- *   dh is not stored; each output is rounded to BF16 once.
+ *   dh is not stored; each output is rounded to BF16 once, from a binary32 evaluation on the sum dh that is within
+ *   2^-17 of the exact function for du and h, and for dg within 2^-17 of |dh u| s (1 + |g| (1 - s)), the size of the
+ *   terms that are added (they cancel around g = -1.27846, where dg is 0); plus 2^-125 (1 + |g|) times |dh|, |u| and
+ *   |dh u|.
  *   fmt       : MXQ_BF16, or MXQ_MXFP8 (A the rowwise copy of the gradient, B the columnwise copy
  *               of W_d). A (M, K), B (inter, K): K the block's output width.
  *   gate_up   : (M, 2 inter) gu_dtype, BF16 as gemm_swiglu keeps it, or FP32.

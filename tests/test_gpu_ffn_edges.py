@@ -1,6 +1,6 @@
 """Edges of the gated feed-forward block and of the 4-bit matrix-vector products on the GPU: expert weights
 past 32-bit offsets, a single row out of a buffer of any width, sums over no K, scale codes at the ends of
-their range, the backward against BF16 weight transposes."""
+their range, gates around the zero of SwiGLU's derivative, the backward against BF16 weight transposes."""
 
 import pytest
 import torch
@@ -125,6 +125,24 @@ def test_mxfp4_scale_codes_at_the_ends(code, rows):
     wt = torch.full((rows, 1), 0.5, device="cuda")
     o = mxq.moe_decode_down(B.MXFP4, x[:, None].contiguous(), idx, wt, q, s, experts=1)
     R.check(o, 0.5 * y, err + 2 * R.F32 * y.abs(), "down")
+
+
+def test_gates_around_the_zero_of_the_derivative():
+    """silu'(g) vanishes at g = -1.27846...: the two terms of 1 + g (1 - sigma) cancel there, and d_gate is held
+    to the size of what is added up, not to its own."""
+    zero = torch.tensor([-1.2784645427610738], dtype=torch.float64, device="cuda")
+    steps = torch.arange(-200, 200, device="cuda", dtype=torch.float64)
+    g = (zero + torch.sign(steps) * torch.exp2(steps.abs() / 8 - 26)).float()
+    M, I = g.numel(), 8
+    gate_up = torch.ones(M, 2 * I, device="cuda")
+    gate_up[:, :I] = g[:, None]
+    d = torch.ones(M, 8, dtype=BF, device="cuda")
+    w = torch.zeros(I, 8, dtype=BF, device="cuda")
+    w[:, 0] = 1.0
+    dgu, h = mxq.gemm_swiglu_backward(B.BF16, d, None, w, None, gate_up)
+    (want, tol), (hw, htol) = R.through(torch.ones(M, I, dtype=torch.float64, device="cuda"), 0.0, gate_up)
+    R.check(dgu, want, tol, "d_gate_up")
+    R.check(h, hw, htol, "h")
 
 
 class Experts:
