@@ -804,7 +804,8 @@ mxq_status gemm_swiglu_backward(mxq_format fmt, int64_t M, int64_t inter, int64_
  *              MXQ_BF16_NVFP4T (B, sB, tB: the forward's NVFP4 W_d, (K, inter) an expert, read
  *              transposed as grouped_gemm_block_scaled reads it; inter % 16 == 0,
  *              K inter / 2 < 2^31). A: BF16 (total, K); the other tensors as gemm_swiglu_backward's,
- *              `total` rows. sB and tB are unused with MXQ_BF16.
+ *              `total` rows. sB and tB are unused with MXQ_BF16. A dense block's backward against its NVFP4 W_d
+ *              is that of one group (offsets 0 and total).
  *   workspace: mxq_workspace_bytes(MXQ_OP_GROUPED_SWIGLU, groups, 0, 0) bytes, 16-byte aligned; NULL where
  *             that is 0 (up to 256 groups).
  * ------------------------------------------------------------------------- */

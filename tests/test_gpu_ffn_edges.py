@@ -9,7 +9,7 @@ import microscaling_precision_quantization_amd as mxq
 from microscaling_precision_quantization_amd import binding as B
 from microscaling_precision_quantization_amd import pipeline
 from tests import ffn_ref as R
-from tests.test_gpu_ffn import BF, FMT, gen, randn, weights4
+from tests.test_gpu_ffn import BF, FMT, gen, randn, test_grouped_gemm_swiglu_backward as grouped_backward, weights4
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,9 @@ def test_backward_without_its_weight_transposes_is_refused(through):
         b.backward(c.d_o, d_gu)
     b.dequantize_weights()
     b.backward(c.d_o, d_gu)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_dense_backward_against_nvfp4_weights_as_one_group(f32):
+    """A dense block's gradient against the forward's NVFP4 W_d: one expert of all rows."""
+    grouped_backward("nvfp4", 272, 72, [300], [0], f32)
