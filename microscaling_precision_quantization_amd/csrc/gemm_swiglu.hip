@@ -9,9 +9,10 @@
 // through LDS) runs beside another tile's main loop only where two workgroups share a CU, so large dense tiles pay
 // for it in full. 16384 x 7168 -> 2 x 2048 BF16 with (g | u) kept 786-811 us (1.19-1.22 PFLOP/s; a library product
 // alone 690), its backward 442-452 (floor 345); 2011 x 2048 -> 2 x 4096 MXFP8 56-59 (48), backward 44-47 (24: 512
-// tiles of 128 x 128, two a CU, which start and end together, so that neither hides the other's start or epilogue); 4096 tokens, 8 of 128 experts, 2048 -> 2 x 768
-// NVFP4 244 (148: conversions, 263 rows an expert on 128-row tiles), backward against the NVFP4 W_d 245 (109 in
-// bytes: FP32 (g | u) read and dGU written behind a main loop that converts the weights).
+// tiles of 128 x 128, two a CU, which start and end together, so that neither hides the other's start or
+// epilogue); 4096 tokens, 8 of 128 experts, 2048 -> 2 x 768 NVFP4 244 (148: conversions, 263 rows an expert on
+// 128-row tiles), backward against the NVFP4 W_d 245 (109 in bytes: FP32 (g | u) read and dGU written behind a
+// main loop that converts the weights). Dense NVFP4, 16384 x 7168 -> 2 x 2048 760 (690).
 // SwiGLU experts whose gate and up projections enter one fused GEMM: remio.ai ("Miles Blackwell RL"),
 // section "Un Cuantizador Compartido Es el Mecanismo Real".
 #include "gemm_tile.h"
